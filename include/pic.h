@@ -91,6 +91,10 @@ enum { PIC_KIND_GQA = 0, PIC_KIND_MLA = 1 };
  * layout [EPIC] "Mathematical Foundations" 1. prints. */
 enum { PIC_PAIRING_NEOX_HALF = 0, PIC_PAIRING_INTERLEAVED = 1 };
 enum { PIC_SCALING_NONE = 0, PIC_SCALING_LLAMA3 = 1 };
+/* Output types of pic_attend_paged. */
+enum { PIC_F32 = 0, PIC_BF16 = 1 };
+#define PIC_MAX_AXES 4       /* position axes of pic_write_tokens */
+#define PIC_STATUS_BYTES 256 /* the status header at the start of every workspace */
 
 /* Device status word bits (pic_query_device_status). */
 #define PIC_DEV_BAD_BLOCK 0x1u /* a block-table entry was < 0 or >= num_cache_blocks */
@@ -99,6 +103,8 @@ enum { PIC_SCALING_NONE = 0, PIC_SCALING_LLAMA3 = 1 };
 #define PIC_DEV_BAD_DOCS 0x8u  /* chunking: document offsets not non-decreasing within [0, n_tokens] */
 #define PIC_DEV_CAPACITY 0x10u /* chunking: more chunks than capacity; the rest were not written */
 #define PIC_DEV_BAD_SPAN 0x20u /* fingerprints: a span outside [0, n_tokens] or with end < start */
+#define PIC_DEV_BAD_LENGTH 0x40u /* decode loop: a sequence length below 0 or beyond its limit */
+#define PIC_DEV_BAD_POS 0x80u  /* token writes: a position beyond +-PIC_MAX_ABS_DELTA */
 
 /*
  * Model geometry and RoPE settings.
@@ -570,6 +576,151 @@ pic_status pic_attend_decode(pic_ctx* ctx, const pic_plan* const* plans, int32_t
                              const void* k_cache, const void* v_cache, int64_t cache_layer_stride_bytes,
                              int32_t layer_begin, int32_t num_layers, float* out, float* lse,
                              void* d_workspace, size_t workspace_bytes, pic_stream_t stream);
+
+/* ------------------------------------------- decode loop over the cache */
+
+/*
+ * The calls a decode loop makes after the stitch, per layer or per step:
+ * write the new tokens into their cache slots, attend them to the cached
+ * sequence, and, when the cache is to stay bounded, evict the tokens that
+ * received least attention.  The pages have no counterpart to them.
+ *
+ * A slot is a token's place in its request's block table: slot s of request r
+ * is row s % block_size of block d_block_tables[r][s / block_size].  After a
+ * stitch the slot of a token is its position; after an eviction it need not
+ * be.  Sequence lengths (slots in use) are device arrays, so a captured graph
+ * of these calls can be replayed while the sequences grow.
+ *
+ * weights: device float [num_cache_blocks][weight_heads][block_size], one
+ * layer of it beside each layer of the cache: the attention weight each
+ * cached token has received so far.  weight_heads is num_kv_heads (each KV
+ * head counts the query heads that read it) or 1 (all query heads together).
+ *
+ * The three calls upload nothing, allocate nothing and may be captured.  Their
+ * status word is sticky: kernels only add PIC_DEV_* bits to the first word of
+ * the workspace, so zero its first PIC_STATUS_BYTES bytes when it is made, and
+ * again after an error; pic_query_device_status reads it whenever the caller
+ * wants to know, for instance once in many steps.  Calls whose work may run at
+ * the same time need workspaces of their own.  Every buffer is memory of the
+ * current device (PIC_ERR_UNSUPPORTED / PIC_ERR_INVALID_ARG otherwise).
+ */
+
+/*
+ * New tokens of one layer.  Frequency f turns its pair by the angle
+ * d_pos[freq_axis[f]][i] * theta_f: with one axis the usual rotary position,
+ * with several (time, height, width) each frequency follows its axis.
+ * Negative positions turn backwards: the call with -d_pos is the inverse (and
+ * the gradient) of the rotation.
+ *   n_tokens     tokens, in any order and of any requests.
+ *   num_q_heads  query heads; 0: no queries (q and q_out are ignored).
+ *   n_axes       1 .. PIC_MAX_AXES.
+ *   freq_axis    host [rope_dim / 2], the axis of each frequency; NULL: axis 0.
+ *   d_pos        device int32 [n_axes][n_tokens], |pos| <= PIC_MAX_ABS_DELTA; a
+ *                token with a position beyond that raises PIC_DEV_BAD_POS and
+ *                is left out, its query too.
+ *   q, q_out     bf16 [n_tokens][num_q_heads][head_dim], q_stride and
+ *                q_out_stride bytes between tokens (heads dense), so that
+ *                slices of a fused projection need no copy; q_out may be q.
+ *   k, v         bf16 [n_tokens][num_kv_heads][head_dim], their strides
+ *                likewise; both NULL: queries only.  MLA: v NULL; only the rope
+ *                slice of a row (and of each query head) is turned.
+ *   d_req        device int32 [n_tokens], block-table row of each token.
+ *   d_slot       device int32 [n_tokens], its slot; below 0: its key and value
+ *                are not written (padding).  A (request, slot) pair may occur
+ *                once.
+ */
+typedef struct pic_new_tokens {
+  int32_t n_tokens;
+  int32_t num_q_heads;
+  int32_t n_axes;
+  const uint8_t* freq_axis;
+  const int32_t* d_pos;
+  const void* q;
+  int64_t q_stride;
+  void* q_out;
+  int64_t q_out_stride;
+  const void* k;
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  const int32_t* d_req;
+  const int32_t* d_slot;
+} pic_new_tokens;
+
+/*
+ * Turns the tokens' queries into q_out and writes their turned keys and their
+ * values into one layer of the paged cache; a weight of a written slot starts
+ * at 0 (d_weights may be NULL).  Rotation: fp32 from exactly reduced angles,
+ * one rounding to bf16.  A slot outside the table or in a block outside the
+ * cache is not written and raises PIC_DEV_BAD_BLOCK.  q, k and v may not
+ * overlap the outputs, but q_out may be q.  d_workspace: PIC_STATUS_BYTES
+ * bytes, 256-byte aligned.
+ */
+pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* tokens, void* k_cache, void* v_cache,
+                            const int32_t* d_block_tables, int32_t n_tables, int32_t max_blocks, float* d_weights,
+                            int32_t weight_heads, void* d_workspace, size_t workspace_bytes, pic_stream_t stream);
+
+/* Workspace bytes of pic_attend_paged (for sequences up to max_seq_len). */
+size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32_t num_q_heads, int32_t max_seq_len,
+                                        int32_t with_weights);
+
+/*
+ * One new token per request attends to its cached sequence, slots
+ * [0, d_seq_lens[r]) of one layer (GQA models; any number of query heads per KV
+ * head):
+ *   s_t = softmax_scale * q . k_t,  p = softmax(s),  out = sum_t p_t v_t,
+ *   lse = log sum_t exp(s_t),  and weights[slot t] += sum over query heads p_t.
+ * A request of length 0 gets out 0 and lse -inf.  A length below 0 or above
+ * max_seq_len raises PIC_DEV_BAD_LENGTH and counts as 0; slots in a block outside
+ * the cache raise PIC_DEV_BAD_BLOCK and are left out.  What the cache holds
+ * behind a sequence's end does not matter.
+ *   q           bf16 [n_req][num_q_heads][head_dim], q_stride bytes between
+ *               requests, rotated (pic_write_tokens' q_out).
+ *   max_seq_len longest sequence (host bound, at most max_blocks * block_size);
+ *               sizes the workspace when weights are kept.
+ *   out         [n_req][num_q_heads][head_dim] of out_type PIC_F32 or PIC_BF16.
+ *   lse         float [n_req][num_q_heads] or NULL.
+ *   d_weights   one layer of the weights, or NULL.
+ * Requests may share blocks, but with d_weights a block may appear once in
+ * all tables.  Results do not depend on timing: no atomics are summed.
+ */
+pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_req, int32_t num_q_heads,
+                            float softmax_scale, const void* k_cache, const void* v_cache,
+                            const int32_t* d_block_tables, int32_t max_blocks, const int32_t* d_seq_lens,
+                            int32_t max_seq_len, void* out, int32_t out_type, float* lse, float* d_weights,
+                            int32_t weight_heads, void* d_workspace, size_t workspace_bytes, pic_stream_t stream);
+
+/* Workspace bytes of pic_evict_tokens. */
+size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t n_req, int32_t weight_heads);
+
+/*
+ * Cuts sequences longer than `budget` to budget tokens, in place, in num_layers
+ * layers starting at k_cache / v_cache / d_weights (layer strides in bytes).
+ * Per layer, request and weight head the first n_first and last n_recent
+ * tokens stay, and of those between the ones of largest weight, equal weights
+ * to the lower slot (NaN counts below everything, -0 as 0).  The kept tokens
+ * move, in order, to slots [0, budget) with their values and weights.
+ *   renumber  0: keys keep the positions they were rotated for (the caller goes
+ *             on counting positions); 1: a key moving from slot s to slot j is
+ *             turned by R(j - s), all axes alike (the sequence is again one of
+ *             positions 0 .. budget - 1).
+ *   d_kept    device int32 [num_layers][n_req][weight_heads][budget]: the slots
+ *             that stayed, ascending; -1 past a shorter sequence's end.
+ *   d_new_lens  device int32 [n_req]: min(length, budget); may be d_seq_lens.
+ * Shorter sequences stay as they are.  Slots from the new length on keep
+ * stale rows.  A request with a length below 0 or beyond its table (renumber:
+ * or beyond PIC_MAX_ABS_DELTA) or with a block outside the cache is left as it
+ * is, its kept list -1, its length unchanged, and raises PIC_DEV_BAD_LENGTH /
+ * PIC_DEV_BAD_BLOCK.  A block in use may appear once in all tables, and no
+ * other request or registered chunk may rely on it: its rows are overwritten
+ * (so not blocks mapped by alias = 1 while their chunk is to be kept).
+ */
+pic_status pic_evict_tokens(pic_ctx* ctx, int32_t num_layers, void* k_cache, void* v_cache,
+                            int64_t cache_layer_stride_bytes, float* d_weights, int64_t weights_layer_stride_bytes,
+                            int32_t weight_heads, const int32_t* d_block_tables, int32_t n_req, int32_t max_blocks,
+                            const int32_t* d_seq_lens, int32_t budget, int32_t n_first, int32_t n_recent,
+                            int32_t renumber, int32_t* d_kept, int32_t* d_new_lens, void* d_workspace,
+                            size_t workspace_bytes, pic_stream_t stream);
 
 /* ------------------------------------------- content-defined chunking */
 

@@ -55,7 +55,21 @@ Pin status of each function (what outside fact each is checked against is in
 * ``xxh64``              pinned against the system xxHash library (libxxhash)
                          when it is installed
 * ``s1_windows``         pinned (brute force)
+* ``rotate_axes``        pinned (equal axes give the one-axis rotation; each
+                         axis turns its own frequencies only)
+* ``attend_paged``       pinned (weights add up to the query heads; equals
+                         ``attention_decode`` of the gathered rows)
+* ``kept_slots`` / ``evict_tokens`` pinned (brute force over subsets; keys
+                         renumbered equal forward RoPE at the new positions)
 """
+
+from .decode_oracle import (  # noqa: F401
+    rotate_axes,
+    write_tokens,
+    attend_paged,
+    kept_slots,
+    evict_tokens,
+)
 
 from .cdc_oracle import (  # noqa: F401
     GEAR_WINDOW,

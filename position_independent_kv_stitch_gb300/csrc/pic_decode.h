@@ -1,0 +1,142 @@
+// Internal interface of the decode-loop operators (pic_write_tokens,
+// pic_attend_paged, pic_evict_tokens): parameters shared by their host entries
+// (pic_decode.cpp) and their kernels (pic_write.cu, pic_paged.cu,
+// pic_evict.cu).  Not part of the public ABI.
+//
+// Everything a launch needs beyond the caller's device buffers travels in its
+// parameters (frequencies included), so the calls upload nothing, wait for
+// nothing and can be captured into a graph.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "pic.h"
+#include "pic_internal.h"
+
+namespace pic {
+
+// What the entries need of a context (defined in pic_host.cpp).
+struct CtxView {
+  const pic_model_desc* model;
+  const float2* freq;  // rope_dim/2 frequencies in turns, (hi, lo)
+  int32_t num_cache_blocks;
+};
+CtxView ctx_view(const pic_ctx* ctx);
+
+constexpr int kMaxFreqs = 128;  // rope_dim / 2 of the widest head
+
+// The paged cache as the kernels see it: one layer's tables and geometry.
+struct PagedView {
+  const int32_t* tables;     // [n_tables][max_blocks]
+  int32_t n_tables;
+  int32_t max_blocks;
+  int32_t num_cache_blocks;
+  int32_t block_size;
+  int32_t block_shift;       // log2(block_size), or -1 when it is no power of two
+};
+
+struct FreqTable {
+  float2 turns[kMaxFreqs];
+};
+
+struct WriteParams {
+  PagedView paged;
+  FreqTable freq;
+  uint8_t axis[kMaxFreqs];   // position axis of each frequency
+  const int32_t* pos;        // [n_axes][n_tokens]
+  int32_t n_axes;
+  int32_t n_tokens;
+  const int32_t* req;        // [n_tokens]
+  const int32_t* slot;       // [n_tokens], < 0: not written
+  const uint8_t* q;
+  uint8_t* q_out;
+  const uint8_t* k;
+  const uint8_t* v;
+  int64_t q_stride, q_out_stride, k_stride, v_stride;  // bytes between tokens
+  int32_t q_heads, kv_heads;
+  int32_t head_bytes;        // bytes of one head (MLA: of the row)
+  int32_t rope_off;          // byte offset of the rope slice in a head
+  int32_t lph_shift;         // log2 of the lanes that turn one head (8 frequencies each)
+  int32_t q_copy_chunks;     // 16-byte chunks of a query head that are only copied (MLA: its latent; 0 in place)
+  int32_t k_copy_chunks;     // the same of a key row
+  int32_t rot_parts, copy_parts;  // warp tasks of one token
+  int32_t rot_iters;         // head steps of one rotating task
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* weights;            // [blocks][weight_heads][block_size] or null
+  int32_t weight_heads;
+  uint32_t* status;
+};
+cudaError_t launch_write(const WriteParams& p, int pairing, int sm_count, cudaStream_t s);
+
+// ---- paged attention
+constexpr int kPagedTile = 16;          // positions of one step of a warp
+constexpr int kPagedWarps = 8;          // warps per CTA, each with its own ring
+constexpr int kPagedMaxCtas = 256;      // grid bound (workspace sizing)
+constexpr int kPagedMinTiles = 4;       // least tiles of one warp's range
+
+struct PagedParams {
+  PagedView paged;
+  const uint8_t* q;
+  int64_t q_stride;          // bytes between requests
+  const int32_t* lens;       // [n_req]
+  int32_t n_req;
+  int32_t max_len;
+  int32_t q_heads, kv_heads, group;
+  int32_t passes;            // 16-head passes over a group
+  int32_t v_heads;           // kv_heads * passes: what warps are dealt to
+  int32_t parts;             // ranges per virtual head
+  float scale_log2;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  int32_t row_bytes;         // one token, all KV heads
+  float* rec_acc;            // [parts + n_req][q_heads][D]
+  float2* rec_ml;            // [parts + n_req][q_heads]: running max (log2 units) and sum
+  float* lse2;               // [n_req][q_heads] log2 units (with weights)
+  float* scores;             // [q_heads][score_stride] log2 units (with weights)
+  int64_t score_stride;
+  void* out;
+  int32_t out_bf16;
+  float* lse;
+  float* weights;
+  int32_t weight_heads;
+  uint32_t* status;
+};
+size_t paged_smem(int head_dim);
+int paged_warps_per_cta(int head_dim);
+cudaError_t launch_paged(const PagedParams& p, int head_dim, int grid, int sm_count, cudaStream_t s);
+
+// ---- eviction
+struct EvictUnit {           // per (layer, request, weight head), in the workspace
+  int32_t n_keep;            // kept tokens (0: nothing to move)
+  int32_t first_moved;       // kept tokens before this rank stay where they are
+};
+struct EvictParams {
+  PagedView paged;
+  FreqTable freq;
+  int32_t layers, n_req;
+  int32_t kv_heads, weight_heads;
+  int32_t head_bytes;        // bytes of one head (MLA: of the row)
+  int32_t rope_off;
+  int32_t rope_items;        // 32-byte items of a head that are turned when renumbering
+  const int32_t* lens;
+  int32_t max_len;           // longest legal length
+  int32_t budget, n_first, n_recent;
+  int32_t renumber;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int64_t cache_ls;
+  float* weights;
+  int64_t weights_ls;        // bytes
+  int32_t* kept;             // [layers][n_req][weight_heads][budget]
+  int32_t* new_lens;
+  int32_t* next_lens;        // workspace [n_req]: what new_lens becomes
+  EvictUnit* units;          // workspace [layers * n_req * weight_heads]
+  uint32_t* status;
+};
+cudaError_t launch_evict(const EvictParams& p, int pairing, int sm_count, cudaStream_t s);
+
+}  // namespace pic

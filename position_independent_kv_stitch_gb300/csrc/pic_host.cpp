@@ -25,6 +25,7 @@
 #include <memory>
 #include <vector>
 
+#include "pic_decode.h"
 #include "pic_internal.h"
 
 using pic::RunDesc;
@@ -1944,7 +1945,8 @@ pic_status pic_query_device_status(pic_ctx* ctx, const void* d_ws, pic_stream_t 
     return fail(ctx, PIC_ERR_DEVICE_CHECK,
                 "kernel reported device status 0x%x (bit 0x1: block-table entry outside the cache, table row %u, "
                 "position %u; bit 0x2: a bounded wait gave up; 0x4: token id outside the Gear table; "
-                "0x8: bad document offsets; 0x10: more chunks than capacity; 0x20: bad span)",
+                "0x8: bad document offsets; 0x10: more chunks than capacity; 0x20: bad span; 0x40: sequence length outside "
+                "its table; 0x80: position beyond 2^24 - 1)",
                 h.status, h.bad_req, h.bad_pos);
   return ok(ctx);
 }
@@ -2232,6 +2234,8 @@ pic_status pic_attend_decode(pic_ctx* ctx, const pic_plan* const* plans, int32_t
 namespace pic {
 
 pic_status set_error(pic_ctx* ctx, pic_status st, const char* msg) { return fail(ctx, st, "%s", msg); }
+
+CtxView ctx_view(const pic_ctx* ctx) { return CtxView{&ctx->model, ctx->freq_turns.data(), ctx->num_cache_blocks}; }
 
 pic_status stitch_with_scratch(pic_ctx* ctx, const pic_plan* const* plans, int32_t n_req,
                                const void* k_pool, const void* v_pool, int64_t pool_ls,

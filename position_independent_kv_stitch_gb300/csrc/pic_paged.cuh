@@ -1,0 +1,32 @@
+// Device helpers of the decode-loop operators: block-table lookups with their
+// bounds check, and the errors they raise.
+#pragma once
+
+#include "pic_decode.h"
+
+namespace pic {
+namespace dev {
+
+__device__ __forceinline__ int block_of(const PagedView& v, int slot) {
+  return v.block_shift >= 0 ? slot >> v.block_shift : slot / v.block_size;
+}
+
+// Absolute cache row of a request's slot, -1 when the table has no such slot
+// or names a block outside the cache.
+__device__ __forceinline__ int64_t paged_row(const PagedView& v, int req, int slot) {
+  const int b = block_of(v, slot);
+  if (b >= v.max_blocks) return -1;
+  const int32_t block = __ldg(v.tables + static_cast<int64_t>(req) * v.max_blocks + b);
+  if (block < 0 || block >= v.num_cache_blocks) return -1;
+  return static_cast<int64_t>(block) * v.block_size + (slot - b * v.block_size);
+}
+
+// The status word and, beside it, where the last bad block was met (WsHeader).
+__device__ __forceinline__ void raise_block(uint32_t* status, int req, int slot) {
+  atomicOr(status, static_cast<uint32_t>(PIC_DEV_BAD_BLOCK));
+  status[1] = static_cast<uint32_t>(req);
+  status[2] = static_cast<uint32_t>(slot);
+}
+
+}  // namespace dev
+}  // namespace pic

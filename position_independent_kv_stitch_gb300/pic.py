@@ -33,6 +33,11 @@ PIC_DEV_BAD_TOKEN = 0x4
 PIC_DEV_BAD_DOCS = 0x8
 PIC_DEV_CAPACITY = 0x10
 PIC_DEV_BAD_SPAN = 0x20
+PIC_DEV_BAD_LENGTH = 0x40
+PIC_DEV_BAD_POS = 0x80
+PIC_F32, PIC_BF16 = 0, 1
+PIC_MAX_AXES = 4
+PIC_STATUS_BYTES = 256
 PIC_VARIANT_REGISTERS, PIC_VARIANT_BULK_PIPELINE = 0, 1
 PIC_VARIANT_TENSOR_CORE_TMEM, PIC_VARIANT_WARP_MMA = 2, 3
 PIC_SEG_COPY_POOL, PIC_SEG_COPY_BLOCKS, PIC_SEG_MAPPED = 0, 1, 2
@@ -69,6 +74,16 @@ class pic_request_desc(ctypes.Structure):
 class pic_shift_seg(ctypes.Structure):
     _fields_ = [("req", ctypes.c_int32), ("start_pos", ctypes.c_int32),
                 ("num_tokens", ctypes.c_int32), ("delta", ctypes.c_int32)]
+
+
+class pic_new_tokens(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+        ("freq_axis", ctypes.c_char_p), ("d_pos", ctypes.c_void_p),
+        ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+        ("q_out_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+        ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64), ("d_req", ctypes.c_void_p), ("d_slot", ctypes.c_void_p),
+    ]
 
 
 _c_void_p = ctypes.c_void_p
@@ -124,10 +139,22 @@ _SIGNATURES = {
     "pic_fingerprint_spans": (ctypes.c_int, [_c_void_p, _i64, _c_void_p, _c_void_p, _i64, ctypes.c_uint64,
                                              _c_void_p, _c_void_p, _c_void_p]),
     "pic_s1_windows": (ctypes.c_int, [_i64, _i64, _i32, _P(_i64), _P(_i64), _i64, _P(_i64)]),
+    "pic_write_tokens": (ctypes.c_int, [_c_void_p, _P(pic_new_tokens), _c_void_p, _c_void_p, _c_void_p, _i32, _i32,
+                                        _c_void_p, _i32, _c_void_p, _sz, _c_void_p]),
+    "pic_attend_paged_workspace_bytes": (_sz, [_c_void_p, _i32, _i32, _i32, _i32]),
+    "pic_attend_paged": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i32, _i32, ctypes.c_float, _c_void_p, _c_void_p,
+                                        _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _i32,
+                                        _c_void_p, _sz, _c_void_p]),
+    "pic_evict_workspace_bytes": (_sz, [_c_void_p, _i32, _i32, _i32]),
+    "pic_evict_tokens": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _i32, _c_void_p,
+                                        _i32, _i32, _c_void_p, _i32, _i32, _i32, _i32, _c_void_p, _c_void_p, _c_void_p,
+                                        _sz, _c_void_p]),
     "pic_debug_stall_next_launch": (ctypes.c_int, [_c_void_p, _i32, _u32]),
 }
 
 _lib = None
+# (cache blocks, block size, KV heads, head dim) of each live context, by handle
+_geometry = {}
 
 
 def lib_path() -> str:
@@ -210,10 +237,12 @@ def pic_create(kind, num_layers, num_kv_heads, head_dim, rope_dim, rope_offset, 
     out = ctypes.c_void_p()
     st = load().pic_create(ctypes.byref(d), int(num_cache_blocks), ctypes.byref(out))
     _check(st, None)
+    _geometry[out.value] = (int(num_cache_blocks), int(block_size), int(num_kv_heads), int(head_dim))
     return out
 
 
 def pic_destroy(ctx):
+    _geometry.pop(getattr(ctx, "value", ctx), None)
     load().pic_destroy(ctx)
 
 
@@ -635,6 +664,185 @@ def pic_attend_decode(ctx, plans, source, q, softmax_scale, k_pool, v_pool, k_ca
                                   _ptr(workspace), workspace.numel() * workspace.element_size(),
                                   _stream_handle(stream))
     _check(st, ctx)
+
+
+# --------------------------------------------------- decode loop over the cache
+
+def _device_of(first, *others):
+    """The buffers' device; one of another device or of the host is refused."""
+    dev = first.device
+    for t in (first,) + others:
+        if t is not None and t.device != dev or not first.is_cuda:
+            raise ValueError("every tensor must be on one CUDA device")
+    return dev
+
+
+def _call_on(dev, stream, fn, ctx):
+    """fn(stream handle) with the buffers' device current."""
+    import torch
+    if dev.index == torch.cuda.current_device():
+        _check(fn(_stream_handle(stream)), ctx)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(_stream_handle(stream)), ctx)
+
+
+def _token_rows(t, name, heads=None):
+    """[tokens][heads][dim] bf16 with dense heads; returns the bytes between tokens."""
+    if not _is_bf16(t) or t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be bf16 [tokens][heads][head_dim] with dense heads")
+    return t.stride(0) * 2
+
+
+def _check_cache(ctx, t, name, dim):
+    """A cache tensor ([layers][blocks][block_size][kv_heads][head_dim] for dim
+    5, one layer of it for dim 4) that holds the context's blocks and rows."""
+    if not _is_bf16(t) or t.dim() != dim or not (t if dim == 4 else t[0]).is_contiguous():
+        raise ValueError(f"{name} must be a bf16 cache tensor of {dim} dims with contiguous rows")
+    blocks, bs, heads, head_dim = _geometry.get(ctx.value, (0,) + tuple(t.shape[-3:]))
+    if t.shape[-4] < blocks or tuple(t.shape[-3:]) != (bs, heads, head_dim):
+        raise ValueError(f"{name} must hold the context's {blocks} blocks of {bs} rows [{heads}][{head_dim}]")
+
+
+def _weight_heads(weights, cache):
+    """Weight heads of a weights tensor [..][blocks][weight_heads][block_size] beside a cache."""
+    import torch
+    if weights is None:
+        return 0
+    if weights.dtype != torch.float32 or weights.dim() != cache.dim() - 1 or \
+            not (weights if weights.dim() == 3 else weights[0]).is_contiguous() or \
+            weights.shape[-3] != cache.shape[-4] or weights.shape[-1] != cache.shape[-3] or \
+            weights.shape[:-3] != cache.shape[:-4]:
+        raise ValueError("weights must be float32 [blocks][weight_heads][block_size], shaped as the cache")
+    return int(weights.shape[-2])
+
+
+def _tables_2d(block_tables, rows=None):
+    _check_device_int32(block_tables, "block_tables")
+    if block_tables.dim() != 2 or (rows is not None and block_tables.shape[0] < rows):
+        raise ValueError("block_tables must be [n_req][max_blocks] with a row per request")
+    return int(block_tables.shape[0]), int(block_tables.shape[1])
+
+
+def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_cache, q=None, q_out=None,
+                     freq_axis=None, weights=None, workspace=None, stream=None):
+    """Writes new tokens into one layer of the paged cache and turns their
+    queries.  positions: CUDA int32 [n_tokens] or [n_axes][n_tokens];
+    freq_axis: the axis of each of the rope_dim/2 frequencies (None: axis 0).
+    k, v: bf16 [n_tokens][kv_heads][head_dim], dense heads, any token stride
+    (v None for MLA; both None: queries only).  req, slot: CUDA int32
+    [n_tokens], slot < 0 writes nothing.  k_cache, v_cache: one layer
+    [blocks][block_size][kv_heads][head_dim].  q, q_out: bf16
+    [n_tokens][q_heads][head_dim], q_out may be q.  weights: float32
+    [blocks][weight_heads][block_size], zeroed at the written slots.
+    workspace: uint8, PIC_STATUS_BYTES, zeroed when made (its status is sticky)."""
+    t = pic_new_tokens()
+    _check_device_int32(positions, "positions")
+    t.n_axes, t.n_tokens = (1, int(positions.shape[0])) if positions.dim() == 1 else map(int, positions.shape)
+    if freq_axis is not None:
+        t.freq_axis = bytes(freq_axis)
+    t.d_pos = positions.data_ptr()
+    if q is not None:
+        if q_out is None or q_out.shape != q.shape or q.shape[0] != t.n_tokens:
+            raise ValueError("q and q_out hold one row per token, of one shape")
+        t.num_q_heads = int(q.shape[1])
+        t.q_stride, t.q_out_stride = _token_rows(q, "q"), _token_rows(q_out, "q_out")
+        t.q, t.q_out = q.data_ptr(), q_out.data_ptr()
+    n_tables = max_blocks = heads = 0
+    if k is not None:
+        t.k, t.k_stride = k.data_ptr(), _token_rows(k, "k")
+        if v is not None:
+            t.v, t.v_stride = v.data_ptr(), _token_rows(v, "v")
+        for rows in (k, v):
+            if rows is not None and (rows.shape[0] != t.n_tokens or rows.shape[1:] != k_cache.shape[2:]):
+                raise ValueError("k and v hold one row per token, shaped as the cache's rows")
+        _check_device_int32(req, "req")
+        _check_device_int32(slot, "slot")
+        if req.numel() != t.n_tokens or slot.numel() != t.n_tokens:
+            raise ValueError("req and slot hold one entry per token")
+        t.d_req, t.d_slot = req.data_ptr(), slot.data_ptr()
+        n_tables, max_blocks = _tables_2d(block_tables)
+        for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            if c is not None:
+                _check_cache(ctx, c, name, 4)
+        heads = _weight_heads(weights, k_cache)
+    dev = _device_of(positions, q, q_out, k, v, req, slot, block_tables, k_cache, v_cache, weights, workspace)
+    _call_on(dev, stream, lambda s: load().pic_write_tokens(
+        ctx, ctypes.byref(t), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), n_tables, max_blocks, _ptr(weights), heads,
+        _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0, s), ctx)
+
+
+def pic_attend_paged_workspace_bytes(ctx, n_req: int, num_q_heads: int, max_seq_len: int, with_weights=False) -> int:
+    return int(load().pic_attend_paged_workspace_bytes(ctx, int(n_req), int(num_q_heads), int(max_seq_len),
+                                                       1 if with_weights else 0))
+
+
+def pic_attend_paged(ctx, q, softmax_scale, k_cache, v_cache, block_tables, seq_lens, max_seq_len: int, out, lse=None,
+                     weights=None, workspace=None, stream=None):
+    """One new token per request over its cached sequence (GQA).  q: bf16
+    [n_req][q_heads][head_dim], any request stride; k_cache, v_cache: one layer
+    [blocks][block_size][kv_heads][head_dim]; seq_lens: CUDA int32 [n_req], at
+    most max_seq_len each; out: float32 or bf16 of q's shape; lse: float32
+    [n_req][q_heads] or None; weights: float32
+    [blocks][weight_heads][block_size] or None, each slot's attention weight is
+    added to it.  workspace: uint8, pic_attend_paged_workspace_bytes, its first
+    PIC_STATUS_BYTES zeroed when made."""
+    import torch
+    n_req, hq, d = (int(x) for x in q.shape)
+    stride = _token_rows(q, "q")
+    _check_device_int32(seq_lens, "seq_lens")
+    _, max_blocks = _tables_2d(block_tables, n_req)
+    for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _check_cache(ctx, c, name, 4)
+    if seq_lens.numel() != n_req or d != k_cache.shape[3]:
+        raise ValueError("seq_lens holds one entry per request, q heads of the cache's head_dim")
+    if out.shape != q.shape or not out.is_contiguous() or out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape")
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n_req * hq or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [n_req][q_heads]")
+    heads = _weight_heads(weights, k_cache)
+    dev = _device_of(q, k_cache, v_cache, block_tables, seq_lens, out, lse, weights, workspace)
+    _call_on(dev, stream, lambda s: load().pic_attend_paged(
+        ctx, _ptr(q), stride, n_req, hq, float(softmax_scale), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks,
+        _ptr(seq_lens), int(max_seq_len), _ptr(out), PIC_BF16 if out.dtype == torch.bfloat16 else PIC_F32, _ptr(lse),
+        _ptr(weights), heads, _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace is not None else 0, s), ctx)
+
+
+def pic_evict_workspace_bytes(ctx, num_layers: int, n_req: int, weight_heads: int) -> int:
+    return int(load().pic_evict_workspace_bytes(ctx, int(num_layers), int(n_req), int(weight_heads)))
+
+
+def pic_evict_tokens(ctx, k_cache, v_cache, weights, block_tables, seq_lens, budget: int, kept, new_lens, n_first: int = 0,
+                     n_recent: int = 0, renumber: bool = False, workspace=None, stream=None):
+    """Cuts sequences longer than budget to their n_first first, n_recent last
+    and heaviest other tokens, in place.  k_cache, v_cache: [layers][blocks]
+    [block_size][kv_heads][head_dim] (v None for MLA); weights: float32
+    [layers][blocks][weight_heads][block_size]; seq_lens, new_lens: CUDA int32
+    [n_req] (may be one tensor); kept: CUDA int32
+    [layers][n_req][weight_heads][budget].  renumber: keys are re-rotated to
+    their new slots.  workspace: uint8, pic_evict_workspace_bytes, its first
+    PIC_STATUS_BYTES zeroed when made."""
+    for t, name in ((seq_lens, "seq_lens"), (kept, "kept"), (new_lens, "new_lens")):
+        _check_device_int32(t, name)
+    n_req, layers = int(seq_lens.numel()), int(k_cache.shape[0])
+    _, max_blocks = _tables_2d(block_tables, n_req)
+    for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if c is not None:
+            _check_cache(ctx, c, name, 5)
+            if c.shape != k_cache.shape or (layers > 1 and c.stride(0) != k_cache.stride(0)):
+                raise ValueError("k_cache and v_cache must share a shape and a layer stride")
+    if weights is None:
+        raise ValueError("weights are required")
+    heads = _weight_heads(weights, k_cache)
+    if new_lens.numel() != n_req or kept.numel() != layers * n_req * heads * int(budget):
+        raise ValueError("kept holds [layers][n_req][weight_heads][budget] entries, new_lens one per request")
+    dev = _device_of(k_cache, v_cache, weights, block_tables, seq_lens, kept, new_lens, workspace)
+    _call_on(dev, stream, lambda s: load().pic_evict_tokens(
+        ctx, layers, _ptr(k_cache), _ptr(v_cache), _layer_stride_bytes(k_cache), _ptr(weights), _layer_stride_bytes(weights),
+        heads, _ptr(block_tables), n_req, max_blocks, _ptr(seq_lens), int(budget), int(n_first), int(n_recent),
+        1 if renumber else 0, _ptr(kept), _ptr(new_lens), _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace is not None else 0, s), ctx)
 
 
 def pic_debug_stall_next_launch(ctx, stall_tile: int, max_spins: int = 0):
