@@ -351,10 +351,26 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
       for (int j = 0; j < NT; j += 2) {
         uint32_t b[4];
         ldsm4_t(vb + v_row * D * 2 + (((j + (mi >> 1)) ^ (v_row & 7)) << 4), b);
+        if (F32) {
+          // the tensor cores round sums towards zero: over a long range that
+          // would show in fp32, so each tile's product is added here instead
+          float y0[4] = {}, y1[4] = {};
 #pragma unroll
-        for (int x = 0; x < NP; ++x) {
-          mma(o[j], pa[x], b[0], b[1]);
-          mma(o[j + 1], pa[x], b[2], b[3]);
+          for (int x = 0; x < NP; ++x) {
+            mma(y0, pa[x], b[0], b[1]);
+            mma(y1, pa[x], b[2], b[3]);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            o[j][x] += y0[x];
+            o[j + 1][x] += y1[x];
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < NP; ++x) {
+            mma(o[j], pa[x], b[0], b[1]);
+            mma(o[j + 1], pa[x], b[2], b[3]);
+          }
         }
       }
       __syncwarp();   // every lane has read the stage before it is refilled
