@@ -690,8 +690,9 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
                             int32_t max_seq_len, void* out, int32_t out_type, float* lse, float* d_weights,
                             int32_t weight_heads, void* d_workspace, size_t workspace_bytes, pic_stream_t stream);
 
-/* Workspace bytes of pic_evict_tokens. */
-size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t n_req, int32_t weight_heads);
+/* Workspace bytes of pic_evict_tokens; budget 0: enough for any budget. */
+size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t n_req, int32_t weight_heads,
+                                 int32_t budget);
 
 /*
  * Cuts sequences longer than `budget` to budget tokens, in place, in num_layers
@@ -708,8 +709,8 @@ size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t
  *             that stayed, ascending; -1 past a shorter sequence's end.
  *   d_new_lens  device int32 [n_req]: min(length, budget); may be d_seq_lens.
  * Shorter sequences stay as they are.  Slots from the new length on keep
- * stale rows.  A request with a length below 0 or beyond its table (renumber:
- * or beyond PIC_MAX_ABS_DELTA) or with a block outside the cache is left as it
+ * stale rows.  A request with a length below 0 or beyond its table or the cache
+ * (renumber: or beyond PIC_MAX_ABS_DELTA) or with a block outside the cache is left as it
  * is, its kept list -1, its length unchanged, and raises PIC_DEV_BAD_LENGTH /
  * PIC_DEV_BAD_BLOCK.  A block in use may appear once in all tables, and no
  * other request or registered chunk may rely on it: its rows are overwritten

@@ -7,21 +7,24 @@
 // 0 .. budget - 1; with `renumber` a key that moved from slot s to j is turned
 // by R(j - s), so that the cache is again a sequence of consecutive positions.
 //
-// Two launches:
-//   * k_evict_select, one CTA per (layer, request, weight head): the weight of
-//     the last token that fits is found by radix selection over the weights'
-//     bits (four passes of 8 bits, counts in shared memory), then one ordered
-//     pass writes the kept slots, ascending.
-//   * k_evict_move, one CTA per (layer, request, KV head) and tensor: moves the
-//     rows in place.  Rank j lands on slot j <= its own, so a tile of ranks
-//     may be read long before the tiles below it are written, and may be
-//     written once every thread of the CTA has read it: tiles are read one
-//     ahead, with one barrier between a tile's reads and its writes.  Kept tokens
-//     before the first evicted one are already in place and not touched.
-// Bound: HBM (moved rows once in and once out) for large evictions, the
-// latency of the passes over the weights for small ones.
-#include <cfloat>
-
+// Two launches, the second a programmatic dependent of the first:
+//
+// k_evict_select, one CTA per (layer, request, weight head).  The weights are
+// read once into shared memory (those past its size are read again from L2).
+// The weight of the last token that fits is found by radix selection over the
+// weights' bits, from the top: 11, 11 and 10 bits, counted in shared memory.
+// Then every warp takes a contiguous run of slots, counts what it keeps, and
+// after a scan over the warps writes its kept slots and their weights, in
+// order and without further barriers.
+//
+// k_evict_move, one CTA per tile of kept rows (16 KB) of one tensor, in place.
+// Rank j lands on slot j, never above its own slot, so a tile may be written
+// once every lower tile of its unit has been read, and reading never has to
+// wait.  CTAs take tiles by a ticket, lowest tiles of all units first: a tile's
+// lower neighbours were taken earlier, by CTAs that are running, and the
+// wait for their "read" flags ends whatever the number of resident CTAs (it
+// is bounded all the same).  So one sequence is moved by as many CTAs as it
+// has tiles.  Kept tokens before the first evicted one are in place already.
 #include "pic_decode.h"
 #include "pic_device.cuh"
 #include "pic_paged.cuh"
@@ -32,8 +35,9 @@ namespace {
 using namespace dev;
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
 
 // Order of the weights as unsigned integers: NaN lowest, -0 equal to 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -42,8 +46,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) != 0 ? ~u : (u | 0x80000000u);
 }
 
-// Sum of v over the CTA's threads before this one, and over all of them.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+// Sum of v over the CTA's threads before this one.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
 #pragma unroll
@@ -54,42 +58,49 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
   __syncthreads();   // warp_sums is free
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  int before = 0;
-  total = 0;
+  int s = warp_sums[lane];
 #pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) {
-    const int s = warp_sums[i];
-    before += i < warp ? s : 0;
-    total += s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(kFull, s, o);
+    if (lane >= o) s += up;
   }
+  const int before = __shfl_sync(kFull, s, warp) - warp_sums[warp];
   return before + incl - v;
 }
 
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictParams P) {
-  __shared__ int s_hist[256];
+  asm volatile("griddepcontrol.launch_dependents;");
+  extern __shared__ float s_w[];   // weights of slots [0, cap)
+  __shared__ int s_hist[kBins];
   __shared__ int s_warp[kSelWarps];
+  __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
   __shared__ int s_pick[2];
   __shared__ int s_first_moved;
+  static_assert(kSelWarps == 32, "one lane per warp in the scans");
   const int64_t unit = blockIdx.x;
   const int wh = static_cast<int>(unit % P.weight_heads);
   const int r = static_cast<int>(unit / P.weight_heads % P.n_req);
   const int64_t layer = unit / P.weight_heads / P.n_req;
   int32_t* kept = P.kept + unit * P.budget;
   const int len = __ldg(P.lens + r);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bs = P.paged.block_size;
+
+  // the move's flags and ticket start at 0
+  for (int64_t i = unit * kSelThreads + tid; i < P.n_flags; i += static_cast<int64_t>(gridDim.x) * kSelThreads) P.flags[i] = 0;
 
   // a request whose length or blocks are not legal keeps all it has
   bool bad = len < 0 || len > P.max_len;
   if (bad) {
     if (tid == 0) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_BAD_LENGTH));
   } else {
-    const int blocks = (len + P.paged.block_size - 1) / P.paged.block_size;
+    const int blocks = (len + bs - 1) / bs;
     bool mine = false;
     for (int b = tid; b < blocks; b += kSelThreads) {
       const int32_t block = __ldg(P.paged.tables + static_cast<int64_t>(r) * P.paged.max_blocks + b);
       if (block < 0 || block >= P.paged.num_cache_blocks) {
         mine = true;
-        raise_block(P.status, r, b * P.paged.block_size);
+        raise_block(P.status, r, b * bs);
       }
     }
     bad = __syncthreads_or(mine);
@@ -101,190 +112,262 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     return;
   }
 
-  const uint8_t* wl = reinterpret_cast<const uint8_t*>(P.weights) + layer * P.weights_ls;
-  auto key_of = [&](int slot) -> uint32_t {
-    const int64_t row = paged_row(P.paged, r, slot);
-    const int64_t block = row / P.paged.block_size, at = row - block * P.paged.block_size;
-    return weight_key(*(reinterpret_cast<const float*>(wl) + (block * P.weight_heads + wh) * P.paged.block_size + at));
+  float* wl = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.weights) + layer * P.weights_ls);
+  auto at = [&](int slot) -> float* {
+    const int b = block_of(P.paged, slot);
+    const int64_t block = __ldg(P.paged.tables + static_cast<int64_t>(r) * P.paged.max_blocks + b);
+    return wl + (block * P.weight_heads + wh) * bs + (slot - b * bs);
   };
+  const int cap = P.sel_cap;
+  auto weight_of = [&](int slot) -> float { return slot < cap ? s_w[slot] : __ldcg(at(slot)); };
   const int lo = P.n_first, hi = len - P.n_recent;     // candidates: slots [lo, hi)
   const int want = P.budget - P.n_first - P.n_recent;  // how many of them stay; fewer than hi - lo
-  uint32_t border = 0xffffffffu;                       // key of the last one that stays
-  int ties = 0;                                        // candidates of that key that stay
+  for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+  if (tid == 0) s_first_moved = P.budget;
+#pragma unroll 4
+  for (int s = tid; s < min(len, cap); s += kSelThreads) s_w[s] = __ldcg(at(s));
+  __syncthreads();
+
+  uint32_t border = 0xffffffffu;  // key of the last candidate that stays
+  int ties = 0;                   // candidates of that key that stay
   if (want > 0) {
     uint32_t prefix = 0, mask = 0;
     int left = want;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) s_hist[i] = 0;
-      __syncthreads();
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
       for (int s = lo + tid; s < hi; s += kSelThreads) {
-        const uint32_t k = key_of(s);
-        if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & 255u], 1);
+        const uint32_t k = weight_key(weight_of(s));
+        if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & digits], 1);
       }
       __syncthreads();
-      // digits from the top: the one in which the count reaches `left`
-      int total;
-      const int n = tid < 256 ? s_hist[255 - tid] : 0;
-      const int above = block_scan(n, s_warp, total);
-      if (tid < 256 && above < left && above + n >= left) {
-        s_pick[0] = 255 - tid;
-        s_pick[1] = left - above;
+      // two digits a thread, from the top: the one in which the count reaches `left`
+      const int d = kBins - 1 - 2 * tid;
+      const int n0 = s_hist[d], n1 = s_hist[d - 1];
+      const int above = block_scan(n0 + n1, s_warp);
+      if (above < left && above + n0 + n1 >= left) {
+        const bool first = above + n0 >= left;
+        s_pick[0] = first ? d : d - 1;
+        s_pick[1] = left - above - (first ? 0 : n0);
       }
+      s_hist[d] = s_hist[d - 1] = 0;
       __syncthreads();
       prefix |= static_cast<uint32_t>(s_pick[0]) << shift;
-      mask |= 255u << shift;
+      mask |= digits << shift;
       left = s_pick[1];
-      __syncthreads();
     }
     border = prefix;
     ties = left;
   }
-  if (tid == 0) s_first_moved = P.budget;
-  int n_kept = 0, n_ties = 0;
-  for (int base = 0; base < len; base += kSelThreads) {
-    const int s = base + tid;
+
+  // every warp's run of slots, a multiple of 32
+  const int run = (len + kSelThreads - 1) / kSelThreads * 32;
+  const int begin = min(len, warp * run), end = min(len, begin + run);
+  auto classify = [&](int s, bool& stays, bool& tie) {
     const bool cand = s >= lo && s < hi;
-    const uint32_t k = cand && want > 0 ? key_of(s) : 0u;
-    const bool tie = cand && want > 0 && k == border;
-    int total;
-    const int ties_before = n_ties + block_scan(tie ? 1 : 0, s_warp, total);
-    n_ties += total;
-    const bool keep = s < len && (!cand || (want > 0 && (k > border || (tie && ties_before < ties))));
-    const int rank = n_kept + block_scan(keep ? 1 : 0, s_warp, total);
-    n_kept += total;
-    if (keep) {
-      kept[rank] = s;
-      if (rank != s) atomicMin(&s_first_moved, rank);
-    }
+    const uint32_t k = cand && want > 0 ? weight_key(weight_of(s)) : 0u;
+    tie = cand && want > 0 && k == border;
+    stays = s < end && (!cand || (want > 0 && k > border));
+  };
+  int gt = 0, eq = 0;
+  for (int s0 = begin; s0 < end; s0 += 32) {
+    bool stays, tie;
+    classify(s0 + lane, stays, tie);
+    gt += __popc(__ballot_sync(kFull, stays));
+    eq += __popc(__ballot_sync(kFull, tie && s0 + lane < end));
+  }
+  if (lane == 0) {
+    s_gt[warp] = gt;
+    s_eq[warp] = eq;
   }
   __syncthreads();
+  int gt_before = lane < warp ? s_gt[lane] : 0, eq_before = lane < warp ? s_eq[lane] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    gt_before += __shfl_xor_sync(kFull, gt_before, o);
+    eq_before += __shfl_xor_sync(kFull, eq_before, o);
+  }
+  const bool all_cached = len <= cap;
+  const unsigned below = (1u << lane) - 1u;
+  int first_out = len;   // first evicted slot of this run
+  for (int s0 = begin; s0 < end; s0 += 32) {
+    const int s = s0 + lane;
+    bool stays, tie;
+    classify(s, stays, tie);
+    tie = tie && s < end;
+    const unsigned gts = __ballot_sync(kFull, stays), eqs = __ballot_sync(kFull, tie);
+    const int eq_mine = eq_before + __popc(eqs & below);
+    const bool keep = stays || (tie && eq_mine < ties);
+    const int rank = gt_before + __popc(gts & below) + min(eq_mine, ties);
+    if (keep) {
+      kept[rank] = s;
+      if (all_cached && rank != s) *at(rank) = s_w[s];
+    }
+    const unsigned out = __ballot_sync(kFull, !keep && s < end);
+    if (out != 0 && first_out == len) first_out = s0 + __ffs(out) - 1;
+    gt_before += __popc(gts);
+    eq_before += __popc(eqs);
+  }
+  if (lane == 0 && first_out < len) atomicMin(&s_first_moved, first_out);
+  __syncthreads();
   if (tid == 0) P.units[unit] = EvictUnit{P.budget, s_first_moved};
+  if (all_cached) return;
+  // some weights are only in memory: move them in order, a tile's reads before its writes
+  for (int base = s_first_moved; base < P.budget; base += kSelThreads) {
+    const int j = base + tid;
+    float x = 0.0f;
+    if (j < P.budget) x = weight_of(kept[j]);
+    // the barrier takes a value made of the loaded one: every load has arrived
+    __syncthreads_or(__float_as_uint(x) == 0x7fc12345u);
+    if (j < P.budget) *at(j) = x;
+  }
 }
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveBatch = 4;    // items in flight per thread and tile
+constexpr int kMoveThreads = 128;
+constexpr int kMoveBatch = kEvictTileItems / kMoveThreads;  // items in flight per thread
+constexpr uint32_t kMaxPolls = 1u << 20;
 
-// grid.x: (layer, request, KV head); grid.y: 0 keys, 1 values, last: the weights.
+// cos / sin of a whole-position shift: the exact reduction of shift_cossin,
+// then the hardware's sine and cosine, whose absolute error on [-pi, pi] is
+// below 2^-21: far inside the rounding to bf16 that follows, at a fifth of the
+// instructions (a moved key has a shift of its own, so nothing is shared).
+__device__ __forceinline__ void shift_cossin_fast(float d, float2 f, float& c, float& s) {
+  const float p = __fmul_rn(d, f.x);
+  const float e = __fmaf_rn(d, f.x, -p);
+  const float r = __fsub_rn(p, rintf(p));
+  const float t = 6.283185307179586f * __fadd_rn(r, __fmaf_rn(d, f.y, e));
+  c = __cosf(t);
+  s = __sinf(t);
+}
+
 template <int PAIRING>
-__global__ void __launch_bounds__(kMoveThreads) k_evict_move(const __grid_constant__ EvictParams P, int tensors) {
+__global__ void __launch_bounds__(kMoveThreads, 8) k_evict_move(const __grid_constant__ EvictParams P) {
   constexpr bool NEOX = PAIRING == kNeox;
-  const int64_t unit = blockIdx.x;
-  const int h = static_cast<int>(unit % P.kv_heads);
-  const int r = static_cast<int>(unit / P.kv_heads % P.n_req);
-  const int64_t layer = unit / P.kv_heads / P.n_req;
-  const int wh = P.weight_heads == 1 ? 0 : h;
-  const int which = blockIdx.y;
-  const int64_t wu = (layer * P.n_req + r) * P.weight_heads + wh;
-  if (unit % P.kv_heads == 0 && layer == 0 && which == 0 && threadIdx.x == 0) P.new_lens[r] = P.next_lens[r];
+  __shared__ int64_t s_ticket;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0) s_ticket = static_cast<int64_t>(atomicAdd(P.flags, 1u));
+  __syncthreads();
+  // ticket = tile * units + unit; unit = ((layer, request), tensor, piece)
+  const int64_t units = static_cast<int64_t>(P.layers) * P.n_req * P.tensors * P.pieces;
+  const int64_t unit = s_ticket % units;
+  const int tile = static_cast<int>(s_ticket / units);
+  const int piece = static_cast<int>(unit % P.pieces);
+  const int tensor = static_cast<int>(unit / P.pieces % P.tensors);
+  const int64_t lr = unit / P.pieces / P.tensors;
+  const int r = static_cast<int>(lr % P.n_req);
+  const int64_t layer = lr / P.n_req;
+  if (tile == 0 && layer == 0 && tensor == 0 && piece == 0 && threadIdx.x == 0) P.new_lens[r] = P.next_lens[r];
+  const int64_t wu = lr * P.weight_heads + (P.weight_heads == 1 ? 0 : piece);
   const EvictUnit u = P.units[wu];
-  if (u.first_moved >= u.n_keep) return;
+  const int base = u.first_moved + tile * P.tile_rows;   // first rank of the tile
+  if (base >= u.n_keep) return;
   const int32_t* kept = P.kept + wu * P.budget;
-  const int bs = P.paged.block_size;
+  uint32_t* flags = P.flags + 1 + unit * P.tiles;
 
-  if (which == tensors) {   // the weights move with their tokens
-    if (h >= P.weight_heads) return;
-    float* wl = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(P.weights) + layer * P.weights_ls);
-    auto at = [&](int slot) -> float* {
-      const int64_t row = paged_row(P.paged, r, slot), block = row / bs;
-      return wl + (block * P.weight_heads + wh) * bs + (row - block * bs);
-    };
-    for (int base = u.first_moved; base < u.n_keep; base += kMoveThreads * kMoveBatch) {
-      float x[kMoveBatch];
-#pragma unroll
-      for (int i = 0; i < kMoveBatch; ++i) {
-        const int j = base + i * kMoveThreads + threadIdx.x;
-        if (j < u.n_keep) x[i] = *at(kept[j]);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kMoveBatch; ++i) {
-        const int j = base + i * kMoveThreads + threadIdx.x;
-        if (j < u.n_keep) *at(j) = x[i];
-      }
+  const int h0 = piece * P.piece_heads;
+  const int items = min(P.piece_heads, P.kv_heads - h0) * P.head_items;   // 32-byte items of a row
+  uint8_t* cache = (tensor == 0 ? P.k_cache : P.v_cache) + layer * P.cache_ls + static_cast<int64_t>(h0) * P.head_bytes;
+  const int64_t row_bytes = static_cast<int64_t>(P.kv_heads) * P.head_bytes;
+  const int rows = min(P.tile_rows, u.n_keep - base);
+
+  // An item is two 16-byte chunks; a key item of the rope slice holds both
+  // members of its 8 pairs.  off_a / off_b: its place in the piece's row.
+  auto chunks = [&](int item, int& off_a, int& off_b, int& freq) {
+    const int h = item / P.head_items, i = item - h * P.head_items;
+    const int ho = h * P.head_bytes;
+    freq = -1;
+    if (tensor == 0 && i < P.rope_items) {
+      off_a = ho + P.rope_off + (NEOX ? i : 2 * i) * 16;
+      off_b = ho + P.rope_off + (NEOX ? i + P.rope_items : 2 * i + 1) * 16;
+      freq = 8 * i;
+    } else {   // copied; MLA rows hold their latent before the rope slice
+      off_a = ho + (tensor == 0 ? i - P.rope_items : i) * 32;
+      off_b = off_a + 16;
     }
+  };
+  uint4 a[kMoveBatch], b[kMoveBatch];
+  int src[kMoveBatch];
+  uint32_t seen = 0;
+#pragma unroll
+  for (int x = 0; x < kMoveBatch; ++x) {
+    const int e = x * kMoveThreads + threadIdx.x, row = e / items;
+    src[x] = row < rows ? __ldcg(kept + base + row) : -1;
+  }
+#pragma unroll
+  for (int x = 0; x < kMoveBatch; ++x) {
+    if (src[x] < 0) continue;
+    const int e = x * kMoveThreads + threadIdx.x;
+    int off_a, off_b, freq;
+    chunks(e % items, off_a, off_b, freq);
+    const uint8_t* p = cache + paged_row(P.paged, r, src[x]) * row_bytes;
+    a[x] = __ldcg(reinterpret_cast<const uint4*>(p + off_a));
+    b[x] = __ldcg(reinterpret_cast<const uint4*>(p + off_b));
+  }
+#pragma unroll
+  for (int x = 0; x < kMoveBatch; ++x)
+    if (src[x] >= 0) seen ^= a[x].x ^ b[x].x;
+  // the barrier takes a value made of the loaded ones: every load of the CTA has arrived
+  __syncthreads_or(seen == 0x7fc12345u);
+  if (threadIdx.x == 0)
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flags + tile), "r"(1u) : "memory");
+  // every lower tile of the unit has been read
+  bool timeout = false;
+  for (int t = threadIdx.x; t < tile; t += kMoveThreads) {
+    uint32_t done = 0;
+    for (uint32_t n = 0; n < kMaxPolls && done == 0; ++n)
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(done) : "l"(flags + t) : "memory");
+    timeout |= done == 0;
+  }
+  if (__syncthreads_or(timeout)) {
+    if (threadIdx.x == 0) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_TIMEOUT));
     return;
   }
-
-  // A row is cut into items of two 16-byte chunks, one per thread: a turned
-  // item holds both members of its 8 pairs.
-  uint8_t* cache = (which == 0 ? P.k_cache : P.v_cache) + layer * P.cache_ls + static_cast<int64_t>(h) * P.head_bytes;
-  const int64_t row_bytes = static_cast<int64_t>(P.kv_heads) * P.head_bytes;
-  const int items = P.head_bytes / 32;
-  const int rows = kMoveThreads / items;              // rows one pass of the CTA covers
-  const int my_row = threadIdx.x / items, item = threadIdx.x - my_row * items;
-  const bool idle = my_row >= rows;
-  const bool turns = which == 0 && P.renumber && item < P.rope_items;
-  const int c0 = 8 * item;                            // first frequency of a turned item
-  int off_a, off_b;
-  if (which == 0 && item < P.rope_items) {
-    off_a = P.rope_off + (NEOX ? item : 2 * item) * 16;
-    off_b = P.rope_off + (NEOX ? item + P.rope_items : 2 * item + 1) * 16;
-  } else {  // copied items; MLA rows hold their latent before the rope slice
-    const int k = which == 0 ? item - P.rope_items : item;
-    off_a = k * 32;
-    off_b = off_a + 16;
-  }
-  const int tile = rows * kMoveBatch;
-  uint4 a[2][kMoveBatch], b[2][kMoveBatch];
-  int src[2][kMoveBatch];
-  auto read = [&](int base, uint4 (&xa)[kMoveBatch], uint4 (&xb)[kMoveBatch], int (&xs)[kMoveBatch]) {
 #pragma unroll
-    for (int i = 0; i < kMoveBatch; ++i) {
-      const int j = base + i * rows + my_row;
-      xs[i] = -1;
-      if (idle || j >= u.n_keep) continue;
-      xs[i] = kept[j];
-      const uint8_t* p = cache + paged_row(P.paged, r, xs[i]) * row_bytes;
-      xa[i] = *reinterpret_cast<const uint4*>(p + off_a);
-      xb[i] = *reinterpret_cast<const uint4*>(p + off_b);
-    }
-  };
-  auto write = [&](int base, uint4 (&xa)[kMoveBatch], uint4 (&xb)[kMoveBatch], int (&xs)[kMoveBatch]) {
+  for (int x = 0; x < kMoveBatch; ++x) {
+    if (src[x] < 0) continue;
+    const int e = x * kMoveThreads + threadIdx.x;
+    const int j = base + e / items;
+    int off_a, off_b, freq;
+    chunks(e % items, off_a, off_b, freq);
+    if (P.renumber && freq >= 0 && src[x] != j) {
+      float c[8], s[8];
 #pragma unroll
-    for (int i = 0; i < kMoveBatch; ++i) {
-      if (xs[i] < 0) continue;
-      const int j = base + i * rows + my_row;
-      if (turns && xs[i] != j) {
-        float c[8], s[8];
-#pragma unroll
-        for (int f = 0; f < 8; ++f) shift_cossin(j - xs[i], P.freq.turns[c0 + f], c[f], s[f]);
-        if (NEOX) {
-          rotate_neox(xa[i], xb[i], c, s);
-        } else {
-          rotate_interleaved(xa[i], c, s);
-          rotate_interleaved(xb[i], c + 4, s + 4);
-        }
+      for (int f = 0; f < 8; ++f) shift_cossin_fast(static_cast<float>(j - src[x]), P.freq.turns[freq + f], c[f], s[f]);
+      if (NEOX) {
+        rotate_neox(a[x], b[x], c, s);
+      } else {
+        rotate_interleaved(a[x], c, s);
+        rotate_interleaved(b[x], c + 4, s + 4);
       }
-      uint8_t* p = cache + paged_row(P.paged, r, j) * row_bytes;
-      *reinterpret_cast<uint4*>(p + off_a) = xa[i];
-      *reinterpret_cast<uint4*>(p + off_b) = xb[i];
     }
-  };
-  read(u.first_moved, a[0], b[0], src[0]);
-  for (int base = u.first_moved; base < u.n_keep; base += 2 * tile) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int at = base + x * tile;
-      if (at >= u.n_keep) break;
-      read(at + tile, a[x ^ 1], b[x ^ 1], src[x ^ 1]);
-      __syncthreads();   // the tile's rows are in registers everywhere
-      write(at, a[x], b[x], src[x]);
-    }
+    uint8_t* p = cache + paged_row(P.paged, r, j) * row_bytes;
+    *reinterpret_cast<uint4*>(p + off_a) = a[x];
+    *reinterpret_cast<uint4*>(p + off_b) = b[x];
   }
 }
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams& p, int pairing, int, cudaStream_t s) {
-  const int64_t units = static_cast<int64_t>(p.layers) * p.n_req;
-  k_evict_select<<<static_cast<unsigned>(units * p.weight_heads), kSelThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+cudaError_t launch_evict(const EvictParams& p, int pairing, cudaStream_t s) {
+  const int64_t lr = static_cast<int64_t>(p.layers) * p.n_req;
+  const int smem = p.sel_cap * static_cast<int>(sizeof(float));
+  cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int tensors = p.v_cache != nullptr ? 2 : 1;
-  const dim3 grid(static_cast<unsigned>(units * p.kv_heads), tensors + 1);
-  if (pairing == kNeox) k_evict_move<kNeox><<<grid, kMoveThreads, 0, s>>>(p, tensors);
-  else k_evict_move<kInterleaved><<<grid, kMoveThreads, 0, s>>>(p, tensors);
-  return cudaGetLastError();
+  k_evict_select<<<static_cast<unsigned>(lr * p.weight_heads), kSelThreads, smem, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(lr * p.tensors * p.pieces * p.tiles));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return pairing == kNeox ? cudaLaunchKernelEx(&cfg, k_evict_move<kNeox>, p)
+                          : cudaLaunchKernelEx(&cfg, k_evict_move<kInterleaved>, p);
 }
 
 }  // namespace pic

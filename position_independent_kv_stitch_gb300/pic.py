@@ -145,7 +145,7 @@ _SIGNATURES = {
     "pic_attend_paged": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i32, _i32, ctypes.c_float, _c_void_p, _c_void_p,
                                         _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _i32,
                                         _c_void_p, _sz, _c_void_p]),
-    "pic_evict_workspace_bytes": (_sz, [_c_void_p, _i32, _i32, _i32]),
+    "pic_evict_workspace_bytes": (_sz, [_c_void_p, _i32, _i32, _i32, _i32]),
     "pic_evict_tokens": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _i32, _c_void_p,
                                         _i32, _i32, _c_void_p, _i32, _i32, _i32, _i32, _c_void_p, _c_void_p, _c_void_p,
                                         _sz, _c_void_p]),
@@ -153,7 +153,7 @@ _SIGNATURES = {
 }
 
 _lib = None
-# (cache blocks, block size, KV heads, head dim) of each live context, by handle
+# (cache blocks, (block size, KV heads, head dim), frequencies) of each live context, by handle
 _geometry = {}
 
 
@@ -237,7 +237,7 @@ def pic_create(kind, num_layers, num_kv_heads, head_dim, rope_dim, rope_offset, 
     out = ctypes.c_void_p()
     st = load().pic_create(ctypes.byref(d), int(num_cache_blocks), ctypes.byref(out))
     _check(st, None)
-    _geometry[out.value] = (int(num_cache_blocks), int(block_size), int(num_kv_heads), int(head_dim))
+    _geometry[out.value] = (int(num_cache_blocks), (int(block_size), int(num_kv_heads), int(head_dim)), int(rope_dim) // 2)
     return out
 
 
@@ -667,61 +667,82 @@ def pic_attend_decode(ctx, plans, source, q, softmax_scale, k_pool, v_pool, k_ca
 
 
 # --------------------------------------------------- decode loop over the cache
+#
+# These calls are made once per layer and token, so the checks are lean: plain
+# integer comparisons, addresses passed as integers, no tensor views.
 
-def _device_of(first, *others):
-    """The buffers' device; one of another device or of the host is refused."""
-    dev = first.device
-    for t in (first,) + others:
-        if t is not None and t.device != dev or not first.is_cuda:
-            raise ValueError("every tensor must be on one CUDA device")
-    return dev
-
-
-def _call_on(dev, stream, fn, ctx):
-    """fn(stream handle) with the buffers' device current."""
+def _launch(ctx, name, tensors, stream, args):
+    """Calls lib.name(ctx, *args, stream) with the tensors' device current; a
+    tensor on another device, or on the host, is refused."""
     import torch
-    if dev.index == torch.cuda.current_device():
-        _check(fn(_stream_handle(stream)), ctx)
-    else:
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            raise ValueError("every tensor must be on one CUDA device")
+    fn = getattr(_lib or load(), name)
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            _check(fn(_stream_handle(stream)), ctx)
+            _check(fn(ctx, *args, _stream_handle(stream)), ctx)
+        return
+    st = fn(ctx, *args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
+    if st != PIC_OK:
+        _check(st, ctx)
 
 
-def _token_rows(t, name, heads=None):
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _size(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _dense_int32(t, name, numel=None):
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous() or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor" +
+                         ("" if numel is None else f" of {numel} entries"))
+
+
+def _token_rows(t, name, n_tokens=None, heads=None):
     """[tokens][heads][dim] bf16 with dense heads; returns the bytes between tokens."""
-    if not _is_bf16(t) or t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name} must be bf16 [tokens][heads][head_dim] with dense heads")
-    return t.stride(0) * 2
+    shape, strides = t.shape, t.stride()
+    if not _is_bf16(t) or len(shape) != 3 or strides[2] != 1 or (shape[1] > 1 and strides[1] != shape[2]) or \
+            (n_tokens is not None and shape[0] != n_tokens) or (heads is not None and shape[1:] != heads):
+        raise ValueError(f"{name} must be bf16 [tokens][heads][head_dim], a row per token, dense heads")
+    return strides[0] * 2
 
 
 def _check_cache(ctx, t, name, dim):
     """A cache tensor ([layers][blocks][block_size][kv_heads][head_dim] for dim
     5, one layer of it for dim 4) that holds the context's blocks and rows."""
-    if not _is_bf16(t) or t.dim() != dim or not (t if dim == 4 else t[0]).is_contiguous():
+    shape = t.shape
+    if not _is_bf16(t) or len(shape) != dim or not (t.is_contiguous() or (dim == 5 and t[0].is_contiguous())):
         raise ValueError(f"{name} must be a bf16 cache tensor of {dim} dims with contiguous rows")
-    blocks, bs, heads, head_dim = _geometry.get(ctx.value, (0,) + tuple(t.shape[-3:]))
-    if t.shape[-4] < blocks or tuple(t.shape[-3:]) != (bs, heads, head_dim):
-        raise ValueError(f"{name} must hold the context's {blocks} blocks of {bs} rows [{heads}][{head_dim}]")
+    want = _geometry.get(ctx.value)
+    if want is not None and (shape[dim - 4] < want[0] or shape[dim - 3:] != want[1]):
+        raise ValueError(f"{name} must hold the context's {want[0]} blocks of {want[1][0]} rows {list(want[1][1:])}")
 
 
 def _weight_heads(weights, cache):
     """Weight heads of a weights tensor [..][blocks][weight_heads][block_size] beside a cache."""
-    import torch
     if weights is None:
         return 0
-    if weights.dtype != torch.float32 or weights.dim() != cache.dim() - 1 or \
-            not (weights if weights.dim() == 3 else weights[0]).is_contiguous() or \
-            weights.shape[-3] != cache.shape[-4] or weights.shape[-1] != cache.shape[-3] or \
-            weights.shape[:-3] != cache.shape[:-4]:
+    import torch
+    w, c = weights.shape, cache.shape
+    n = len(w)
+    if weights.dtype != torch.float32 or n != len(c) - 1 or w[n - 1] != c[n - 2] or w[:n - 2] != c[:n - 2] or \
+            not (weights.is_contiguous() or (n == 4 and weights[0].is_contiguous())):
         raise ValueError("weights must be float32 [blocks][weight_heads][block_size], shaped as the cache")
-    return int(weights.shape[-2])
+    return w[n - 2]
 
 
-def _tables_2d(block_tables, rows=None):
-    _check_device_int32(block_tables, "block_tables")
-    if block_tables.dim() != 2 or (rows is not None and block_tables.shape[0] < rows):
+def _max_blocks(block_tables, rows=0):
+    _dense_int32(block_tables, "block_tables")
+    shape = block_tables.shape
+    if len(shape) != 2 or shape[0] < rows:
         raise ValueError("block_tables must be [n_req][max_blocks] with a row per request")
-    return int(block_tables.shape[0]), int(block_tables.shape[1])
+    return shape[1]
 
 
 def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_cache, q=None, q_out=None,
@@ -736,40 +757,35 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
     [n_tokens][q_heads][head_dim], q_out may be q.  weights: float32
     [blocks][weight_heads][block_size], zeroed at the written slots.
     workspace: uint8, PIC_STATUS_BYTES, zeroed when made (its status is sticky)."""
-    t = pic_new_tokens()
-    _check_device_int32(positions, "positions")
-    t.n_axes, t.n_tokens = (1, int(positions.shape[0])) if positions.dim() == 1 else map(int, positions.shape)
-    if freq_axis is not None:
-        t.freq_axis = bytes(freq_axis)
-    t.d_pos = positions.data_ptr()
+    _dense_int32(positions, "positions")
+    shape = positions.shape
+    axes, n = (1, shape[0]) if len(shape) == 1 else shape
+    q_heads = q_stride = out_stride = k_stride = v_stride = n_tables = max_blocks = heads = 0
     if q is not None:
-        if q_out is None or q_out.shape != q.shape or q.shape[0] != t.n_tokens:
-            raise ValueError("q and q_out hold one row per token, of one shape")
-        t.num_q_heads = int(q.shape[1])
-        t.q_stride, t.q_out_stride = _token_rows(q, "q"), _token_rows(q_out, "q_out")
-        t.q, t.q_out = q.data_ptr(), q_out.data_ptr()
-    n_tables = max_blocks = heads = 0
+        q_heads = q.shape[1]
+        q_stride, out_stride = _token_rows(q, "q", n), _token_rows(q_out, "q_out", n, q.shape[1:])
+        if ctx.value in _geometry and q.shape[2] != _geometry[ctx.value][1][2]:
+            raise ValueError("q heads must have the context's head_dim")
     if k is not None:
-        t.k, t.k_stride = k.data_ptr(), _token_rows(k, "k")
-        if v is not None:
-            t.v, t.v_stride = v.data_ptr(), _token_rows(v, "v")
-        for rows in (k, v):
-            if rows is not None and (rows.shape[0] != t.n_tokens or rows.shape[1:] != k_cache.shape[2:]):
-                raise ValueError("k and v hold one row per token, shaped as the cache's rows")
-        _check_device_int32(req, "req")
-        _check_device_int32(slot, "slot")
-        if req.numel() != t.n_tokens or slot.numel() != t.n_tokens:
-            raise ValueError("req and slot hold one entry per token")
-        t.d_req, t.d_slot = req.data_ptr(), slot.data_ptr()
-        n_tables, max_blocks = _tables_2d(block_tables)
         for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
             if c is not None:
                 _check_cache(ctx, c, name, 4)
+        rows = k_cache.shape[2:]
+        k_stride = _token_rows(k, "k", n, rows)
+        v_stride = 0 if v is None else _token_rows(v, "v", n, rows)
+        _dense_int32(req, "req", n)
+        _dense_int32(slot, "slot", n)
+        n_tables, max_blocks = block_tables.shape[0], _max_blocks(block_tables)
         heads = _weight_heads(weights, k_cache)
-    dev = _device_of(positions, q, q_out, k, v, req, slot, block_tables, k_cache, v_cache, weights, workspace)
-    _call_on(dev, stream, lambda s: load().pic_write_tokens(
-        ctx, ctypes.byref(t), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), n_tables, max_blocks, _ptr(weights), heads,
-        _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0, s), ctx)
+    half = _geometry[ctx.value][2] if ctx.value in _geometry else None
+    if freq_axis is not None and half is not None and len(freq_axis) != half:
+        raise ValueError(f"freq_axis holds an axis for each of the {half} frequencies")
+    t = pic_new_tokens(n, q_heads, axes, None if freq_axis is None else bytes(freq_axis), positions.data_ptr(), _addr(q),
+                       q_stride, _addr(q_out), out_stride, _addr(k), k_stride, _addr(v), v_stride, _addr(req), _addr(slot))
+    _launch(ctx, "pic_write_tokens",
+            (positions, q, q_out, k, v, req, slot, block_tables, k_cache, v_cache, weights, workspace), stream,
+            (t, _addr(k_cache), _addr(v_cache), _addr(block_tables), n_tables, max_blocks, _addr(weights), heads,
+             _addr(workspace), _size(workspace)))
 
 
 def pic_attend_paged_workspace_bytes(ctx, n_req: int, num_q_heads: int, max_seq_len: int, with_weights=False) -> int:
@@ -788,29 +804,27 @@ def pic_attend_paged(ctx, q, softmax_scale, k_cache, v_cache, block_tables, seq_
     added to it.  workspace: uint8, pic_attend_paged_workspace_bytes, its first
     PIC_STATUS_BYTES zeroed when made."""
     import torch
-    n_req, hq, d = (int(x) for x in q.shape)
     stride = _token_rows(q, "q")
-    _check_device_int32(seq_lens, "seq_lens")
-    _, max_blocks = _tables_2d(block_tables, n_req)
-    for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check_cache(ctx, c, name, 4)
-    if seq_lens.numel() != n_req or d != k_cache.shape[3]:
-        raise ValueError("seq_lens holds one entry per request, q heads of the cache's head_dim")
-    if out.shape != q.shape or not out.is_contiguous() or out.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape")
+    n_req, hq, d = q.shape
+    _dense_int32(seq_lens, "seq_lens", n_req)
+    max_blocks = _max_blocks(block_tables, n_req)
+    _check_cache(ctx, k_cache, "k_cache", 4)
+    _check_cache(ctx, v_cache, "v_cache", 4)
+    out_type = out.dtype
+    if d != k_cache.shape[3] or out.shape != q.shape or not out.is_contiguous() or \
+            (out_type != torch.float32 and out_type != torch.bfloat16):
+        raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape, heads of the cache's head_dim")
     if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n_req * hq or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [n_req][q_heads]")
-    heads = _weight_heads(weights, k_cache)
-    dev = _device_of(q, k_cache, v_cache, block_tables, seq_lens, out, lse, weights, workspace)
-    _call_on(dev, stream, lambda s: load().pic_attend_paged(
-        ctx, _ptr(q), stride, n_req, hq, float(softmax_scale), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks,
-        _ptr(seq_lens), int(max_seq_len), _ptr(out), PIC_BF16 if out.dtype == torch.bfloat16 else PIC_F32, _ptr(lse),
-        _ptr(weights), heads, _ptr(workspace),
-        workspace.numel() * workspace.element_size() if workspace is not None else 0, s), ctx)
+    _launch(ctx, "pic_attend_paged", (q, k_cache, v_cache, block_tables, seq_lens, out, lse, weights, workspace), stream,
+            (q.data_ptr(), stride, n_req, hq, softmax_scale, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+             max_blocks, seq_lens.data_ptr(), max_seq_len, out.data_ptr(), PIC_F32 if out_type == torch.float32 else PIC_BF16,
+             _addr(lse), _addr(weights), _weight_heads(weights, k_cache), _addr(workspace), _size(workspace)))
 
 
-def pic_evict_workspace_bytes(ctx, num_layers: int, n_req: int, weight_heads: int) -> int:
-    return int(load().pic_evict_workspace_bytes(ctx, int(num_layers), int(n_req), int(weight_heads)))
+def pic_evict_workspace_bytes(ctx, num_layers: int, n_req: int, weight_heads: int, budget: int = 0) -> int:
+    """Bytes for evictions to `budget` (0: to any budget)."""
+    return int(load().pic_evict_workspace_bytes(ctx, int(num_layers), int(n_req), int(weight_heads), int(budget)))
 
 
 def pic_evict_tokens(ctx, k_cache, v_cache, weights, block_tables, seq_lens, budget: int, kept, new_lens, n_first: int = 0,
@@ -823,26 +837,23 @@ def pic_evict_tokens(ctx, k_cache, v_cache, weights, block_tables, seq_lens, bud
     [layers][n_req][weight_heads][budget].  renumber: keys are re-rotated to
     their new slots.  workspace: uint8, pic_evict_workspace_bytes, its first
     PIC_STATUS_BYTES zeroed when made."""
-    for t, name in ((seq_lens, "seq_lens"), (kept, "kept"), (new_lens, "new_lens")):
-        _check_device_int32(t, name)
-    n_req, layers = int(seq_lens.numel()), int(k_cache.shape[0])
-    _, max_blocks = _tables_2d(block_tables, n_req)
-    for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if c is not None:
-            _check_cache(ctx, c, name, 5)
-            if c.shape != k_cache.shape or (layers > 1 and c.stride(0) != k_cache.stride(0)):
-                raise ValueError("k_cache and v_cache must share a shape and a layer stride")
+    n_req, layers = seq_lens.numel(), k_cache.shape[0]
+    max_blocks = _max_blocks(block_tables, n_req)
+    _check_cache(ctx, k_cache, "k_cache", 5)
+    if v_cache is not None:
+        _check_cache(ctx, v_cache, "v_cache", 5)
+        if v_cache.shape != k_cache.shape or (layers > 1 and v_cache.stride(0) != k_cache.stride(0)):
+            raise ValueError("k_cache and v_cache must share a shape and a layer stride")
     if weights is None:
         raise ValueError("weights are required")
     heads = _weight_heads(weights, k_cache)
-    if new_lens.numel() != n_req or kept.numel() != layers * n_req * heads * int(budget):
-        raise ValueError("kept holds [layers][n_req][weight_heads][budget] entries, new_lens one per request")
-    dev = _device_of(k_cache, v_cache, weights, block_tables, seq_lens, kept, new_lens, workspace)
-    _call_on(dev, stream, lambda s: load().pic_evict_tokens(
-        ctx, layers, _ptr(k_cache), _ptr(v_cache), _layer_stride_bytes(k_cache), _ptr(weights), _layer_stride_bytes(weights),
-        heads, _ptr(block_tables), n_req, max_blocks, _ptr(seq_lens), int(budget), int(n_first), int(n_recent),
-        1 if renumber else 0, _ptr(kept), _ptr(new_lens), _ptr(workspace),
-        workspace.numel() * workspace.element_size() if workspace is not None else 0, s), ctx)
+    _dense_int32(seq_lens, "seq_lens")
+    _dense_int32(new_lens, "new_lens", n_req)
+    _dense_int32(kept, "kept", layers * n_req * heads * budget)
+    _launch(ctx, "pic_evict_tokens", (k_cache, v_cache, weights, block_tables, seq_lens, kept, new_lens, workspace), stream,
+            (layers, k_cache.data_ptr(), _addr(v_cache), k_cache.stride(0) * 2, weights.data_ptr(), weights.stride(0) * 4, heads,
+             block_tables.data_ptr(), n_req, max_blocks, seq_lens.data_ptr(), budget, n_first, n_recent, 1 if renumber else 0,
+             kept.data_ptr(), new_lens.data_ptr(), _addr(workspace), _size(workspace)))
 
 
 def pic_debug_stall_next_launch(ctx, stall_tile: int, max_spins: int = 0):
