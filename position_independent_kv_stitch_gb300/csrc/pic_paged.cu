@@ -26,6 +26,7 @@
 // hi + lo parts (a third part when the output is fp32), each a product of its
 // own, so P keeps 16 (24) significant bits.  With up to 8 query heads the hi and
 // lo parts share one product, in rows g and g + 8.
+#include <algorithm>
 #include <cfloat>
 
 #include <cuda_bf16.h>
@@ -148,6 +149,7 @@ struct Place {
   int64_t first;   // the request's first tile in the list
 };
 __device__ __forceinline__ void advance(const PagedParams& P, Place& x) {
+  if (x.req >= P.n_req) return;   // past the list
   const int n = (x.len + TT - 1) / TT;
   if (++x.tile < n) return;
   x.first += n;
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
   constexpr int NS = paged_stages(D);
   constexpr int ROWS = 32 / CH > 0 ? 32 / CH : 1;     // rows one warp-wide copy covers
   constexpr int COPIES = TT * CH / 32;                // warp-wide copies of a K (or V) tile
+  asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + warp * NS * stage_bytes(D);
@@ -402,45 +405,95 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
   }
 }
 
-// One CTA per (request, query head): joins the records of its ranges.
-constexpr int kJoinThreads = 128;
+// One CTA per (request, query head): joins the records of its ranges.  The
+// warps take the records in turn, a lane D / 32 neighbouring dims of each, and
+// add up their sums in warp order at the end.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinRecords = 512;   // record weights held in shared memory at a time
+
+__device__ __forceinline__ float block_reduce(float v, bool is_max, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float w = __shfl_xor_sync(kFull, v, o);
+    v = is_max ? fmaxf(v, w) : v + w;
+  }
+  __syncthreads();   // red is free
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) v = is_max ? fmaxf(v, red[w]) : v + red[w];
+  return v;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ PagedParams P) {
+  constexpr int V = D / 32;   // dims of a lane
   __shared__ int64_t s_first;
   __shared__ TileList s_list;
+  __shared__ float s_red[kJoinWarps];
+  __shared__ float s_e[kJoinRecords];
+  __shared__ float s_acc[kJoinWarps][D];
+  asm volatile("griddepcontrol.launch_dependents;");
   const int r = blockIdx.x, hq = blockIdx.y;
-  if (threadIdx.x < 32) {
-    const TileList L = tile_list(P, threadIdx.x, false);
-    const int64_t f = first_tile(P, r, threadIdx.x);
-    if (threadIdx.x == 0) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    const TileList L = tile_list(P, lane, false);
+    const int64_t f = first_tile(P, r, lane);
+    if (lane == 0) {
       s_list = L;
       s_first = f;
     }
   }
-  __syncthreads();
   const int n = tiles_of(P, r, false);
-  const int64_t out_at = (static_cast<int64_t>(r) * P.q_heads + hq) * D;
-  float M = -FLT_MAX, sum = 0.0f;
-  int64_t p0 = 0, p1 = 0;   // ranges that cross the request
+  __syncthreads();
+  int64_t rec0 = 0;   // the request's first record
+  int recs = 0;
   if (n > 0) {
     const TileList L = s_list;
     // the range of tile t is the largest p with begin(p) <= t
-    p0 = ((s_first + 1) * L.parts - 1) / L.total;
-    p1 = ((s_first + n) * L.parts - 1) / L.total + 1;
-    for (int64_t p = p0; p < p1; ++p) M = fmaxf(M, P.rec_ml[(p + r) * P.q_heads + hq].x);
-    for (int64_t p = p0; p < p1; ++p) {
-      const float2 ml = P.rec_ml[(p + r) * P.q_heads + hq];
-      sum += ml.y * exp2f(ml.x - M);
+    const int64_t p0 = ((s_first + 1) * L.parts - 1) / L.total;
+    recs = static_cast<int>(((s_first + n) * L.parts - 1) / L.total - p0 + 1);
+    rec0 = p0 + r;
+  }
+  // everything above came from the caller's lengths; the records are the previous kernel's
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float2* ml = P.rec_ml + rec0 * P.q_heads + hq;
+  const float* acc_in = P.rec_acc + (rec0 * P.q_heads + hq) * D;
+  float mx = -FLT_MAX;
+  for (int k = threadIdx.x; k < recs; k += kJoinThreads) mx = fmaxf(mx, ml[static_cast<int64_t>(k) * P.q_heads].x);
+  const float M = block_reduce(mx, true, s_red);
+  float part = 0.0f;
+  float acc[V] = {};
+  for (int k0 = 0; k0 < recs; k0 += kJoinRecords) {
+    const int m = min(kJoinRecords, recs - k0);
+    __syncthreads();   // s_e is free
+    for (int k = threadIdx.x; k < m; k += kJoinThreads) {
+      const float2 x = ml[static_cast<int64_t>(k0 + k) * P.q_heads];
+      const float e = exp2f(x.x - M);
+      s_e[k] = e;
+      part += e * x.y;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int k = warp; k < m; k += kJoinWarps) {
+      const float e = s_e[k];
+      const float* a = acc_in + static_cast<int64_t>(k0 + k) * P.q_heads * D + lane * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += e * a[i];
     }
   }
+  const float sum = block_reduce(part, false, s_red);
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
+  __syncthreads();
+  const int64_t out_at = (static_cast<int64_t>(r) * P.q_heads + hq) * D;
   for (int d = threadIdx.x; d < D; d += kJoinThreads) {
-    float acc = 0.0f;
-    for (int64_t p = p0; p < p1; ++p) {
-      const int64_t rec = (p + r) * P.q_heads + hq;
-      acc += exp2f(P.rec_ml[rec].x - M) * P.rec_acc[rec * D + d];
-    }
-    const float v = n > 0 ? acc / sum : 0.0f;
+    float x = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) x += s_acc[w][d];
+    const float v = n > 0 ? x / sum : 0.0f;
     if (P.out_bf16) static_cast<__nv_bfloat16*>(P.out)[out_at + d] = __float2bfloat16_rn(v);
     else static_cast<float*>(P.out)[out_at + d] = v;
   }
@@ -451,13 +504,17 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_consta
   }
 }
 
-// Adds each slot's attention weight: one warp per run of tiles and weight
-// head, one lane per slot, the query heads summed in order (no atomics: a slot
-// belongs to one lane).
+// Adds each slot's attention weight: a warp takes a run of tiles for one
+// weight head, half a warp a tile, one lane a slot; the query heads are summed
+// in order (no atomics: a slot belongs to one lane).  A lane looks up four
+// slots, then loads their scores and old weights together: the step is a
+// chain of two memory round trips, not bandwidth, so few of them count.
 constexpr int kWeightThreads = 256;
+constexpr int kWeightCtas = 6;      // per SM
+constexpr int kWeightBatch = 4;
 
-__global__ void __launch_bounds__(kWeightThreads) k_paged_weights(const __grid_constant__ PagedParams P) {
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kWeightThreads, kWeightCtas) k_paged_weights(const __grid_constant__ PagedParams P) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, sl = lane & (TT - 1);
   const int64_t w = static_cast<int64_t>(blockIdx.x) * (kWeightThreads / 32) + (threadIdx.x >> 5);
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kWeightThreads / 32) / P.weight_heads;
   const int wh = static_cast<int>(w % P.weight_heads);
@@ -471,22 +528,59 @@ __global__ void __launch_bounds__(kWeightThreads) k_paged_weights(const __grid_c
   find_tile(P, t_begin, lane, x.req, x.first);
   x.tile = static_cast<int>(t_begin - x.first);
   x.len = legal_len(__ldg(P.lens + x.req), P.max_len, P.status, false);
-  for (int64_t t = t_begin; t < t_end; ++t) {
-    const int slot = x.tile * TT + lane;
-    if (lane < TT && slot < x.len) {
-      const int64_t row = paged_row(P.paged, x.req, slot);
-      if (row >= 0) {
-        float sum = 0.0f;
-        for (int h = 0; h < heads; ++h) {
-          const int hq = wh * heads + h;
-          sum += exp2f(P.scores[hq * P.score_stride + t * TT + lane] - P.lse2[static_cast<int64_t>(x.req) * P.q_heads + hq]);
-        }
-        const int64_t block = row / P.paged.block_size, at = row % P.paged.block_size;
-        P.weights[(block * P.weight_heads + wh) * P.paged.block_size + at] += sum;
+  if (half != 0) advance(P, x);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int64_t t = t_begin + half; t < t_end; t += 2 * kWeightBatch) {
+    int64_t at[kWeightBatch];
+    int req[kWeightBatch];
+#pragma unroll
+    for (int u = 0; u < kWeightBatch; ++u) {
+      at[u] = -1;
+      req[u] = x.req;
+      if (t + 2 * u >= t_end) continue;
+      const int slot = x.tile * TT + sl;
+      if (slot < x.len) {
+        const int b = block_of(P.paged, slot);
+        const int32_t block = __ldg(P.paged.tables + static_cast<int64_t>(x.req) * P.paged.max_blocks + b);
+        if (block >= 0 && block < P.paged.num_cache_blocks)
+          at[u] = (static_cast<int64_t>(block) * P.weight_heads + wh) * P.paged.block_size + (slot - b * P.paged.block_size);
       }
+      advance(P, x);
+      advance(P, x);
     }
-    if (t + 1 < t_end) advance(P, x);
+    float old[kWeightBatch], sum[kWeightBatch];
+#pragma unroll
+    for (int u = 0; u < kWeightBatch; ++u) {
+      sum[u] = 0.0f;
+      if (at[u] >= 0) old[u] = P.weights[at[u]];
+    }
+    const float* sc = P.scores + wh * heads * P.score_stride + t * TT + sl;
+#pragma unroll 2
+    for (int h = 0; h < heads; ++h, sc += P.score_stride) {
+#pragma unroll
+      for (int u = 0; u < kWeightBatch; ++u)
+        if (at[u] >= 0)
+          sum[u] += exp2f(__ldcs(sc + 2 * u * TT) - P.lse2[static_cast<int64_t>(req[u]) * P.q_heads + wh * heads + h]);
+    }
+#pragma unroll
+    for (int u = 0; u < kWeightBatch; ++u)
+      if (at[u] >= 0) P.weights[at[u]] = old[u] + sum[u];
   }
+}
+
+// A kernel launched as a programmatic dependent of the one before it.
+template <typename Kern>
+cudaError_t launch_after(Kern kern, dim3 grid, int threads, const PagedParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int D, bool WIDE, bool F32>
@@ -506,12 +600,10 @@ cudaError_t launch_d(const PagedParams& p, int grid, int sm_count, cudaStream_t 
   if (wide) e = p.out_bf16 ? launch_attend_d<D, true, false>(p, grid, s) : launch_attend_d<D, true, true>(p, grid, s);
   else e = p.out_bf16 ? launch_attend_d<D, false, false>(p, grid, s) : launch_attend_d<D, false, true>(p, grid, s);
   if (e != cudaSuccess) return e;
-  k_paged_join<D><<<dim3(p.n_req, p.q_heads), kJoinThreads, 0, s>>>(p);
-  e = cudaGetLastError();
+  e = launch_after(k_paged_join<D>, dim3(p.n_req, p.q_heads), kJoinThreads, p, s);
   if (e != cudaSuccess || p.weights == nullptr) return e;
   const int need = (p.weight_heads + kWeightThreads / 32 - 1) / (kWeightThreads / 32);
-  k_paged_weights<<<sm_count * 4 > need ? sm_count * 4 : need, kWeightThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(k_paged_weights, dim3(std::max(sm_count * kWeightCtas, need)), kWeightThreads, p, s);
 }
 
 }  // namespace
