@@ -270,8 +270,10 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
     return fail(ctx, PIC_ERR_INVALID_ARG, "null q, cache, block table, lengths, out or workspace");
   const int64_t q_bytes = static_cast<int64_t>(num_q_heads) * m.head_dim * 2;
   const int64_t row_bytes = static_cast<int64_t>(m.num_kv_heads) * m.head_dim * 2;
-  if (row_bytes > std::numeric_limits<int32_t>::max() || num_q_heads > 65535 || q_bytes > std::numeric_limits<int32_t>::max())
+  if (row_bytes > std::numeric_limits<int32_t>::max() || num_q_heads > kPagedMaxHeads || q_bytes > std::numeric_limits<int32_t>::max())
     return fail(ctx, PIC_ERR_RANGE, "too many heads");
+  if (static_cast<int64_t>(n_req) * num_q_heads > std::numeric_limits<int32_t>::max() / 2)
+    return fail(ctx, PIC_ERR_RANGE, "more than 2^30 query heads in all");
   if (n_req > 1 && q_stride < q_bytes) return fail(ctx, PIC_ERR_RANGE, "q_stride smaller than a request's heads");
   if (max_seq_len > table_capacity(c, max_blocks))
     return fail(ctx, PIC_ERR_RANGE, "max_seq_len %d exceeds the %d slots a block table holds", max_seq_len,
@@ -303,7 +305,7 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
   p.passes = paged_passes(p.group);
   p.v_heads = p.kv_heads * p.passes;
   const int warps = paged_warps_per_cta(m.head_dim);
-  const int grid = std::max(std::min(sms, kPagedMaxCtas), (p.v_heads + warps - 1) / warps);
+  const int grid = std::min(sms, kPagedMaxCtas);   // one CTA per SM (its rings fill shared memory)
   p.parts = static_cast<int32_t>(std::max<int64_t>(1, static_cast<int64_t>(grid) * warps / p.v_heads));
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.k_cache = static_cast<const uint8_t*>(k_cache);

@@ -76,6 +76,7 @@ cudaError_t launch_write(const WriteParams& p, int pairing, int sm_count, cudaSt
 constexpr int kPagedTile = 16;          // positions of one step of a warp
 constexpr int kPagedWarps = 8;          // warps per CTA, each with its own ring
 constexpr int kPagedMaxCtas = 256;      // grid bound (workspace sizing)
+constexpr int kPagedMaxHeads = 4096;    // query heads
 constexpr int kPagedMinTiles = 4;       // least tiles of one warp's range
 
 struct PagedParams {
@@ -103,9 +104,10 @@ struct PagedParams {
   float* lse;
   float* weights;
   int32_t weight_heads;
+  int32_t weight_ctas;       // CTAs of the last kernel that add weights (the others join records)
+  int32_t join_wide;         // 1: one per (request, query head); 0: one warp for each
   uint32_t* status;
 };
-size_t paged_smem(int head_dim);
 int paged_warps_per_cta(int head_dim);
 cudaError_t launch_paged(const PagedParams& p, int head_dim, int grid, int sm_count, cudaStream_t s);
 

@@ -10,9 +10,13 @@
 // list, and each warp takes a contiguous, equally long range of it for one
 // KV head, whatever the requests' lengths are.  A warp keeps a running
 // maximum, sum and weighted values for the query heads of its KV head (online
-// softmax) and leaves one record per request it crosses; a second kernel
-// joins the records.  Range p and request r cross at most once and both only
-// grow along the list, so record p + r is unique without any bookkeeping.
+// softmax) and leaves one record per request it crosses.  Range p and request
+// r cross at most once and both only grow along the list, so record p + r is
+// unique without any bookkeeping.  Later kernels (programmatic dependents) join
+// the records into the outputs and add each slot's weight from the scores kept
+// meanwhile.  One cooperative kernel with a grid barrier instead took 13.0 us
+// against 11.0 for one request of 777 slots, and its eight warps per SM were
+// too few for the weights.
 //
 // Warps work alone: each streams its rows through its own ring in shared
 // memory with cp.async (16 bytes a lane, rows past the end filled with zeros)
@@ -26,7 +30,6 @@
 // hi + lo parts (a third part when the output is fp32), each a product of its
 // own, so P keeps 16 (24) significant bits.  With up to 8 query heads the hi and
 // lo parts share one product, in rows g and g + 8.
-#include <algorithm>
 #include <cfloat>
 
 #include <cuda_bf16.h>
@@ -47,10 +50,17 @@ constexpr float kLn2 = 0.69314718055994531f;
 __host__ __device__ constexpr int paged_stages(int D) { return D <= 64 ? 6 : (D <= 128 ? 3 : 2); }
 __host__ __device__ constexpr int paged_warps(int D) { return D <= 128 ? kPagedWarps : kPagedWarps * 3 / 4; }
 __host__ __device__ constexpr int stage_bytes(int D) { return 2 * TT * D * 2; }
+// Scores leave a warp several tiles at a time, one bulk copy per head.
+__host__ __device__ constexpr int score_tiles(bool wide) { return wide ? 4 : 8; }
+__host__ __device__ constexpr int score_pitch(bool wide) { return score_tiles(wide) * TT + 4; }  // floats, bank-shifted
+__host__ __device__ constexpr int score_stage(bool wide) { return (wide ? 16 : 8) * score_pitch(wide); }
 
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool live, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0),
+               "l"(policy)
+               : "memory");
 }
+__device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -71,6 +81,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 2^x to 2 units in the last place; results below 2^-126 become 0
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 // (x, y) as a bf16 pair, and what the pair leaves out
 __device__ __forceinline__ uint32_t take_bf16(float& x, float& y) {
@@ -163,19 +179,15 @@ __device__ __forceinline__ void advance(const PagedParams& P, Place& x) {
 // WIDE: 9 to 16 query heads per warp, one per row of the products; else up to
 // 8, in rows 0-7 (rows 8-15 carry the lo parts of P).  F32: fp32 output.
 template <int D, bool WIDE, bool F32>
-__global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const __grid_constant__ PagedParams P) {
+__device__ __forceinline__ void attend_range(const PagedParams& P, const TileList& L, int64_t w, uint8_t* smem) {
   constexpr int KS = D / 16, NT = D / 8, CH = D / 8;  // k-steps, output n-tiles, 16-byte chunks of a row
   constexpr int NS = paged_stages(D);
   constexpr int ROWS = 32 / CH > 0 ? 32 / CH : 1;     // rows one warp-wide copy covers
   constexpr int COPIES = TT * CH / 32;                // warp-wide copies of a K (or V) tile
-  asm volatile("griddepcontrol.launch_dependents;");
-  extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + warp * NS * stage_bytes(D);
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * paged_warps(D) + warp;
   const int vh = static_cast<int>(w % P.v_heads);
   const int64_t part = w / P.v_heads;
-  const TileList L = tile_list(P, lane, w == 0);
   if (part >= L.parts || L.total == 0) return;
   const int64_t t_begin = L.begin(part), t_end = L.begin(part + 1);
   if (t_begin >= t_end) return;
@@ -185,6 +197,9 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
   const int n_heads = min(16, P.group - g0);
   const int hq0 = hk * P.group + g0;
   const int g = lane >> 2, tq = lane & 3;
+  // the rows pass through L2 once; the scores, read again at the end, may stay
+  uint64_t stream_once;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream_once));
 
   Place load;
   find_tile(P, t_begin, lane, load.req, load.first);
@@ -210,8 +225,8 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
       const bool live = src_row >= 0;
       const int64_t off = static_cast<int64_t>(live ? src_row : 0) * P.row_bytes + hk * D * 2 + c * 16;
       const uint32_t dst = r * D * 2 + ((c ^ (r & 7)) << 4);
-      cp_async16_zfill(k_dst + dst, P.k_cache + off, live);
-      cp_async16_zfill(v_dst + dst, P.v_cache + off, live);
+      cp_async16_zfill(k_dst + dst, P.k_cache + off, live, stream_once);
+      cp_async16_zfill(v_dst + dst, P.v_cache + off, live, stream_once);
     }
   };
 
@@ -241,6 +256,8 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
   const int mi = lane >> 3, ri = lane & 7;
   const int k_row = ri + ((mi & 2) ? 8 : 0), v_row = ri + ((mi & 1) ? 8 : 0);
   bool opened = false;
+  float* stage = reinterpret_cast<float*>(smem + paged_warps(D) * NS * stage_bytes(D)) + warp * score_stage(WIDE);
+  int n_staged = 0;   // tiles whose scores wait in the stage
 
   int64_t t = t_begin;
   while (t < t_end) {
@@ -283,6 +300,10 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
       cp_wait<NS - 1>();
       __syncwarp();
       const uint32_t kb = ring + st * stage_bytes(D), vb = kb + TT * D * 2;
+      if (P.scores != nullptr && n_staged == 0) {
+        bulk_wait_read_all();   // the stage has been copied out
+        __syncwarp();
+      }
       // ---- scores of the tile's 16 slots
       float s0[4] = {}, s1[4] = {};
 #pragma unroll
@@ -309,13 +330,13 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
         mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 1));
         mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 2));
         const float m_new = fmaxf(m_run[hf], mt);
-        alpha[hf] = exp2f(m_run[hf] - m_new);
+        alpha[hf] = ex2(m_run[hf] - m_new);
         m_run[hf] = m_new;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[hf][i] = exp2f(sc[hf][i] - m_new);
+        for (int i = 0; i < 4; ++i) p[hf][i] = ex2(sc[hf][i] - m_new);
         l_run[hf] = l_run[hf] * alpha[hf] + ((p[hf][0] + p[hf][1]) + (p[hf][2] + p[hf][3]));
         if (P.scores != nullptr && g + 8 * hf < n_heads) {
-          float* sp = P.scores + static_cast<int64_t>(hq0 + g + 8 * hf) * P.score_stride + t * TT + 2 * tq;
+          float* sp = stage + (g + 8 * hf) * score_pitch(WIDE) + n_staged * TT + 2 * tq;
           *reinterpret_cast<float2*>(sp) = make_float2(sc[hf][0], sc[hf][1]);
           *reinterpret_cast<float2*>(sp + 8) = make_float2(sc[hf][2], sc[hf][3]);
         }
@@ -378,6 +399,16 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
       }
       __syncwarp();   // every lane has read the stage before it is refilled
       ++t;
+      if (P.scores != nullptr && (++n_staged == score_tiles(WIDE) || t == t_end)) {
+        // the staged tiles, one bulk copy a head
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane < n_heads)
+          bulk_store(P.scores + (hq0 + lane) * P.score_stride + (t - n_staged) * TT, stage + lane * score_pitch(WIDE),
+                     n_staged * TT * sizeof(float));
+        bulk_commit();
+        n_staged = 0;
+      }
       const int n_tiles = (cur.len + TT - 1) / TT;
       if (cur.tile + 1 == n_tiles || t == t_end) {
         // ---- the record of this range and request
@@ -403,177 +434,270 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
       if (t < t_end) advance(P, cur);
     }
   }
+  bulk_wait_all();
 }
 
-// One CTA per (request, query head): joins the records of its ranges.  The
-// warps take the records in turn, a lane D / 32 neighbouring dims of each, and
-// add up their sums in warp order at the end.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinRecords = 512;   // record weights held in shared memory at a time
+template <int D, bool WIDE, bool F32>
+__global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const __grid_constant__ PagedParams P) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  extern __shared__ __align__(128) uint8_t smem[];
+  const TileList L = tile_list(P, threadIdx.x & 31, blockIdx.x == 0 && threadIdx.x < 32);
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * paged_warps(D);
+  // one range each; more only when there are more heads than warps
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * paged_warps(D) + (threadIdx.x >> 5);
+       w < static_cast<int64_t>(P.parts) * P.v_heads; w += warps)
+    attend_range<D, WIDE, F32>(P, L, w, smem);
+}
 
-__device__ __forceinline__ float block_reduce(float v, bool is_max, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float w = __shfl_xor_sync(kFull, v, o);
-    v = is_max ? fmaxf(v, w) : v + w;
+// ---- the join
+constexpr int kFinishThreads = 256;
+constexpr int kFinishWarps = kFinishThreads / 32;
+constexpr int kFinishWeightCtas = 3;   // per SM, of 4 that fit: the joins run beside them
+
+
+
+// The records of request r: the ranges that cross its n tiles (first: its
+// first tile in the list).
+struct Records {
+  int64_t first;
+  int count;
+};
+__device__ __forceinline__ Records records_of(const TileList& L, int64_t first, int n, int r) {
+  Records x{0, 0};
+  if (n > 0) {
+    // the range of tile t is the largest p with begin(p) <= t
+    const int64_t p0 = ((first + 1) * L.parts - 1) / L.total;
+    x.count = static_cast<int>(((first + n) * L.parts - 1) / L.total - p0 + 1);
+    x.first = p0 + r;
   }
-  __syncthreads();   // red is free
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
+  return x;
+}
+__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) v = is_max ? fmaxf(v, red[w]) : v + red[w];
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
   return v;
 }
-
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+__device__ __forceinline__ float2 load_ml(const PagedParams& P, const Records& x, int k, int hq) {
+  return __ldcg(P.rec_ml + (x.first + k) * P.q_heads + hq);
+}
+// Largest running maximum of a query head's records, and the sum of their
+// sums brought to it (warp-wide).
+__device__ __forceinline__ void join_stats(const PagedParams& P, const Records& x, int hq, int lane, float& M, float& sum) {
+  float m = -FLT_MAX, s = 0.0f;
+  for (int k = lane; k < x.count; k += 32) {
+    const float2 ml = load_ml(P, x, k, hq);
+    const float up = fmaxf(m, ml.x);
+    s = s * ex2(m - up) + ml.y * ex2(ml.x - up);
+    m = up;
+  }
+  M = warp_max(m);
+  sum = warp_sum(s * ex2(m - M));
+}
+// sum of the records k = begin, begin + step, ... of a query head, lane: dims lane V .. lane V + V - 1
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const __grid_constant__ PagedParams P) {
-  constexpr int V = D / 32;   // dims of a lane
-  __shared__ int64_t s_first;
-  __shared__ TileList s_list;
-  __shared__ float s_red[kJoinWarps];
-  __shared__ float s_e[kJoinRecords];
-  __shared__ float s_acc[kJoinWarps][D];
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int r = blockIdx.x, hq = blockIdx.y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp == 0) {
-    const TileList L = tile_list(P, lane, false);
-    const int64_t f = first_tile(P, r, lane);
-    if (lane == 0) {
-      s_list = L;
-      s_first = f;
+__device__ __forceinline__ void join_values(const PagedParams& P, const Records& x, int hq, int lane, float M, int begin,
+                                            int step, float (&acc)[D / 32]) {
+  constexpr int V = D / 32;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll 8
+  for (int k = begin; k < x.count; k += step) {
+    const float e = ex2(load_ml(P, x, k, hq).x - M);
+    const float* a = P.rec_acc + ((x.first + k) * P.q_heads + hq) * D + lane * V;
+    float v[V];
+    if constexpr (V == 2) {
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(a));
+      v[0] = y.x, v[1] = y.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(a + i));
+        v[i] = y.x, v[i + 1] = y.y, v[i + 2] = y.z, v[i + 3] = y.w;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += e * v[i];
   }
+}
+__device__ __forceinline__ void store_out(const PagedParams& P, int64_t at, float v) {
+  if (P.out_bf16) static_cast<__nv_bfloat16*>(P.out)[at] = __float2bfloat16_rn(v);
+  else static_cast<float*>(P.out)[at] = v;
+}
+
+// out and lse of (request, query head) `task`, by one warp or (ALL) by all
+// warps of the CTA, which share the records.
+template <int D, bool ALL>
+__device__ __forceinline__ void join_output(const PagedParams& P, const TileList& L, int64_t first, int r, int hq, float* part) {
+  constexpr int V = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = tiles_of(P, r, false);
-  __syncthreads();
-  int64_t rec0 = 0;   // the request's first record
-  int recs = 0;
-  if (n > 0) {
-    const TileList L = s_list;
-    // the range of tile t is the largest p with begin(p) <= t
-    const int64_t p0 = ((s_first + 1) * L.parts - 1) / L.total;
-    recs = static_cast<int>(((s_first + n) * L.parts - 1) / L.total - p0 + 1);
-    rec0 = p0 + r;
-  }
-  // everything above came from the caller's lengths; the records are the previous kernel's
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float2* ml = P.rec_ml + rec0 * P.q_heads + hq;
-  const float* acc_in = P.rec_acc + (rec0 * P.q_heads + hq) * D;
-  float mx = -FLT_MAX;
-  for (int k = threadIdx.x; k < recs; k += kJoinThreads) mx = fmaxf(mx, ml[static_cast<int64_t>(k) * P.q_heads].x);
-  const float M = block_reduce(mx, true, s_red);
-  float part = 0.0f;
-  float acc[V] = {};
-  for (int k0 = 0; k0 < recs; k0 += kJoinRecords) {
-    const int m = min(kJoinRecords, recs - k0);
-    __syncthreads();   // s_e is free
-    for (int k = threadIdx.x; k < m; k += kJoinThreads) {
-      const float2 x = ml[static_cast<int64_t>(k0 + k) * P.q_heads];
-      const float e = exp2f(x.x - M);
-      s_e[k] = e;
-      part += e * x.y;
-    }
+  const Records x = records_of(L, first, n, r);
+  float M, sum, acc[V];
+  join_stats(P, x, hq, lane, M, sum);
+  join_values<D>(P, x, hq, lane, M, ALL ? warp : 0, ALL ? kFinishWarps : 1, acc);
+  const int64_t task = static_cast<int64_t>(r) * P.q_heads + hq;
+  if (ALL) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) part[warp * D + lane * V + i] = acc[i];
     __syncthreads();
-#pragma unroll 4
-    for (int k = warp; k < m; k += kJoinWarps) {
-      const float e = s_e[k];
-      const float* a = acc_in + static_cast<int64_t>(k0 + k) * P.q_heads * D + lane * V;
+    for (int d = threadIdx.x; d < D; d += kFinishThreads) {
+      float v = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += e * a[i];
+      for (int w = 0; w < kFinishWarps; ++w) v += part[w * D + d];
+      store_out(P, task * D + d, n > 0 ? v / sum : 0.0f);
     }
-  }
-  const float sum = block_reduce(part, false, s_red);
+  } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
-  __syncthreads();
-  const int64_t out_at = (static_cast<int64_t>(r) * P.q_heads + hq) * D;
-  for (int d = threadIdx.x; d < D; d += kJoinThreads) {
-    float x = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) x += s_acc[w][d];
-    const float v = n > 0 ? x / sum : 0.0f;
-    if (P.out_bf16) static_cast<__nv_bfloat16*>(P.out)[out_at + d] = __float2bfloat16_rn(v);
-    else static_cast<float*>(P.out)[out_at + d] = v;
+    for (int i = 0; i < V; ++i) store_out(P, task * D + lane * V + i, n > 0 ? acc[i] / sum : 0.0f);
   }
-  if (threadIdx.x == 0) {
-    const float l2 = n > 0 ? M + log2f(sum) : -INFINITY;
-    if (P.lse != nullptr) P.lse[static_cast<int64_t>(r) * P.q_heads + hq] = l2 * kLn2;
-    if (P.lse2 != nullptr) P.lse2[static_cast<int64_t>(r) * P.q_heads + hq] = l2;
-  }
+  if (P.lse != nullptr && lane == 0 && (warp == 0 || !ALL)) P.lse[task] = n > 0 ? (M + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Adds each slot's attention weight: a warp takes a run of tiles for one
-// weight head, half a warp a tile, one lane a slot; the query heads are summed
-// in order (no atomics: a slot belongs to one lane).  A lane looks up four
-// slots, then loads their scores and old weights together: the step is a
-// chain of two memory round trips, not bandwidth, so few of them count.
-constexpr int kWeightThreads = 256;
-constexpr int kWeightCtas = 6;      // per SM
-constexpr int kWeightBatch = 4;
+// weight head, four lanes a tile, a lane four slots (one 16-byte load of each
+// head's scores); the query heads are summed in order, and no atomics are
+// needed: a slot belongs to one lane.  Few warps wait for long latencies
+// here, so every load of a step is issued unconditionally (places past the run
+// are read again from its last tile and dropped) and 16 tiles are in flight.
+constexpr int kWeightBatch = 2;
 
-__global__ void __launch_bounds__(kWeightThreads, kWeightCtas) k_paged_weights(const __grid_constant__ PagedParams P) {
-  const int lane = threadIdx.x & 31, half = lane >> 4, sl = lane & (TT - 1);
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * (kWeightThreads / 32) + (threadIdx.x >> 5);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kWeightThreads / 32) / P.weight_heads;
-  const int wh = static_cast<int>(w % P.weight_heads);
+__device__ __forceinline__ void add_weights(const PagedParams& P, const TileList& L, int64_t w, int64_t all) {
+  const int lane = threadIdx.x & 31, c = (lane & 3) * 4;
   const int64_t part = w / P.weight_heads;
-  if (part >= warps) return;
-  const TileList L = tile_list(P, lane, false);
-  const int64_t t_begin = L.total * part / warps, t_end = L.total * (part + 1) / warps;
+  const int wh = static_cast<int>(w % P.weight_heads);
+  const int64_t t_begin = L.total * part / all, t_end = L.total * (part + 1) / all;
   if (t_begin >= t_end) return;
   const int heads = P.q_heads / P.weight_heads;   // query heads of a weight head
-  Place x;
-  find_tile(P, t_begin, lane, x.req, x.first);
-  x.tile = static_cast<int>(t_begin - x.first);
-  x.len = legal_len(__ldg(P.lens + x.req), P.max_len, P.status, false);
-  if (half != 0) advance(P, x);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int64_t t = t_begin + half; t < t_end; t += 2 * kWeightBatch) {
-    int64_t at[kWeightBatch];
-    int req[kWeightBatch];
-#pragma unroll
-    for (int u = 0; u < kWeightBatch; ++u) {
-      at[u] = -1;
-      req[u] = x.req;
-      if (t + 2 * u >= t_end) continue;
-      const int slot = x.tile * TT + sl;
-      if (slot < x.len) {
+  const int hq0 = wh * heads;
+  const int bs = P.paged.block_size;
+  const bool vec = (bs & 3) == 0 && (reinterpret_cast<uintptr_t>(P.weights) & 15) == 0;  // a lane's slots lie together
+  const float* scores = P.scores + hq0 * P.score_stride + c;
+  int r;
+  int64_t first;
+  find_tile(P, t_begin, lane, r, first);
+  for (int64_t t0 = t_begin; t0 < t_end;) {
+    const int len = legal_len(__ldg(P.lens + r), P.max_len, P.status, false);
+    const int n = (len + TT - 1) / TT;
+    const int64_t piece = min(t_end, first + n);   // tiles [t0, piece) are of request r
+    if (t0 < piece) {
+      const float* lse2 = P.lse2 + static_cast<int64_t>(r) * P.q_heads + hq0;
+      const int32_t* table = P.paged.tables + static_cast<int64_t>(r) * P.paged.max_blocks;
+      // element of a slot's weight, -1 for a block outside the cache
+      auto place = [&](int slot) -> int64_t {
         const int b = block_of(P.paged, slot);
-        const int32_t block = __ldg(P.paged.tables + static_cast<int64_t>(x.req) * P.paged.max_blocks + b);
-        if (block >= 0 && block < P.paged.num_cache_blocks)
-          at[u] = (static_cast<int64_t>(block) * P.weight_heads + wh) * P.paged.block_size + (slot - b * P.paged.block_size);
+        const int32_t block = __ldg(table + b);
+        return block >= 0 && block < P.paged.num_cache_blocks
+                   ? (static_cast<int64_t>(block) * P.weight_heads + wh) * bs + (slot - b * bs)
+                   : -1;
+      };
+      for (int64_t t = t0 + (lane >> 2); t - (lane >> 2) < piece; t += 8 * kWeightBatch) {
+        int64_t at[kWeightBatch], tile[kWeightBatch];
+        int slot[kWeightBatch];
+        float4 sum[kWeightBatch], old[kWeightBatch];
+#pragma unroll
+        for (int u = 0; u < kWeightBatch; ++u) {
+          const bool mine = t + 8 * u < piece;
+          tile[u] = mine ? t + 8 * u : piece - 1;
+          slot[u] = static_cast<int>(tile[u] - first) * TT + c;
+          at[u] = place(min(slot[u], len - 1));
+          if (!mine || slot[u] >= len) at[u] = -1;
+          sum[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        if (vec) {
+#pragma unroll
+          for (int u = 0; u < kWeightBatch; ++u)
+            old[u] = __ldcg(reinterpret_cast<const float4*>(P.weights + (at[u] < 0 ? 0 : at[u])));
+        }
+#pragma unroll 4
+        for (int h = 0; h < heads; ++h) {
+          const float l2 = __ldcg(lse2 + h);
+#pragma unroll
+          for (int u = 0; u < kWeightBatch; ++u) {
+            const float4 s = __ldcg(reinterpret_cast<const float4*>(scores + h * P.score_stride + tile[u] * TT));
+            sum[u].x += ex2(s.x - l2);
+            sum[u].y += ex2(s.y - l2);
+            sum[u].z += ex2(s.z - l2);
+            sum[u].w += ex2(s.w - l2);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kWeightBatch; ++u) {
+          if (vec && at[u] >= 0 && slot[u] + 4 <= len) {
+            *reinterpret_cast<float4*>(P.weights + at[u]) =
+                make_float4(old[u].x + sum[u].x, old[u].y + sum[u].y, old[u].z + sum[u].z, old[u].w + sum[u].w);
+          } else if (t + 8 * u < piece) {
+            const float x[4] = {sum[u].x, sum[u].y, sum[u].z, sum[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (slot[u] + i >= len) continue;
+              const int64_t e = place(slot[u] + i);
+              if (e >= 0) P.weights[e] += x[i];
+            }
+          }
+        }
       }
-      advance(P, x);
-      advance(P, x);
     }
-    float old[kWeightBatch], sum[kWeightBatch];
-#pragma unroll
-    for (int u = 0; u < kWeightBatch; ++u) {
-      sum[u] = 0.0f;
-      if (at[u] >= 0) old[u] = P.weights[at[u]];
-    }
-    const float* sc = P.scores + wh * heads * P.score_stride + t * TT + sl;
-#pragma unroll 2
-    for (int h = 0; h < heads; ++h, sc += P.score_stride) {
-#pragma unroll
-      for (int u = 0; u < kWeightBatch; ++u)
-        if (at[u] >= 0)
-          sum[u] += exp2f(__ldcs(sc + 2 * u * TT) - P.lse2[static_cast<int64_t>(req[u]) * P.q_heads + wh * heads + h]);
-    }
-#pragma unroll
-    for (int u = 0; u < kWeightBatch; ++u)
-      if (at[u] >= 0) P.weights[at[u]] = old[u] + sum[u];
+    t0 = max(t0, piece);
+    first += n;
+    ++r;
   }
 }
 
+// One warp per (request, query head): its log-sum-exp in log2 units, for the
+// weights (their warps are many: each joining the records itself took 5 us
+// longer on one request of 128k slots).
+__global__ void __launch_bounds__(kFinishThreads) k_paged_lse(const __grid_constant__ PagedParams P) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31;
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * kFinishWarps + (threadIdx.x >> 5);
+  const int r = static_cast<int>(task / P.q_heads), hq = static_cast<int>(task % P.q_heads);
+  if (r >= P.n_req) return;
+  const TileList L = tile_list(P, lane, false);
+  const Records x = records_of(L, first_tile(P, r, lane), tiles_of(P, r, false), r);
+  // everything so far came from the caller's lengths; the records are the previous kernel's
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float M, sum;
+  join_stats(P, x, hq, lane, M, sum);
+  if (lane == 0) P.lse2[task] = M + log2f(sum);
+}
+
+// The first CTAs add the weights (the longer part); the others join the
+// records into the outputs: one CTA per (request, query head) while these are
+// few (few requests, each cut into many ranges), else one warp for each.
+template <int D>
+__global__ void __launch_bounds__(kFinishThreads, 4) k_paged_finish(const __grid_constant__ PagedParams P) {
+  __shared__ float s_part[kFinishWarps * D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const TileList L = tile_list(P, lane, false);
+  const int block = static_cast<int>(blockIdx.x) - P.weight_ctas;
+  if (block >= 0) {
+    const bool all = P.join_wide != 0;
+    const int64_t task = all ? block : static_cast<int64_t>(block) * kFinishWarps + warp;
+    const int r = static_cast<int>(task / P.q_heads), hq = static_cast<int>(task % P.q_heads);
+    if (r >= P.n_req) return;
+    const int64_t first = first_tile(P, r, lane);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (all) join_output<D, true>(P, L, first, r, hq, s_part);
+    else join_output<D, false>(P, L, first, r, hq, s_part);
+    return;
+  }
+  const int64_t warps = static_cast<int64_t>(P.weight_ctas) * kFinishWarps;
+  const int64_t all = warps / P.weight_heads > 0 ? warps / P.weight_heads : 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * kFinishWarps + warp; w < all * P.weight_heads; w += warps)
+    add_weights(P, L, w, all);
+}
+
 // A kernel launched as a programmatic dependent of the one before it.
-template <typename Kern>
-cudaError_t launch_after(Kern kern, dim3 grid, int threads, const PagedParams& p, cudaStream_t s) {
+cudaError_t launch_after(void (*kern)(PagedParams), unsigned grid, const PagedParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kFinishThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -586,7 +710,8 @@ cudaError_t launch_after(Kern kern, dim3 grid, int threads, const PagedParams& p
 template <int D, bool WIDE, bool F32>
 cudaError_t launch_attend_d(const PagedParams& p, int grid, cudaStream_t s) {
   auto kern = k_paged_attend<D, WIDE, F32>;
-  const int smem = static_cast<int>(paged_smem(D));
+  constexpr int smem = paged_warps(D) * (paged_stages(D) * stage_bytes(D) + score_stage(WIDE) * static_cast<int>(sizeof(float)));
+  static_assert(smem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<grid, 32 * paged_warps(D), smem, s>>>(p);
@@ -594,23 +719,24 @@ cudaError_t launch_attend_d(const PagedParams& p, int grid, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t launch_d(const PagedParams& p, int grid, int sm_count, cudaStream_t s) {
+cudaError_t launch_d(PagedParams p, int grid, int sm_count, cudaStream_t s) {
   const bool wide = p.group > 8;
   cudaError_t e;
   if (wide) e = p.out_bf16 ? launch_attend_d<D, true, false>(p, grid, s) : launch_attend_d<D, true, true>(p, grid, s);
   else e = p.out_bf16 ? launch_attend_d<D, false, false>(p, grid, s) : launch_attend_d<D, false, true>(p, grid, s);
   if (e != cudaSuccess) return e;
-  e = launch_after(k_paged_join<D>, dim3(p.n_req, p.q_heads), kJoinThreads, p, s);
-  if (e != cudaSuccess || p.weights == nullptr) return e;
-  const int need = (p.weight_heads + kWeightThreads / 32 - 1) / (kWeightThreads / 32);
-  return launch_after(k_paged_weights, dim3(std::max(sm_count * kWeightCtas, need)), kWeightThreads, p, s);
+  const int64_t tasks = static_cast<int64_t>(p.n_req) * p.q_heads;
+  p.join_wide = tasks <= 2 * sm_count;
+  p.weight_ctas = p.weights != nullptr ? kFinishWeightCtas * sm_count : 0;
+  const int64_t join_ctas = p.join_wide ? tasks : (tasks + kFinishWarps - 1) / kFinishWarps;
+  if (p.weights != nullptr) {
+    e = launch_after(k_paged_lse, static_cast<unsigned>((tasks + kFinishWarps - 1) / kFinishWarps), p, s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_after(k_paged_finish<D>, static_cast<unsigned>(p.weight_ctas + join_ctas), p, s);
 }
 
 }  // namespace
-
-size_t paged_smem(int head_dim) {
-  return static_cast<size_t>(paged_warps(head_dim)) * paged_stages(head_dim) * stage_bytes(head_dim);
-}
 
 int paged_warps_per_cta(int head_dim) { return paged_warps(head_dim); }
 

@@ -614,3 +614,10 @@ def test_decode_loop_after_a_stitch():
             a, b = s.tables[0][j // s.bs], s.tables[0][src // s.bs]
             assert torch.equal(s.v_cache[0, a, j % s.bs, h], before[0, b, src % s.bs, h])
     s.close()
+
+
+def test_attend_paged_more_heads_than_warps():
+    """1,500 KV heads: every warp of the launch serves more than one."""
+    c = Cache(heads=1500, d=64, bs=4, lens=[9, 3], seed=30)
+    _attend(c, 1500, torch.bfloat16)
+    c.close()
