@@ -77,7 +77,6 @@ constexpr int kPagedTile = 16;          // positions of one step of a warp
 constexpr int kPagedWarps = 8;          // warps per CTA, each with its own ring
 constexpr int kPagedMaxCtas = 256;      // grid bound (workspace sizing)
 constexpr int kPagedMaxHeads = 4096;    // query heads
-constexpr int kPagedMinTiles = 4;       // least tiles of one warp's range
 
 struct PagedParams {
   PagedView paged;

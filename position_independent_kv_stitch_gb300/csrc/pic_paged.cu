@@ -121,8 +121,7 @@ __device__ __forceinline__ TileList tile_list(const PagedParams& P, int lane, bo
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
   TileList L;
   L.total = n;
-  const int64_t want = (n + kPagedMinTiles - 1) / kPagedMinTiles;
-  L.parts = want < P.parts ? (want < 1 ? 1 : want) : P.parts;
+  L.parts = n < P.parts ? (n < 1 ? 1 : n) : P.parts;   // at least a tile each
   return L;
 }
 // The request that holds tile t of the list, and its first tile (warp-wide;

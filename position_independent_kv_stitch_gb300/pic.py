@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -86,6 +87,10 @@ class pic_new_tokens(ctypes.Structure):
     ]
 
 
+_NEW_TOKENS = struct.Struct("@iii4xPPPqPqPqPqPP")
+assert _NEW_TOKENS.size == ctypes.sizeof(pic_new_tokens)
+_axis_arrays = {}   # frequency axes in use, as C arrays
+
 _c_void_p = ctypes.c_void_p
 _i32, _i64, _u32, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
 _P = ctypes.POINTER
@@ -139,7 +144,7 @@ _SIGNATURES = {
     "pic_fingerprint_spans": (ctypes.c_int, [_c_void_p, _i64, _c_void_p, _c_void_p, _i64, ctypes.c_uint64,
                                              _c_void_p, _c_void_p, _c_void_p]),
     "pic_s1_windows": (ctypes.c_int, [_i64, _i64, _i32, _P(_i64), _P(_i64), _i64, _P(_i64)]),
-    "pic_write_tokens": (ctypes.c_int, [_c_void_p, _P(pic_new_tokens), _c_void_p, _c_void_p, _c_void_p, _i32, _i32,
+    "pic_write_tokens": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i32,
                                         _c_void_p, _i32, _c_void_p, _sz, _c_void_p]),
     "pic_attend_paged_workspace_bytes": (_sz, [_c_void_p, _i32, _i32, _i32, _i32]),
     "pic_attend_paged": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i32, _i32, ctypes.c_float, _c_void_p, _c_void_p,
@@ -153,6 +158,7 @@ _SIGNATURES = {
 }
 
 _lib = None
+_torch = _BF16 = _F32 = _I32 = None   # set by load()
 # (cache blocks, (block size, KV heads, head dim), frequencies) of each live context, by handle
 _geometry = {}
 
@@ -163,7 +169,7 @@ def lib_path() -> str:
 
 def load(build_if_missing: bool = False):
     """Loads libpic.so (building it first only when asked); raises if absent."""
-    global _lib
+    global _lib, _torch, _BF16, _F32, _I32
     if _lib is not None:
         return _lib
     if build_if_missing and (not os.path.exists(_build.LIB_PATH) or _build.is_stale()):
@@ -176,6 +182,8 @@ def load(build_if_missing: bool = False):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    import torch
+    _torch, _BF16, _F32, _I32 = torch, torch.bfloat16, torch.float32, torch.int32
     _lib = lib
     return lib
 
@@ -668,23 +676,23 @@ def pic_attend_decode(ctx, plans, source, q, softmax_scale, k_pool, v_pool, k_ca
 
 # --------------------------------------------------- decode loop over the cache
 #
-# These calls are made once per layer and token, so the checks are lean: plain
-# integer comparisons, addresses passed as integers, no tensor views.
+# These calls are made once per layer and token, so the checks are lean: shapes
+# fetched once and compared whole, addresses passed as integers, no views.
 
-def _launch(ctx, name, tensors, stream, args):
-    """Calls lib.name(ctx, *args, stream) with the tensors' device current; a
-    tensor on another device, or on the host, is refused."""
-    import torch
+def _launch(ctx, fn, tensors, stream, args):
+    """fn(ctx, *args, stream) with the tensors' device current; a tensor on
+    another device, or on the host, is refused."""
     dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.get_device() != dev or dev < 0:
-            raise ValueError("every tensor must be on one CUDA device")
-    fn = getattr(_lib or load(), name)
-    if dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        raise ValueError("every tensor must be on one CUDA device")
+    if dev != _torch._C._cuda_getDevice():
+        with _torch.cuda.device(dev):
             _check(fn(ctx, *args, _stream_handle(stream)), ctx)
         return
-    st = fn(ctx, *args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
+    st = fn(ctx, *args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
     if st != PIC_OK:
         _check(st, ctx)
 
@@ -698,51 +706,55 @@ def _size(t):
 
 
 def _dense_int32(t, name, numel=None):
-    import torch
-    if t.dtype != torch.int32 or not t.is_contiguous() or (numel is not None and t.numel() != numel):
+    if t.dtype is not _I32 or not t.is_contiguous() or (numel is not None and t.numel() != numel):
         raise ValueError(f"{name} must be a contiguous CUDA int32 tensor" +
                          ("" if numel is None else f" of {numel} entries"))
 
 
-def _token_rows(t, name, n_tokens=None, heads=None):
-    """[tokens][heads][dim] bf16 with dense heads; returns the bytes between tokens."""
-    shape, strides = t.shape, t.stride()
-    if not _is_bf16(t) or len(shape) != 3 or strides[2] != 1 or (shape[1] > 1 and strides[1] != shape[2]) or \
-            (n_tokens is not None and shape[0] != n_tokens) or (heads is not None and shape[1:] != heads):
-        raise ValueError(f"{name} must be bf16 [tokens][heads][head_dim], a row per token, dense heads")
-    return strides[0] * 2
+def _token_rows(t, name, want=None):
+    """Bytes between the tokens of a bf16 [tokens][heads][dim] with dense heads (of shape `want`)."""
+    shape = t.shape
+    ok = t.dtype is _BF16 and len(shape) == 3 and (want is None or shape == want)
+    if ok and t.is_contiguous():
+        return shape[1] * shape[2] * 2
+    if ok:
+        strides = t.stride()
+        if strides[2] == 1 and (shape[1] <= 1 or strides[1] == shape[2]):
+            return strides[0] * 2
+    raise ValueError(f"{name} must be bf16 [tokens][heads][head_dim], a row per token, dense heads")
 
 
 def _check_cache(ctx, t, name, dim):
-    """A cache tensor ([layers][blocks][block_size][kv_heads][head_dim] for dim
-    5, one layer of it for dim 4) that holds the context's blocks and rows."""
+    """The shape of a cache tensor ([layers][blocks][block_size][kv_heads]
+    [head_dim] for dim 5, one layer of it for dim 4) that holds the context's
+    blocks and rows."""
     shape = t.shape
-    if not _is_bf16(t) or len(shape) != dim or not (t.is_contiguous() or (dim == 5 and t[0].is_contiguous())):
+    if t.dtype is not _BF16 or len(shape) != dim or not (t.is_contiguous() or (dim == 5 and t[0].is_contiguous())):
         raise ValueError(f"{name} must be a bf16 cache tensor of {dim} dims with contiguous rows")
+    blocks, bs, heads, d = shape if dim == 4 else shape[1:]
     want = _geometry.get(ctx.value)
-    if want is not None and (shape[dim - 4] < want[0] or shape[dim - 3:] != want[1]):
+    if want is not None and (blocks < want[0] or (bs, heads, d) != want[1]):
         raise ValueError(f"{name} must hold the context's {want[0]} blocks of {want[1][0]} rows {list(want[1][1:])}")
+    return shape
 
 
-def _weight_heads(weights, cache):
-    """Weight heads of a weights tensor [..][blocks][weight_heads][block_size] beside a cache."""
+def _weight_heads(weights, cache_shape):
+    """Weight heads of a weights tensor [..][blocks][weight_heads][block_size] beside a cache of that shape."""
     if weights is None:
         return 0
-    import torch
-    w, c = weights.shape, cache.shape
-    n = len(w)
-    if weights.dtype != torch.float32 or n != len(c) - 1 or w[n - 1] != c[n - 2] or w[:n - 2] != c[:n - 2] or \
-            not (weights.is_contiguous() or (n == 4 and weights[0].is_contiguous())):
+    w, n = weights.shape, len(cache_shape) - 1
+    if weights.dtype is not _F32 or len(w) != n or w[n - 1] != cache_shape[n - 2] or w[n - 3] != cache_shape[n - 3] or \
+            w[0] != cache_shape[0] or not (weights.is_contiguous() or (n == 4 and weights[0].is_contiguous())):
         raise ValueError("weights must be float32 [blocks][weight_heads][block_size], shaped as the cache")
     return w[n - 2]
 
 
-def _max_blocks(block_tables, rows=0):
+def _table_shape(block_tables, rows=0):
     _dense_int32(block_tables, "block_tables")
     shape = block_tables.shape
     if len(shape) != 2 or shape[0] < rows:
         raise ValueError("block_tables must be [n_req][max_blocks] with a row per request")
-    return shape[1]
+    return shape
 
 
 def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_cache, q=None, q_out=None,
@@ -757,32 +769,41 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
     [n_tokens][q_heads][head_dim], q_out may be q.  weights: float32
     [blocks][weight_heads][block_size], zeroed at the written slots.
     workspace: uint8, PIC_STATUS_BYTES, zeroed when made (its status is sticky)."""
+    lib = _lib or load()
     _dense_int32(positions, "positions")
     shape = positions.shape
-    axes, n = (1, shape[0]) if len(shape) == 1 else shape
+    axes, n = shape if len(shape) == 2 else (1, shape[0])
+    want = _geometry.get(ctx.value)
     q_heads = q_stride = out_stride = k_stride = v_stride = n_tables = max_blocks = heads = 0
     if q is not None:
-        q_heads = q.shape[1]
-        q_stride, out_stride = _token_rows(q, "q", n), _token_rows(q_out, "q_out", n, q.shape[1:])
-        if ctx.value in _geometry and q.shape[2] != _geometry[ctx.value][1][2]:
-            raise ValueError("q heads must have the context's head_dim")
+        shape = q.shape
+        q_stride, out_stride = _token_rows(q, "q"), _token_rows(q_out, "q_out", shape)
+        tokens, q_heads, d = shape
+        if tokens != n or (want is not None and d != want[1][2]):
+            raise ValueError("q holds a row per token, heads of the context's head_dim")
     if k is not None:
-        for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-            if c is not None:
-                _check_cache(ctx, c, name, 4)
-        rows = k_cache.shape[2:]
-        k_stride = _token_rows(k, "k", n, rows)
-        v_stride = 0 if v is None else _token_rows(v, "v", n, rows)
+        shape = _check_cache(ctx, k_cache, "k_cache", 4)
+        rows = (n, shape[2], shape[3])
+        k_stride = _token_rows(k, "k", rows)
+        if v is not None:
+            v_stride = _token_rows(v, "v", rows)
+        if v_cache is not None:
+            _check_cache(ctx, v_cache, "v_cache", 4)
         _dense_int32(req, "req", n)
         _dense_int32(slot, "slot", n)
-        n_tables, max_blocks = block_tables.shape[0], _max_blocks(block_tables)
-        heads = _weight_heads(weights, k_cache)
-    half = _geometry[ctx.value][2] if ctx.value in _geometry else None
-    if freq_axis is not None and half is not None and len(freq_axis) != half:
-        raise ValueError(f"freq_axis holds an axis for each of the {half} frequencies")
-    t = pic_new_tokens(n, q_heads, axes, None if freq_axis is None else bytes(freq_axis), positions.data_ptr(), _addr(q),
-                       q_stride, _addr(q_out), out_stride, _addr(k), k_stride, _addr(v), v_stride, _addr(req), _addr(slot))
-    _launch(ctx, "pic_write_tokens",
+        n_tables, max_blocks = _table_shape(block_tables)
+        heads = _weight_heads(weights, shape)
+    if freq_axis is not None:
+        if want is not None and len(freq_axis) != want[2]:
+            raise ValueError(f"freq_axis holds an axis for each of the {want[2]} frequencies")
+        axis_bytes = bytes(freq_axis)
+        if axis_bytes not in _axis_arrays:
+            _axis_arrays[axis_bytes] = ctypes.create_string_buffer(axis_bytes, len(axis_bytes))
+        freq_axis = ctypes.addressof(_axis_arrays[axis_bytes])
+    # a pic_new_tokens, packed (filling in a ctypes structure takes longer than the call)
+    t = _NEW_TOKENS.pack(n, q_heads, axes, freq_axis or 0, positions.data_ptr(), _addr(q) or 0, q_stride, _addr(q_out) or 0,
+                         out_stride, _addr(k) or 0, k_stride, _addr(v) or 0, v_stride, _addr(req) or 0, _addr(slot) or 0)
+    _launch(ctx, lib.pic_write_tokens,
             (positions, q, q_out, k, v, req, slot, block_tables, k_cache, v_cache, weights, workspace), stream,
             (t, _addr(k_cache), _addr(v_cache), _addr(block_tables), n_tables, max_blocks, _addr(weights), heads,
              _addr(workspace), _size(workspace)))
@@ -803,23 +824,23 @@ def pic_attend_paged(ctx, q, softmax_scale, k_cache, v_cache, block_tables, seq_
     [blocks][weight_heads][block_size] or None, each slot's attention weight is
     added to it.  workspace: uint8, pic_attend_paged_workspace_bytes, its first
     PIC_STATUS_BYTES zeroed when made."""
-    import torch
+    lib = _lib or load()
     stride = _token_rows(q, "q")
-    n_req, hq, d = q.shape
+    shape = q.shape
+    n_req, hq, d = shape
     _dense_int32(seq_lens, "seq_lens", n_req)
-    max_blocks = _max_blocks(block_tables, n_req)
-    _check_cache(ctx, k_cache, "k_cache", 4)
+    _, max_blocks = _table_shape(block_tables, n_req)
+    cache = _check_cache(ctx, k_cache, "k_cache", 4)
     _check_cache(ctx, v_cache, "v_cache", 4)
-    out_type = out.dtype
-    if d != k_cache.shape[3] or out.shape != q.shape or not out.is_contiguous() or \
-            (out_type != torch.float32 and out_type != torch.bfloat16):
+    out_type = PIC_F32 if out.dtype is _F32 else PIC_BF16
+    if d != cache[3] or out.shape != shape or not out.is_contiguous() or (out_type == PIC_BF16 and out.dtype is not _BF16):
         raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape, heads of the cache's head_dim")
-    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n_req * hq or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not _F32 or lse.numel() != n_req * hq or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [n_req][q_heads]")
-    _launch(ctx, "pic_attend_paged", (q, k_cache, v_cache, block_tables, seq_lens, out, lse, weights, workspace), stream,
+    _launch(ctx, lib.pic_attend_paged, (q, k_cache, v_cache, block_tables, seq_lens, out, lse, weights, workspace), stream,
             (q.data_ptr(), stride, n_req, hq, softmax_scale, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-             max_blocks, seq_lens.data_ptr(), max_seq_len, out.data_ptr(), PIC_F32 if out_type == torch.float32 else PIC_BF16,
-             _addr(lse), _addr(weights), _weight_heads(weights, k_cache), _addr(workspace), _size(workspace)))
+             max_blocks, seq_lens.data_ptr(), max_seq_len, out.data_ptr(), out_type, _addr(lse), _addr(weights),
+             _weight_heads(weights, cache), _addr(workspace), _size(workspace)))
 
 
 def pic_evict_workspace_bytes(ctx, num_layers: int, n_req: int, weight_heads: int, budget: int = 0) -> int:
@@ -837,21 +858,24 @@ def pic_evict_tokens(ctx, k_cache, v_cache, weights, block_tables, seq_lens, bud
     [layers][n_req][weight_heads][budget].  renumber: keys are re-rotated to
     their new slots.  workspace: uint8, pic_evict_workspace_bytes, its first
     PIC_STATUS_BYTES zeroed when made."""
-    n_req, layers = seq_lens.numel(), k_cache.shape[0]
-    max_blocks = _max_blocks(block_tables, n_req)
-    _check_cache(ctx, k_cache, "k_cache", 5)
+    lib = _lib or load()
+    n_req = seq_lens.numel()
+    _, max_blocks = _table_shape(block_tables, n_req)
+    cache = _check_cache(ctx, k_cache, "k_cache", 5)
+    layers = cache[0]
+    stride = k_cache.stride()[0]
     if v_cache is not None:
         _check_cache(ctx, v_cache, "v_cache", 5)
-        if v_cache.shape != k_cache.shape or (layers > 1 and v_cache.stride(0) != k_cache.stride(0)):
+        if v_cache.shape != cache or (layers > 1 and v_cache.stride()[0] != stride):
             raise ValueError("k_cache and v_cache must share a shape and a layer stride")
     if weights is None:
         raise ValueError("weights are required")
-    heads = _weight_heads(weights, k_cache)
+    heads = _weight_heads(weights, cache)
     _dense_int32(seq_lens, "seq_lens")
     _dense_int32(new_lens, "new_lens", n_req)
     _dense_int32(kept, "kept", layers * n_req * heads * budget)
-    _launch(ctx, "pic_evict_tokens", (k_cache, v_cache, weights, block_tables, seq_lens, kept, new_lens, workspace), stream,
-            (layers, k_cache.data_ptr(), _addr(v_cache), k_cache.stride(0) * 2, weights.data_ptr(), weights.stride(0) * 4, heads,
+    _launch(ctx, lib.pic_evict_tokens, (k_cache, v_cache, weights, block_tables, seq_lens, kept, new_lens, workspace), stream,
+            (layers, k_cache.data_ptr(), _addr(v_cache), stride * 2, weights.data_ptr(), weights.stride()[0] * 4, heads,
              block_tables.data_ptr(), n_req, max_blocks, seq_lens.data_ptr(), budget, n_first, n_recent, 1 if renumber else 0,
              kept.data_ptr(), new_lens.data_ptr(), _addr(workspace), _size(workspace)))
 

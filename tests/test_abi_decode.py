@@ -163,6 +163,6 @@ def test_binding_refuses_host_tensors_and_foreign_shapes(gqa):
             pic._check_cache(gqa, bad, "k_cache", 4)
     pic._check_cache(gqa, cache, "k_cache", 4)
     with pytest.raises(ValueError):
-        pic._weight_heads(torch.zeros(64, 2, 8), cache)
+        pic._weight_heads(torch.zeros(64, 2, 8), cache.shape)
     with pytest.raises(ValueError):
         pic._token_rows(cache.transpose(1, 2)[0], "q")
