@@ -690,9 +690,8 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
                             int32_t max_seq_len, void* out, int32_t out_type, float* lse, float* d_weights,
                             int32_t weight_heads, void* d_workspace, size_t workspace_bytes, pic_stream_t stream);
 
-/* Workspace bytes of pic_evict_tokens; budget 0: enough for any budget. */
-size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t n_req, int32_t weight_heads,
-                                 int32_t budget);
+/* Workspace bytes of pic_evict_tokens. */
+size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t n_req, int32_t weight_heads);
 
 /*
  * Cuts sequences longer than `budget` to budget tokens, in place, in num_layers

@@ -112,34 +112,43 @@ bool paged_heads_ok(const CtxView& c, int32_t num_q_heads) {
   return c.model->kind == PIC_KIND_GQA && num_q_heads > 0 && num_q_heads % c.model->num_kv_heads == 0;
 }
 
-// How the move cuts its work: pieces of at most kEvictPieceItems 32-byte items
-// (a head each when the heads keep sets of their own), tiles of ranks.
+// How finely the move slices the kept rows of each (layer, request, tensor,
+// and head where heads keep sets of their own): into as many slices of whole
+// 32-byte items as fill the resident CTAs best.  Slices below 128 bytes cost
+// DRAM efficiency (weighed 0.7 and 0.5, by the time of one request's layer).
 struct EvictShape {
-  int32_t tensors, piece_heads, pieces, tile_rows, tiles;
+  int32_t tensors, pieces, piece_heads, slices, slice_items;
 };
-EvictShape evict_shape(const CtxView& c, int32_t weight_heads, int32_t budget) {
+EvictShape evict_shape(const CtxView& c, int32_t weight_heads, int64_t units, int sm_count) {
   const pic_model_desc& m = *c.model;
-  budget = std::max(1, std::min(budget, cache_rows(c)));  // no sequence is longer than the cache
-  const int32_t head_items = m.head_dim * 2 / 32;
   EvictShape s{};
   s.tensors = m.kind == PIC_KIND_GQA ? 2 : 1;
-  s.piece_heads = weight_heads > 1 ? 1 : std::min(m.num_kv_heads, kEvictPieceItems / head_items);
-  s.pieces = (m.num_kv_heads + s.piece_heads - 1) / s.piece_heads;
-  s.tile_rows = kEvictTileItems / (s.piece_heads * head_items);
-  s.tiles = (budget - 1) / s.tile_rows + 1;
+  s.pieces = weight_heads > 1 ? m.num_kv_heads : 1;
+  s.piece_heads = weight_heads > 1 ? 1 : m.num_kv_heads;
+  const int32_t items = s.piece_heads * (m.head_dim * 2 / 32);
+  const int64_t streams = units * s.tensors * s.pieces, room = static_cast<int64_t>(sm_count) * kEvictMoveCtas;
+  double best = -1.0;
+  for (int32_t per = std::min(items, kEvictMoveThreads); per >= 1; --per) {
+    if (items % per != 0) continue;
+    const int64_t n = streams * (items / per), waves = (n + room - 1) / room;
+    const double fill = static_cast<double>(n) / static_cast<double>(waves * room);
+    const double score = fill * (per >= 4 ? 1.0 : (per >= 2 ? 0.7 : 0.5));
+    if (score > best * 1.02) {   // the widest of equals
+      best = score;
+      s.slices = items / per;
+      s.slice_items = per;
+    }
+  }
   return s;
 }
 struct EvictLayout {
-  size_t next_lens, units, flags, total;
-  int64_t n_flags;
+  size_t next_lens, units, total;
 };
-EvictLayout evict_layout(const EvictShape& s, int64_t layers, int64_t n_req, int64_t weight_heads) {
+EvictLayout evict_layout(int64_t layers, int64_t n_req, int64_t weight_heads) {
   EvictLayout L{};
-  L.n_flags = 1 + layers * n_req * s.tensors * s.pieces * s.tiles;
   L.next_lens = sizeof(WsHeader);
   L.units = align_up(L.next_lens + n_req * sizeof(int32_t), kWsAlign);
-  L.flags = align_up(L.units + layers * n_req * weight_heads * sizeof(EvictUnit), kWsAlign);
-  L.total = align_up(L.flags + L.n_flags * sizeof(uint32_t), kWsAlign);
+  L.total = align_up(L.units + layers * n_req * weight_heads * sizeof(EvictUnit), kWsAlign);
   return L;
 }
 
@@ -327,13 +336,9 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
   return set_error(ctx, PIC_OK, "");
 }
 
-size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t n_req, int32_t weight_heads,
-                                 int32_t budget) {
-  if (!ctx || num_layers <= 0 || n_req < 0 || budget < 0) return 0;
-  const CtxView c = ctx_view(ctx);
-  if (!weight_heads_ok(c, weight_heads)) return 0;
-  if (budget == 0) budget = cache_rows(c);
-  return evict_layout(evict_shape(c, weight_heads, budget), num_layers, n_req, weight_heads).total;
+size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t n_req, int32_t weight_heads) {
+  if (!ctx || num_layers <= 0 || n_req < 0 || !weight_heads_ok(ctx_view(ctx), weight_heads)) return 0;
+  return evict_layout(num_layers, n_req, weight_heads).total;
 }
 
 pic_status pic_evict_tokens(pic_ctx* ctx, int32_t num_layers, void* k_cache, void* v_cache, int64_t cache_ls,
@@ -362,11 +367,9 @@ pic_status pic_evict_tokens(pic_ctx* ctx, int32_t num_layers, void* k_cache, voi
   if (!aligned(d_weights, 4) || (weights_ls & 3) || !aligned(d_tables, 4) || !aligned(d_seq_lens, 4) ||
       !aligned(d_kept, 4) || !aligned(d_new_lens, 4) || !aligned(d_ws, kWsAlign))
     return fail(ctx, PIC_ERR_ALIGNMENT, "weights, tables, lengths and lists must be 4-byte aligned, the workspace 256-byte");
-  const EvictShape shape = evict_shape(c, weight_heads, budget);
-  const EvictLayout L = evict_layout(shape, num_layers, n_req, weight_heads);
-  if (static_cast<int64_t>(num_layers) * n_req > std::numeric_limits<int32_t>::max() / m.num_kv_heads ||
-      L.n_flags > std::numeric_limits<int32_t>::max())
-    return fail(ctx, PIC_ERR_RANGE, "more than 2^31 tiles to move: evict fewer layers or requests at a time");
+  if (static_cast<int64_t>(num_layers) * n_req * (row_bytes / 32) > std::numeric_limits<int32_t>::max() / 2)
+    return fail(ctx, PIC_ERR_RANGE, "layers x requests x row slices must stay below 2^30");
+  const EvictLayout L = evict_layout(num_layers, n_req, weight_heads);
   if (ws_bytes < L.total) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, L.total);
   if (n_req == 0) return set_error(ctx, PIC_OK, "");
   const Buffer bufs[] = {{"k_cache", k_cache}, {"v_cache", v_cache}, {"weights", d_weights}, {"block tables", d_tables},
@@ -403,14 +406,13 @@ pic_status pic_evict_tokens(pic_ctx* ctx, int32_t num_layers, void* k_cache, voi
   p.new_lens = d_new_lens;
   p.next_lens = reinterpret_cast<int32_t*>(ws + L.next_lens);
   p.units = reinterpret_cast<EvictUnit*>(ws + L.units);
-  p.flags = reinterpret_cast<uint32_t*>(ws + L.flags);
-  p.n_flags = L.n_flags;
-  p.sel_cap = std::min(p.max_len, kEvictCachedSlots);
+  p.sel_cap = static_cast<int32_t>(std::min<int64_t>((static_cast<int64_t>(p.max_len) + 3) / 4 * 4, kEvictCachedSlots));
+  const EvictShape shape = evict_shape(c, weight_heads, static_cast<int64_t>(num_layers) * n_req, sms);
   p.tensors = shape.tensors;
   p.pieces = shape.pieces;
   p.piece_heads = shape.piece_heads;
-  p.tile_rows = shape.tile_rows;
-  p.tiles = shape.tiles;
+  p.slices = shape.slices;
+  p.slice_items = shape.slice_items;
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
   const cudaError_t e = launch_evict(p, m.pairing, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(ctx, e, "eviction launch");

@@ -115,8 +115,8 @@ struct EvictUnit {           // per (layer, request, weight head), in the worksp
   int32_t n_keep;            // kept tokens (0: nothing to move)
   int32_t first_moved;       // kept tokens before this rank stay where they are
 };
-constexpr int kEvictTileItems = 512;     // 32-byte items of one tile of the move
-constexpr int kEvictPieceItems = 256;    // most items of one row piece
+constexpr int kEvictMoveThreads = 256;   // threads and
+constexpr int kEvictMoveCtas = 4;        // CTAs per SM of the move
 constexpr int kEvictCachedSlots = 48000; // weights the selection keeps in shared memory
 struct EvictParams {
   PagedView paged;
@@ -132,9 +132,9 @@ struct EvictParams {
   int32_t budget, n_first, n_recent;
   int32_t renumber;
   int32_t sel_cap;           // weights the selection keeps in shared memory
-  // the move: units (layer, request, tensor, piece of the heads) x tiles of ranks
+  // the move: a CTA per (layer, request, tensor, piece of the heads, slice of the piece)
   int32_t tensors, pieces, piece_heads;
-  int32_t tile_rows, tiles;
+  int32_t slices, slice_items;
   uint8_t* k_cache;
   uint8_t* v_cache;
   int64_t cache_ls;
@@ -144,8 +144,6 @@ struct EvictParams {
   int32_t* new_lens;
   int32_t* next_lens;        // workspace [n_req]: what new_lens becomes
   EvictUnit* units;          // workspace [layers * n_req * weight_heads]
-  uint32_t* flags;           // workspace: the ticket, then a "read" flag per unit and tile
-  int64_t n_flags;
   uint32_t* status;
 };
 cudaError_t launch_evict(const EvictParams& p, int pairing, cudaStream_t s);

@@ -7,24 +7,28 @@
 // 0 .. budget - 1; with `renumber` a key that moved from slot s to j is turned
 // by R(j - s), so that the cache is again a sequence of consecutive positions.
 //
-// Two launches, the second a programmatic dependent of the first:
+// Two launches.  (The second is no programmatic dependent of the first: its CTAs
+// live long, and those placed early would crowd the few SMs the first leaves
+// free.)
 //
 // k_evict_select, one CTA per (layer, request, weight head).  The weights are
 // read once into shared memory (those past its size are read again from L2).
 // The weight of the last token that fits is found by radix selection over the
 // weights' bits, from the top: 11, 11 and 10 bits, counted in shared memory.
 // Then every warp takes a contiguous run of slots, counts what it keeps, and
-// after a scan over the warps writes its kept slots and their weights, in
-// order and without further barriers.
+// after a scan over the warps writes its kept slots, in order and without
+// further barriers; the weights follow from shared memory.
 //
-// k_evict_move, one CTA per tile of kept rows (16 KB) of one tensor, in place.
-// Rank j lands on slot j, never above its own slot, so a tile may be written
-// once every lower tile of its unit has been read, and reading never has to
-// wait.  CTAs take tiles by a ticket, lowest tiles of all units first: a tile's
-// lower neighbours were taken earlier, by CTAs that are running, and the
-// wait for their "read" flags ends whatever the number of resident CTAs (it
-// is bounded all the same).  So one sequence is moved by as many CTAs as it
-// has tiles.  Kept tokens before the first evicted one are in place already.
+// k_evict_move, in place: one CTA per slice (32 bytes to whole rows) of the
+// kept rows of one tensor, which it walks in order.  Rank j lands on slot j,
+// never above its own slot, so rows may be read any time before, and a tile may
+// be written once the CTA has read it: the next tile's rows and the list of the
+// one after are on their way while a tile is written, with one barrier each.
+// Slices share no byte, so CTAs never wait for one another; how finely rows
+// are sliced is chosen so that the slices fill the GPU.  (Tiles of whole rows
+// dealt to all CTAs by tickets, each waiting for the lower tiles to be read,
+// moved 3.4-4.7 TB/s: a chain of five round trips to memory per tile.)  Kept
+// tokens before the first evicted one are in place already.
 #include "pic_decode.h"
 #include "pic_device.cuh"
 #include "pic_paged.cuh"
@@ -69,8 +73,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
 }
 
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictParams P) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  extern __shared__ float s_w[];   // weights of slots [0, cap)
+  extern __shared__ __align__(16) float s_w[];   // weights of the first slots
   __shared__ int s_hist[kBins];
   __shared__ int s_warp[kSelWarps];
   __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
@@ -85,9 +88,6 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   const int len = __ldg(P.lens + r);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bs = P.paged.block_size;
-
-  // the move's flags and ticket start at 0
-  for (int64_t i = unit * kSelThreads + tid; i < P.n_flags; i += static_cast<int64_t>(gridDim.x) * kSelThreads) P.flags[i] = 0;
 
   // a request whose length or blocks are not legal keeps all it has
   bool bad = len < 0 || len > P.max_len;
@@ -105,8 +105,9 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     }
     bad = __syncthreads_or(mine);
   }
-  if (tid == 0 && layer == 0 && wh == 0) P.next_lens[r] = bad || len <= P.budget ? len : P.budget;
-  if (bad || len <= P.budget) {
+  const bool cut = !bad && len > P.budget;
+  if (tid == 0 && layer == 0 && wh == 0) P.next_lens[r] = cut ? P.budget : len;
+  if (!cut) {
     for (int j = tid; j < P.budget; j += kSelThreads) kept[j] = !bad && j < len ? j : -1;
     if (tid == 0) P.units[unit] = EvictUnit{0, 0};
     return;
@@ -118,14 +119,31 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     const int64_t block = __ldg(P.paged.tables + static_cast<int64_t>(r) * P.paged.max_blocks + b);
     return wl + (block * P.weight_heads + wh) * bs + (slot - b * bs);
   };
-  const int cap = P.sel_cap;
-  auto weight_of = [&](int slot) -> float { return slot < cap ? s_w[slot] : __ldcg(at(slot)); };
+  const int cached = min(len, P.sel_cap);   // slots whose weights are in shared memory
+  // the weights of slots s .. s + 3 (0 past the end; s a multiple of 4)
+  auto load4 = [&](int s, float (&v)[4]) {
+    if (s + 4 <= cached) {
+      const float4 x = *reinterpret_cast<const float4*>(s_w + s);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = s + i >= len ? 0.0f : (s + i < cached ? s_w[s + i] : __ldcg(at(s + i)));
+    }
+  };
   const int lo = P.n_first, hi = len - P.n_recent;     // candidates: slots [lo, hi)
   const int want = P.budget - P.n_first - P.n_recent;  // how many of them stay; fewer than hi - lo
   for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
   if (tid == 0) s_first_moved = P.budget;
+  // four neighbouring slots lie together when blocks hold a multiple of four
+  const bool vec = (bs & 3) == 0 && ((reinterpret_cast<uintptr_t>(P.weights) | static_cast<uintptr_t>(P.weights_ls)) & 15) == 0;
+  if (vec) {
 #pragma unroll 4
-  for (int s = tid; s < min(len, cap); s += kSelThreads) s_w[s] = __ldcg(at(s));
+    for (int s = 4 * tid; s < cached; s += 4 * kSelThreads)
+      *reinterpret_cast<float4*>(s_w + s) = __ldcg(reinterpret_cast<const float4*>(at(s)));
+  } else {
+#pragma unroll 4
+    for (int s = tid; s < cached; s += kSelThreads) s_w[s] = __ldcg(at(s));
+  }
   __syncthreads();
 
   uint32_t border = 0xffffffffu;  // key of the last candidate that stays
@@ -137,9 +155,15 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
       const uint32_t digits = pass == 2 ? 1023u : 2047u;
-      for (int s = lo + tid; s < hi; s += kSelThreads) {
-        const uint32_t k = weight_key(weight_of(s));
-        if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & digits], 1);
+#pragma unroll 2
+      for (int s = 4 * tid; s < hi; s += 4 * kSelThreads) {
+        float v[4];
+        load4(s, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t k = weight_key(v[i]);
+          if (s + i >= lo && s + i < hi && (k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & digits], 1);
+        }
       }
       __syncthreads();
       // two digits a thread, from the top: the one in which the count reaches `left`
@@ -161,25 +185,38 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     ties = left;
   }
 
-  // every warp's run of slots, a multiple of 32
-  const int run = (len + kSelThreads - 1) / kSelThreads * 32;
+  // Every warp's run of slots, 128 a step, four neighbours a lane.  Per lane:
+  // bits of the slots that stay whatever happens, and of those with the
+  // border's key.
+  const int run = (len + kSelThreads * 4 - 1) / (kSelThreads * 4) * 128;
   const int begin = min(len, warp * run), end = min(len, begin + run);
-  auto classify = [&](int s, bool& stays, bool& tie) {
-    const bool cand = s >= lo && s < hi;
-    const uint32_t k = cand && want > 0 ? weight_key(weight_of(s)) : 0u;
-    tie = cand && want > 0 && k == border;
-    stays = s < end && (!cand || (want > 0 && k > border));
+  auto classify = [&](int s, uint32_t& stays, uint32_t& tie) {
+    float v[4];
+    load4(s, v);
+    stays = tie = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool cand = s + i >= lo && s + i < hi;
+      const uint32_t k = weight_key(v[i]);
+      if (s + i < end && (!cand || (want > 0 && k > border))) stays |= 1u << i;
+      if (cand && want > 0 && s + i < end && k == border) tie |= 1u << i;
+    }
   };
-  int gt = 0, eq = 0;
-  for (int s0 = begin; s0 < end; s0 += 32) {
-    bool stays, tie;
-    classify(s0 + lane, stays, tie);
-    gt += __popc(__ballot_sync(kFull, stays));
-    eq += __popc(__ballot_sync(kFull, tie && s0 + lane < end));
+  int mine = 0, mine_ties = 0;
+  for (int s0 = begin; s0 < end; s0 += 128) {
+    uint32_t stays, tie;
+    classify(s0 + 4 * lane, stays, tie);
+    mine += __popc(stays);
+    mine_ties += __popc(tie);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mine += __shfl_xor_sync(kFull, mine, o);
+    mine_ties += __shfl_xor_sync(kFull, mine_ties, o);
   }
   if (lane == 0) {
-    s_gt[warp] = gt;
-    s_eq[warp] = eq;
+    s_gt[warp] = mine;
+    s_eq[warp] = mine_ties;
   }
   __syncthreads();
   int gt_before = lane < warp ? s_gt[lane] : 0, eq_before = lane < warp ? s_eq[lane] : 0;
@@ -188,45 +225,65 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     gt_before += __shfl_xor_sync(kFull, gt_before, o);
     eq_before += __shfl_xor_sync(kFull, eq_before, o);
   }
-  const bool all_cached = len <= cap;
-  const unsigned below = (1u << lane) - 1u;
-  int first_out = len;   // first evicted slot of this run
-  for (int s0 = begin; s0 < end; s0 += 32) {
-    const int s = s0 + lane;
-    bool stays, tie;
+  int first_out = len;   // first evicted slot of this lane's
+  for (int s0 = begin; s0 < end; s0 += 128) {
+    const int s = s0 + 4 * lane;
+    uint32_t stays, tie;
     classify(s, stays, tie);
-    tie = tie && s < end;
-    const unsigned gts = __ballot_sync(kFull, stays), eqs = __ballot_sync(kFull, tie);
-    const int eq_mine = eq_before + __popc(eqs & below);
-    const bool keep = stays || (tie && eq_mine < ties);
-    const int rank = gt_before + __popc(gts & below) + min(eq_mine, ties);
-    if (keep) {
-      kept[rank] = s;
-      if (all_cached && rank != s) *at(rank) = s_w[s];
+    const int n = __popc(stays) | __popc(tie) << 16;   // 128 of each at most
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += up;
     }
-    const unsigned out = __ballot_sync(kFull, !keep && s < end);
-    if (out != 0 && first_out == len) first_out = s0 + __ffs(out) - 1;
-    gt_before += __popc(gts);
-    eq_before += __popc(eqs);
+    int gt = gt_before + ((incl - n) & 0xffff), eq = eq_before + ((incl - n) >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool is_tie = (tie >> i) & 1u, keep = ((stays >> i) & 1u) || (is_tie && eq < ties);
+      if (keep) kept[gt + min(eq, ties)] = s + i;
+      else if (s + i < end) first_out = min(first_out, s + i);
+      gt += (stays >> i) & 1u;
+      eq += is_tie ? 1 : 0;
+    }
+    const int all = __shfl_sync(kFull, incl, 31);
+    gt_before += all & 0xffff;
+    eq_before += all >> 16;
   }
-  if (lane == 0 && first_out < len) atomicMin(&s_first_moved, first_out);
+  if (first_out < len) atomicMin(&s_first_moved, first_out);
   __syncthreads();
   if (tid == 0) P.units[unit] = EvictUnit{P.budget, s_first_moved};
-  if (all_cached) return;
-  // some weights are only in memory: move them in order, a tile's reads before its writes
+  // the weights move with their tokens (kept[] is this CTA's own, written above)
+  if (cached == len) {
+    for (int j = s_first_moved + tid; j < P.budget; j += kSelThreads) *at(j) = s_w[kept[j]];
+    return;
+  }
+  // some are only in memory: in order, a tile's reads before its writes
   for (int base = s_first_moved; base < P.budget; base += kSelThreads) {
     const int j = base + tid;
     float x = 0.0f;
-    if (j < P.budget) x = weight_of(kept[j]);
+    if (j < P.budget) {
+      const int s = kept[j];
+      x = s < cached ? s_w[s] : __ldcg(at(s));
+    }
     // the barrier takes a value made of the loaded one: every load has arrived
     __syncthreads_or(__float_as_uint(x) == 0x7fc12345u);
     if (j < P.budget) *at(j) = x;
   }
 }
 
-constexpr int kMoveThreads = 128;
-constexpr int kMoveBatch = kEvictTileItems / kMoveThreads;  // items in flight per thread
-constexpr uint32_t kMaxPolls = 1u << 20;
+constexpr int kMoveThreads = kEvictMoveThreads;
+constexpr int kMoveCtas = kEvictMoveCtas;
+constexpr int kMoveBatch = 1;    // items per thread and tile
+constexpr int kMoveStages = 5;   // tiles in shared memory, most of them on their way
+constexpr int kMoveSmem = kMoveStages * kMoveBatch * kMoveThreads * (2 * 16 + 4);
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // cos / sin of a whole-position shift: the exact reduction of shift_cossin,
 // then the hardware's sine and cosine, whose absolute error on [-pi, pi] is
@@ -242,109 +299,147 @@ __device__ __forceinline__ void shift_cossin_fast(float d, float2 f, float& c, f
 }
 
 template <int PAIRING>
-__global__ void __launch_bounds__(kMoveThreads, 8) k_evict_move(const __grid_constant__ EvictParams P) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __grid_constant__ EvictParams P) {
   constexpr bool NEOX = PAIRING == kNeox;
-  __shared__ int64_t s_ticket;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (threadIdx.x == 0) s_ticket = static_cast<int64_t>(atomicAdd(P.flags, 1u));
-  __syncthreads();
-  // ticket = tile * units + unit; unit = ((layer, request), tensor, piece)
-  const int64_t units = static_cast<int64_t>(P.layers) * P.n_req * P.tensors * P.pieces;
-  const int64_t unit = s_ticket % units;
-  const int tile = static_cast<int>(s_ticket / units);
-  const int piece = static_cast<int>(unit % P.pieces);
-  const int tensor = static_cast<int>(unit / P.pieces % P.tensors);
-  const int64_t lr = unit / P.pieces / P.tensors;
+  // stream = ((layer, request), tensor, piece of the heads, slice of the piece)
+  const int64_t stream = blockIdx.x;
+  const int slice = static_cast<int>(stream % P.slices);
+  const int piece = static_cast<int>(stream / P.slices % P.pieces);
+  const int tensor = static_cast<int>(stream / P.slices / P.pieces % P.tensors);
+  const int64_t lr = stream / P.slices / P.pieces / P.tensors;
   const int r = static_cast<int>(lr % P.n_req);
   const int64_t layer = lr / P.n_req;
-  if (tile == 0 && layer == 0 && tensor == 0 && piece == 0 && threadIdx.x == 0) P.new_lens[r] = P.next_lens[r];
+  const int tid = threadIdx.x;
+  if (layer == 0 && tensor == 0 && piece == 0 && slice == 0 && tid == 0) P.new_lens[r] = P.next_lens[r];
   const int64_t wu = lr * P.weight_heads + (P.weight_heads == 1 ? 0 : piece);
   const EvictUnit u = P.units[wu];
-  const int base = u.first_moved + tile * P.tile_rows;   // first rank of the tile
-  if (base >= u.n_keep) return;
+  if (u.first_moved >= u.n_keep) return;
   const int32_t* kept = P.kept + wu * P.budget;
-  uint32_t* flags = P.flags + 1 + unit * P.tiles;
 
-  const int h0 = piece * P.piece_heads;
-  const int items = min(P.piece_heads, P.kv_heads - h0) * P.head_items;   // 32-byte items of a row
-  uint8_t* cache = (tensor == 0 ? P.k_cache : P.v_cache) + layer * P.cache_ls + static_cast<int64_t>(h0) * P.head_bytes;
+  // A row's slice is cut into items of two 16-byte chunks, one per thread, that
+  // lie half a head apart (in the latent of an MLA row: half a latent), so that
+  // neighbouring threads cover whole sectors and a neox item holds both
+  // members of its 8 pairs.
+  const int per_pass = kMoveThreads / P.slice_items;   // rows one pass of the CTA covers
+  const int my_row = tid / P.slice_items;
+  const bool idle = my_row >= per_pass;
+  const int item = slice * P.slice_items + tid - my_row * P.slice_items;   // within the piece
+  const int h = item / P.head_items, in_head = item - h * P.head_items;
+  const bool rope = tensor == 0 && in_head < P.rope_items;
+  const bool turns = rope && P.renumber;
+  const int run = tensor != 0 || rope ? P.rope_items : P.head_items - P.rope_items;   // items (GQA: the head's) between the two chunks
+  const int off_a = h * P.head_bytes + (rope ? P.rope_off + in_head * 16 : (tensor == 0 ? in_head - P.rope_items : in_head) * 16);
+  const int off_b = off_a + run * 16;
+  uint8_t* cache = (tensor == 0 ? P.k_cache : P.v_cache) + layer * P.cache_ls +
+                   static_cast<int64_t>(piece) * P.piece_heads * P.head_bytes;
   const int64_t row_bytes = static_cast<int64_t>(P.kv_heads) * P.head_bytes;
-  const int rows = min(P.tile_rows, u.n_keep - base);
-
-  // An item is two 16-byte chunks; a key item of the rope slice holds both
-  // members of its 8 pairs.  off_a / off_b: its place in the piece's row.
-  auto chunks = [&](int item, int& off_a, int& off_b, int& freq) {
-    const int h = item / P.head_items, i = item - h * P.head_items;
-    const int ho = h * P.head_bytes;
-    freq = -1;
-    if (tensor == 0 && i < P.rope_items) {
-      off_a = ho + P.rope_off + (NEOX ? i : 2 * i) * 16;
-      off_b = ho + P.rope_off + (NEOX ? i + P.rope_items : 2 * i + 1) * 16;
-      freq = 8 * i;
-    } else {   // copied; MLA rows hold their latent before the rope slice
-      off_a = ho + (tensor == 0 ? i - P.rope_items : i) * 32;
-      off_b = off_a + 16;
+  // Rows on their way wait in shared memory, each thread's items in places of
+  // its own: what a thread reads back it copied in itself, and the barrier
+  // only orders the CTA's reads of a tile before its writes.
+  extern __shared__ __align__(16) uint4 s_ring[];   // [stage][item][2][thread], then the slots [stage][item][thread]
+  int* s_slot = reinterpret_cast<int*>(s_ring + kMoveStages * kMoveBatch * 2 * kMoveThreads);
+  __shared__ __align__(16) float2 s_freq[kMaxFreqs];
+  if (tid < kMaxFreqs) s_freq[tid] = P.freq.turns[tid];
+  __syncthreads();
+  auto place = [&](int stage, int i) { return stage * kMoveBatch + i; };
+  auto load_slots = [&](int base, int (&slot)[kMoveBatch]) {
+#pragma unroll
+    for (int i = 0; i < kMoveBatch; ++i) {
+      const int j = base + i * per_pass + my_row;
+      slot[i] = !idle && j < u.n_keep ? __ldcg(kept + j) : -1;
     }
   };
-  uint4 a[kMoveBatch], b[kMoveBatch];
-  int src[kMoveBatch];
-  uint32_t seen = 0;
+  // A slot's block (the selection has checked the table).  Kept raw until its
+  // row is needed: arithmetic on a load that has not arrived stops the warp.
+  const int32_t* table = P.paged.tables + static_cast<int64_t>(r) * P.paged.max_blocks;
+  const int bs = P.paged.block_size;
+  auto load_blocks = [&](const int (&slot)[kMoveBatch], int (&block)[kMoveBatch]) {
 #pragma unroll
-  for (int x = 0; x < kMoveBatch; ++x) {
-    const int e = x * kMoveThreads + threadIdx.x, row = e / items;
-    src[x] = row < rows ? __ldcg(kept + base + row) : -1;
-  }
+    for (int i = 0; i < kMoveBatch; ++i) block[i] = slot[i] >= 0 ? __ldg(table + block_of(P.paged, slot[i])) : 0;
+  };
+  auto load_dst_blocks = [&](int base, int (&block)[kMoveBatch]) {
 #pragma unroll
-  for (int x = 0; x < kMoveBatch; ++x) {
-    if (src[x] < 0) continue;
-    const int e = x * kMoveThreads + threadIdx.x;
-    int off_a, off_b, freq;
-    chunks(e % items, off_a, off_b, freq);
-    const uint8_t* p = cache + paged_row(P.paged, r, src[x]) * row_bytes;
-    a[x] = __ldcg(reinterpret_cast<const uint4*>(p + off_a));
-    b[x] = __ldcg(reinterpret_cast<const uint4*>(p + off_b));
-  }
-#pragma unroll
-  for (int x = 0; x < kMoveBatch; ++x)
-    if (src[x] >= 0) seen ^= a[x].x ^ b[x].x;
-  // the barrier takes a value made of the loaded ones: every load of the CTA has arrived
-  __syncthreads_or(seen == 0x7fc12345u);
-  if (threadIdx.x == 0)
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flags + tile), "r"(1u) : "memory");
-  // every lower tile of the unit has been read
-  bool timeout = false;
-  for (int t = threadIdx.x; t < tile; t += kMoveThreads) {
-    uint32_t done = 0;
-    for (uint32_t n = 0; n < kMaxPolls && done == 0; ++n)
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(done) : "l"(flags + t) : "memory");
-    timeout |= done == 0;
-  }
-  if (__syncthreads_or(timeout)) {
-    if (threadIdx.x == 0) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_TIMEOUT));
-    return;
-  }
-#pragma unroll
-  for (int x = 0; x < kMoveBatch; ++x) {
-    if (src[x] < 0) continue;
-    const int e = x * kMoveThreads + threadIdx.x;
-    const int j = base + e / items;
-    int off_a, off_b, freq;
-    chunks(e % items, off_a, off_b, freq);
-    if (P.renumber && freq >= 0 && src[x] != j) {
-      float c[8], s[8];
-#pragma unroll
-      for (int f = 0; f < 8; ++f) shift_cossin_fast(static_cast<float>(j - src[x]), P.freq.turns[freq + f], c[f], s[f]);
-      if (NEOX) {
-        rotate_neox(a[x], b[x], c, s);
-      } else {
-        rotate_interleaved(a[x], c, s);
-        rotate_interleaved(b[x], c + 4, s + 4);
-      }
+    for (int i = 0; i < kMoveBatch; ++i) {
+      const int j = base + i * per_pass + my_row;
+      block[i] = j < u.n_keep ? __ldg(table + block_of(P.paged, j)) : 0;
     }
-    uint8_t* p = cache + paged_row(P.paged, r, j) * row_bytes;
-    *reinterpret_cast<uint4*>(p + off_a) = a[x];
-    *reinterpret_cast<uint4*>(p + off_b) = b[x];
+  };
+  auto row_at = [&](int block, int slot) -> uint8_t* {
+    return cache + (static_cast<int64_t>(block) * bs + (slot - block_of(P.paged, slot) * bs)) * row_bytes;
+  };
+  auto fetch = [&](int stage, const int (&slot)[kMoveBatch], const int (&block)[kMoveBatch]) {
+#pragma unroll
+    for (int i = 0; i < kMoveBatch; ++i) {
+      if (slot[i] >= 0) {
+        const uint8_t* p = row_at(block[i], slot[i]);
+        cp_async16(s_ring + place(stage, i) * 2 * kMoveThreads + tid, p + off_a);
+        cp_async16(s_ring + (place(stage, i) * 2 + 1) * kMoveThreads + tid, p + off_b);
+      }
+      s_slot[place(stage, i) * kMoveThreads + tid] = slot[i];
+    }
+    cp_commit();
+  };
+  // The kept list runs two tiles ahead of the fetches, the table lookups of
+  // source and destination one ahead of their use.
+  const int tile = per_pass * kMoveBatch;
+  int slots[2][kMoveBatch], from[2][kMoveBatch], to[2][kMoveBatch];
+  {
+    int s[kMoveStages - 1][kMoveBatch], f[kMoveStages - 1][kMoveBatch];
+#pragma unroll
+    for (int k = 0; k < kMoveStages - 1; ++k) load_slots(u.first_moved + k * tile, s[k]);
+    load_slots(u.first_moved + (kMoveStages - 1) * tile, slots[0]);
+    load_slots(u.first_moved + kMoveStages * tile, slots[1]);
+    load_dst_blocks(u.first_moved, to[0]);
+#pragma unroll
+    for (int k = 0; k < kMoveStages - 1; ++k) load_blocks(s[k], f[k]);
+    load_blocks(slots[0], from[0]);
+#pragma unroll
+    for (int k = 0; k < kMoveStages - 1; ++k) fetch(k, s[k], f[k]);
   }
+  int stage = 0;
+  for (int base0 = u.first_moved; base0 < u.n_keep; base0 += 2 * tile) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int base = base0 + x * tile;
+      if (base >= u.n_keep) break;
+      fetch(stage == 0 ? kMoveStages - 1 : stage - 1, slots[x], from[x]);
+      load_slots(base + (kMoveStages + 1) * tile, slots[x]);
+      load_blocks(slots[x ^ 1], from[x ^ 1]);
+      load_dst_blocks(base + tile, to[x ^ 1]);
+      cp_wait<kMoveStages - 1>();
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kMoveBatch; ++i) {
+        const int slot = s_slot[place(stage, i) * kMoveThreads + tid];
+        if (slot < 0) continue;
+        const int j = base + i * per_pass + my_row;
+        uint4 a = s_ring[place(stage, i) * 2 * kMoveThreads + tid], b = s_ring[(place(stage, i) * 2 + 1) * kMoveThreads + tid];
+        if (turns && slot != j) {
+          const float shift = static_cast<float>(j - slot);
+          float c[8], s[8];
+          // neox: frequencies 8 i ..; interleaved: 4 i .. of the first chunk, 4 (i + run) .. of the second
+          const int f0 = NEOX ? 8 * in_head : 4 * in_head, f1 = NEOX ? f0 + 4 : 4 * (in_head + run);
+#pragma unroll
+          for (int f = 0; f < 8; f += 2) {
+            const float4 w = *reinterpret_cast<const float4*>(s_freq + (f < 4 ? f0 + f : f1 + f - 4));
+            shift_cossin_fast(shift, make_float2(w.x, w.y), c[f], s[f]);
+            shift_cossin_fast(shift, make_float2(w.z, w.w), c[f + 1], s[f + 1]);
+          }
+          if (NEOX) {
+            rotate_neox(a, b, c, s);
+          } else {
+            rotate_interleaved(a, c, s);
+            rotate_interleaved(b, c + 4, s + 4);
+          }
+        }
+        uint8_t* p = row_at(to[x][i], j);
+        *reinterpret_cast<uint4*>(p + off_a) = a;
+        *reinterpret_cast<uint4*>(p + off_b) = b;
+      }
+      stage = stage + 1 == kMoveStages ? 0 : stage + 1;
+    }
+  }
+  cp_wait<0>();
 }
 
 }  // namespace
@@ -357,17 +452,11 @@ cudaError_t launch_evict(const EvictParams& p, int pairing, cudaStream_t s) {
   k_evict_select<<<static_cast<unsigned>(lr * p.weight_heads), kSelThreads, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(lr * p.tensors * p.pieces * p.tiles));
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return pairing == kNeox ? cudaLaunchKernelEx(&cfg, k_evict_move<kNeox>, p)
-                          : cudaLaunchKernelEx(&cfg, k_evict_move<kInterleaved>, p);
+  auto move = pairing == kNeox ? k_evict_move<kNeox> : k_evict_move<kInterleaved>;
+  e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+  if (e != cudaSuccess) return e;
+  move<<<static_cast<unsigned>(lr * p.tensors * p.pieces * p.slices), kMoveThreads, kMoveSmem, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace pic

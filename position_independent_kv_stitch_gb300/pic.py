@@ -150,7 +150,7 @@ _SIGNATURES = {
     "pic_attend_paged": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i32, _i32, ctypes.c_float, _c_void_p, _c_void_p,
                                         _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _i32,
                                         _c_void_p, _sz, _c_void_p]),
-    "pic_evict_workspace_bytes": (_sz, [_c_void_p, _i32, _i32, _i32, _i32]),
+    "pic_evict_workspace_bytes": (_sz, [_c_void_p, _i32, _i32, _i32]),
     "pic_evict_tokens": (ctypes.c_int, [_c_void_p, _i32, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _i32, _c_void_p,
                                         _i32, _i32, _c_void_p, _i32, _i32, _i32, _i32, _c_void_p, _c_void_p, _c_void_p,
                                         _sz, _c_void_p]),
@@ -843,9 +843,8 @@ def pic_attend_paged(ctx, q, softmax_scale, k_cache, v_cache, block_tables, seq_
              _weight_heads(weights, cache), _addr(workspace), _size(workspace)))
 
 
-def pic_evict_workspace_bytes(ctx, num_layers: int, n_req: int, weight_heads: int, budget: int = 0) -> int:
-    """Bytes for evictions to `budget` (0: to any budget)."""
-    return int(load().pic_evict_workspace_bytes(ctx, int(num_layers), int(n_req), int(weight_heads), int(budget)))
+def pic_evict_workspace_bytes(ctx, num_layers: int, n_req: int, weight_heads: int) -> int:
+    return int(load().pic_evict_workspace_bytes(ctx, int(num_layers), int(n_req), int(weight_heads)))
 
 
 def pic_evict_tokens(ctx, k_cache, v_cache, weights, block_tables, seq_lens, budget: int, kept, new_lens, n_first: int = 0,
