@@ -239,14 +239,20 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache
   p.weights = with_k ? d_weights : nullptr;
   p.weight_heads = weight_heads;
   p.status = &static_cast<WsHeader*>(d_ws)->status;
+  // A warp's run of heads: all of a token's when there are tokens for 32 warps
+  // per SM, so that their cos / sin are made once; shorter runs, down to four
+  // steps, when there are few and latency counts.
   const int hpi = 32 / lanes;
-  const int iters = (p.q_heads + p.kv_heads + hpi - 1) / hpi;
-  p.rot_iters = 4;
-  p.rot_parts = (iters + p.rot_iters - 1) / p.rot_iters;
+  const int64_t iters = (static_cast<int64_t>(p.q_heads) + p.kv_heads + hpi - 1) / hpi;
+  const int64_t wanted = (static_cast<int64_t>(sms) * 32 + t->n_tokens - 1) / t->n_tokens;
+  p.rot_iters = static_cast<int32_t>(std::max<int64_t>(std::min<int64_t>(iters, 4), (iters + wanted - 1) / wanted));
+  p.rot_parts = static_cast<int32_t>((iters + p.rot_iters - 1) / p.rot_iters);
   const int64_t chunks = static_cast<int64_t>(p.q_heads) * p.q_copy_chunks + p.k_copy_chunks +
                          (t->v ? row_bytes / 16 : 0);
   p.copy_parts = static_cast<int32_t>((chunks + 255) / 256);
-  const cudaError_t e = launch_write(p, m.pairing, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (static_cast<int64_t>(t->n_tokens) * (p.rot_parts + p.copy_parts) > std::numeric_limits<int32_t>::max())
+    return fail(ctx, PIC_ERR_RANGE, "more than 2^31 warps of work: write fewer tokens at a time");
+  const cudaError_t e = launch_write(p, m.pairing, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(ctx, e, "token write launch");
   return set_error(ctx, PIC_OK, "");
 }

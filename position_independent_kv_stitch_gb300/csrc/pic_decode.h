@@ -70,7 +70,7 @@ struct WriteParams {
   int32_t weight_heads;
   uint32_t* status;
 };
-cudaError_t launch_write(const WriteParams& p, int pairing, int sm_count, cudaStream_t s);
+cudaError_t launch_write(const WriteParams& p, int pairing, cudaStream_t s);
 
 // ---- paged attention
 constexpr int kPagedTile = 16;          // positions of one step of a warp

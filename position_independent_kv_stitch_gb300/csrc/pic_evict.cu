@@ -285,19 +285,6 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// cos / sin of a whole-position shift: the exact reduction of shift_cossin,
-// then the hardware's sine and cosine, whose absolute error on [-pi, pi] is
-// below 2^-21: far inside the rounding to bf16 that follows, at a fifth of the
-// instructions (a moved key has a shift of its own, so nothing is shared).
-__device__ __forceinline__ void shift_cossin_fast(float d, float2 f, float& c, float& s) {
-  const float p = __fmul_rn(d, f.x);
-  const float e = __fmaf_rn(d, f.x, -p);
-  const float r = __fsub_rn(p, rintf(p));
-  const float t = 6.283185307179586f * __fadd_rn(r, __fmaf_rn(d, f.y, e));
-  c = __cosf(t);
-  s = __sinf(t);
-}
-
 template <int PAIRING>
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __grid_constant__ EvictParams P) {
   constexpr bool NEOX = PAIRING == kNeox;
@@ -422,8 +409,8 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __
 #pragma unroll
           for (int f = 0; f < 8; f += 2) {
             const float4 w = *reinterpret_cast<const float4*>(s_freq + (f < 4 ? f0 + f : f1 + f - 4));
-            shift_cossin_fast(shift, make_float2(w.x, w.y), c[f], s[f]);
-            shift_cossin_fast(shift, make_float2(w.z, w.w), c[f + 1], s[f + 1]);
+            turn_cossin(shift, make_float2(w.x, w.y), c[f], s[f]);
+            turn_cossin(shift, make_float2(w.z, w.w), c[f + 1], s[f + 1]);
           }
           if (NEOX) {
             rotate_neox(a, b, c, s);
