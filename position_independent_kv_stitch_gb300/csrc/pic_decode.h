@@ -74,7 +74,6 @@ cudaError_t launch_write(const WriteParams& p, int pairing, cudaStream_t s);
 
 // ---- paged attention
 constexpr int kPagedTile = 16;          // positions of one step of a warp
-constexpr int kPagedWarps = 8;          // warps per CTA, each with its own ring
 constexpr int kPagedMaxCtas = 256;      // grid bound (workspace sizing)
 constexpr int kPagedMaxHeads = 4096;    // query heads
 

@@ -47,13 +47,17 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int TT = kPagedTile;
 constexpr float kLn2 = 0.69314718055994531f;
 
-__host__ __device__ constexpr int paged_stages(int D) { return D <= 64 ? 6 : (D <= 128 ? 3 : 2); }
-__host__ __device__ constexpr int paged_warps(int D) { return D <= 128 ? kPagedWarps : kPagedWarps * 3 / 4; }
+// Warps and ring depth: as many warps as the registers of the running values
+// allow, and the ring that then fits.  Measured (bf16 out, no weights, GB/s): 64
+// dims 12 x 4 5,490 (8 x 6 4,510, 16 x 2 5,570 but spilling), 128 dims 8 x 3
+// 6,780 (12 x 2 6,560, 6 x 4 6,570), 256 dims 4 x 3 5,100 (6 x 2 4,900).
+__host__ __device__ constexpr int paged_warps(int D) { return D <= 64 ? 12 : (D <= 128 ? 8 : 4); }
+__host__ __device__ constexpr int paged_stages(int D) { return D <= 64 ? 4 : 3; }
 __host__ __device__ constexpr int stage_bytes(int D) { return 2 * TT * D * 2; }
 // Scores leave a warp several tiles at a time, one bulk copy per head.
-__host__ __device__ constexpr int score_tiles(bool wide) { return wide ? 4 : 8; }
-__host__ __device__ constexpr int score_pitch(bool wide) { return score_tiles(wide) * TT + 4; }  // floats, bank-shifted
-__host__ __device__ constexpr int score_stage(bool wide) { return (wide ? 16 : 8) * score_pitch(wide); }
+__host__ __device__ constexpr int score_tiles(int D, bool wide) { return (wide ? 2 : 4) * (D <= 64 ? 1 : 2); }
+__host__ __device__ constexpr int score_pitch(int D, bool wide) { return score_tiles(D, wide) * TT + 4; }  // floats, bank-shifted
+__host__ __device__ constexpr int score_stage(int D, bool wide) { return (wide ? 16 : 8) * score_pitch(D, wide); }
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool live, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0),
@@ -255,7 +259,7 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
   const int mi = lane >> 3, ri = lane & 7;
   const int k_row = ri + ((mi & 2) ? 8 : 0), v_row = ri + ((mi & 1) ? 8 : 0);
   bool opened = false;
-  float* stage = reinterpret_cast<float*>(smem + paged_warps(D) * NS * stage_bytes(D)) + warp * score_stage(WIDE);
+  float* stage = reinterpret_cast<float*>(smem + paged_warps(D) * NS * stage_bytes(D)) + warp * score_stage(D, WIDE);
   int n_staged = 0;   // tiles whose scores wait in the stage
 
   int64_t t = t_begin;
@@ -335,7 +339,7 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
         for (int i = 0; i < 4; ++i) p[hf][i] = ex2(sc[hf][i] - m_new);
         l_run[hf] = l_run[hf] * alpha[hf] + ((p[hf][0] + p[hf][1]) + (p[hf][2] + p[hf][3]));
         if (P.scores != nullptr && g + 8 * hf < n_heads) {
-          float* sp = stage + (g + 8 * hf) * score_pitch(WIDE) + n_staged * TT + 2 * tq;
+          float* sp = stage + (g + 8 * hf) * score_pitch(D, WIDE) + n_staged * TT + 2 * tq;
           *reinterpret_cast<float2*>(sp) = make_float2(sc[hf][0], sc[hf][1]);
           *reinterpret_cast<float2*>(sp + 8) = make_float2(sc[hf][2], sc[hf][3]);
         }
@@ -398,12 +402,12 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
       }
       __syncwarp();   // every lane has read the stage before it is refilled
       ++t;
-      if (P.scores != nullptr && (++n_staged == score_tiles(WIDE) || t == t_end)) {
+      if (P.scores != nullptr && (++n_staged == score_tiles(D, WIDE) || t == t_end)) {
         // the staged tiles, one bulk copy a head
         fence_proxy_async_smem();
         __syncwarp();
         if (lane < n_heads)
-          bulk_store(P.scores + (hq0 + lane) * P.score_stride + (t - n_staged) * TT, stage + lane * score_pitch(WIDE),
+          bulk_store(P.scores + (hq0 + lane) * P.score_stride + (t - n_staged) * TT, stage + lane * score_pitch(D, WIDE),
                      n_staged * TT * sizeof(float));
         bulk_commit();
         n_staged = 0;
@@ -709,7 +713,7 @@ cudaError_t launch_after(void (*kern)(PagedParams), unsigned grid, const PagedPa
 template <int D, bool WIDE, bool F32>
 cudaError_t launch_attend_d(const PagedParams& p, int grid, cudaStream_t s) {
   auto kern = k_paged_attend<D, WIDE, F32>;
-  constexpr int smem = paged_warps(D) * (paged_stages(D) * stage_bytes(D) + score_stage(WIDE) * static_cast<int>(sizeof(float)));
+  constexpr int smem = paged_warps(D) * (paged_stages(D) * stage_bytes(D) + score_stage(D, WIDE) * static_cast<int>(sizeof(float)));
   static_assert(smem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
