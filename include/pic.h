@@ -667,10 +667,10 @@ size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32
 /*
  * One new token per request attends to its cached sequence, slots
  * [0, d_seq_lens[r]) of one layer (GQA models; any number of query heads per KV
- * head):
+ * head, at most 4,096 in all):
  *   s_t = softmax_scale * q . k_t,  p = softmax(s),  out = sum_t p_t v_t,
  *   lse = log sum_t exp(s_t),  and weights[slot t] += sum over query heads p_t.
- * A request of length 0 gets out 0 and lse -inf.  A length below 0 or above
+ * A request with nothing to attend (length 0) gets out 0 and lse -inf.  A length below 0 or above
  * max_seq_len raises PIC_DEV_BAD_LENGTH and counts as 0; slots in a block outside
  * the cache raise PIC_DEV_BAD_BLOCK and are left out.  What the cache holds
  * behind a sequence's end does not matter.

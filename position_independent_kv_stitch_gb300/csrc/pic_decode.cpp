@@ -73,8 +73,9 @@ PagedView paged_view(const CtxView& c, const int32_t* d_tables, int32_t n_tables
 
 void fill_freq(const CtxView& c, FreqTable* t) { std::memcpy(t->turns, c.freq, c.model->rope_dim / 2 * sizeof(float2)); }
 
-// Longest sequence a block table can hold.
+// Longest sequence a block table can hold (none, where the cache has no block).
 int32_t table_capacity(const CtxView& c, int32_t max_blocks) {
+  if (c.num_cache_blocks == 0) return 0;
   const int64_t n = static_cast<int64_t>(max_blocks) * c.model->block_size;
   return static_cast<int32_t>(std::min<int64_t>(n, std::numeric_limits<int32_t>::max() - 2 * kPagedTile));
 }
@@ -192,6 +193,8 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache
   if (t->n_tokens > 1 && ((with_q && (t->q_stride < q_bytes || t->q_out_stride < q_bytes)) ||
                           (with_k && (t->k_stride < row_bytes || (!mla && t->v_stride < row_bytes)))))
     return fail(ctx, PIC_ERR_RANGE, "token strides smaller than a token");
+  if (with_q && t->q == t->q_out && t->n_tokens > 1 && t->q_stride != t->q_out_stride)
+    return fail(ctx, PIC_ERR_INVALID_ARG, "queries turned in place need one stride");
   if (!aligned(t->q, 16) || !aligned(t->q_out, 16) || !aligned(t->k, 16) || !aligned(t->v, 16) || !aligned(k_cache, 16) ||
       !aligned(v_cache, 16) || (t->q_stride & 15) || (t->q_out_stride & 15) || (t->k_stride & 15) || (t->v_stride & 15))
     return fail(ctx, PIC_ERR_ALIGNMENT, "tokens, caches and strides must be 16-byte aligned");

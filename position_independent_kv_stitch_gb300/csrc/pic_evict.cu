@@ -434,7 +434,9 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __
 cudaError_t launch_evict(const EvictParams& p, int pairing, cudaStream_t s) {
   const int64_t lr = static_cast<int64_t>(p.layers) * p.n_req;
   const int smem = p.sel_cap * static_cast<int>(sizeof(float));
-  cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the same limit whatever this call needs: another thread may be between the two calls
+  cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kEvictCachedSlots * static_cast<int>(sizeof(float)));
   if (e != cudaSuccess) return e;
   k_evict_select<<<static_cast<unsigned>(lr * p.weight_heads), kSelThreads, smem, s>>>(p);
   e = cudaGetLastError();

@@ -538,8 +538,7 @@ template <int D, bool ALL>
 __device__ __forceinline__ void join_output(const PagedParams& P, const TileList& L, int64_t first, int r, int hq, float* part) {
   constexpr int V = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = tiles_of(P, r, false);
-  const Records x = records_of(L, first, n, r);
+  const Records x = records_of(L, first, tiles_of(P, r, false), r);
   float M, sum, acc[V];
   join_stats(P, x, hq, lane, M, sum);
   join_values<D>(P, x, hq, lane, M, ALL ? warp : 0, ALL ? kFinishWarps : 1, acc);
@@ -552,13 +551,13 @@ __device__ __forceinline__ void join_output(const PagedParams& P, const TileList
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kFinishWarps; ++w) v += part[w * D + d];
-      store_out(P, task * D + d, n > 0 ? v / sum : 0.0f);
+      store_out(P, task * D + d, sum == 0.0f ? 0.0f : v / sum);   // nothing attended: 0
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) store_out(P, task * D + lane * V + i, n > 0 ? acc[i] / sum : 0.0f);
+    for (int i = 0; i < V; ++i) store_out(P, task * D + lane * V + i, sum == 0.0f ? 0.0f : acc[i] / sum);
   }
-  if (P.lse != nullptr && lane == 0 && (warp == 0 || !ALL)) P.lse[task] = n > 0 ? (M + log2f(sum)) * kLn2 : -INFINITY;
+  if (P.lse != nullptr && lane == 0 && (warp == 0 || !ALL)) P.lse[task] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
 // Adds each slot's attention weight: a warp takes a run of tiles for one
@@ -666,7 +665,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_paged_lse(const __grid_const
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float M, sum;
   join_stats(P, x, hq, lane, M, sum);
-  if (lane == 0) P.lse2[task] = M + log2f(sum);
+  if (lane == 0) P.lse2[task] = sum == 0.0f ? INFINITY : M + log2f(sum);   // nothing attended: every share 0
 }
 
 // The first CTAs add the weights (the longer part); the others join the

@@ -66,6 +66,7 @@ def _write(ctx, mla=False, **over):
     (dict(n_tables=-1), INVALID), (dict(max_blocks=-1), INVALID), (dict(heads=3), INVALID), (dict(heads=0), INVALID),
     (dict(q_stride=1008), RANGE), (dict(q_out_stride=0), RANGE), (dict(k_stride=496), RANGE), (dict(v_stride=256), RANGE),
     (dict(num_q_heads=1 << 24, q_stride=1 << 40, q_out_stride=1 << 40), RANGE),
+    (dict(n_tokens=2 ** 31 - 1, num_q_heads=0, k_stride=496), RANGE), (dict(q_stride=2048), INVALID), (dict(q_out_stride=2048), INVALID),
     (dict(q=P + 8), ALIGNMENT), (dict(k_stride=520), ALIGNMENT), (dict(v_cache=P + 2), ALIGNMENT), (dict(d_slot=P + 1), ALIGNMENT),
     (dict(ws=P + 16), ALIGNMENT), (dict(weights=P + 2), ALIGNMENT),
 ])
@@ -101,6 +102,12 @@ def _attend(ctx, **over):
 def test_attend_refusals(gqa, over, status):
     assert _attend(gqa, **over) == status
     assert pic.pic_last_error(gqa)
+
+
+def test_a_cache_without_blocks_holds_no_sequence():
+    c = _ctx(nb=0)
+    assert _attend(c, max_len=1) == RANGE and _attend(c, max_len=0, n_req=0) == 0
+    pic.pic_destroy(c)
 
 
 def test_attend_sizes(gqa, mla):

@@ -362,6 +362,40 @@ def test_attend_paged_bad_lengths_and_blocks():
     c.close()
 
 
+def test_attend_paged_nothing_attended():
+    """A request all of whose blocks are bad, and one whose scores are all -inf: out 0, lse -inf, no weight added."""
+    c = Cache(heads=2, d=128, bs=16, lens=[40, 33, 20], seed=17)
+    q = c.normal(3, 8, 128)
+    q[1] = 1.0
+    c.k[0, torch.from_numpy(c.tables[1]).long().to(DEV)] = float("-inf")
+    tables = c.d_tables.clone()
+    tables[0] = -1
+    before = c.w.clone()
+    out, lse, ws = torch.full((3, 8, 128), 7.0, device=DEV), torch.full((3, 8), 7.0, device=DEV), \
+        _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, 3, 8, 48, True))
+    pic.pic_attend_paged(c.ctx, q, 0.1, c.k[0], c.v[0], tables, c.d_lens, 48, out, lse=lse, weights=c.w[0], workspace=ws)
+    assert _status(c, ws) == pic.PIC_DEV_BAD_BLOCK
+    assert bool((out[:2] == 0).all()) and bool(torch.isneginf(lse[:2]).all()) and bool(torch.isfinite(out[2]).all())
+    for r in (0, 1):
+        mine = torch.from_numpy(c.tables[r]).long().to(DEV)
+        assert torch.equal(c.w[0, mine], before[0, mine])
+    c.close()
+
+
+def test_attend_paged_infinite_and_nan_scores():
+    """A +inf score or a NaN in a key makes its request's heads NaN, as the definition does, and touches no other."""
+    c = Cache(heads=2, d=128, bs=16, lens=[40, 33, 20], seed=18)
+    q = torch.ones(3, 8, 128, device=DEV, dtype=torch.bfloat16)
+    clean, _ = _attend(c, 8, torch.float32, weights=False, q=q)
+    for r, bad in ((0, float("inf")), (1, float("nan"))):
+        c.k[0, int(c.tables[r][1]), 3, 0] = bad
+    out, ws = torch.empty(3, 8, 128, device=DEV), _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, 3, 8, 40))
+    pic.pic_attend_paged(c.ctx, q, 128 ** -0.5, c.k[0], c.v[0], c.d_tables, c.d_lens, 40, out, workspace=ws)
+    assert bool(torch.isnan(out[:2, :4]).all())
+    assert torch.equal(out[:2, 4:], clean[:2, 4:]) and torch.equal(out[2], clean[2])
+    c.close()
+
+
 def test_attend_paged_shared_prefix_blocks():
     """Requests that share their first blocks (no weights kept)."""
     c = Cache(heads=2, d=128, bs=16, lens=[64, 80, 70], seed=8)
@@ -575,6 +609,69 @@ def test_decode_loop(renumber, graph):
     c.w.zero_()
     _decode_steps(c, 14, 36, 5, 6, renumber, graph)
     c.close()
+
+
+def test_evict_captured_and_replayed():
+    """An eviction in a graph, replayed: the second replay finds sequences within the budget and leaves them."""
+    c = Cache(heads=2, d=64, bs=16, layers=2, lens=[200, 90, 61], seed=41)
+    k, v, w, lens = c.k.clone(), c.v.clone(), c.w.clone(), c.d_lens.clone()
+    kept = torch.empty(2, 3, 2, 70, dtype=torch.int32, device=DEV)
+    ws = _ws(pic.pic_evict_workspace_bytes(c.ctx, 2, 3, 2))
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            pic.pic_evict_tokens(c.ctx, k, v, w, c.d_tables, lens, 70, kept, lens, n_first=2, n_recent=9, renumber=True, workspace=ws)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert lens.tolist() == [70, 70, 61]
+    once = k.clone()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(k, once) and kept[0, 0, 0].tolist() == list(range(70))
+    d = c.d_lens.clone()
+    pic.pic_evict_tokens(c.ctx, c.k, c.v, c.w, c.d_tables, d, 70, kept, d, n_first=2, n_recent=9, renumber=True, workspace=ws)
+    assert _status(c, ws) == 0
+    assert torch.equal(c.k, once) and torch.equal(c.v, v) and torch.equal(c.w, w)
+    c.close()
+
+
+def test_offsets_beyond_32_bits():
+    """A layer of 6.6 GB: rows, weights and pages at its far end."""
+    bs, heads, d, nb = 16, 8, 128, 200_000
+    m = W.Model("far", "gqa", 1, heads, d, d, 0, "neox", 5e5, bs)
+    ctx = pic.create_from_spec(pic.model_spec_from(m), nb)
+    k, v = (torch.empty(1, nb, bs, heads, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    w = torch.empty(1, nb, heads, bs, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    pages = [nb - 1, 7, nb - 3, nb - 2, 150_001]
+    for p in pages:
+        k[0, p].normal_(generator=g)
+        v[0, p].normal_(generator=g)
+        w[0, p].uniform_(generator=g)
+    tables = _i32([pages])
+    new = [torch.randn((2, h, d), generator=g, device=DEV).to(torch.bfloat16) for h in (16, heads, heads)]
+    small = Cache(heads=heads, d=d, bs=bs, lens=[70], room=10, seed=1)   # the same pages in a small cache
+    small.tables = np.arange(5, dtype=np.int32)[None]
+    small.d_tables = torch.from_numpy(small.tables).to(DEV)
+    small.k[0, :5], small.v[0, :5], small.w[0, :5] = k[0, pages], v[0, pages], w[0, pages]
+    for c, kk, vv, ww, tt in ((ctx, k, v, w, tables), (small.ctx, small.k, small.v, small.w, small.d_tables)):
+        q_out, lens = torch.empty_like(new[0]), _i32([72])
+        ws = _ws(1 << 24)
+        pic.pic_write_tokens(c, _i32([70, 71]), new[1], new[2], _i32([0, 0]), _i32([70, 71]), tt, kk[0], vv[0], q=new[0], q_out=q_out,
+                             weights=ww[0], workspace=ws)
+        out = torch.empty(1, 16, d, device=DEV)
+        pic.pic_attend_paged(c, q_out[1:], 0.1, kk[0], vv[0], tt, lens, 72, out, weights=ww[0], workspace=ws)
+        kept = torch.empty(1, 1, heads, 33, dtype=torch.int32, device=DEV)
+        pic.pic_evict_tokens(c, kk, vv, ww, tt, lens, 33, kept, lens, n_first=1, n_recent=4, renumber=True, workspace=ws)
+        assert pic.pic_query_device_status(c, ws) == 0
+        if c is ctx:
+            want = (out, kept)
+    assert torch.equal(out, want[0]) and torch.equal(kept, want[1])
+    assert torch.equal(small.k[0, :5], k[0, pages]) and torch.equal(small.v[0, :5], v[0, pages])
+    assert torch.equal(small.w[0, :5], w[0, pages])
+    pic.pic_destroy(ctx)
+    small.close()
 
 
 def test_decode_loop_after_a_stitch():
