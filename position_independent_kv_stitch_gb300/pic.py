@@ -679,20 +679,16 @@ def pic_attend_decode(ctx, plans, source, q, softmax_scale, k_pool, v_pool, k_ca
 # These calls are made once per layer and token, so the checks are lean: shapes
 # fetched once and compared whole, addresses passed as integers, no views.
 
-def _launch(ctx, fn, tensors, stream, args):
-    """fn(ctx, *args, stream) with the tensors' device current; a tensor on
-    another device, or on the host, is refused."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            dev = -1
-    if dev < 0:
+def _launch(ctx, fn, device, stream, args):
+    """fn(ctx, *args, stream) with `device` (an index) current.  The library
+    itself refuses buffers of another device or of the host."""
+    if device < 0:
         raise ValueError("every tensor must be on one CUDA device")
-    if dev != _torch._C._cuda_getDevice():
-        with _torch.cuda.device(dev):
+    if device != _torch._C._cuda_getDevice():
+        with _torch.cuda.device(device):
             _check(fn(ctx, *args, _stream_handle(stream)), ctx)
         return
-    st = fn(ctx, *args, _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream))
+    st = fn(ctx, *args, _torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream_handle(stream))
     if st != PIC_OK:
         _check(st, ctx)
 
@@ -705,37 +701,42 @@ def _size(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _int32_error(name, numel=None):
+    raise ValueError(f"{name} must be a contiguous CUDA int32 tensor" + ("" if numel is None else f" of {numel} entries"))
+
+
 def _dense_int32(t, name, numel=None):
     if t.dtype is not _I32 or not t.is_contiguous() or (numel is not None and t.numel() != numel):
-        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor" +
-                         ("" if numel is None else f" of {numel} entries"))
+        _int32_error(name, numel)
 
 
-def _token_rows(t, name, want=None):
-    """Bytes between the tokens of a bf16 [tokens][heads][dim] with dense heads (of shape `want`)."""
-    shape = t.shape
-    ok = t.dtype is _BF16 and len(shape) == 3 and (want is None or shape == want)
-    if ok and t.is_contiguous():
-        return shape[1] * shape[2] * 2
-    if ok:
+def _token_rows(t, name, want):
+    """Bytes between the tokens of a bf16 [tokens][heads][dim] of shape `want` with dense heads."""
+    if t.dtype is _BF16 and t.shape == want:
+        if t.is_contiguous():
+            return want[1] * want[2] * 2
         strides = t.stride()
-        if strides[2] == 1 and (shape[1] <= 1 or strides[1] == shape[2]):
+        if strides[2] == 1 and (want[1] <= 1 or strides[1] == want[2]):
             return strides[0] * 2
-    raise ValueError(f"{name} must be bf16 [tokens][heads][head_dim], a row per token, dense heads")
+    raise ValueError(f"{name} must be bf16 {list(want)} ([tokens][heads][head_dim]) with dense heads")
 
 
-def _check_cache(ctx, t, name, dim):
-    """The shape of a cache tensor ([layers][blocks][block_size][kv_heads]
-    [head_dim] for dim 5, one layer of it for dim 4) that holds the context's
-    blocks and rows."""
-    shape = t.shape
-    if t.dtype is not _BF16 or len(shape) != dim or not (t.is_contiguous() or (dim == 5 and t[0].is_contiguous())):
-        raise ValueError(f"{name} must be a bf16 cache tensor of {dim} dims with contiguous rows")
-    blocks, bs, heads, d = shape if dim == 4 else shape[1:]
+def _check_caches(ctx, k, v, dim):
+    """The shape of the cache tensors ([layers][blocks][block_size][kv_heads]
+    [head_dim] for dim 5, one layer of it for dim 4; v may be None), which
+    hold the context's blocks and rows; and what is known of the context."""
+    shape = k.shape
+    if k.dtype is not _BF16 or len(shape) != dim or not (k.is_contiguous() or (dim == 5 and k[0].is_contiguous())):
+        raise ValueError(f"k_cache must be a bf16 cache tensor of {dim} dims with contiguous rows")
+    if v is not None and (v.dtype is not _BF16 or v.shape != shape or
+                          not (v.is_contiguous() or (dim == 5 and v[0].is_contiguous()))):
+        raise ValueError("v_cache must be a bf16 tensor of k_cache's shape with contiguous rows")
     want = _geometry.get(ctx.value)
-    if want is not None and (blocks < want[0] or (bs, heads, d) != want[1]):
-        raise ValueError(f"{name} must hold the context's {want[0]} blocks of {want[1][0]} rows {list(want[1][1:])}")
-    return shape
+    if want is not None:
+        blocks, bs, heads, d = shape if dim == 4 else shape[1:]
+        if blocks < want[0] or (bs, heads, d) != want[1]:
+            raise ValueError(f"the caches must hold the context's {want[0]} blocks of {want[1][0]} rows {list(want[1][1:])}")
+    return shape, want
 
 
 def _weight_heads(weights, cache_shape):
@@ -750,10 +751,9 @@ def _weight_heads(weights, cache_shape):
 
 
 def _table_shape(block_tables, rows=0):
-    _dense_int32(block_tables, "block_tables")
     shape = block_tables.shape
-    if len(shape) != 2 or shape[0] < rows:
-        raise ValueError("block_tables must be [n_req][max_blocks] with a row per request")
+    if block_tables.dtype is not _I32 or len(shape) != 2 or shape[0] < rows or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous CUDA int32 tensor [n_req][max_blocks] with a row per request")
     return shape
 
 
@@ -770,29 +770,31 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
     [blocks][weight_heads][block_size], zeroed at the written slots.
     workspace: uint8, PIC_STATUS_BYTES, zeroed when made (its status is sticky)."""
     lib = _lib or load()
-    _dense_int32(positions, "positions")
     shape = positions.shape
     axes, n = shape if len(shape) == 2 else (1, shape[0])
-    want = _geometry.get(ctx.value)
+    if positions.dtype is not _I32 or not positions.is_contiguous():
+        _int32_error("positions")
     q_heads = q_stride = out_stride = k_stride = v_stride = n_tables = max_blocks = heads = 0
-    if q is not None:
-        shape = q.shape
-        q_stride, out_stride = _token_rows(q, "q"), _token_rows(q_out, "q_out", shape)
-        tokens, q_heads, d = shape
-        if tokens != n or (want is not None and d != want[1][2]):
-            raise ValueError("q holds a row per token, heads of the context's head_dim")
     if k is not None:
-        shape = _check_cache(ctx, k_cache, "k_cache", 4)
-        rows = (n, shape[2], shape[3])
+        cache, want = _check_caches(ctx, k_cache, v_cache, 4)
+        rows = (n, cache[2], cache[3])
         k_stride = _token_rows(k, "k", rows)
         if v is not None:
             v_stride = _token_rows(v, "v", rows)
-        if v_cache is not None:
-            _check_cache(ctx, v_cache, "v_cache", 4)
-        _dense_int32(req, "req", n)
-        _dense_int32(slot, "slot", n)
+        if req.dtype is not _I32 or slot.dtype is not _I32 or req.numel() != n or slot.numel() != n or \
+                not req.is_contiguous() or not slot.is_contiguous():
+            _int32_error("req and slot", n)
         n_tables, max_blocks = _table_shape(block_tables)
-        heads = _weight_heads(weights, shape)
+        if weights is not None:
+            heads = _weight_heads(weights, cache)
+    else:
+        want = _geometry.get(ctx.value)
+    if q is not None:
+        shape = q.shape
+        q_stride, out_stride = _token_rows(q, "q", shape), _token_rows(q_out, "q_out", shape)
+        tokens, q_heads, d = shape
+        if tokens != n or (want is not None and d != want[1][2]):
+            raise ValueError("q holds a row per token, heads of the context's head_dim")
     if freq_axis is not None:
         if want is not None and len(freq_axis) != want[2]:
             raise ValueError(f"freq_axis holds an axis for each of the {want[2]} frequencies")
@@ -801,10 +803,12 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
             _axis_arrays[axis_bytes] = ctypes.create_string_buffer(axis_bytes, len(axis_bytes))
         freq_axis = ctypes.addressof(_axis_arrays[axis_bytes])
     # a pic_new_tokens, packed (filling in a ctypes structure takes longer than the call)
-    t = _NEW_TOKENS.pack(n, q_heads, axes, freq_axis or 0, positions.data_ptr(), _addr(q) or 0, q_stride, _addr(q_out) or 0,
-                         out_stride, _addr(k) or 0, k_stride, _addr(v) or 0, v_stride, _addr(req) or 0, _addr(slot) or 0)
-    _launch(ctx, lib.pic_write_tokens,
-            (positions, q, q_out, k, v, req, slot, block_tables, k_cache, v_cache, weights, workspace), stream,
+    t = _NEW_TOKENS.pack(
+        n, q_heads, axes, freq_axis or 0, positions.data_ptr(),
+        0 if q is None else q.data_ptr(), q_stride, 0 if q is None else q_out.data_ptr(), out_stride,
+        0 if k is None else k.data_ptr(), k_stride, 0 if v is None else v.data_ptr(), v_stride,
+        0 if k is None else req.data_ptr(), 0 if k is None else slot.data_ptr())
+    _launch(ctx, lib.pic_write_tokens, positions.get_device(), stream,
             (t, _addr(k_cache), _addr(v_cache), _addr(block_tables), n_tables, max_blocks, _addr(weights), heads,
              _addr(workspace), _size(workspace)))
 
@@ -825,19 +829,19 @@ def pic_attend_paged(ctx, q, softmax_scale, k_cache, v_cache, block_tables, seq_
     added to it.  workspace: uint8, pic_attend_paged_workspace_bytes, its first
     PIC_STATUS_BYTES zeroed when made."""
     lib = _lib or load()
-    stride = _token_rows(q, "q")
     shape = q.shape
+    stride = _token_rows(q, "q", shape)
     n_req, hq, d = shape
-    _dense_int32(seq_lens, "seq_lens", n_req)
-    _, max_blocks = _table_shape(block_tables, n_req)
-    cache = _check_cache(ctx, k_cache, "k_cache", 4)
-    _check_cache(ctx, v_cache, "v_cache", 4)
+    if seq_lens.dtype is not _I32 or seq_lens.numel() != n_req or not seq_lens.is_contiguous():
+        _int32_error("seq_lens", n_req)
+    max_blocks = _table_shape(block_tables, n_req)[1]
+    cache, _ = _check_caches(ctx, k_cache, v_cache, 4)
     out_type = PIC_F32 if out.dtype is _F32 else PIC_BF16
     if d != cache[3] or out.shape != shape or not out.is_contiguous() or (out_type == PIC_BF16 and out.dtype is not _BF16):
         raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape, heads of the cache's head_dim")
     if lse is not None and (lse.dtype is not _F32 or lse.numel() != n_req * hq or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [n_req][q_heads]")
-    _launch(ctx, lib.pic_attend_paged, (q, k_cache, v_cache, block_tables, seq_lens, out, lse, weights, workspace), stream,
+    _launch(ctx, lib.pic_attend_paged, q.get_device(), stream,
             (q.data_ptr(), stride, n_req, hq, softmax_scale, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
              max_blocks, seq_lens.data_ptr(), max_seq_len, out.data_ptr(), out_type, _addr(lse), _addr(weights),
              _weight_heads(weights, cache), _addr(workspace), _size(workspace)))
@@ -859,21 +863,19 @@ def pic_evict_tokens(ctx, k_cache, v_cache, weights, block_tables, seq_lens, bud
     PIC_STATUS_BYTES zeroed when made."""
     lib = _lib or load()
     n_req = seq_lens.numel()
-    _, max_blocks = _table_shape(block_tables, n_req)
-    cache = _check_cache(ctx, k_cache, "k_cache", 5)
+    max_blocks = _table_shape(block_tables, n_req)[1]
+    cache, _ = _check_caches(ctx, k_cache, v_cache, 5)
     layers = cache[0]
     stride = k_cache.stride()[0]
-    if v_cache is not None:
-        _check_cache(ctx, v_cache, "v_cache", 5)
-        if v_cache.shape != cache or (layers > 1 and v_cache.stride()[0] != stride):
-            raise ValueError("k_cache and v_cache must share a shape and a layer stride")
+    if v_cache is not None and layers > 1 and v_cache.stride()[0] != stride:
+        raise ValueError("k_cache and v_cache must share a layer stride")
     if weights is None:
         raise ValueError("weights are required")
     heads = _weight_heads(weights, cache)
     _dense_int32(seq_lens, "seq_lens")
     _dense_int32(new_lens, "new_lens", n_req)
     _dense_int32(kept, "kept", layers * n_req * heads * budget)
-    _launch(ctx, lib.pic_evict_tokens, (k_cache, v_cache, weights, block_tables, seq_lens, kept, new_lens, workspace), stream,
+    _launch(ctx, lib.pic_evict_tokens, k_cache.get_device(), stream,
             (layers, k_cache.data_ptr(), _addr(v_cache), stride * 2, weights.data_ptr(), weights.stride()[0] * 4, heads,
              block_tables.data_ptr(), n_req, max_blocks, seq_lens.data_ptr(), budget, n_first, n_recent, 1 if renumber else 0,
              kept.data_ptr(), new_lens.data_ptr(), _addr(workspace), _size(workspace)))

@@ -167,9 +167,11 @@ def test_binding_refuses_host_tensors_and_foreign_shapes(gqa):
         pic.pic_evict_tokens(gqa, cache[None], cache[None], torch.zeros(1, 64, 2, 16), i.view(2, 1), i, 4, i, i)
     for bad in (cache[:63], cache.float(), cache[:, :8], cache.transpose(0, 1), cache[0]):
         with pytest.raises(ValueError):
-            pic._check_cache(gqa, bad, "k_cache", 4)
-    pic._check_cache(gqa, cache, "k_cache", 4)
+            pic._check_caches(gqa, bad, None, 4)
+        with pytest.raises(ValueError):
+            pic._check_caches(gqa, cache, bad, 4)
+    pic._check_caches(gqa, cache, cache, 4)
     with pytest.raises(ValueError):
         pic._weight_heads(torch.zeros(64, 2, 8), cache.shape)
     with pytest.raises(ValueError):
-        pic._token_rows(cache.transpose(1, 2)[0], "q")
+        pic._token_rows(cache.transpose(1, 2)[0], "q", (2, 16, 128))
