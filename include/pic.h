@@ -666,19 +666,22 @@ size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32
 
 /*
  * One new token per request attends to its cached sequence, slots
- * [0, d_seq_lens[r]) of one layer (GQA models; any number of query heads per KV
- * head, at most 4,096 in all):
+ * [0, d_seq_lens[r]) of one layer (any number of query heads per KV head, at
+ * most 4,096 in all):
  *   s_t = softmax_scale * q . k_t,  p = softmax(s),  out = sum_t p_t v_t,
  *   lse = log sum_t exp(s_t),  and weights[slot t] += sum over query heads p_t.
  * A request with nothing to attend (length 0) gets out 0 and lse -inf.  A length below 0 or above
  * max_seq_len raises PIC_DEV_BAD_LENGTH and counts as 0; slots in a block outside
  * the cache raise PIC_DEV_BAD_BLOCK and are left out.  What the cache holds
  * behind a sequence's end does not matter.
+ * MLA models: k_t is the whole row (q absorbed into the latent space, as for
+ * pic_attend_decode), v_t its latent; v_cache is ignored and may be NULL.
  *   q           bf16 [n_req][num_q_heads][head_dim], q_stride bytes between
  *               requests, rotated (pic_write_tokens' q_out).
  *   max_seq_len longest sequence (host bound, at most max_blocks * block_size);
  *               sizes the workspace when weights are kept.
- *   out         [n_req][num_q_heads][head_dim] of out_type PIC_F32 or PIC_BF16.
+ *   out         [n_req][num_q_heads][head_dim] (MLA: the 512 latent dims) of
+ *               out_type PIC_F32 or PIC_BF16.
  *   lse         float [n_req][num_q_heads] or NULL.
  *   d_weights   one layer of the weights, or NULL.
  * Requests may share blocks, but with d_weights a block may appear once in

@@ -48,9 +48,10 @@ def write_tokens(q, k, v, positions, freq_axis, theta, pairing, rope_offset, rop
 
 
 def attend_paged(q, k_cache, v_cache, tables, lens, block_size, scale, weights=None):
-    """q [n_req][Hq][D].  Returns (out, lse, weights); an empty sequence gives out 0, lse -inf."""
-    n_req, hq, d = q.shape
-    out = np.zeros((n_req, hq, d))
+    """q [n_req][Hq][D].  Returns (out, lse, weights); an empty sequence gives
+    out 0, lse -inf.  MLA: v_cache is the latent slice of k_cache."""
+    n_req, hq, _ = q.shape
+    out = np.zeros((n_req, hq, v_cache.shape[-1]))
     lse = np.full((n_req, hq), -np.inf)
     weights = None if weights is None else weights.astype(np.float64).copy()
     for r in range(n_req):

@@ -92,14 +92,19 @@ struct PagedLayout {
   size_t lse2, rec_ml, rec_acc, scores, total;
   int64_t score_stride;
 };
-int32_t paged_passes(int32_t group) { return (group + 15) / 16; }
+int32_t paged_passes(const CtxView& c, int32_t group) {
+  const int32_t heads = c.model->kind == PIC_KIND_MLA ? 32 : 16;
+  return (group + heads - 1) / heads;
+}
+// Width of an output row: the head's, or the latent's.
+int32_t paged_out_dim(const CtxView& c) { return c.model->kind == PIC_KIND_MLA ? c.model->rope_offset : c.model->head_dim; }
 int64_t paged_max_parts(int32_t v_heads, int head_dim) {
-  return std::max<int64_t>(1, static_cast<int64_t>(kPagedMaxCtas) * paged_warps_per_cta(head_dim) / v_heads);
+  return std::max<int64_t>(1, static_cast<int64_t>(kPagedMaxCtas) * paged_ranges_per_cta(head_dim) / v_heads);
 }
 PagedLayout paged_layout(const CtxView& c, int64_t n_req, int64_t q_heads, int64_t max_len, bool weights) {
-  const int d = c.model->head_dim;
+  const int d = paged_out_dim(c);
   const int32_t group = static_cast<int32_t>(q_heads / c.model->num_kv_heads);
-  const int64_t recs = paged_max_parts(c.model->num_kv_heads * paged_passes(group), d) + n_req;
+  const int64_t recs = paged_max_parts(c.model->num_kv_heads * paged_passes(c, group), c.model->head_dim) + n_req;
   PagedLayout L{};
   L.score_stride = weights ? n_req * ((max_len + kPagedTile - 1) / kPagedTile) * kPagedTile : 0;
   L.lse2 = sizeof(WsHeader);
@@ -110,7 +115,7 @@ PagedLayout paged_layout(const CtxView& c, int64_t n_req, int64_t q_heads, int64
   return L;
 }
 bool paged_heads_ok(const CtxView& c, int32_t num_q_heads) {
-  return c.model->kind == PIC_KIND_GQA && num_q_heads > 0 && num_q_heads % c.model->num_kv_heads == 0;
+  return num_q_heads > 0 && num_q_heads % c.model->num_kv_heads == 0;
 }
 
 // How finely the move slices the kept rows of each (layer, request, tensor,
@@ -276,15 +281,15 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
   if (!ctx) return fail(nullptr, PIC_ERR_INVALID_ARG, "null ctx");
   const CtxView c = ctx_view(ctx);
   const pic_model_desc& m = *c.model;
-  if (m.kind != PIC_KIND_GQA)
-    return fail(ctx, PIC_ERR_UNSUPPORTED, "paged attention covers GQA models (MLA: pic_attend_decode)");
+  const bool mla = m.kind == PIC_KIND_MLA;
   if (!paged_heads_ok(c, num_q_heads))
     return fail(ctx, PIC_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
   if (n_req < 0 || max_blocks < 0 || max_seq_len < 0) return fail(ctx, PIC_ERR_INVALID_ARG, "negative size");
   if (out_type != PIC_F32 && out_type != PIC_BF16) return fail(ctx, PIC_ERR_INVALID_ARG, "unknown out_type %d", out_type);
   if (d_weights && !weight_heads_ok(c, weight_heads))
     return fail(ctx, PIC_ERR_INVALID_ARG, "weight_heads must be 1 or num_kv_heads");
-  if (!q || !k_cache || !v_cache || !d_tables || !d_seq_lens || !out || !d_ws)
+  if (mla) v_cache = nullptr;  // the latent serves as value
+  if (!q || !k_cache || (!mla && !v_cache) || !d_tables || !d_seq_lens || !out || !d_ws)
     return fail(ctx, PIC_ERR_INVALID_ARG, "null q, cache, block table, lengths, out or workspace");
   const int64_t q_bytes = static_cast<int64_t>(num_q_heads) * m.head_dim * 2;
   const int64_t row_bytes = static_cast<int64_t>(m.num_kv_heads) * m.head_dim * 2;
@@ -320,11 +325,11 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
   p.q_heads = num_q_heads;
   p.kv_heads = m.num_kv_heads;
   p.group = num_q_heads / m.num_kv_heads;
-  p.passes = paged_passes(p.group);
+  p.passes = paged_passes(c, p.group);
   p.v_heads = p.kv_heads * p.passes;
-  const int warps = paged_warps_per_cta(m.head_dim);
-  const int grid = std::min(sms, kPagedMaxCtas);   // one CTA per SM (its rings fill shared memory)
-  p.parts = static_cast<int32_t>(std::max<int64_t>(1, static_cast<int64_t>(grid) * warps / p.v_heads));
+  const int ranges = paged_ranges_per_cta(m.head_dim);
+  const int grid = std::min(sms, kPagedMaxCtas);   // one CTA per SM (its rows fill shared memory)
+  p.parts = static_cast<int32_t>(std::max<int64_t>(1, static_cast<int64_t>(grid) * ranges / p.v_heads));
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.k_cache = static_cast<const uint8_t*>(k_cache);
   p.v_cache = static_cast<const uint8_t*>(v_cache);

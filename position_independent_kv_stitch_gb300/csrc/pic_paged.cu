@@ -452,6 +452,274 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
     attend_range<D, WIDE, F32>(P, L, w, smem);
 }
 
+// ---- MLA: latent rows
+//
+// Every query head reads the same rows (512 latent dims and a 64-dim rope key,
+// the latent also the value), so a CTA takes a range for up to 32 heads and
+// works on it together: 64 slots of one request a step, in shared memory twice
+// over, copied in with cp.async while the step before is computed.  Warp w
+// scores slots 8 w .. 8 w + 7 against every head (36 k-steps over the 576
+// dims); the row maxima meet in shared memory; P goes through shared memory in
+// bf16 parts, as above; warp w then adds latent dims 64 w .. 64 w + 63 of every
+// head.  Each of the three barriers of a step separates these.  Heads beyond 32
+// (passes) read the rows again, mostly from L2.
+// Bound: mma.sync for 32 heads (1,600 products a step against 73 KB of rows),
+// HBM for 16.
+constexpr int kLatDims = 512, kLatRow = 576;
+constexpr int kLatRowBytes = kLatRow * 2, kLatChunks = kLatRowBytes / 16;
+constexpr int kLatSlots = 64;            // slots of a step
+constexpr int kLatTiles = kLatSlots / TT;
+constexpr int kLatThreads = 256;
+__host__ __device__ constexpr int lat_smem(int MT, bool f32) {
+  return 2 * kLatSlots * kLatRowBytes + MT * 16 * kLatRowBytes + (f32 ? 3 : 2) * MT * 16 * kLatSlots * 2 + 8 * MT * 16 * 4 +
+         2 * kLatSlots;
+}
+
+template <int MT, bool F32>   // MT: 16-head tiles of a CTA
+__global__ void __launch_bounds__(kLatThreads, 1) k_paged_latent(const __grid_constant__ PagedParams P) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  constexpr int HM = MT * 16, NP = F32 ? 3 : 2, NT = kLatDims / 8 / 8;   // output n-tiles of a warp
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t kv_s = smem_u32(smem), q_s = kv_s + 2 * kLatSlots * kLatRowBytes, p_s = q_s + HM * kLatRowBytes;
+  uint8_t* p_buf = smem + 2 * kLatSlots * kLatRowBytes + HM * kLatRowBytes;
+  float* wmax = reinterpret_cast<float*>(p_buf + NP * HM * kLatSlots * 2);   // [warp][head]
+  uint8_t* s_live = reinterpret_cast<uint8_t*>(wmax + 8 * HM);               // [stage][slot]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  const TileList L = tile_list(P, lane, blockIdx.x == 0 && warp == 0);
+  uint64_t policy;   // rows that no other CTA reads pass through L2 first-out
+  if (P.passes == 1) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+
+  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(P.parts) * P.v_heads; w += gridDim.x) {
+    const int vh = static_cast<int>(w % P.v_heads);
+    const int64_t part = w / P.v_heads;
+    if (part >= L.parts || L.total == 0) continue;
+    const int64_t t_begin = L.begin(part), t_end = L.begin(part + 1);
+    if (t_begin >= t_end) continue;
+    const int hq0 = vh * HM, n_heads = min(HM, P.q_heads - hq0);
+
+    // A step: up to four tiles of one request.
+    auto step_tiles = [&](const Place& x, int64_t t) {
+      return static_cast<int>(min(min(static_cast<int64_t>(kLatTiles), t_end - t), static_cast<int64_t>((x.len + TT - 1) / TT - x.tile)));
+    };
+    auto skip = [&](Place& x, int n) {
+      for (int i = 0; i < n; ++i) advance(P, x);
+    };
+    const int my_row = tid >> 2;   // four threads copy a row
+    // this thread's cache row of a step, -1 past its end or for a bad block
+    auto row_of = [&](const Place& x, int n) -> int {
+      const int slot = x.tile * TT + my_row;
+      if (my_row >= n * TT || slot >= x.len) return -1;
+      const int64_t row = paged_row(P.paged, x.req, slot);
+      if (row < 0 && (tid & 3) == 0) raise_block(P.status, x.req, slot);
+      return static_cast<int>(row);
+    };
+    auto issue = [&](int stage, int row) {
+      const uint8_t* src = P.k_cache + static_cast<int64_t>(row < 0 ? 0 : row) * kLatRowBytes;
+      const uint32_t dst = kv_s + (stage * kLatSlots + my_row) * kLatRowBytes;
+#pragma unroll
+      for (int i = 0; i < kLatChunks / 4; ++i) {
+        const int c = (tid & 3) + 4 * i;
+        cp_async16_zfill(dst + ((c ^ (my_row & 7)) << 4), src + c * 16, row >= 0, policy);
+      }
+      if ((tid & 3) == 0) s_live[stage * kLatSlots + my_row] = row >= 0;
+    };
+
+    Place load;
+    find_tile(P, t_begin, lane, load.req, load.first);
+    load.tile = static_cast<int>(t_begin - load.first);
+    load.len = load.req < P.n_req ? legal_len(__ldg(P.lens + load.req), P.max_len, P.status, false) : 0;
+    Place cur = load;
+    int64_t t_load = t_begin;
+    __syncthreads();   // the previous range is done with shared memory
+    {
+      const int n = step_tiles(load, t_load);
+      issue(0, row_of(load, n));
+      cp_commit();
+      t_load += n;
+      skip(load, n);
+    }
+    float o[MT][NT][4], m_run[MT][2], l_run[MT][2];
+    bool opened = false;
+    int stage = 0;
+    for (int64_t t = t_begin; t < t_end; stage ^= 1) {
+      const int n = step_tiles(cur, t);
+      if (t_load < t_end) {
+        const int nl = step_tiles(load, t_load);
+        issue(stage ^ 1, row_of(load, nl));
+        t_load += nl;
+        skip(load, nl);
+      }
+      cp_commit();
+      if (!opened) {
+        opened = true;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          m_run[mt][0] = m_run[mt][1] = -FLT_MAX;
+          l_run[mt][0] = l_run[mt][1] = 0.0f;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.0f;
+        }
+        const uint8_t* qp = P.q + cur.req * P.q_stride + static_cast<int64_t>(hq0) * kLatRowBytes;
+        uint8_t* qd = smem + 2 * kLatSlots * kLatRowBytes;
+        for (int i = tid; i < HM * kLatChunks; i += kLatThreads) {
+          const int h = i / kLatChunks, c = i % kLatChunks;
+          const uint4 v = h < n_heads ? __ldg(reinterpret_cast<const uint4*>(qp + i * 16)) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(qd + h * kLatRowBytes + ((c ^ (h & 7)) << 4)) = v;
+        }
+      }
+      cp_wait<1>();
+      __syncthreads();   // the step's rows and the queries are in place
+      const uint32_t kv = kv_s + stage * kLatSlots * kLatRowBytes;
+      // ---- scores of this warp's 8 slots (even and odd k-steps apart: shorter chains)
+      float s[MT][2][4] = {};
+      const int k_row = warp * 8 + (lane & 7), a_row = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll 3
+      for (int i = 0; i < kLatChunks / 4; ++i) {
+        uint32_t b[4];
+        ldsm4(kv + k_row * kLatRowBytes + (((4 * i + (lane >> 3)) ^ (k_row & 7)) << 4), b);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t a[4];
+            ldsm4(q_s + (mt * 16 + a_row) * kLatRowBytes + (((4 * i + 2 * x + (lane >> 4)) ^ (a_row & 7)) << 4), a);
+            mma(s[mt][x], a, b[2 * x], b[2 * x + 1]);
+          }
+        }
+      }
+      const uint8_t* live = s_live + stage * kLatSlots + warp * 8 + 2 * tq;
+      const bool live0 = live[0] != 0, live1 = live[1] != 0;
+      float sc[MT][4];   // [head g: two slots, head g + 8: two slots]
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          sc[mt][2 * hf] = live0 ? (s[mt][0][2 * hf] + s[mt][1][2 * hf]) * P.scale_log2 : -INFINITY;
+          sc[mt][2 * hf + 1] = live1 ? (s[mt][0][2 * hf + 1] + s[mt][1][2 * hf + 1]) * P.scale_log2 : -INFINITY;
+          float mx = fmaxf(sc[mt][2 * hf], sc[mt][2 * hf + 1]);
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+          if (tq == 0) wmax[warp * HM + mt * 16 + hf * 8 + g] = mx;
+          const int h = mt * 16 + hf * 8 + g;
+          if (P.scores != nullptr && h < n_heads && warp * 8 < n * TT)
+            *reinterpret_cast<float2*>(P.scores + (hq0 + h) * P.score_stride + t * TT + warp * 8 + 2 * tq) =
+                make_float2(sc[mt][2 * hf], sc[mt][2 * hf + 1]);
+        }
+      }
+      __syncthreads();   // every warp's row maxima
+      bool same = true;
+      float alpha[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int h = mt * 16 + hf * 8 + g;
+          float mx = m_run[mt][hf];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) mx = fmaxf(mx, wmax[x * HM + h]);
+          alpha[mt][hf] = ex2(m_run[mt][hf] - mx);
+          same &= alpha[mt][hf] == 1.0f;
+          m_run[mt][hf] = mx;
+          float p0 = ex2(sc[mt][2 * hf] - mx), p1 = ex2(sc[mt][2 * hf + 1] - mx);
+          l_run[mt][hf] = l_run[mt][hf] * alpha[mt][hf] + (p0 + p1);
+#pragma unroll
+          for (int x = 0; x < NP; ++x)
+            *reinterpret_cast<uint32_t*>(p_buf + (x * HM + h) * kLatSlots * 2 + ((warp ^ (h & 7)) << 4) + tq * 4) = take_bf16(p0, p1);
+        }
+      }
+      if (!__all_sync(kFull, same)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            o[mt][j][0] *= alpha[mt][0];
+            o[mt][j][1] *= alpha[mt][0];
+            o[mt][j][2] *= alpha[mt][1];
+            o[mt][j][3] *= alpha[mt][1];
+          }
+      }
+      __syncthreads();   // P is in place
+      // ---- this warp's 64 latent dims of every head
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int x = 0; x < NP; ++x) {
+          uint32_t a[kLatTiles][4];
+#pragma unroll
+          for (int ks = 0; ks < kLatTiles; ++ks)
+            ldsm4(p_s + (x * HM + mt * 16 + a_row) * kLatSlots * 2 + (((2 * ks + (lane >> 4)) ^ (a_row & 7)) << 4), a[ks]);
+#pragma unroll
+          for (int j = 0; j < NT; j += 2) {
+            float y0[4] = {}, y1[4] = {};
+#pragma unroll
+            for (int ks = 0; ks < kLatTiles; ++ks) {
+              const int v_row = ks * 16 + a_row;
+              uint32_t b[4];
+              ldsm4_t(kv + v_row * kLatRowBytes + (((warp * NT + j + (lane >> 4)) ^ (v_row & 7)) << 4), b);
+              if (F32) {   // added outside the tensor cores, as above
+                mma(y0, a[ks], b[0], b[1]);
+                mma(y1, a[ks], b[2], b[3]);
+              } else {
+                mma(o[mt][j], a[ks], b[0], b[1]);
+                mma(o[mt][j + 1], a[ks], b[2], b[3]);
+              }
+            }
+            if (F32) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                o[mt][j][e] += y0[e];
+                o[mt][j + 1][e] += y1[e];
+              }
+            }
+          }
+        }
+      }
+      t += n;
+      const bool last = cur.tile + n == (cur.len + TT - 1) / TT || t == t_end;
+      if (last) {
+        // ---- the record of this range and request: the warps' sums meet in shared memory
+        const int64_t rec = part + cur.req;
+        __syncthreads();   // wmax is free
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float l = l_run[mt][hf];
+            l += __shfl_xor_sync(kFull, l, 1);
+            l += __shfl_xor_sync(kFull, l, 2);
+            const int h = mt * 16 + hf * 8 + g;
+            if (tq == 0) wmax[warp * HM + h] = l;
+            if (h < n_heads) {
+              float* acc = P.rec_acc + (rec * P.q_heads + hq0 + h) * kLatDims + warp * 64 + 2 * tq;
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+                *reinterpret_cast<float2*>(acc + 8 * j) = make_float2(o[mt][j][2 * hf], o[mt][j][2 * hf + 1]);
+            }
+          }
+        }
+        __syncthreads();
+        if (warp == 0 && tq == 0) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int h = mt * 16 + hf * 8 + g;
+              float l = 0.0f;
+#pragma unroll
+              for (int x = 0; x < 8; ++x) l += wmax[x * HM + h];
+              if (h < n_heads) P.rec_ml[rec * P.q_heads + hq0 + h] = make_float2(m_run[mt][hf], l);
+            }
+        }
+        opened = false;
+      }
+      if (t < t_end) skip(cur, n);
+      __syncthreads();   // the step's rows, P and wmax may be overwritten
+    }
+    cp_wait<0>();
+  }
+}
+
 // ---- the join
 constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
@@ -508,7 +776,7 @@ __device__ __forceinline__ void join_values(const PagedParams& P, const Records&
   constexpr int V = D / 32;
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-#pragma unroll 8
+#pragma unroll (V > 8 ? 2 : 8)
   for (int k = begin; k < x.count; k += step) {
     const float e = ex2(load_ml(P, x, k, hq).x - M);
     const float* a = P.rec_acc + ((x.first + k) * P.q_heads + hq) * D + lane * V;
@@ -720,29 +988,50 @@ cudaError_t launch_attend_d(const PagedParams& p, int grid, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_d(PagedParams p, int grid, int sm_count, cudaStream_t s) {
-  const bool wide = p.group > 8;
-  cudaError_t e;
-  if (wide) e = p.out_bf16 ? launch_attend_d<D, true, false>(p, grid, s) : launch_attend_d<D, true, true>(p, grid, s);
-  else e = p.out_bf16 ? launch_attend_d<D, false, false>(p, grid, s) : launch_attend_d<D, false, true>(p, grid, s);
+template <int MT, bool F32>
+cudaError_t launch_latent(const PagedParams& p, int grid, cudaStream_t s) {
+  auto kern = k_paged_latent<MT, F32>;
+  constexpr int smem = lat_smem(MT, F32);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  kern<<<grid, kLatThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+// The kernels after the attention: D is the width of an output row.
+template <int D>
+cudaError_t launch_join(PagedParams p, int sm_count, cudaStream_t s) {
   const int64_t tasks = static_cast<int64_t>(p.n_req) * p.q_heads;
   p.join_wide = tasks <= 2 * sm_count;
   p.weight_ctas = p.weights != nullptr ? kFinishWeightCtas * sm_count : 0;
   const int64_t join_ctas = p.join_wide ? tasks : (tasks + kFinishWarps - 1) / kFinishWarps;
   if (p.weights != nullptr) {
-    e = launch_after(k_paged_lse, static_cast<unsigned>((tasks + kFinishWarps - 1) / kFinishWarps), p, s);
+    const cudaError_t e = launch_after(k_paged_lse, static_cast<unsigned>((tasks + kFinishWarps - 1) / kFinishWarps), p, s);
     if (e != cudaSuccess) return e;
   }
   return launch_after(k_paged_finish<D>, static_cast<unsigned>(p.weight_ctas + join_ctas), p, s);
 }
 
+template <int D>
+cudaError_t launch_d(const PagedParams& p, int grid, int sm_count, cudaStream_t s) {
+  cudaError_t e;
+  if (p.group > 8) e = p.out_bf16 ? launch_attend_d<D, true, false>(p, grid, s) : launch_attend_d<D, true, true>(p, grid, s);
+  else e = p.out_bf16 ? launch_attend_d<D, false, false>(p, grid, s) : launch_attend_d<D, false, true>(p, grid, s);
+  return e != cudaSuccess ? e : launch_join<D>(p, sm_count, s);
+}
+
 }  // namespace
 
-int paged_warps_per_cta(int head_dim) { return paged_warps(head_dim); }
+int paged_ranges_per_cta(int head_dim) { return head_dim == kLatRow ? 1 : paged_warps(head_dim); }
 
 cudaError_t launch_paged(const PagedParams& p, int head_dim, int grid, int sm_count, cudaStream_t s) {
+  if (head_dim == kLatRow) {
+    cudaError_t e;
+    if (p.group <= 16) e = p.out_bf16 ? launch_latent<1, false>(p, grid, s) : launch_latent<1, true>(p, grid, s);
+    else e = p.out_bf16 ? launch_latent<2, false>(p, grid, s) : launch_latent<2, true>(p, grid, s);
+    return e != cudaSuccess ? e : launch_join<kLatDims>(p, sm_count, s);
+  }
   if (head_dim == 64) return launch_d<64>(p, grid, sm_count, s);
   if (head_dim == 128) return launch_d<128>(p, grid, sm_count, s);
   return launch_d<256>(p, grid, sm_count, s);

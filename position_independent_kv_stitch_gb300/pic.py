@@ -39,6 +39,7 @@ PIC_DEV_BAD_POS = 0x80
 PIC_F32, PIC_BF16 = 0, 1
 PIC_MAX_AXES = 4
 PIC_STATUS_BYTES = 256
+PIC_LATENT_DIM = 512
 PIC_VARIANT_REGISTERS, PIC_VARIANT_BULK_PIPELINE = 0, 1
 PIC_VARIANT_TENSOR_CORE_TMEM, PIC_VARIANT_WARP_MMA = 2, 3
 PIC_SEG_COPY_POOL, PIC_SEG_COPY_BLOCKS, PIC_SEG_MAPPED = 0, 1, 2
@@ -820,10 +821,11 @@ def pic_attend_paged_workspace_bytes(ctx, n_req: int, num_q_heads: int, max_seq_
 
 def pic_attend_paged(ctx, q, softmax_scale, k_cache, v_cache, block_tables, seq_lens, max_seq_len: int, out, lse=None,
                      weights=None, workspace=None, stream=None):
-    """One new token per request over its cached sequence (GQA).  q: bf16
+    """One new token per request over its cached sequence.  q: bf16
     [n_req][q_heads][head_dim], any request stride; k_cache, v_cache: one layer
-    [blocks][block_size][kv_heads][head_dim]; seq_lens: CUDA int32 [n_req], at
-    most max_seq_len each; out: float32 or bf16 of q's shape; lse: float32
+    [blocks][block_size][kv_heads][head_dim] (MLA: v_cache None); seq_lens: CUDA int32 [n_req], at
+    most max_seq_len each; out: float32 or bf16 of q's shape (MLA:
+    [n_req][q_heads][512]); lse: float32
     [n_req][q_heads] or None; weights: float32
     [blocks][weight_heads][block_size] or None, each slot's attention weight is
     added to it.  workspace: uint8, pic_attend_paged_workspace_bytes, its first
@@ -837,12 +839,14 @@ def pic_attend_paged(ctx, q, softmax_scale, k_cache, v_cache, block_tables, seq_
     max_blocks = _table_shape(block_tables, n_req)[1]
     cache, _ = _check_caches(ctx, k_cache, v_cache, 4)
     out_type = PIC_F32 if out.dtype is _F32 else PIC_BF16
-    if d != cache[3] or out.shape != shape or not out.is_contiguous() or (out_type == PIC_BF16 and out.dtype is not _BF16):
-        raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape, heads of the cache's head_dim")
+    want = shape if v_cache is not None else (n_req, hq, PIC_LATENT_DIM)
+    if d != cache[3] or out.shape != want or not out.is_contiguous() or (out_type == PIC_BF16 and out.dtype is not _BF16):
+        raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape (MLA: the latent's), heads of the "
+                         "cache's head_dim")
     if lse is not None and (lse.dtype is not _F32 or lse.numel() != n_req * hq or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [n_req][q_heads]")
     _launch(ctx, lib.pic_attend_paged, q.get_device(), stream,
-            (q.data_ptr(), stride, n_req, hq, softmax_scale, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            (q.data_ptr(), stride, n_req, hq, softmax_scale, k_cache.data_ptr(), _addr(v_cache), block_tables.data_ptr(),
              max_blocks, seq_lens.data_ptr(), max_seq_len, out.data_ptr(), out_type, _addr(lse), _addr(weights),
              _weight_heads(weights, cache), _addr(workspace), _size(workspace)))
 

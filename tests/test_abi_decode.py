@@ -8,7 +8,7 @@ import pytest
 from harness import lib
 from position_independent_kv_stitch_gb300 import pic
 
-INVALID, CAPACITY, RANGE, ALIGNMENT, UNSUPPORTED = 1, 5, 6, 7, 10
+INVALID, CAPACITY, RANGE, ALIGNMENT = 1, 5, 6, 7
 P = 0x10000   # a 256-byte aligned address that is never read
 
 
@@ -111,14 +111,15 @@ def test_a_cache_without_blocks_holds_no_sequence():
 
 
 def test_attend_sizes(gqa, mla):
-    assert _attend(mla) == UNSUPPORTED
+    assert _attend(mla, hq=16, q_stride=16 * 1152, n_req=0, v=None) == 0
+    assert _attend(mla, hq=16, q_stride=16 * 1152 - 16) == RANGE
     assert _attend(gqa, n_req=0) == 0
     bare = pic.pic_attend_paged_workspace_bytes(gqa, 2, 4, 64)
     kept = pic.pic_attend_paged_workspace_bytes(gqa, 2, 4, 64, True)
     # the scores of 2 x 64 slots under 4 heads, and their log-sum-exps
     assert 256 < bare and bare + 2 * 64 * 4 * 4 <= kept <= bare + 2 * 64 * 4 * 4 + 1024
     assert _attend(gqa, ws_bytes=bare - 1) == CAPACITY and _attend(gqa, ws_bytes=kept - 1, weights=P, heads=1) == CAPACITY
-    for bad in ((gqa, -1, 4, 64), (gqa, 2, 3, 64), (gqa, 2, 4, -1), (mla, 2, 16, 64), (None, 2, 4, 64)):
+    for bad in ((gqa, -1, 4, 64), (gqa, 2, 3, 64), (gqa, 2, 4, -1), (mla, 2, 0, 64), (None, 2, 4, 64)):
         assert pic.load().pic_attend_paged_workspace_bytes(*bad, 0) == 0
 
 

@@ -219,12 +219,13 @@ def _attend(c, hq, out_type, layer=0, weights=True, scale=None, q=None):
     scale = 1.0 / math.sqrt(c.d) if scale is None else scale
     q = c.normal(n, hq, c.d) * 2 if q is None else q
     kh, vh, wh = c.host(layer)
+    vh = kh[..., :512] if vh is None else vh
     want = oracle.attend_paged(_f64(q), kh, vh, c.tables, c.lens, c.bs, scale, wh)
     max_len = max(1, max(c.lens))
-    out = torch.full((n, hq, c.d), 7.0, dtype=out_type, device=DEV)
+    out = torch.full((n, hq, vh.shape[-1]), 7.0, dtype=out_type, device=DEV)
     lse = torch.full((n, hq), 7.0, device=DEV)
     ws = _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, n, hq, max_len, weights))
-    pic.pic_attend_paged(c.ctx, q, scale, c.k[layer], c.v[layer], c.d_tables, c.d_lens, max_len, out, lse=lse,
+    pic.pic_attend_paged(c.ctx, q, scale, c.k[layer], None if c.v is None else c.v[layer], c.d_tables, c.d_lens, max_len, out, lse=lse,
                          weights=c.w[layer] if weights else None, workspace=ws)
     assert _status(c, ws) == 0
     _check_attend(c, q, kh, vh, wh, want, out, lse, scale, c.w[layer] if weights else None)
@@ -277,6 +278,43 @@ def test_attend_paged(heads, hq, d, bs, out_type):
 def test_attend_paged_lengths(lens, weights):
     c = Cache(heads=2, d=128, bs=16, lens=lens, seed=len(lens))
     _attend(c, 8, torch.float32, weights=weights)
+    c.close()
+
+
+@pytest.mark.parametrize("out_type", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hq,bs", [(1, 16), (16, 16), (20, 7), (32, 64), (64, 16), (128, 1), (100, 256)])
+def test_attend_paged_mla(hq, bs, out_type):
+    """Latent rows: 1 to 128 query heads over lengths around the 64-slot steps."""
+    c = Cache("mla", bs=bs, lens=[1, 0, 63, 64, 65, 200, 17, 130], seed=hq)
+    _attend(c, hq, out_type, scale=0.03)
+    c.close()
+
+
+@pytest.mark.parametrize("lens", [[3000], [0], [5000, 0, 16, 700], [40] * 200])
+def test_attend_paged_mla_lengths(lens):
+    c = Cache("mla", lens=lens, seed=len(lens))
+    _attend(c, 16, torch.float32, scale=0.03)
+    c.close()
+
+
+def test_attend_paged_mla_junk_and_bad_blocks():
+    """Rows behind the end hold NaN; a block outside the cache is left out."""
+    c = Cache("mla", lens=[70, 33, 100], seed=3)
+    q = c.normal(3, 32, 576)
+    clean, _ = _attend(c, 32, torch.float32, scale=0.03, weights=False, q=q)
+    for r, n in enumerate(c.lens):
+        for s in range(n, c.tables.shape[1] * 16):
+            c.k[0, int(c.tables[r][s // 16]), s % 16] = float("nan")
+    tables = c.d_tables.clone()
+    tables[1, 1] = c.nb
+    out, ws = torch.empty(3, 32, 512, device=DEV), _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, 3, 32, 100))
+    pic.pic_attend_paged(c.ctx, q, 0.03, c.k[0], None, tables, c.d_lens, 100, out, workspace=ws)
+    assert _status(c, ws) == pic.PIC_DEV_BAD_BLOCK
+    assert torch.equal(out[[0, 2]], clean[[0, 2]])
+    kh = c.host()[0]
+    rows = np.stack([kh[c.tables[1][s // 16], s % 16] for s in range(33) if s // 16 != 1])
+    want, _ = oracle.attention_decode(_f64(q[1]), rows, rows[..., :512], 0.03)
+    np.testing.assert_allclose(_f64(out[1]), want, atol=1e-4)
     c.close()
 
 
@@ -608,6 +646,45 @@ def test_decode_loop(renumber, graph):
     c = Cache(heads=2, d=64, bs=8, layers=2, lens=[30, 12, 44], room=30, seed=20 + renumber)
     c.w.zero_()
     _decode_steps(c, 14, 36, 5, 6, renumber, graph)
+    c.close()
+
+
+def test_decode_loop_mla():
+    """Write, attend and evict over latent rows, step by step against the oracle."""
+    c = Cache("mla", bs=16, lens=[20, 33], room=30, seed=50)
+    c.w.zero_()
+    hq, budget, scale = 16, 36, 0.03
+    q_out, out = torch.empty(2, hq, 576, dtype=torch.bfloat16, device=DEV), torch.empty(2, hq, 512, device=DEV)
+    lse, lens, ws = torch.empty(2, hq, device=DEV), c.d_lens, _ws(1 << 24)
+    kept = torch.empty(1, 2, 1, budget, dtype=torch.int32, device=DEV)
+    for step in range(8):
+        slot = lens.clone()
+        lens.add_(1)
+        c.lens = lens.tolist()
+        q, k = c.normal(2, hq, 576), c.normal(2, 1, 576)
+        kh, _, wh = c.host()
+        want = oracle.write_tokens(_f64(q), _f64(k), None, slot.cpu().numpy()[None], [0] * 32, c.theta, c.pairing, 512, 64, [0, 1],
+                                   slot.tolist(), c.tables, c.bs, kh, None, wh)
+        pic.pic_write_tokens(c.ctx, slot, k, None, _i32([0, 1]), slot, c.d_tables, c.k[0], None, q=q, q_out=q_out, weights=c.w[0],
+                             workspace=ws)
+        pic.pic_attend_paged(c.ctx, q_out, scale, c.k[0], None, c.d_tables, lens, c.tables.shape[1] * 16, out, lse=lse,
+                             weights=c.w[0], workspace=ws)
+        _assert_rotated(_f64(q_out), want[0], c, "q")
+        kn = c.host()[0]
+        _assert_rotated(kn, want[1], c, "k")
+        att = oracle.attend_paged(_f64(q_out), kn, kn[..., :512], c.tables, c.lens, c.bs, scale, want[3])
+        _check_attend(c, q_out, kn, kn[..., :512], want[3], att, out, lse, scale, c.w[0])
+        if max(c.lens) > budget + 3:
+            host = c.host()
+            pic.pic_evict_tokens(c.ctx, c.k, None, c.w, c.d_tables, lens, budget, kept, lens, n_first=1, n_recent=4, renumber=True,
+                                 workspace=ws)
+            kn, _, wn, keep, new = oracle.evict_tokens(*host, c.tables, np.array(c.lens), c.bs, budget, 1, 4, True, c.theta, c.pairing,
+                                                       512, 64)
+            np.testing.assert_array_equal(kept[0].cpu().numpy(), keep)
+            np.testing.assert_array_equal(_f64(c.w[0]), wn)
+            _assert_rotated(_f64(c.k[0]), kn, c, "k after eviction")
+            assert lens.tolist() == new.tolist()
+    assert _status(c, ws) == 0
     c.close()
 
 
