@@ -92,19 +92,16 @@ struct PagedLayout {
   size_t lse2, rec_ml, rec_acc, scores, total;
   int64_t score_stride;
 };
-int32_t paged_passes(const CtxView& c, int32_t group) {
-  const int32_t heads = c.model->kind == PIC_KIND_MLA ? 32 : 16;
-  return (group + heads - 1) / heads;
-}
+int32_t paged_passes(int32_t group) { return (group + 15) / 16; }
 // Width of an output row: the head's, or the latent's.
 int32_t paged_out_dim(const CtxView& c) { return c.model->kind == PIC_KIND_MLA ? c.model->rope_offset : c.model->head_dim; }
 int64_t paged_max_parts(int32_t v_heads, int head_dim) {
-  return std::max<int64_t>(1, static_cast<int64_t>(kPagedMaxCtas) * paged_ranges_per_cta(head_dim) / v_heads);
+  return std::max<int64_t>(1, static_cast<int64_t>(kPagedMaxSms) * paged_ranges_per_sm(head_dim) / v_heads);
 }
 PagedLayout paged_layout(const CtxView& c, int64_t n_req, int64_t q_heads, int64_t max_len, bool weights) {
   const int d = paged_out_dim(c);
   const int32_t group = static_cast<int32_t>(q_heads / c.model->num_kv_heads);
-  const int64_t recs = paged_max_parts(c.model->num_kv_heads * paged_passes(c, group), c.model->head_dim) + n_req;
+  const int64_t recs = paged_max_parts(c.model->num_kv_heads * paged_passes(group), c.model->head_dim) + n_req;
   PagedLayout L{};
   L.score_stride = weights ? n_req * ((max_len + kPagedTile - 1) / kPagedTile) * kPagedTile : 0;
   L.lse2 = sizeof(WsHeader);
@@ -325,11 +322,10 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
   p.q_heads = num_q_heads;
   p.kv_heads = m.num_kv_heads;
   p.group = num_q_heads / m.num_kv_heads;
-  p.passes = paged_passes(c, p.group);
+  p.passes = paged_passes(p.group);
   p.v_heads = p.kv_heads * p.passes;
-  const int ranges = paged_ranges_per_cta(m.head_dim);
-  const int grid = std::min(sms, kPagedMaxCtas);   // one CTA per SM (its rows fill shared memory)
-  p.parts = static_cast<int32_t>(std::max<int64_t>(1, static_cast<int64_t>(grid) * ranges / p.v_heads));
+  const int used = std::min(sms, kPagedMaxSms);
+  p.parts = static_cast<int32_t>(std::max<int64_t>(1, static_cast<int64_t>(used) * paged_ranges_per_sm(m.head_dim) / p.v_heads));
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.k_cache = static_cast<const uint8_t*>(k_cache);
   p.v_cache = static_cast<const uint8_t*>(v_cache);
@@ -345,7 +341,7 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
   p.weights = d_weights;
   p.weight_heads = weight_heads;
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
-  const cudaError_t e = launch_paged(p, m.head_dim, grid, sms, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_paged(p, m.head_dim, used, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(ctx, e, "paged attention launch");
   return set_error(ctx, PIC_OK, "");
 }

@@ -74,7 +74,7 @@ cudaError_t launch_write(const WriteParams& p, int pairing, cudaStream_t s);
 
 // ---- paged attention
 constexpr int kPagedTile = 16;          // positions of one step of a warp
-constexpr int kPagedMaxCtas = 256;      // grid bound (workspace sizing)
+constexpr int kPagedMaxSms = 256;       // SMs used (workspace sizing)
 constexpr int kPagedMaxHeads = 4096;    // query heads
 
 struct PagedParams {
@@ -85,7 +85,7 @@ struct PagedParams {
   int32_t n_req;
   int32_t max_len;
   int32_t q_heads, kv_heads, group;
-  int32_t passes;            // passes over a group, of 16 heads (MLA: 32)
+  int32_t passes;            // 16-head passes over a group
   int32_t v_heads;           // kv_heads * passes: what ranges are dealt to
   int32_t parts;             // ranges per virtual head
   float scale_log2;
@@ -106,8 +106,8 @@ struct PagedParams {
   int32_t join_wide;         // 1: one per (request, query head); 0: one warp for each
   uint32_t* status;
 };
-int paged_ranges_per_cta(int head_dim);  // ranges a CTA works on at a time (head_dim 576: MLA rows)
-cudaError_t launch_paged(const PagedParams& p, int head_dim, int grid, int sm_count, cudaStream_t s);
+int paged_ranges_per_sm(int head_dim);  // ranges an SM works on at a time (head_dim 576: MLA rows)
+cudaError_t launch_paged(const PagedParams& p, int head_dim, int sm_count, cudaStream_t s);
 
 // ---- eviction
 struct EvictUnit {           // per (layer, request, weight head), in the workspace

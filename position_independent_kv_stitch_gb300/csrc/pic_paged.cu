@@ -455,36 +455,43 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
 // ---- MLA: latent rows
 //
 // Every query head reads the same rows (512 latent dims and a 64-dim rope key,
-// the latent also the value), so a CTA takes a range for up to 32 heads and
-// works on it together: 64 slots of one request a step, in shared memory twice
-// over, copied in with cp.async while the step before is computed.  Warp w
-// scores slots 8 w .. 8 w + 7 against every head (36 k-steps over the 576
-// dims); the row maxima meet in shared memory; P goes through shared memory in
-// bf16 parts, as above; warp w then adds latent dims 64 w .. 64 w + 63 of every
-// head.  Each of the three barriers of a step separates these.  Heads beyond 32
-// (passes) read the rows again, mostly from L2.
-// Bound: mma.sync for 32 heads (1,600 products a step against 73 KB of rows),
-// HBM for 16.
+// the latent also the value), so a CTA takes a range for 16 heads (more heads:
+// more passes, whose CTAs read the same rows side by side) and works on it
+// together, 32 slots of one request a step, the next step's rows on their way:
+//   * warp w scores slots 8 (w % 4) .. + 7 over half of the 576 dims (18 k-steps);
+//     the halves meet in shared memory;
+//   * sixteen threads a head add them, keep the running maximum and sum (two
+//     scores each) and leave P in bf16 parts, as above;
+//   * warp w adds latent dims 64 w .. 64 w + 63 of every head.
+// The three barriers of a step come between these; two CTAs per SM cover each
+// other's.  Bound: mma.sync (400 products a step of 37 KB).
 constexpr int kLatDims = 512, kLatRow = 576;
 constexpr int kLatRowBytes = kLatRow * 2, kLatChunks = kLatRowBytes / 16;
-constexpr int kLatSlots = 64;            // slots of a step
-constexpr int kLatTiles = kLatSlots / TT;
+constexpr int kLatHeads = 16;
+constexpr int kLatSlots = 32, kLatTiles = kLatSlots / TT;   // of a step
 constexpr int kLatThreads = 256;
-__host__ __device__ constexpr int lat_smem(int MT, bool f32) {
-  return 2 * kLatSlots * kLatRowBytes + MT * 16 * kLatRowBytes + (f32 ? 3 : 2) * MT * 16 * kLatSlots * 2 + 8 * MT * 16 * 4 +
-         2 * kLatSlots;
-}
+constexpr int kLatCtas = 2;              // per SM
+constexpr int kLatPitch = 80;            // bytes of a head's P: eight rows in distinct banks
+constexpr int kLatScorePitch = kLatSlots + 4;
+struct LatSmem {
+  alignas(128) uint8_t kv[2][kLatSlots][kLatRowBytes];
+  alignas(128) uint8_t q[kLatHeads][kLatRowBytes];
+  alignas(16) uint8_t p[3][kLatHeads][kLatPitch];
+  alignas(16) float s[2][kLatHeads][kLatScorePitch];   // scores over either half of the dims
+  float alpha[kLatHeads];
+  uint8_t live[2][kLatSlots];
+};
 
-template <int MT, bool F32>   // MT: 16-head tiles of a CTA
-__global__ void __launch_bounds__(kLatThreads, 1) k_paged_latent(const __grid_constant__ PagedParams P) {
+template <bool F32>
+__global__ void __launch_bounds__(kLatThreads, kLatCtas) k_paged_latent(const __grid_constant__ PagedParams P) {
   asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int HM = MT * 16, NP = F32 ? 3 : 2, NT = kLatDims / 8 / 8;   // output n-tiles of a warp
+  constexpr int NP = F32 ? 3 : 2, NT = kLatDims / 8 / 8;   // parts of P, output n-tiles of a warp
   extern __shared__ __align__(128) uint8_t smem[];
-  const uint32_t kv_s = smem_u32(smem), q_s = kv_s + 2 * kLatSlots * kLatRowBytes, p_s = q_s + HM * kLatRowBytes;
-  uint8_t* p_buf = smem + 2 * kLatSlots * kLatRowBytes + HM * kLatRowBytes;
-  float* wmax = reinterpret_cast<float*>(p_buf + NP * HM * kLatSlots * 2);   // [warp][head]
-  uint8_t* s_live = reinterpret_cast<uint8_t*>(wmax + 8 * HM);               // [stage][slot]
+  LatSmem& S = *reinterpret_cast<LatSmem*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  const int a_row = (lane & 7) + ((lane >> 3) & 1) * 8;    // ldmatrix row of a 16-row operand
+  const int my_row = tid >> 3;                             // eight threads copy a row
+  const int my_head = tid >> 4, my_slot = (tid & 15) * 2;  // sixteen threads weigh a head's slots
   const TileList L = tile_list(P, lane, blockIdx.x == 0 && warp == 0);
   uint64_t policy;   // rows that no other CTA reads pass through L2 first-out
   if (P.passes == 1) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
@@ -496,33 +503,32 @@ __global__ void __launch_bounds__(kLatThreads, 1) k_paged_latent(const __grid_co
     if (part >= L.parts || L.total == 0) continue;
     const int64_t t_begin = L.begin(part), t_end = L.begin(part + 1);
     if (t_begin >= t_end) continue;
-    const int hq0 = vh * HM, n_heads = min(HM, P.q_heads - hq0);
+    const int hq0 = vh * kLatHeads, n_heads = min(kLatHeads, P.q_heads - hq0);
 
-    // A step: up to four tiles of one request.
+    // tiles of the step that begins at a place: up to two, of one request
     auto step_tiles = [&](const Place& x, int64_t t) {
       return static_cast<int>(min(min(static_cast<int64_t>(kLatTiles), t_end - t), static_cast<int64_t>((x.len + TT - 1) / TT - x.tile)));
     };
     auto skip = [&](Place& x, int n) {
       for (int i = 0; i < n; ++i) advance(P, x);
     };
-    const int my_row = tid >> 2;   // four threads copy a row
     // this thread's cache row of a step, -1 past its end or for a bad block
     auto row_of = [&](const Place& x, int n) -> int {
       const int slot = x.tile * TT + my_row;
       if (my_row >= n * TT || slot >= x.len) return -1;
       const int64_t row = paged_row(P.paged, x.req, slot);
-      if (row < 0 && (tid & 3) == 0) raise_block(P.status, x.req, slot);
+      if (row < 0 && (tid & 7) == 0) raise_block(P.status, x.req, slot);
       return static_cast<int>(row);
     };
     auto issue = [&](int stage, int row) {
       const uint8_t* src = P.k_cache + static_cast<int64_t>(row < 0 ? 0 : row) * kLatRowBytes;
-      const uint32_t dst = kv_s + (stage * kLatSlots + my_row) * kLatRowBytes;
+      const uint32_t dst = smem_u32(S.kv[stage][my_row]);
 #pragma unroll
-      for (int i = 0; i < kLatChunks / 4; ++i) {
-        const int c = (tid & 3) + 4 * i;
+      for (int i = 0; i < kLatChunks / 8; ++i) {
+        const int c = (tid & 7) + 8 * i;
         cp_async16_zfill(dst + ((c ^ (my_row & 7)) << 4), src + c * 16, row >= 0, policy);
       }
-      if ((tid & 3) == 0) s_live[stage * kLatSlots + my_row] = row >= 0;
+      if ((tid & 7) == 0) S.live[stage][my_row] = row >= 0;
     };
 
     Place load;
@@ -531,190 +537,150 @@ __global__ void __launch_bounds__(kLatThreads, 1) k_paged_latent(const __grid_co
     load.len = load.req < P.n_req ? legal_len(__ldg(P.lens + load.req), P.max_len, P.status, false) : 0;
     Place cur = load;
     int64_t t_load = t_begin;
-    __syncthreads();   // the previous range is done with shared memory
-    {
-      const int n = step_tiles(load, t_load);
-      issue(0, row_of(load, n));
+    int next_row = -1;   // of the step to be loaded next, looked up a step ahead
+    auto look_up = [&]() {
+      if (t_load >= t_end) return;
+      next_row = row_of(load, step_tiles(load, t_load));
+    };
+    auto load_step = [&](int stage) {
+      if (t_load < t_end) {
+        const int n = step_tiles(load, t_load);
+        issue(stage, next_row);
+        t_load += n;
+        skip(load, n);
+      }
       cp_commit();
-      t_load += n;
-      skip(load, n);
-    }
-    float o[MT][NT][4], m_run[MT][2], l_run[MT][2];
+    };
+    __syncthreads();   // the previous range is done with shared memory
+    look_up();
+    load_step(0);
+    look_up();
+    float o[NT][4], m_run = -FLT_MAX, l_run = 0.0f;
     bool opened = false;
     int stage = 0;
     for (int64_t t = t_begin; t < t_end; stage ^= 1) {
       const int n = step_tiles(cur, t);
-      if (t_load < t_end) {
-        const int nl = step_tiles(load, t_load);
-        issue(stage ^ 1, row_of(load, nl));
-        t_load += nl;
-        skip(load, nl);
-      }
-      cp_commit();
       if (!opened) {
         opened = true;
+        m_run = -FLT_MAX;
+        l_run = 0.0f;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          m_run[mt][0] = m_run[mt][1] = -FLT_MAX;
-          l_run[mt][0] = l_run[mt][1] = 0.0f;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.0f;
-        }
+        for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
         const uint8_t* qp = P.q + cur.req * P.q_stride + static_cast<int64_t>(hq0) * kLatRowBytes;
-        uint8_t* qd = smem + 2 * kLatSlots * kLatRowBytes;
-        for (int i = tid; i < HM * kLatChunks; i += kLatThreads) {
+        for (int i = tid; i < kLatHeads * kLatChunks; i += kLatThreads) {
           const int h = i / kLatChunks, c = i % kLatChunks;
           const uint4 v = h < n_heads ? __ldg(reinterpret_cast<const uint4*>(qp + i * 16)) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(qd + h * kLatRowBytes + ((c ^ (h & 7)) << 4)) = v;
+          *reinterpret_cast<uint4*>(S.q[h] + ((c ^ (h & 7)) << 4)) = v;
         }
       }
-      cp_wait<1>();
-      __syncthreads();   // the step's rows and the queries are in place
-      const uint32_t kv = kv_s + stage * kLatSlots * kLatRowBytes;
-      // ---- scores of this warp's 8 slots (even and odd k-steps apart: shorter chains)
-      float s[MT][2][4] = {};
-      const int k_row = warp * 8 + (lane & 7), a_row = (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll 3
-      for (int i = 0; i < kLatChunks / 4; ++i) {
-        uint32_t b[4];
-        ldsm4(kv + k_row * kLatRowBytes + (((4 * i + (lane >> 3)) ^ (k_row & 7)) << 4), b);
+      cp_wait<0>();
+      __syncthreads();   // the step's rows and the queries are in place; the other stage is free
+      load_step(stage ^ 1);
+      look_up();
+      // ---- scores of 8 slots over half of the dims (even and odd k-steps apart: shorter chains)
+      {
+        float s[2][4] = {};
+        const int half = warp >> 2, col = (warp & 3) * 8, k_row = col + (lane & 7);
+        const uint32_t ka = smem_u32(S.kv[stage][k_row]), qa = smem_u32(S.q[a_row]);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int i = 0; i < kLatChunks / 8; ++i) {
+          const int c = half * (kLatChunks / 2) + 4 * i;
+          uint32_t b[4];
+          ldsm4(ka + (((c + (lane >> 3)) ^ (k_row & 7)) << 4), b);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             uint32_t a[4];
-            ldsm4(q_s + (mt * 16 + a_row) * kLatRowBytes + (((4 * i + 2 * x + (lane >> 4)) ^ (a_row & 7)) << 4), a);
-            mma(s[mt][x], a, b[2 * x], b[2 * x + 1]);
+            ldsm4(qa + (((c + 2 * x + (lane >> 4)) ^ (a_row & 7)) << 4), a);
+            mma(s[x], a, b[2 * x], b[2 * x + 1]);
           }
         }
+        *reinterpret_cast<float2*>(&S.s[half][g][col + 2 * tq]) = make_float2(s[0][0] + s[1][0], s[0][1] + s[1][1]);
+        *reinterpret_cast<float2*>(&S.s[half][g + 8][col + 2 * tq]) = make_float2(s[0][2] + s[1][2], s[0][3] + s[1][3]);
       }
-      const uint8_t* live = s_live + stage * kLatSlots + warp * 8 + 2 * tq;
-      const bool live0 = live[0] != 0, live1 = live[1] != 0;
-      float sc[MT][4];   // [head g: two slots, head g + 8: two slots]
+      __syncthreads();   // both halves of the scores
+      {
+        const float2 x = *reinterpret_cast<const float2*>(&S.s[0][my_head][my_slot]);
+        const float2 y = *reinterpret_cast<const float2*>(&S.s[1][my_head][my_slot]);
+        const float s0 = S.live[stage][my_slot] != 0 ? (x.x + y.x) * P.scale_log2 : -INFINITY;
+        const float s1 = S.live[stage][my_slot + 1] != 0 ? (x.y + y.y) * P.scale_log2 : -INFINITY;
+        if (P.scores != nullptr && my_head < n_heads && my_slot < n * TT)
+          *reinterpret_cast<float2*>(P.scores + (hq0 + my_head) * P.score_stride + t * TT + my_slot) = make_float2(s0, s1);
+        float m = fmaxf(s0, s1);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+        for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+        m = fmaxf(m_run, m);
+        const float alpha = ex2(m_run - m);
+        m_run = m;
+        float p0 = ex2(s0 - m), p1 = ex2(s1 - m);
+        l_run = l_run * alpha + (p0 + p1);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          sc[mt][2 * hf] = live0 ? (s[mt][0][2 * hf] + s[mt][1][2 * hf]) * P.scale_log2 : -INFINITY;
-          sc[mt][2 * hf + 1] = live1 ? (s[mt][0][2 * hf + 1] + s[mt][1][2 * hf + 1]) * P.scale_log2 : -INFINITY;
-          float mx = fmaxf(sc[mt][2 * hf], sc[mt][2 * hf + 1]);
-          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-          if (tq == 0) wmax[warp * HM + mt * 16 + hf * 8 + g] = mx;
-          const int h = mt * 16 + hf * 8 + g;
-          if (P.scores != nullptr && h < n_heads && warp * 8 < n * TT)
-            *reinterpret_cast<float2*>(P.scores + (hq0 + h) * P.score_stride + t * TT + warp * 8 + 2 * tq) =
-                make_float2(sc[mt][2 * hf], sc[mt][2 * hf + 1]);
-        }
-      }
-      __syncthreads();   // every warp's row maxima
-      bool same = true;
-      float alpha[MT][2];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int h = mt * 16 + hf * 8 + g;
-          float mx = m_run[mt][hf];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) mx = fmaxf(mx, wmax[x * HM + h]);
-          alpha[mt][hf] = ex2(m_run[mt][hf] - mx);
-          same &= alpha[mt][hf] == 1.0f;
-          m_run[mt][hf] = mx;
-          float p0 = ex2(sc[mt][2 * hf] - mx), p1 = ex2(sc[mt][2 * hf + 1] - mx);
-          l_run[mt][hf] = l_run[mt][hf] * alpha[mt][hf] + (p0 + p1);
-#pragma unroll
-          for (int x = 0; x < NP; ++x)
-            *reinterpret_cast<uint32_t*>(p_buf + (x * HM + h) * kLatSlots * 2 + ((warp ^ (h & 7)) << 4) + tq * 4) = take_bf16(p0, p1);
-        }
-      }
-      if (!__all_sync(kFull, same)) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            o[mt][j][0] *= alpha[mt][0];
-            o[mt][j][1] *= alpha[mt][0];
-            o[mt][j][2] *= alpha[mt][1];
-            o[mt][j][3] *= alpha[mt][1];
-          }
+        for (int i = 0; i < NP; ++i) *reinterpret_cast<uint32_t*>(&S.p[i][my_head][my_slot * 2]) = take_bf16(p0, p1);
+        if ((tid & 15) == 0) S.alpha[my_head] = alpha;
       }
       __syncthreads();   // P is in place
       // ---- this warp's 64 latent dims of every head
+      {
+        const float a0 = S.alpha[g], a1 = S.alpha[g + 8];
+        if (!__all_sync(kFull, a0 == 1.0f && a1 == 1.0f)) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+          for (int j = 0; j < NT; ++j) {
+            o[j][0] *= a0;
+            o[j][1] *= a0;
+            o[j][2] *= a1;
+            o[j][3] *= a1;
+          }
+        }
+        uint32_t a[NP][kLatTiles][4];
 #pragma unroll
-        for (int x = 0; x < NP; ++x) {
-          uint32_t a[kLatTiles][4];
+        for (int i = 0; i < NP; ++i)
 #pragma unroll
-          for (int ks = 0; ks < kLatTiles; ++ks)
-            ldsm4(p_s + (x * HM + mt * 16 + a_row) * kLatSlots * 2 + (((2 * ks + (lane >> 4)) ^ (a_row & 7)) << 4), a[ks]);
+          for (int ks = 0; ks < kLatTiles; ++ks) ldsm4(smem_u32(S.p[i][a_row]) + (2 * ks + (lane >> 4)) * 16, a[i][ks]);
 #pragma unroll
-          for (int j = 0; j < NT; j += 2) {
-            float y0[4] = {}, y1[4] = {};
+        for (int j = 0; j < NT; j += 2) {
+          float y0[4] = {}, y1[4] = {};
 #pragma unroll
-            for (int ks = 0; ks < kLatTiles; ++ks) {
-              const int v_row = ks * 16 + a_row;
-              uint32_t b[4];
-              ldsm4_t(kv + v_row * kLatRowBytes + (((warp * NT + j + (lane >> 4)) ^ (v_row & 7)) << 4), b);
+          for (int ks = 0; ks < kLatTiles; ++ks) {
+            uint32_t b[4];
+            ldsm4_t(smem_u32(S.kv[stage][ks * 16 + a_row]) + (((warp * NT + j + (lane >> 4)) ^ (a_row & 7)) << 4), b);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
               if (F32) {   // added outside the tensor cores, as above
-                mma(y0, a[ks], b[0], b[1]);
-                mma(y1, a[ks], b[2], b[3]);
+                mma(y0, a[i][ks], b[0], b[1]);
+                mma(y1, a[i][ks], b[2], b[3]);
               } else {
-                mma(o[mt][j], a[ks], b[0], b[1]);
-                mma(o[mt][j + 1], a[ks], b[2], b[3]);
+                mma(o[j], a[i][ks], b[0], b[1]);
+                mma(o[j + 1], a[i][ks], b[2], b[3]);
               }
             }
-            if (F32) {
+          }
+          if (F32) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[mt][j][e] += y0[e];
-                o[mt][j + 1][e] += y1[e];
-              }
+            for (int e = 0; e < 4; ++e) {
+              o[j][e] += y0[e];
+              o[j + 1][e] += y1[e];
             }
           }
         }
       }
       t += n;
-      const bool last = cur.tile + n == (cur.len + TT - 1) / TT || t == t_end;
-      if (last) {
-        // ---- the record of this range and request: the warps' sums meet in shared memory
-        const int64_t rec = part + cur.req;
-        __syncthreads();   // wmax is free
+      if (cur.tile + n == (cur.len + TT - 1) / TT || t == t_end) {
+        // ---- the record of this range and request
+        const int64_t rec = (part + cur.req) * P.q_heads + hq0;
+        float l = l_run;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int d = 1; d < 16; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
+        if ((tid & 15) == 0 && my_head < n_heads) P.rec_ml[rec + my_head] = make_float2(m_run, l);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float l = l_run[mt][hf];
-            l += __shfl_xor_sync(kFull, l, 1);
-            l += __shfl_xor_sync(kFull, l, 2);
-            const int h = mt * 16 + hf * 8 + g;
-            if (tq == 0) wmax[warp * HM + h] = l;
-            if (h < n_heads) {
-              float* acc = P.rec_acc + (rec * P.q_heads + hq0 + h) * kLatDims + warp * 64 + 2 * tq;
+        for (int hf = 0; hf < 2; ++hf) {
+          const int h = g + 8 * hf;
+          if (h >= n_heads) continue;
+          float* acc = P.rec_acc + (rec + h) * kLatDims + warp * 64 + 2 * tq;
 #pragma unroll
-              for (int j = 0; j < NT; ++j)
-                *reinterpret_cast<float2*>(acc + 8 * j) = make_float2(o[mt][j][2 * hf], o[mt][j][2 * hf + 1]);
-            }
-          }
-        }
-        __syncthreads();
-        if (warp == 0 && tq == 0) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const int h = mt * 16 + hf * 8 + g;
-              float l = 0.0f;
-#pragma unroll
-              for (int x = 0; x < 8; ++x) l += wmax[x * HM + h];
-              if (h < n_heads) P.rec_ml[rec * P.q_heads + hq0 + h] = make_float2(m_run[mt][hf], l);
-            }
+          for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(acc + 8 * j) = make_float2(o[j][2 * hf], o[j][2 * hf + 1]);
         }
         opened = false;
       }
       if (t < t_end) skip(cur, n);
-      __syncthreads();   // the step's rows, P and wmax may be overwritten
     }
     cp_wait<0>();
   }
@@ -988,14 +954,14 @@ cudaError_t launch_attend_d(const PagedParams& p, int grid, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int MT, bool F32>
-cudaError_t launch_latent(const PagedParams& p, int grid, cudaStream_t s) {
-  auto kern = k_paged_latent<MT, F32>;
-  constexpr int smem = lat_smem(MT, F32);
-  static_assert(smem <= 227 * 1024, "shared memory");
+template <bool F32>
+cudaError_t launch_latent(const PagedParams& p, int sm_count, cudaStream_t s) {
+  auto kern = k_paged_latent<F32>;
+  constexpr int smem = sizeof(LatSmem);
+  static_assert(kLatCtas * (smem + 1024) <= 228 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kLatThreads, smem, s>>>(p);
+  kern<<<sm_count * kLatCtas, kLatThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -1014,7 +980,8 @@ cudaError_t launch_join(PagedParams p, int sm_count, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t launch_d(const PagedParams& p, int grid, int sm_count, cudaStream_t s) {
+cudaError_t launch_d(const PagedParams& p, int sm_count, cudaStream_t s) {
+  const int grid = sm_count;   // one CTA per SM: its rings fill shared memory
   cudaError_t e;
   if (p.group > 8) e = p.out_bf16 ? launch_attend_d<D, true, false>(p, grid, s) : launch_attend_d<D, true, true>(p, grid, s);
   else e = p.out_bf16 ? launch_attend_d<D, false, false>(p, grid, s) : launch_attend_d<D, false, true>(p, grid, s);
@@ -1023,18 +990,16 @@ cudaError_t launch_d(const PagedParams& p, int grid, int sm_count, cudaStream_t 
 
 }  // namespace
 
-int paged_ranges_per_cta(int head_dim) { return head_dim == kLatRow ? 1 : paged_warps(head_dim); }
+int paged_ranges_per_sm(int head_dim) { return head_dim == kLatRow ? kLatCtas : paged_warps(head_dim); }
 
-cudaError_t launch_paged(const PagedParams& p, int head_dim, int grid, int sm_count, cudaStream_t s) {
+cudaError_t launch_paged(const PagedParams& p, int head_dim, int sm_count, cudaStream_t s) {
   if (head_dim == kLatRow) {
-    cudaError_t e;
-    if (p.group <= 16) e = p.out_bf16 ? launch_latent<1, false>(p, grid, s) : launch_latent<1, true>(p, grid, s);
-    else e = p.out_bf16 ? launch_latent<2, false>(p, grid, s) : launch_latent<2, true>(p, grid, s);
+    const cudaError_t e = p.out_bf16 ? launch_latent<false>(p, sm_count, s) : launch_latent<true>(p, sm_count, s);
     return e != cudaSuccess ? e : launch_join<kLatDims>(p, sm_count, s);
   }
-  if (head_dim == 64) return launch_d<64>(p, grid, sm_count, s);
-  if (head_dim == 128) return launch_d<128>(p, grid, sm_count, s);
-  return launch_d<256>(p, grid, sm_count, s);
+  if (head_dim == 64) return launch_d<64>(p, sm_count, s);
+  if (head_dim == 128) return launch_d<128>(p, sm_count, s);
+  return launch_d<256>(p, sm_count, s);
 }
 
 }  // namespace pic

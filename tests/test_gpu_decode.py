@@ -655,7 +655,7 @@ def test_decode_loop_mla():
     c.w.zero_()
     hq, budget, scale = 16, 36, 0.03
     q_out, out = torch.empty(2, hq, 576, dtype=torch.bfloat16, device=DEV), torch.empty(2, hq, 512, device=DEV)
-    lse, lens, ws = torch.empty(2, hq, device=DEV), c.d_lens, _ws(1 << 24)
+    lse, lens, ws = torch.empty(2, hq, device=DEV), c.d_lens, _ws(1 << 25)
     kept = torch.empty(1, 2, 1, budget, dtype=torch.int32, device=DEV)
     for step in range(8):
         slot = lens.clone()
@@ -734,7 +734,7 @@ def test_offsets_beyond_32_bits():
     small.k[0, :5], small.v[0, :5], small.w[0, :5] = k[0, pages], v[0, pages], w[0, pages]
     for c, kk, vv, ww, tt in ((ctx, k, v, w, tables), (small.ctx, small.k, small.v, small.w, small.d_tables)):
         q_out, lens = torch.empty_like(new[0]), _i32([72])
-        ws = _ws(1 << 24)
+        ws = _ws(1 << 25)
         pic.pic_write_tokens(c, _i32([70, 71]), new[1], new[2], _i32([0, 0]), _i32([70, 71]), tt, kk[0], vv[0], q=new[0], q_out=q_out,
                              weights=ww[0], workspace=ws)
         out = torch.empty(1, 16, d, device=DEV)
