@@ -458,8 +458,9 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
 // the latent also the value), so a CTA takes a range for 16 heads (more heads:
 // more passes, whose CTAs read the same rows side by side) and works on it
 // together, 32 slots of one request a step, the next step's rows on their way:
-//   * warp w scores slots 8 (w % 4) .. + 7 over half of the 576 dims (18 k-steps);
-//     the halves meet in shared memory;
+//   * warp w scores slots 16 (w / 4) .. + 15 over a quarter of the 576 dims (9
+//     k-steps, whose query fragments stay in registers); the quarters meet in
+//     shared memory;
 //   * sixteen threads a head add them, keep the running maximum and sum (two
 //     scores each) and leave P in bf16 parts, as above;
 //   * warp w adds latent dims 64 w .. 64 w + 63 of every head.
@@ -470,14 +471,16 @@ constexpr int kLatRowBytes = kLatRow * 2, kLatChunks = kLatRowBytes / 16;
 constexpr int kLatHeads = 16;
 constexpr int kLatSlots = 32, kLatTiles = kLatSlots / TT;   // of a step
 constexpr int kLatThreads = 256;
+constexpr int kLatSteps = kLatRow / 16 / 4;   // k-steps of a quarter
 constexpr int kLatCtas = 2;              // per SM
 constexpr int kLatPitch = 80;            // bytes of a head's P: eight rows in distinct banks
 constexpr int kLatScorePitch = kLatSlots + 4;
+constexpr int kLatRowPitch = kLatRowBytes + 16;   // an odd number of 16-byte chunks: eight rows in distinct banks
 struct LatSmem {
-  alignas(128) uint8_t kv[2][kLatSlots][kLatRowBytes];
-  alignas(128) uint8_t q[kLatHeads][kLatRowBytes];
+  alignas(128) uint8_t kv[2][kLatSlots][kLatRowPitch];
+  alignas(16) uint8_t q[kLatHeads][kLatRowPitch];
   alignas(16) uint8_t p[3][kLatHeads][kLatPitch];
-  alignas(16) float s[2][kLatHeads][kLatScorePitch];   // scores over either half of the dims
+  alignas(16) float s[4][kLatHeads][kLatScorePitch];   // scores over each quarter of the dims
   float alpha[kLatHeads];
   uint8_t live[2][kLatSlots];
 };
@@ -492,180 +495,171 @@ __global__ void __launch_bounds__(kLatThreads, kLatCtas) k_paged_latent(const __
   const int a_row = (lane & 7) + ((lane >> 3) & 1) * 8;    // ldmatrix row of a 16-row operand
   const int my_row = tid >> 3;                             // eight threads copy a row
   const int my_head = tid >> 4, my_slot = (tid & 15) * 2;  // sixteen threads weigh a head's slots
+  const int quarter = warp & 3, col = (warp >> 2) * 16;    // this warp's part of the scores
+  // ldmatrix addresses (stage 0): queries; keys as two n-tiles of 8 slots, both
+  // halves of a k-step; the latent dims of this warp as value rows; P
+  const uint32_t q_at = smem_u32(S.q[a_row]) + (2 * quarter * kLatSteps + (lane >> 4)) * 16;
+  const uint32_t k_at = smem_u32(S.kv[0][col + (lane & 7) + (lane >> 4) * 8]) + (2 * quarter * kLatSteps + ((lane >> 3) & 1)) * 16;
+  const uint32_t v_at = smem_u32(S.kv[0][a_row]) + (warp * NT + (lane >> 4)) * 16;
+  const uint32_t p_at = smem_u32(S.p[0][a_row]) + (lane >> 4) * 16;
+  const uint32_t row_at = smem_u32(S.kv[0][my_row]) + (tid & 7) * 16;
+  constexpr uint32_t kStage = kLatSlots * kLatRowPitch;
   const TileList L = tile_list(P, lane, blockIdx.x == 0 && warp == 0);
   uint64_t policy;   // rows that no other CTA reads pass through L2 first-out
   if (P.passes == 1) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
 
   for (int64_t w = blockIdx.x; w < static_cast<int64_t>(P.parts) * P.v_heads; w += gridDim.x) {
-    const int vh = static_cast<int>(w % P.v_heads);
+    const int hq0 = static_cast<int>(w % P.v_heads) * kLatHeads, n_heads = min(kLatHeads, P.q_heads - hq0);
     const int64_t part = w / P.v_heads;
     if (part >= L.parts || L.total == 0) continue;
-    const int64_t t_begin = L.begin(part), t_end = L.begin(part + 1);
-    if (t_begin >= t_end) continue;
-    const int hq0 = vh * kLatHeads, n_heads = min(kLatHeads, P.q_heads - hq0);
-
-    // tiles of the step that begins at a place: up to two, of one request
-    auto step_tiles = [&](const Place& x, int64_t t) {
-      return static_cast<int>(min(min(static_cast<int64_t>(kLatTiles), t_end - t), static_cast<int64_t>((x.len + TT - 1) / TT - x.tile)));
-    };
-    auto skip = [&](Place& x, int n) {
-      for (int i = 0; i < n; ++i) advance(P, x);
-    };
-    // this thread's cache row of a step, -1 past its end or for a bad block
-    auto row_of = [&](const Place& x, int n) -> int {
-      const int slot = x.tile * TT + my_row;
-      if (my_row >= n * TT || slot >= x.len) return -1;
-      const int64_t row = paged_row(P.paged, x.req, slot);
-      if (row < 0 && (tid & 7) == 0) raise_block(P.status, x.req, slot);
-      return static_cast<int>(row);
-    };
-    auto issue = [&](int stage, int row) {
-      const uint8_t* src = P.k_cache + static_cast<int64_t>(row < 0 ? 0 : row) * kLatRowBytes;
-      const uint32_t dst = smem_u32(S.kv[stage][my_row]);
+    const int64_t t_end = L.begin(part + 1);
+    int64_t t = L.begin(part), first;
+    int r;
+    find_tile(P, t, lane, r, first);
+    // the range, request by request: slots [s0, s_end) of request r, in tiles up to slot s_pad
+    for (; t < t_end; ++r) {
+      const int len = legal_len(__ldg(P.lens + r), P.max_len, P.status, false);
+      const int n_tiles = (len + TT - 1) / TT;
+      const int s0 = static_cast<int>(t - first) * TT;
+      const int s_pad = static_cast<int>(min(t_end - first, static_cast<int64_t>(n_tiles))) * TT, s_end = min(s_pad, len);
+      if (s0 < s_pad) {
+        const int64_t score_at = t * TT - s0;   // a slot's place in the scores
+        // The block of this thread's slot, looked up a step ahead and looked at
+        // only when its row is asked for: a warp stops where it touches a load
+        // that has not arrived.
+        const int32_t* table = P.paged.tables + static_cast<int64_t>(r) * P.paged.max_blocks;
+        auto block_at = [&](int step_slot) {
+          const int slot = step_slot + my_row;
+          return slot < s_end ? __ldg(table + block_of(P.paged, slot)) : -1;
+        };
+        auto issue = [&](int stage, int step_slot, int block) {
+          const int slot = step_slot + my_row;
+          const bool live = block >= 0 && block < P.paged.num_cache_blocks;
+          if (!live && slot < s_end && (tid & 7) == 0) raise_block(P.status, r, slot);
+          const int64_t row = live ? static_cast<int64_t>(block) * P.paged.block_size + (slot - block_of(P.paged, slot) * P.paged.block_size) : 0;
+          const uint8_t* src = P.k_cache + row * kLatRowBytes + (tid & 7) * 16;
 #pragma unroll
-      for (int i = 0; i < kLatChunks / 8; ++i) {
-        const int c = (tid & 7) + 8 * i;
-        cp_async16_zfill(dst + ((c ^ (my_row & 7)) << 4), src + c * 16, row >= 0, policy);
-      }
-      if ((tid & 7) == 0) S.live[stage][my_row] = row >= 0;
-    };
-
-    Place load;
-    find_tile(P, t_begin, lane, load.req, load.first);
-    load.tile = static_cast<int>(t_begin - load.first);
-    load.len = load.req < P.n_req ? legal_len(__ldg(P.lens + load.req), P.max_len, P.status, false) : 0;
-    Place cur = load;
-    int64_t t_load = t_begin;
-    int next_row = -1;   // of the step to be loaded next, looked up a step ahead
-    auto look_up = [&]() {
-      if (t_load >= t_end) return;
-      next_row = row_of(load, step_tiles(load, t_load));
-    };
-    auto load_step = [&](int stage) {
-      if (t_load < t_end) {
-        const int n = step_tiles(load, t_load);
-        issue(stage, next_row);
-        t_load += n;
-        skip(load, n);
-      }
-      cp_commit();
-    };
-    __syncthreads();   // the previous range is done with shared memory
-    look_up();
-    load_step(0);
-    look_up();
-    float o[NT][4], m_run = -FLT_MAX, l_run = 0.0f;
-    bool opened = false;
-    int stage = 0;
-    for (int64_t t = t_begin; t < t_end; stage ^= 1) {
-      const int n = step_tiles(cur, t);
-      if (!opened) {
-        opened = true;
-        m_run = -FLT_MAX;
-        l_run = 0.0f;
+          for (int i = 0; i < kLatChunks / 8; ++i)
+            cp_async16_zfill(row_at + stage * kStage + i * 128, src + i * 128, live, policy);
+          if ((tid & 7) == 0) S.live[stage][my_row] = live;
+        };
+        __syncthreads();   // shared memory is free
+        issue(0, s0, block_at(s0));
+        cp_commit();
+        int next_block = block_at(s0 + kLatSlots);
+        const uint8_t* qp = P.q + r * P.q_stride + static_cast<int64_t>(hq0) * kLatRowBytes;
+        for (int i = tid; i < kLatHeads * kLatChunks; i += kLatThreads) {
+          const int h = i / kLatChunks, c = i - h * kLatChunks;
+          *reinterpret_cast<uint4*>(S.q[h] + c * 16) =
+              h < n_heads ? __ldg(reinterpret_cast<const uint4*>(qp + i * 16)) : make_uint4(0, 0, 0, 0);
+        }
+        __syncthreads();
+        uint32_t qf[kLatSteps][4];
+#pragma unroll
+        for (int kk = 0; kk < kLatSteps; ++kk) ldsm4(q_at + kk * 32, qf[kk]);
+        float o[NT][4], m_run = -FLT_MAX, l_run = 0.0f;
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-        const uint8_t* qp = P.q + cur.req * P.q_stride + static_cast<int64_t>(hq0) * kLatRowBytes;
-        for (int i = tid; i < kLatHeads * kLatChunks; i += kLatThreads) {
-          const int h = i / kLatChunks, c = i % kLatChunks;
-          const uint4 v = h < n_heads ? __ldg(reinterpret_cast<const uint4*>(qp + i * 16)) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(S.q[h] + ((c ^ (h & 7)) << 4)) = v;
-        }
-      }
-      cp_wait<0>();
-      __syncthreads();   // the step's rows and the queries are in place; the other stage is free
-      load_step(stage ^ 1);
-      look_up();
-      // ---- scores of 8 slots over half of the dims (even and odd k-steps apart: shorter chains)
-      {
-        float s[2][4] = {};
-        const int half = warp >> 2, col = (warp & 3) * 8, k_row = col + (lane & 7);
-        const uint32_t ka = smem_u32(S.kv[stage][k_row]), qa = smem_u32(S.q[a_row]);
+        int stage = 0;
+        for (int slot0 = s0; slot0 < s_pad; slot0 += kLatSlots, stage ^= 1) {
+          cp_wait<0>();
+          __syncthreads();   // the step's rows are in place; the other stage is free
+          if (slot0 + kLatSlots < s_pad) issue(stage ^ 1, slot0 + kLatSlots, next_block);
+          cp_commit();
+          next_block = block_at(slot0 + 2 * kLatSlots);
+          const uint32_t off = stage * kStage;
+          // ---- scores of 16 slots over a quarter of the dims
+          {
+            float s0a[4] = {}, s1a[4] = {};
 #pragma unroll
-        for (int i = 0; i < kLatChunks / 8; ++i) {
-          const int c = half * (kLatChunks / 2) + 4 * i;
-          uint32_t b[4];
-          ldsm4(ka + (((c + (lane >> 3)) ^ (k_row & 7)) << 4), b);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t a[4];
-            ldsm4(qa + (((c + 2 * x + (lane >> 4)) ^ (a_row & 7)) << 4), a);
-            mma(s[x], a, b[2 * x], b[2 * x + 1]);
+            for (int kk = 0; kk < kLatSteps; ++kk) {
+              uint32_t b[4];
+              ldsm4(k_at + off + kk * 32, b);
+              mma(s0a, qf[kk], b[0], b[1]);
+              mma(s1a, qf[kk], b[2], b[3]);
+            }
+            float* sp = &S.s[quarter][g][col + 2 * tq];
+            *reinterpret_cast<float2*>(sp) = make_float2(s0a[0], s0a[1]);
+            *reinterpret_cast<float2*>(sp + 8) = make_float2(s1a[0], s1a[1]);
+            sp += 8 * kLatScorePitch;
+            *reinterpret_cast<float2*>(sp) = make_float2(s0a[2], s0a[3]);
+            *reinterpret_cast<float2*>(sp + 8) = make_float2(s1a[2], s1a[3]);
           }
-        }
-        *reinterpret_cast<float2*>(&S.s[half][g][col + 2 * tq]) = make_float2(s[0][0] + s[1][0], s[0][1] + s[1][1]);
-        *reinterpret_cast<float2*>(&S.s[half][g + 8][col + 2 * tq]) = make_float2(s[0][2] + s[1][2], s[0][3] + s[1][3]);
-      }
-      __syncthreads();   // both halves of the scores
-      {
-        const float2 x = *reinterpret_cast<const float2*>(&S.s[0][my_head][my_slot]);
-        const float2 y = *reinterpret_cast<const float2*>(&S.s[1][my_head][my_slot]);
-        const float s0 = S.live[stage][my_slot] != 0 ? (x.x + y.x) * P.scale_log2 : -INFINITY;
-        const float s1 = S.live[stage][my_slot + 1] != 0 ? (x.y + y.y) * P.scale_log2 : -INFINITY;
-        if (P.scores != nullptr && my_head < n_heads && my_slot < n * TT)
-          *reinterpret_cast<float2*>(P.scores + (hq0 + my_head) * P.score_stride + t * TT + my_slot) = make_float2(s0, s1);
-        float m = fmaxf(s0, s1);
+          __syncthreads();   // all quarters of the scores
+          {
+            float2 x = *reinterpret_cast<const float2*>(&S.s[0][my_head][my_slot]);
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-        m = fmaxf(m_run, m);
-        const float alpha = ex2(m_run - m);
-        m_run = m;
-        float p0 = ex2(s0 - m), p1 = ex2(s1 - m);
-        l_run = l_run * alpha + (p0 + p1);
+            for (int i = 1; i < 4; ++i) {
+              const float2 y = *reinterpret_cast<const float2*>(&S.s[i][my_head][my_slot]);
+              x.x += y.x;
+              x.y += y.y;
+            }
+            const uint16_t live = *reinterpret_cast<const uint16_t*>(&S.live[stage][my_slot]);
+            const float sc0 = (live & 0xff) != 0 ? x.x * P.scale_log2 : -INFINITY;
+            const float sc1 = (live >> 8) != 0 ? x.y * P.scale_log2 : -INFINITY;
+            if (P.scores != nullptr && my_head < n_heads && slot0 + my_slot < s_pad)
+              *reinterpret_cast<float2*>(P.scores + (hq0 + my_head) * P.score_stride + score_at + slot0 + my_slot) =
+                  make_float2(sc0, sc1);
+            float m = fmaxf(sc0, sc1);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) *reinterpret_cast<uint32_t*>(&S.p[i][my_head][my_slot * 2]) = take_bf16(p0, p1);
-        if ((tid & 15) == 0) S.alpha[my_head] = alpha;
-      }
-      __syncthreads();   // P is in place
-      // ---- this warp's 64 latent dims of every head
-      {
-        const float a0 = S.alpha[g], a1 = S.alpha[g + 8];
-        if (!__all_sync(kFull, a0 == 1.0f && a1 == 1.0f)) {
+            for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+            m = fmaxf(m_run, m);
+            const float alpha = ex2(m_run - m);
+            m_run = m;
+            float p0 = ex2(sc0 - m), p1 = ex2(sc1 - m);
+            l_run = l_run * alpha + (p0 + p1);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            o[j][0] *= a0;
-            o[j][1] *= a0;
-            o[j][2] *= a1;
-            o[j][3] *= a1;
+            for (int i = 0; i < NP; ++i) *reinterpret_cast<uint32_t*>(&S.p[i][my_head][my_slot * 2]) = take_bf16(p0, p1);
+            if ((tid & 15) == 0) S.alpha[my_head] = alpha;
           }
-        }
-        uint32_t a[NP][kLatTiles][4];
+          __syncthreads();   // P is in place
+          // ---- this warp's 64 latent dims of every head
+          const float a0 = S.alpha[g], a1 = S.alpha[g + 8];
+          if (!__all_sync(kFull, a0 == 1.0f && a1 == 1.0f)) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
+            for (int j = 0; j < NT; ++j) {
+              o[j][0] *= a0;
+              o[j][1] *= a0;
+              o[j][2] *= a1;
+              o[j][3] *= a1;
+            }
+          }
+          uint32_t a[NP][kLatTiles][4];
 #pragma unroll
-          for (int ks = 0; ks < kLatTiles; ++ks) ldsm4(smem_u32(S.p[i][a_row]) + (2 * ks + (lane >> 4)) * 16, a[i][ks]);
+          for (int i = 0; i < NP; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-          float y0[4] = {}, y1[4] = {};
+            for (int ks = 0; ks < kLatTiles; ++ks) ldsm4(p_at + i * kLatHeads * kLatPitch + ks * 32, a[i][ks]);
 #pragma unroll
-          for (int ks = 0; ks < kLatTiles; ++ks) {
-            uint32_t b[4];
-            ldsm4_t(smem_u32(S.kv[stage][ks * 16 + a_row]) + (((warp * NT + j + (lane >> 4)) ^ (a_row & 7)) << 4), b);
+          for (int j = 0; j < NT; j += 2) {
+            float y0[4] = {}, y1[4] = {};
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-              if (F32) {   // added outside the tensor cores, as above
-                mma(y0, a[i][ks], b[0], b[1]);
-                mma(y1, a[i][ks], b[2], b[3]);
-              } else {
-                mma(o[j], a[i][ks], b[0], b[1]);
-                mma(o[j + 1], a[i][ks], b[2], b[3]);
+            for (int ks = 0; ks < kLatTiles; ++ks) {
+              uint32_t b[4];
+              ldsm4_t(v_at + off + ks * 16 * kLatRowPitch + j * 16, b);
+#pragma unroll
+              for (int i = 0; i < NP; ++i) {
+                if (F32) {   // added outside the tensor cores, as above
+                  mma(y0, a[i][ks], b[0], b[1]);
+                  mma(y1, a[i][ks], b[2], b[3]);
+                } else {
+                  mma(o[j], a[i][ks], b[0], b[1]);
+                  mma(o[j + 1], a[i][ks], b[2], b[3]);
+                }
+              }
+            }
+            if (F32) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                o[j][e] += y0[e];
+                o[j + 1][e] += y1[e];
               }
             }
           }
-          if (F32) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              o[j][e] += y0[e];
-              o[j + 1][e] += y1[e];
-            }
-          }
         }
-      }
-      t += n;
-      if (cur.tile + n == (cur.len + TT - 1) / TT || t == t_end) {
+        cp_wait<0>();
         // ---- the record of this range and request
-        const int64_t rec = (part + cur.req) * P.q_heads + hq0;
+        const int64_t rec = (part + r) * P.q_heads + hq0;
         float l = l_run;
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
@@ -678,11 +672,10 @@ __global__ void __launch_bounds__(kLatThreads, kLatCtas) k_paged_latent(const __
 #pragma unroll
           for (int j = 0; j < NT; ++j) *reinterpret_cast<float2*>(acc + 8 * j) = make_float2(o[j][2 * hf], o[j][2 * hf + 1]);
         }
-        opened = false;
       }
-      if (t < t_end) skip(cur, n);
+      first += n_tiles;
+      t = max(t, min(first, t_end));
     }
-    cp_wait<0>();
   }
 }
 
