@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kLatThreads, kLatCtas) k_paged_latent(const __
 // ---- the join
 constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
-constexpr int kFinishWeightCtas = 3;   // per SM, of 4 that fit: the joins run beside them
+constexpr int kFinishWeightCtas = 2;   // per SM, of 3 that fit: the joins run beside them
 
 
 
@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_paged_lse(const __grid_const
 // records into the outputs: one CTA per (request, query head) while these are
 // few (few requests, each cut into many ranges), else one warp for each.
 template <int D>
-__global__ void __launch_bounds__(kFinishThreads, 4) k_paged_finish(const __grid_constant__ PagedParams P) {
+__global__ void __launch_bounds__(kFinishThreads, 3) k_paged_finish(const __grid_constant__ PagedParams P) {
   __shared__ float s_part[kFinishWarps * D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const TileList L = tile_list(P, lane, false);
