@@ -116,7 +116,7 @@ struct EvictUnit {           // per (layer, request, weight head), in the worksp
 };
 constexpr int kEvictMoveThreads = 256;   // threads and
 constexpr int kEvictMoveCtas = 4;        // CTAs per SM of the move
-constexpr int kEvictCachedSlots = 48000; // weights the selection keeps in shared memory
+constexpr int kEvictCachedSlots = 46000; // weights the selection keeps in shared memory
 struct EvictParams {
   PagedView paged;
   FreqTable freq;

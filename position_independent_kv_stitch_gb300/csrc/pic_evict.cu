@@ -15,8 +15,10 @@
 // read once into shared memory (those past its size are read again from L2).
 // The weight of the last token that fits is found by radix selection over the
 // weights' bits, from the top: 11, 11 and 10 bits, counted in shared memory.
-// Then every warp takes a contiguous run of slots, counts what it keeps, and
-// after a scan over the warps writes its kept slots, in order and without
+// Every warp takes a contiguous run of slots; a sweep counts what surely stays in
+// each and lists the members of the border's top digit, and the lower digits
+// are looked for in that list (in all weights, should it overflow).  After a
+// scan over the warps a last sweep writes the kept slots, in order and without
 // further barriers; the weights follow from shared memory.
 //
 // k_evict_move, in place: one CTA per slice (32 bytes to whole rows) of the
@@ -42,6 +44,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kSelList = 2048;
 
 // Order of the weights as unsigned integers: NaN lowest, -0 equal to 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -78,6 +81,8 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   __shared__ int s_warp[kSelWarps];
   __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
   __shared__ int s_pick[2];
+  __shared__ uint2 s_list[kSelList];   // keys of the border's top digit, and the warps whose runs they lie in
+  __shared__ int s_listed;
   __shared__ int s_first_moved;
   static_assert(kSelWarps == 32, "one lane per warp in the scans");
   const int64_t unit = blockIdx.x;
@@ -134,91 +139,155 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   const int want = P.budget - P.n_first - P.n_recent;  // how many of them stay; fewer than hi - lo
   for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
   if (tid == 0) s_first_moved = P.budget;
-  // four neighbouring slots lie together when blocks hold a multiple of four
+  if (tid == 0) s_listed = 0;
+  __syncthreads();
+  // The weights come in, and the top digits of the candidates' keys are counted.
+  // Four neighbouring slots lie together when blocks hold a multiple of four.
   const bool vec = (bs & 3) == 0 && ((reinterpret_cast<uintptr_t>(P.weights) | static_cast<uintptr_t>(P.weights_ls)) & 15) == 0;
+  auto count_top = [&](int s, float w) {
+    if (s >= lo && s < hi) atomicAdd(&s_hist[weight_key(w) >> 21], 1);
+  };
   if (vec) {
 #pragma unroll 4
-    for (int s = 4 * tid; s < cached; s += 4 * kSelThreads)
-      *reinterpret_cast<float4*>(s_w + s) = __ldcg(reinterpret_cast<const float4*>(at(s)));
+    for (int s = 4 * tid; s < cached; s += 4 * kSelThreads) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(at(s)));
+      *reinterpret_cast<float4*>(s_w + s) = x;
+      const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (s + i < len) count_top(s + i, v[i]);
+    }
   } else {
 #pragma unroll 4
-    for (int s = tid; s < cached; s += kSelThreads) s_w[s] = __ldcg(at(s));
+    for (int s = tid; s < cached; s += kSelThreads) {
+      const float x = __ldcg(at(s));
+      s_w[s] = x;
+      count_top(s, x);
+    }
   }
+  for (int s = cached + tid; s < len; s += kSelThreads) count_top(s, __ldcg(at(s)));
   __syncthreads();
 
-  uint32_t border = 0xffffffffu;  // key of the last candidate that stays
-  int ties = 0;                   // candidates of that key that stay
-  if (want > 0) {
-    uint32_t prefix = 0, mask = 0;
-    int left = want;
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const uint32_t digits = pass == 2 ? 1023u : 2047u;
-#pragma unroll 2
-      for (int s = 4 * tid; s < hi; s += 4 * kSelThreads) {
-        float v[4];
-        load4(s, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t k = weight_key(v[i]);
-          if (s + i >= lo && s + i < hi && (k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & digits], 1);
-        }
-      }
-      __syncthreads();
-      // two digits a thread, from the top: the one in which the count reaches `left`
-      const int d = kBins - 1 - 2 * tid;
-      const int n0 = s_hist[d], n1 = s_hist[d - 1];
-      const int above = block_scan(n0 + n1, s_warp);
-      if (above < left && above + n0 + n1 >= left) {
-        const bool first = above + n0 >= left;
-        s_pick[0] = first ? d : d - 1;
-        s_pick[1] = left - above - (first ? 0 : n0);
-      }
-      s_hist[d] = s_hist[d - 1] = 0;
-      __syncthreads();
-      prefix |= static_cast<uint32_t>(s_pick[0]) << shift;
-      mask |= digits << shift;
-      left = s_pick[1];
+  // The digit in which the count from the top reaches `left`, two digits a
+  // thread; what is left within it.  The counts return to 0.
+  auto pick = [&](int& left) -> uint32_t {
+    const int d = kBins - 1 - 2 * tid;
+    const int n0 = s_hist[d], n1 = s_hist[d - 1];
+    const int above = block_scan(n0 + n1, s_warp);
+    if (above < left && above + n0 + n1 >= left) {
+      const bool first = above + n0 >= left;
+      s_pick[0] = first ? d : d - 1;
+      s_pick[1] = left - above - (first ? 0 : n0);
     }
-    border = prefix;
-    ties = left;
-  }
-
+    s_hist[d] = s_hist[d - 1] = 0;
+    __syncthreads();
+    left = s_pick[1];
+    return static_cast<uint32_t>(s_pick[0]);
+  };
   // Every warp's run of slots, 128 a step, four neighbours a lane.  Per lane:
-  // bits of the slots that stay whatever happens, and of those with the
-  // border's key.
+  // bits of the slots that stay whatever happens (their key is above `above`),
+  // and of those whose key, shifted, is `border`.
   const int run = (len + kSelThreads * 4 - 1) / (kSelThreads * 4) * 128;
   const int begin = min(len, warp * run), end = min(len, begin + run);
-  auto classify = [&](int s, uint32_t& stays, uint32_t& tie) {
+  auto classify = [&](int s, int shift, uint32_t border, uint32_t& stays, uint32_t& tie, uint32_t (&key)[4]) {
     float v[4];
     load4(s, v);
     stays = tie = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool cand = s + i >= lo && s + i < hi;
-      const uint32_t k = weight_key(v[i]);
-      if (s + i < end && (!cand || (want > 0 && k > border))) stays |= 1u << i;
-      if (cand && want > 0 && s + i < end && k == border) tie |= 1u << i;
+      key[i] = weight_key(v[i]);
+      if (s + i < end && (!cand || (want > 0 && (key[i] >> shift) > border))) stays |= 1u << i;
+      if (cand && want > 0 && s + i < end && (key[i] >> shift) == border) tie |= 1u << i;
     }
   };
-  int mine = 0, mine_ties = 0;
-  for (int s0 = begin; s0 < end; s0 += 128) {
-    uint32_t stays, tie;
-    classify(s0 + 4 * lane, stays, tie);
-    mine += __popc(stays);
-    mine_ties += __popc(tie);
-  }
+  // Counts this warp's run against a border digit; lists the members of the digit when asked to.
+  auto count_run = [&](int shift, uint32_t border, bool list) {
+    int mine = 0, mine_ties = 0;
+    for (int s0 = begin; s0 < end; s0 += 128) {
+      uint32_t stays, tie, key[4];
+      classify(s0 + 4 * lane, shift, border, stays, tie, key);
+      mine += __popc(stays);
+      mine_ties += __popc(tie);
+      if (list && __any_sync(kFull, tie != 0)) {
+        int n = __popc(tie), incl = n;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mine += __shfl_xor_sync(kFull, mine, o);
-    mine_ties += __shfl_xor_sync(kFull, mine_ties, o);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(kFull, incl, o);
+          if (lane >= o) incl += up;
+        }
+        int base = 0;
+        if (lane == 31) base = atomicAdd(&s_listed, incl);
+        base = __shfl_sync(kFull, base, 31) + incl - n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((tie >> i) & 1u) {
+            if (base < kSelList) s_list[base] = make_uint2(key[i], warp);
+            ++base;
+          }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mine += __shfl_xor_sync(kFull, mine, o);
+      mine_ties += __shfl_xor_sync(kFull, mine_ties, o);
+    }
+    if (lane == 0) {
+      s_gt[warp] = mine;
+      s_eq[warp] = mine_ties;
+    }
+    __syncthreads();
+  };
+
+  uint32_t border = 0xffffffffu;  // key of the last candidate that stays
+  int ties = 0;                   // candidates of that key that stay
+  if (want == 0) {
+    count_run(0, border, false);
+  } else {
+    int left = want;
+    border = pick(left);
+    count_run(21, border, true);
+    const bool listed = s_listed <= kSelList;
+    // the two lower digits: over the list, or over everything when too many share the top digit
+#pragma unroll
+    for (int pass = 1; pass < 3; ++pass) {
+      const int shift = pass == 1 ? 10 : 0, bits = pass == 1 ? 11 : 10;
+      const uint32_t digits = (1u << bits) - 1u;
+      if (listed) {
+        for (int i = tid; i < s_listed; i += kSelThreads) {
+          const uint32_t k = s_list[i].x;
+          if ((k >> (shift + bits)) == border) atomicAdd(&s_hist[(k >> shift) & digits], 1);
+        }
+      } else {
+#pragma unroll 2
+        for (int s = 4 * tid; s < hi; s += 4 * kSelThreads) {
+          float v[4];
+          load4(s, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t k = weight_key(v[i]);
+            if (s + i >= lo && s + i < hi && (k >> (shift + bits)) == border) atomicAdd(&s_hist[(k >> shift) & digits], 1);
+          }
+        }
+      }
+      __syncthreads();
+      const uint32_t digit = pick(left);
+      border = border << bits | digit;
+    }
+    ties = left;
+    if (listed) {   // the counts of the runs, from the list's members
+      if (lane == 0) s_eq[warp] = 0;
+      __syncthreads();
+      for (int i = tid; i < s_listed; i += kSelThreads) {
+        const uint2 x = s_list[i];
+        if (x.x > border) atomicAdd(&s_gt[x.y], 1);
+        else if (x.x == border) atomicAdd(&s_eq[x.y], 1);
+      }
+      __syncthreads();
+    } else {
+      count_run(0, border, false);
+    }
   }
-  if (lane == 0) {
-    s_gt[warp] = mine;
-    s_eq[warp] = mine_ties;
-  }
-  __syncthreads();
   int gt_before = lane < warp ? s_gt[lane] : 0, eq_before = lane < warp ? s_eq[lane] : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -228,8 +297,8 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   int first_out = len;   // first evicted slot of this lane's
   for (int s0 = begin; s0 < end; s0 += 128) {
     const int s = s0 + 4 * lane;
-    uint32_t stays, tie;
-    classify(s, stays, tie);
+    uint32_t stays, tie, key[4];
+    classify(s, 0, border, stays, tie, key);
     const int n = __popc(stays) | __popc(tie) << 16;   // 128 of each at most
     int incl = n;
 #pragma unroll

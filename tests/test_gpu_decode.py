@@ -795,3 +795,27 @@ def test_attend_paged_more_heads_than_warps():
     c = Cache(heads=1500, d=64, bs=4, lens=[9, 3], seed=30)
     _attend(c, 1500, torch.bfloat16)
     c.close()
+
+
+@pytest.mark.parametrize("n", [4099, 60000])
+@pytest.mark.parametrize("kind", ["one digit", "many ties", "spread"])
+def test_evict_selection_borders(kind, n):
+    """Long sequences (beyond the weights that shared memory holds, too) whose
+    weights share their top bits, or are equal, or are spread: the kept list."""
+    c = Cache(heads=1, d=64, bs=16, lens=[n], seed=n)
+    if kind == "one digit":
+        c.w = 1.0 + c.w / 1024.0
+    elif kind == "many ties":
+        c.w = torch.floor(c.w * 3.0) * 0.5
+    kept, new = torch.empty(1, 1, 1, n // 3, dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    w = c.w.clone()
+    ws = _ws(pic.pic_evict_workspace_bytes(c.ctx, 1, 1, 1))
+    pic.pic_evict_tokens(c.ctx, c.k, c.v, c.w, c.d_tables, c.d_lens, n // 3, kept, new, n_first=3, n_recent=50, workspace=ws)
+    assert _status(c, ws) == 0
+    s = np.arange(n)
+    by_slot = w[0, torch.from_numpy(c.tables[0][s // 16]).long().to(DEV), 0, torch.from_numpy(s % 16).to(DEV)].double().cpu().numpy()
+    want = oracle.kept_slots(by_slot, n, n // 3, 3, 50)
+    assert kept[0, 0, 0].tolist() == want
+    got = c.w[0, torch.from_numpy(c.tables[0][np.arange(n // 3) // 16]).long().to(DEV), 0, torch.from_numpy(np.arange(n // 3) % 16).to(DEV)]
+    np.testing.assert_array_equal(got.double().cpu().numpy(), by_slot[want])
+    c.close()
