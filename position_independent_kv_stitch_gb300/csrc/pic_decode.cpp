@@ -40,8 +40,13 @@ pic_status check_device(pic_ctx* ctx, const Buffer* bufs, int n, int* sm_count) 
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaGetDevice");
-  e = cudaDeviceGetAttribute(sm_count, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaDeviceGetAttribute");
+  static std::atomic<int> sms_of[32];   // 0: not asked for yet
+  *sm_count = dev < 32 ? sms_of[dev].load(std::memory_order_relaxed) : 0;
+  if (*sm_count == 0) {
+    e = cudaDeviceGetAttribute(sm_count, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaDeviceGetAttribute");
+    if (dev < 32) sms_of[dev].store(*sm_count, std::memory_order_relaxed);
+  }
   for (int i = 0; i < n; ++i) {
     if (!bufs[i].ptr) continue;
     cudaPointerAttributes a;

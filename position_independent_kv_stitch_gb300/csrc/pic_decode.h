@@ -8,6 +8,7 @@
 // nothing and can be captured into a graph.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -17,6 +18,20 @@
 #include "pic_internal.h"
 
 namespace pic {
+
+// Gives a kernel its dynamic shared memory, once per device (the limit of a
+// kernel never changes, so threads may race here).
+template <typename Kern>
+inline cudaError_t allow_smem(Kern kern, int bytes, std::atomic<uint32_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint32_t bit = dev < 32 ? 1u << dev : 0u;
+  if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // What the entries need of a context (defined in pic_host.cpp).
 struct CtxView {

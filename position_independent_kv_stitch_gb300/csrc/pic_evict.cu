@@ -503,15 +503,14 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __
 cudaError_t launch_evict(const EvictParams& p, int pairing, cudaStream_t s) {
   const int64_t lr = static_cast<int64_t>(p.layers) * p.n_req;
   const int smem = p.sel_cap * static_cast<int>(sizeof(float));
-  // the same limit whatever this call needs: another thread may be between the two calls
-  cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kEvictCachedSlots * static_cast<int>(sizeof(float)));
+  static std::atomic<uint32_t> select_done{0}, move_done[2] = {{0}, {0}};
+  cudaError_t e = allow_smem(k_evict_select, kEvictCachedSlots * static_cast<int>(sizeof(float)), select_done);
   if (e != cudaSuccess) return e;
   k_evict_select<<<static_cast<unsigned>(lr * p.weight_heads), kSelThreads, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   auto move = pairing == kNeox ? k_evict_move<kNeox> : k_evict_move<kInterleaved>;
-  e = cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+  e = allow_smem(move, kMoveSmem, move_done[pairing == kNeox ? 0 : 1]);
   if (e != cudaSuccess) return e;
   move<<<static_cast<unsigned>(lr * p.tensors * p.pieces * p.slices), kMoveThreads, kMoveSmem, s>>>(p);
   return cudaGetLastError();

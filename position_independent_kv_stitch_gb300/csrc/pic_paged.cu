@@ -941,7 +941,8 @@ cudaError_t launch_attend_d(const PagedParams& p, int grid, cudaStream_t s) {
   auto kern = k_paged_attend<D, WIDE, F32>;
   constexpr int smem = paged_warps(D) * (paged_stages(D) * stage_bytes(D) + score_stage(D, WIDE) * static_cast<int>(sizeof(float)));
   static_assert(smem <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint32_t> done{0};
+  const cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   kern<<<grid, 32 * paged_warps(D), smem, s>>>(p);
   return cudaGetLastError();
@@ -952,7 +953,8 @@ cudaError_t launch_latent(const PagedParams& p, int sm_count, cudaStream_t s) {
   auto kern = k_paged_latent<F32>;
   constexpr int smem = sizeof(LatSmem);
   static_assert(kLatCtas * (smem + 1024) <= 228 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint32_t> done{0};
+  const cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
   kern<<<sm_count * kLatCtas, kLatThreads, smem, s>>>(p);
   return cudaGetLastError();
