@@ -777,6 +777,8 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
         _int32_error("positions")
     q_heads = q_stride = out_stride = k_stride = v_stride = n_tables = max_blocks = heads = 0
     if k is not None:
+        if k_cache is None or req is None or slot is None or block_tables is None:
+            raise ValueError("keys need a cache, block tables, req and slot")
         cache, want = _check_caches(ctx, k_cache, v_cache, 4)
         rows = (n, cache[2], cache[3])
         k_stride = _token_rows(k, "k", rows)
@@ -791,6 +793,8 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
     else:
         want = _geometry.get(ctx.value)
     if q is not None:
+        if q_out is None:
+            raise ValueError("queries need a q_out (it may be q)")
         shape = q.shape
         q_stride, out_stride = _token_rows(q, "q", shape), _token_rows(q_out, "q_out", shape)
         tokens, q_heads, d = shape

@@ -163,6 +163,10 @@ def test_binding_refuses_host_tensors_and_foreign_shapes(gqa):
     with pytest.raises(ValueError):
         pic.pic_write_tokens(gqa, i, cache[0, :2], cache[0, :2], i, i, i.view(1, 2), cache, cache)
     with pytest.raises(ValueError):
+        pic.pic_write_tokens(gqa, i, None, None, None, None, None, None, None, q=cache[0, :2])
+    with pytest.raises(ValueError):
+        pic.pic_write_tokens(gqa, i, cache[0, :2], cache[0, :2], None, i, i.view(1, 2), cache, cache)
+    with pytest.raises(ValueError):
         pic.pic_attend_paged(gqa, cache[0, :2], 1.0, cache, cache, i.view(2, 1), i, 16, torch.empty(2, 2, 128))
     with pytest.raises(ValueError):
         pic.pic_evict_tokens(gqa, cache[None], cache[None], torch.zeros(1, 64, 2, 16), i.view(2, 1), i, 4, i, i)
