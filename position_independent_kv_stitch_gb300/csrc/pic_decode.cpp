@@ -94,7 +94,7 @@ int32_t cache_rows(const CtxView& c) {
 bool weight_heads_ok(const CtxView& c, int32_t n) { return n == 1 || n == c.model->num_kv_heads; }
 
 struct PagedLayout {
-  size_t lse2, rec_ml, rec_acc, scores, total;
+  size_t first, lse2, rec_ml, rec_acc, scores, total;
   int64_t score_stride;
 };
 int32_t paged_passes(int32_t group) { return (group + 15) / 16; }
@@ -109,7 +109,8 @@ PagedLayout paged_layout(const CtxView& c, int64_t n_req, int64_t q_heads, int64
   const int64_t recs = paged_max_parts(c.model->num_kv_heads * paged_passes(group), c.model->head_dim) + n_req;
   PagedLayout L{};
   L.score_stride = weights ? n_req * ((max_len + kPagedTile - 1) / kPagedTile) * kPagedTile : 0;
-  L.lse2 = sizeof(WsHeader);
+  L.first = sizeof(WsHeader);
+  L.lse2 = align_up(L.first + (n_req + 1) * sizeof(int64_t), kWsAlign);
   L.rec_ml = align_up(L.lse2 + (weights ? n_req * q_heads * sizeof(float) : 0), kWsAlign);
   L.rec_acc = align_up(L.rec_ml + recs * q_heads * sizeof(float2), kWsAlign);
   L.scores = align_up(L.rec_acc + recs * q_heads * d * sizeof(float), kWsAlign);
@@ -335,6 +336,7 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
   p.k_cache = static_cast<const uint8_t*>(k_cache);
   p.v_cache = static_cast<const uint8_t*>(v_cache);
   p.row_bytes = static_cast<int32_t>(row_bytes);
+  p.first = n_req > kPagedWalkRequests ? reinterpret_cast<int64_t*>(ws + L.first) : nullptr;
   p.rec_acc = reinterpret_cast<float*>(ws + L.rec_acc);
   p.rec_ml = reinterpret_cast<float2*>(ws + L.rec_ml);
   p.lse2 = d_weights ? reinterpret_cast<float*>(ws + L.lse2) : nullptr;

@@ -123,6 +123,9 @@ struct TileList {
 __device__ __forceinline__ int tiles_of(const PagedParams& P, int r, bool raise) {
   return (legal_len(__ldg(P.lens + r), P.max_len, P.status, raise) + TT - 1) / TT;
 }
+__device__ __forceinline__ int64_t parts_of(const PagedParams& P, int64_t total) {   // at least a tile each
+  return total < P.parts ? (total < 1 ? 1 : total) : P.parts;
+}
 __device__ __forceinline__ TileList tile_list(const PagedParams& P, int lane, bool raise) {
   int64_t n = 0;
   for (int r = lane; r < P.n_req; r += 32) n += tiles_of(P, r, raise);
@@ -130,7 +133,7 @@ __device__ __forceinline__ TileList tile_list(const PagedParams& P, int lane, bo
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
   TileList L;
   L.total = n;
-  L.parts = n < P.parts ? (n < 1 ? 1 : n) : P.parts;   // at least a tile each
+  L.parts = parts_of(P, n);
   return L;
 }
 // The request that holds tile t of the list, and its first tile (warp-wide;
@@ -165,6 +168,22 @@ __device__ __forceinline__ int64_t first_tile(const PagedParams& P, int r, int l
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
   return n;
+}
+// Leaves the first tiles of the requests that begin in tiles [t, t_end) of the
+// list to the joins (warp-wide; t is in request r, whose first tile is `base`).
+__device__ __forceinline__ void leave_first_tiles(const PagedParams& P, int64_t t, int64_t t_end, int r, int64_t base, int lane) {
+  for (; r < P.n_req && base < t_end; r += 32) {
+    const int64_t n = r + lane < P.n_req ? tiles_of(P, r + lane, false) : 0;
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const int64_t at = base + incl - n;
+    if (n > 0 && at >= t && at < t_end) P.first[r + lane] = at;
+    base += __shfl_sync(kFull, incl, 31);
+  }
 }
 
 // A place in the list: tile `tile` of request `req`.
@@ -211,6 +230,7 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
 
   Place load;
   find_tile(P, t_begin, lane, load.req, load.first);
+  if (P.first != nullptr && vh == 0) leave_first_tiles(P, t_begin, t_end, load.req, load.first, lane);
   load.tile = static_cast<int>(t_begin - load.first);
   load.len = load.req < P.n_req ? legal_len(__ldg(P.lens + load.req), P.max_len, P.status, false) : 0;
   Place cur = load;
@@ -450,6 +470,7 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(128) uint8_t smem[];
   const TileList L = tile_list(P, threadIdx.x & 31, blockIdx.x == 0 && threadIdx.x < 32);
+  if (P.first != nullptr && blockIdx.x == 0 && threadIdx.x == 0) P.first[P.n_req] = L.total;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * paged_warps(D);
   // one range each; more only when there are more heads than warps
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * paged_warps(D) + (threadIdx.x >> 5);
@@ -516,6 +537,7 @@ __global__ void __launch_bounds__(kLatThreads, kLatCtas) k_paged_latent(const __
   uint64_t policy;   // rows that no other CTA reads pass through L2 first-out
   if (P.passes == 1) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+  if (P.first != nullptr && blockIdx.x == 0 && tid == 0) P.first[P.n_req] = L.total;
 
   for (int64_t w = blockIdx.x; w < static_cast<int64_t>(P.parts) * P.v_heads; w += gridDim.x) {
     const int hq0 = static_cast<int>(w % P.v_heads) * kLatHeads, n_heads = min(kLatHeads, P.q_heads - hq0);
@@ -525,6 +547,7 @@ __global__ void __launch_bounds__(kLatThreads, kLatCtas) k_paged_latent(const __
     int64_t t = L.begin(part), first;
     int r;
     find_tile(P, t, lane, r, first);
+    if (P.first != nullptr && hq0 == 0 && warp == 0) leave_first_tiles(P, t, t_end, r, first, lane);
     // the range, request by request: slots [s0, s_end) of request r, in tiles up to slot s_pad
     for (; t < t_end; ++r) {
       const int len = legal_len(__ldg(P.lens + r), P.max_len, P.status, false);
@@ -710,6 +733,25 @@ __device__ __forceinline__ Records records_of(const TileList& L, int64_t first, 
   }
   return x;
 }
+// The same for a join, which waits here for the kernel that wrote the records.
+// Of few requests the lengths are walked again, before the wait; of many
+// (P.first set) the attention kernel has left what is needed in the workspace:
+// the total, and the first tile of each request that has any.
+__device__ __forceinline__ Records join_records(const PagedParams& P, const TileList& walked, int r, int lane) {
+  const int n = tiles_of(P, r, false);
+  Records x;
+  if (P.first == nullptr) {
+    x = records_of(walked, first_tile(P, r, lane), n, r);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    TileList L;
+    L.total = __ldcg(P.first + P.n_req);
+    L.parts = parts_of(P, L.total);
+    x = records_of(L, n > 0 ? __ldcg(P.first + r) : 0, n, r);
+  }
+  return x;
+}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
@@ -770,10 +812,9 @@ __device__ __forceinline__ void store_out(const PagedParams& P, int64_t at, floa
 // out and lse of (request, query head) `task`, by one warp or (ALL) by all
 // warps of the CTA, which share the records.
 template <int D, bool ALL>
-__device__ __forceinline__ void join_output(const PagedParams& P, const TileList& L, int64_t first, int r, int hq, float* part) {
+__device__ __forceinline__ void join_output(const PagedParams& P, const Records& x, int r, int hq, float* part) {
   constexpr int V = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Records x = records_of(L, first, tiles_of(P, r, false), r);
   float M, sum, acc[V];
   join_stats(P, x, hq, lane, M, sum);
   join_values<D>(P, x, hq, lane, M, ALL ? warp : 0, ALL ? kFinishWarps : 1, acc);
@@ -803,20 +844,35 @@ __device__ __forceinline__ void join_output(const PagedParams& P, const TileList
 // are read again from its last tile and dropped) and 16 tiles are in flight.
 constexpr int kWeightBatch = 2;
 
-__device__ __forceinline__ void add_weights(const PagedParams& P, const TileList& L, int64_t w, int64_t all) {
-  const int lane = threadIdx.x & 31, c = (lane & 3) * 4;
+// Tiles [begin, end) of the list for weight head wh; the first tile of request
+// r, which holds `begin`, is `first`.
+struct WeightRun {
+  int64_t begin, end, first;
+  int r, wh;
+};
+// Part w / weight_heads of `all` equal parts (warp-wide; from the lengths alone).
+__device__ __forceinline__ WeightRun weight_run(const PagedParams& P, const TileList& L, int64_t w, int64_t all, int lane) {
+  WeightRun x;
   const int64_t part = w / P.weight_heads;
-  const int wh = static_cast<int>(w % P.weight_heads);
-  const int64_t t_begin = L.total * part / all, t_end = L.total * (part + 1) / all;
-  if (t_begin >= t_end) return;
+  x.wh = static_cast<int>(w - part * P.weight_heads);
+  x.begin = L.total * part / all;
+  x.end = L.total * (part + 1) / all;
+  x.r = 0;
+  x.first = 0;
+  if (x.begin < x.end) find_tile(P, x.begin, lane, x.r, x.first);
+  return x;
+}
+__device__ __forceinline__ void add_weights(const PagedParams& P, const WeightRun& run) {
+  const int lane = threadIdx.x & 31, c = (lane & 3) * 4;
+  const int wh = run.wh;
+  const int64_t t_begin = run.begin, t_end = run.end;
   const int heads = P.q_heads / P.weight_heads;   // query heads of a weight head
   const int hq0 = wh * heads;
   const int bs = P.paged.block_size;
   const bool vec = (bs & 3) == 0 && (reinterpret_cast<uintptr_t>(P.weights) & 15) == 0;  // a lane's slots lie together
   const float* scores = P.scores + hq0 * P.score_stride + c;
-  int r;
-  int64_t first;
-  find_tile(P, t_begin, lane, r, first);
+  int r = run.r;
+  int64_t first = run.first;
   for (int64_t t0 = t_begin; t0 < t_end;) {
     const int len = legal_len(__ldg(P.lens + r), P.max_len, P.status, false);
     const int n = (len + TT - 1) / TT;
@@ -894,10 +950,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_paged_lse(const __grid_const
   const int64_t task = static_cast<int64_t>(blockIdx.x) * kFinishWarps + (threadIdx.x >> 5);
   const int r = static_cast<int>(task / P.q_heads), hq = static_cast<int>(task % P.q_heads);
   if (r >= P.n_req) return;
-  const TileList L = tile_list(P, lane, false);
-  const Records x = records_of(L, first_tile(P, r, lane), tiles_of(P, r, false), r);
-  // everything so far came from the caller's lengths; the records are the previous kernel's
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Records x = join_records(P, P.first == nullptr ? tile_list(P, lane, false) : TileList{0, 1}, r, lane);
   float M, sum;
   join_stats(P, x, hq, lane, M, sum);
   if (lane == 0) P.lse2[task] = sum == 0.0f ? INFINITY : M + log2f(sum);   // nothing attended: every share 0
@@ -910,24 +963,25 @@ template <int D>
 __global__ void __launch_bounds__(kFinishThreads, 3) k_paged_finish(const __grid_constant__ PagedParams P) {
   __shared__ float s_part[kFinishWarps * D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const TileList L = tile_list(P, lane, false);
   const int block = static_cast<int>(blockIdx.x) - P.weight_ctas;
+  const TileList L = P.first == nullptr || block < 0 ? tile_list(P, lane, false) : TileList{0, 1};
   if (block >= 0) {
     const bool all = P.join_wide != 0;
     const int64_t task = all ? block : static_cast<int64_t>(block) * kFinishWarps + warp;
     const int r = static_cast<int>(task / P.q_heads), hq = static_cast<int>(task % P.q_heads);
     if (r >= P.n_req) return;
-    const int64_t first = first_tile(P, r, lane);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (all) join_output<D, true>(P, L, first, r, hq, s_part);
-    else join_output<D, false>(P, L, first, r, hq, s_part);
+    const Records x = join_records(P, L, r, lane);
+    if (all) join_output<D, true>(P, x, r, hq, s_part);
+    else join_output<D, false>(P, x, r, hq, s_part);
     return;
   }
   const int64_t warps = static_cast<int64_t>(P.weight_ctas) * kFinishWarps;
   const int64_t all = warps / P.weight_heads > 0 ? warps / P.weight_heads : 1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * kFinishWarps + warp; w < all * P.weight_heads; w += warps)
-    add_weights(P, L, w, all);
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * kFinishWarps + warp; w < all * P.weight_heads; w += warps) {
+    const WeightRun run = weight_run(P, L, w, all, lane);
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the scores and log-sum-exps; at once when it has been passed
+    add_weights(P, run);
+  }
 }
 
 // A kernel launched as a programmatic dependent of the one before it.

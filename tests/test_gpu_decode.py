@@ -325,6 +325,31 @@ def test_attend_paged_many_short_requests():
     c.close()
 
 
+def test_attend_paged_thousands_of_requests():
+    """3,000 requests, half of them empty: what a join needs of the list does not depend on how many came before."""
+    rng = np.random.default_rng(5)
+    lens = [int(x) * (i % 2) for i, x in enumerate(rng.integers(1, 50, size=3000))]
+    c = Cache(heads=1, d=64, bs=16, lens=lens, seed=2)
+    q = c.normal(3000, 4, 64)
+    out, lse, ws = torch.empty(3000, 4, 64, device=DEV), torch.empty(3000, 4, device=DEV), \
+        _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, 3000, 4, 64, True))
+    w = c.w[0].clone()
+    pic.pic_attend_paged(c.ctx, q, 0.125, c.k[0], c.v[0], c.d_tables, c.d_lens, 64, out, lse=lse, weights=w, workspace=ws)
+    assert _status(c, ws) == 0
+    k = c.k[0][c.d_tables.long()].reshape(3000, 64, 64).double()
+    v = c.v[0][c.d_tables.long()].reshape(3000, 64, 64).double()
+    x = torch.einsum("rhd,rtd->rht", q.double(), k) * 0.125
+    x.masked_fill_(torch.arange(64, device=DEV)[None, None] >= c.d_lens[:, None, None], float("-inf"))
+    p = torch.softmax(x, -1).nan_to_num(0.0)
+    torch.testing.assert_close(out.double(), torch.einsum("rht,rtd->rhd", p, v), rtol=1e-4, atol=1e-5)
+    live = c.d_lens > 0
+    torch.testing.assert_close(lse[live].double(), torch.logsumexp(x, -1)[live], rtol=1e-5, atol=1e-5)
+    want = c.w[0].double()
+    want[c.d_tables.long().flatten(), 0] += p.sum(1).reshape(-1, 16)
+    torch.testing.assert_close(w.double(), want, rtol=1e-4, atol=1e-5)
+    c.close()
+
+
 def test_attend_paged_ignores_what_lies_behind_the_end():
     lens = [33, 0, 50, 16]
     c = Cache(heads=2, d=128, bs=16, lens=lens, room=16, seed=2)
