@@ -350,6 +350,31 @@ def test_attend_paged_thousands_of_requests():
     c.close()
 
 
+@pytest.mark.parametrize("n", [1, 17, 1000, 40000, 100000, 200000])
+def test_attend_paged_weights_of_many_heads(n):
+    """32 query heads a weight: a warp's runs from one tile (its lanes share the heads) to more than it holds at once."""
+    c = Cache(heads=2, d=64, bs=16, lens=[n], seed=n)
+    q = c.normal(1, 64, 64)
+    out, ws = torch.empty(1, 64, 64, device=DEV), _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, 1, 64, n, True))
+    w = c.w[0].clone()
+    pic.pic_attend_paged(c.ctx, q, 0.125, c.k[0], c.v[0], c.d_tables, c.d_lens, n, out, weights=w, workspace=ws)
+    assert _status(c, ws) == 0
+    rows = c.k[0][c.d_tables[0].long()].reshape(-1, 2, 64)[:n].double()
+    heads = q[0].double().reshape(2, 32, 64)
+    p = torch.softmax(torch.einsum("ghd,tgd->ght", heads, rows) * 0.125, -1).sum(1)
+    s_err = 0.125 * torch.einsum("ghd,tgd->ght", heads.abs(), rows.abs()).max().item() * (64 + 8) * 2.0 ** -23
+    rel = 2 * s_err + 2.0 ** -20 + n * 2.0 ** -23
+    slots = torch.arange(n, device=DEV)
+    at = c.d_tables[0].long()[slots // 16]
+    got = w[at, :, slots % 16].T.double()
+    old = c.w[0][at, :, slots % 16].T.double()
+    assert bool(((got - old - p).abs() <= rel * p + 2.0 ** -22 * (old + p)).all())
+    want = c.w[0].clone()
+    want[at, :, slots % 16] = w[at, :, slots % 16]
+    assert torch.equal(w, want)      # no other place
+    c.close()
+
+
 def test_attend_paged_ignores_what_lies_behind_the_end():
     lens = [33, 0, 50, 16]
     c = Cache(heads=2, d=128, bs=16, lens=lens, room=16, seed=2)
