@@ -40,6 +40,7 @@ PIC_F32, PIC_BF16 = 0, 1
 PIC_MAX_AXES = 4
 PIC_STATUS_BYTES = 256
 PIC_LATENT_DIM = 512
+_LATENT_ROW = PIC_LATENT_DIM + 64   # an MLA cache row
 PIC_VARIANT_REGISTERS, PIC_VARIANT_BULK_PIPELINE = 0, 1
 PIC_VARIANT_TENSOR_CORE_TMEM, PIC_VARIANT_WARP_MMA = 2, 3
 PIC_SEG_COPY_POOL, PIC_SEG_COPY_BLOCKS, PIC_SEG_MAPPED = 0, 1, 2
@@ -843,7 +844,7 @@ def pic_attend_paged(ctx, q, softmax_scale, k_cache, v_cache, block_tables, seq_
     max_blocks = _table_shape(block_tables, n_req)[1]
     cache, _ = _check_caches(ctx, k_cache, v_cache, 4)
     out_type = PIC_F32 if out.dtype is _F32 else PIC_BF16
-    want = shape if v_cache is not None else (n_req, hq, PIC_LATENT_DIM)
+    want = shape if d != _LATENT_ROW else (n_req, hq, PIC_LATENT_DIM)
     if d != cache[3] or out.shape != want or not out.is_contiguous() or (out_type == PIC_BF16 and out.dtype is not _BF16):
         raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape (MLA: the latent's), heads of the "
                          "cache's head_dim")

@@ -180,3 +180,15 @@ def test_binding_refuses_host_tensors_and_foreign_shapes(gqa):
         pic._weight_heads(torch.zeros(64, 2, 8), cache.shape)
     with pytest.raises(ValueError):
         pic._token_rows(cache.transpose(1, 2)[0], "q", (2, 16, 128))
+
+
+def test_binding_wants_latent_outputs_whether_or_not_a_value_cache_is_given(mla):
+    import torch
+    i = torch.zeros(2, dtype=torch.int32)
+    cache = torch.zeros(64, 16, 1, 576, dtype=torch.bfloat16)
+    q = torch.zeros(2, 4, 576, dtype=torch.bfloat16)
+    for v in (None, cache):
+        with pytest.raises(ValueError, match="out must be"):
+            pic.pic_attend_paged(mla, q, 1.0, cache, v, i.view(2, 1), i, 16, torch.empty(2, 4, 576))
+        with pytest.raises(ValueError, match="CUDA device"):
+            pic.pic_attend_paged(mla, q, 1.0, cache, v, i.view(2, 1), i, 16, torch.empty(2, 4, 512))
