@@ -70,9 +70,10 @@ PagedView paged_view(const CtxView& c, const int32_t* d_tables, int32_t n_tables
   v.max_blocks = max_blocks;
   v.num_cache_blocks = c.num_cache_blocks;
   v.block_size = c.model->block_size;
-  v.block_shift = -1;
-  for (int s = 0; s <= 8; ++s)
-    if (v.block_size == 1 << s) v.block_shift = s;
+  int32_t log2 = 0;
+  while (int64_t{1} << log2 < v.block_size) ++log2;
+  v.block_shift = 31 + log2;
+  v.block_mul = static_cast<uint32_t>(((uint64_t{1} << v.block_shift) + v.block_size - 1) / v.block_size);
   return v;
 }
 

@@ -50,7 +50,11 @@ struct PagedView {
   int32_t max_blocks;
   int32_t num_cache_blocks;
   int32_t block_size;
-  int32_t block_shift;       // log2(block_size), or -1 when it is no power of two
+  // slot / block_size = slot * block_mul >> block_shift for every 0 <= slot < 2^31:
+  // with 2^(L - 1) < block_size <= 2^L, block_mul = ceil(2^(31 + L) / block_size) is
+  // less than 1 too large, which adds less than slot / 2^(31 + L) < 1 / block_size
+  uint32_t block_mul;
+  int32_t block_shift;       // 31 + L
 };
 
 struct FreqTable {

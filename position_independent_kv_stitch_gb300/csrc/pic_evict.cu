@@ -12,7 +12,8 @@
 // free.)
 //
 // k_evict_select, one CTA per (layer, request, weight head).  The weights are
-// read once into shared memory (those past its size are read again from L2).
+// read once and kept in shared memory as sort keys (those past its size are read
+// again from L2); a NaN comes back from its key as the plain NaN, -0 as 0.
 // The weight of the last token that fits is found by radix selection over the
 // weights' bits, from the top: 11, 11 and 10 bits, counted in shared memory.
 // Every warp takes a contiguous run of slots; a sweep counts what surely stays in
@@ -33,10 +34,10 @@
 // tokens before the first evicted one are in place already.
 //
 // Measured on fresh weights (GB300): 32k -> 4k tokens in 16 layers of 8 heads, each
-// head its own set, keys turned, 143 us (selection 35; 559 MB, 3.9 TB/s); 12 of
-// 16 sequences cut to 2k in 8 layers, heads together, 266 us (1.61 GB, 6.1 TB/s);
-// MLA, 16k -> 8k, 3 sequences, 16 layers 225 us (910 MB, 4.1 TB/s); 2,064 -> 2,048
-// in one layer 12 us.
+// head its own set, keys turned, 129 us (selection 28; 559 MB, 4.3 TB/s); 12 of
+// 16 sequences cut to 2k in 8 layers, heads together, 257 us (1.61 GB, 6.3 TB/s);
+// MLA, 16k -> 8k, 3 sequences, 16 layers 205 us (910 MB, 4.4 TB/s); 2,064 -> 2,048
+// in one layer 11.5 us.
 #include "pic_decode.h"
 #include "pic_device.cuh"
 #include "pic_paged.cuh"
@@ -58,6 +59,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   const uint32_t u = __float_as_uint(w + 0.0f);
   return (u & 0x80000000u) != 0 ? ~u : (u | 0x80000000u);
 }
+// The weight of a key (a NaN for any NaN, 0 for -0).
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  return __uint_as_float(k == 0u ? 0x7fffffffu : ((k & 0x80000000u) != 0 ? k ^ 0x80000000u : ~k));
+}
+// Bits i of 4 with i < n.
+__device__ __forceinline__ uint32_t below(int n) { return 0xfu >> (4 - min(max(n, 0), 4)); }
 
 // Sum of v over the CTA's threads before this one.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
@@ -82,7 +89,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
 }
 
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictParams P) {
-  extern __shared__ __align__(16) float s_w[];   // weights of the first slots
+  extern __shared__ __align__(16) uint32_t s_key[];   // keys of the first slots' weights
   __shared__ int s_hist[kBins];
   __shared__ int s_warp[kSelWarps];
   __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
@@ -130,15 +137,15 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     const int64_t block = __ldg(P.paged.tables + static_cast<int64_t>(r) * P.paged.max_blocks + b);
     return wl + (block * P.weight_heads + wh) * bs + (slot - b * bs);
   };
-  const int cached = min(len, P.sel_cap);   // slots whose weights are in shared memory
-  // the weights of slots s .. s + 3 (0 past the end; s a multiple of 4)
-  auto load4 = [&](int s, float (&v)[4]) {
+  const int cached = min(len, P.sel_cap);   // slots whose keys are in shared memory
+  // the keys of slots s .. s + 3 (0 past the end; s a multiple of 4)
+  auto load4 = [&](int s, uint32_t (&k)[4]) {
     if (s + 4 <= cached) {
-      const float4 x = *reinterpret_cast<const float4*>(s_w + s);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      const uint4 x = *reinterpret_cast<const uint4*>(s_key + s);
+      k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = s + i >= len ? 0.0f : (s + i < cached ? s_w[s + i] : __ldcg(at(s + i)));
+      for (int i = 0; i < 4; ++i) k[i] = s + i >= len ? 0u : (s + i < cached ? s_key[s + i] : weight_key(__ldcg(at(s + i))));
     }
   };
   const int lo = P.n_first, hi = len - P.n_recent;     // candidates: slots [lo, hi)
@@ -150,28 +157,30 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   // The weights come in, and the top digits of the candidates' keys are counted.
   // Four neighbouring slots lie together when blocks hold a multiple of four.
   const bool vec = (bs & 3) == 0 && ((reinterpret_cast<uintptr_t>(P.weights) | static_cast<uintptr_t>(P.weights_ls)) & 15) == 0;
-  auto count_top = [&](int s, float w) {
-    if (s >= lo && s < hi) atomicAdd(&s_hist[weight_key(w) >> 21], 1);
-  };
+  auto count_top = [&](uint32_t key) { atomicAdd(&s_hist[key >> 21], 1); };
+  auto is_cand = [&](int s) { return s >= lo && s < hi; };
   if (vec) {
 #pragma unroll 4
     for (int s = 4 * tid; s < cached; s += 4 * kSelThreads) {
       const float4 x = __ldcg(reinterpret_cast<const float4*>(at(s)));
-      *reinterpret_cast<float4*>(s_w + s) = x;
-      const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (s + i < len) count_top(s + i, v[i]);
+      const uint4 k = make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
+      *reinterpret_cast<uint4*>(s_key + s) = k;
+      const uint32_t cand = below(hi - s) & ~below(lo - s);
+      if (cand & 1u) count_top(k.x);
+      if (cand & 2u) count_top(k.y);
+      if (cand & 4u) count_top(k.z);
+      if (cand & 8u) count_top(k.w);
     }
   } else {
 #pragma unroll 4
     for (int s = tid; s < cached; s += kSelThreads) {
-      const float x = __ldcg(at(s));
-      s_w[s] = x;
-      count_top(s, x);
+      const uint32_t k = weight_key(__ldcg(at(s)));
+      s_key[s] = k;
+      if (is_cand(s)) count_top(k);
     }
   }
-  for (int s = cached + tid; s < len; s += kSelThreads) count_top(s, __ldcg(at(s)));
+  for (int s = cached + tid; s < len; s += kSelThreads)
+    if (is_cand(s)) count_top(weight_key(__ldcg(at(s))));
   __syncthreads();
 
   // The digit in which the count from the top reaches `left`, two digits a
@@ -191,45 +200,37 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     return static_cast<uint32_t>(s_pick[0]);
   };
   // Every warp's run of slots, 128 a step, four neighbours a lane.  Per lane:
-  // bits of the slots that stay whatever happens (their key is above `above`),
-  // and of those whose key, shifted, is `border`.
+  // bits of the slots that stay whatever happens (their key is above `top`, or
+  // they are no candidates), and of those whose key lies in [base, top].
   const int run = (len + kSelThreads * 4 - 1) / (kSelThreads * 4) * 128;
   const int begin = min(len, warp * run), end = min(len, begin + run);
-  auto classify = [&](int s, int shift, uint32_t border, uint32_t& stays, uint32_t& tie, uint32_t (&key)[4]) {
-    float v[4];
-    load4(s, v);
-    stays = tie = 0;
+  auto classify = [&](int s, uint32_t base, uint32_t top, uint32_t& stays, uint32_t& tie, uint32_t (&key)[4]) {
+    load4(s, key);
+    uint32_t ge = 0, gt = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool cand = s + i >= lo && s + i < hi;
-      key[i] = weight_key(v[i]);
-      if (s + i < end && (!cand || (want > 0 && (key[i] >> shift) > border))) stays |= 1u << i;
-      if (cand && want > 0 && s + i < end && (key[i] >> shift) == border) tie |= 1u << i;
+      ge |= key[i] >= base ? 1u << i : 0u;
+      gt |= key[i] > top ? 1u << i : 0u;
     }
+    const uint32_t in = below(end - s), cand = below(hi - s) & ~below(lo - s);
+    stays = in & (gt | ~cand);
+    tie = in & cand & ge & ~gt;
   };
-  // Counts this warp's run against a border digit; lists the members of the digit when asked to.
-  auto count_run = [&](int shift, uint32_t border, bool list) {
+  // Counts this warp's run against a border, the keys [base, top]; lists its members when asked to.
+  auto count_run = [&](uint32_t base, uint32_t top, bool list) {
     int mine = 0, mine_ties = 0;
     for (int s0 = begin; s0 < end; s0 += 128) {
       uint32_t stays, tie, key[4];
-      classify(s0 + 4 * lane, shift, border, stays, tie, key);
+      classify(s0 + 4 * lane, base, top, stays, tie, key);
       mine += __popc(stays);
       mine_ties += __popc(tie);
-      if (list && __any_sync(kFull, tie != 0)) {
-        int n = __popc(tie), incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(kFull, incl, o);
-          if (lane >= o) incl += up;
-        }
-        int base = 0;
-        if (lane == 31) base = atomicAdd(&s_listed, incl);
-        base = __shfl_sync(kFull, base, 31) + incl - n;
+      if (list && tie != 0) {   // few: in no order
+        int at_list = atomicAdd(&s_listed, __popc(tie));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if ((tie >> i) & 1u) {
-            if (base < kSelList) s_list[base] = make_uint2(key[i], warp);
-            ++base;
+            if (at_list < kSelList) s_list[at_list] = make_uint2(key[i], warp);
+            ++at_list;
           }
       }
     }
@@ -248,11 +249,11 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   uint32_t border = 0xffffffffu;  // key of the last candidate that stays
   int ties = 0;                   // candidates of that key that stay
   if (want == 0) {
-    count_run(0, border, false);
+    count_run(border, border, false);   // no key is that high
   } else {
     int left = want;
     border = pick(left);
-    count_run(21, border, true);
+    count_run(border << 21, border << 21 | 0x1fffffu, true);
     const bool listed = s_listed <= kSelList;
     // the two lower digits: over the list, or over everything when too many share the top digit
 #pragma unroll
@@ -267,13 +268,11 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
       } else {
 #pragma unroll 2
         for (int s = 4 * tid; s < hi; s += 4 * kSelThreads) {
-          float v[4];
-          load4(s, v);
+          uint32_t k[4];
+          load4(s, k);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t k = weight_key(v[i]);
-            if (s + i >= lo && s + i < hi && (k >> (shift + bits)) == border) atomicAdd(&s_hist[(k >> shift) & digits], 1);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (is_cand(s + i) && (k[i] >> (shift + bits)) == border) atomicAdd(&s_hist[(k[i] >> shift) & digits], 1);
         }
       }
       __syncthreads();
@@ -291,7 +290,7 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
       }
       __syncthreads();
     } else {
-      count_run(0, border, false);
+      count_run(border, border, false);
     }
   }
   int gt_before = lane < warp ? s_gt[lane] : 0, eq_before = lane < warp ? s_eq[lane] : 0;
@@ -304,7 +303,7 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   for (int s0 = begin; s0 < end; s0 += 128) {
     const int s = s0 + 4 * lane;
     uint32_t stays, tie, key[4];
-    classify(s, 0, border, stays, tie, key);
+    classify(s, border, border, stays, tie, key);
     const int n = __popc(stays) | __popc(tie) << 16;   // 128 of each at most
     int incl = n;
 #pragma unroll
@@ -313,14 +312,18 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
       if (lane >= o) incl += up;
     }
     int gt = gt_before + ((incl - n) & 0xffff), eq = eq_before + ((incl - n) >> 16);
+    uint32_t out = below(end - s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool is_tie = (tie >> i) & 1u, keep = ((stays >> i) & 1u) || (is_tie && eq < ties);
-      if (keep) kept[gt + min(eq, ties)] = s + i;
-      else if (s + i < end) first_out = min(first_out, s + i);
+      if (keep) {
+        kept[gt + min(eq, ties)] = s + i;
+        out ^= 1u << i;
+      }
       gt += (stays >> i) & 1u;
       eq += is_tie ? 1 : 0;
     }
+    if (out != 0) first_out = min(first_out, s + __ffs(out) - 1);
     const int all = __shfl_sync(kFull, incl, 31);
     gt_before += all & 0xffff;
     eq_before += all >> 16;
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   if (tid == 0) P.units[unit] = EvictUnit{P.budget, s_first_moved};
   // the weights move with their tokens (kept[] is this CTA's own, written above)
   if (cached == len) {
-    for (int j = s_first_moved + tid; j < P.budget; j += kSelThreads) *at(j) = s_w[kept[j]];
+    for (int j = s_first_moved + tid; j < P.budget; j += kSelThreads) *at(j) = key_weight(s_key[kept[j]]);
     return;
   }
   // some are only in memory: in order, a tile's reads before its writes
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     float x = 0.0f;
     if (j < P.budget) {
       const int s = kept[j];
-      x = s < cached ? s_w[s] : __ldcg(at(s));
+      x = s < cached ? key_weight(s_key[s]) : __ldcg(at(s));
     }
     // the barrier takes a value made of the loaded one: every load has arrived
     __syncthreads_or(__float_as_uint(x) == 0x7fc12345u);

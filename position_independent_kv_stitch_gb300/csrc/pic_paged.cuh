@@ -8,8 +8,10 @@
 namespace pic {
 namespace dev {
 
+// Block of a slot (0 <= slot): slot / block_size, as a product (no branch and no
+// division, whatever the size).
 __device__ __forceinline__ int block_of(const PagedView& v, int slot) {
-  return v.block_shift >= 0 ? slot >> v.block_shift : slot / v.block_size;
+  return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(slot)) * v.block_mul >> v.block_shift);
 }
 
 // Absolute cache row of a request's slot, -1 when the table has no such slot

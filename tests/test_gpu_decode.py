@@ -212,6 +212,23 @@ def test_write_bad_tokens_are_left_out():
     c.close()
 
 
+@pytest.mark.parametrize("bs", [1, 2, 3, 7, 48, 100, 255, 256])
+def test_write_tokens_finds_every_slot(bs):
+    """Slots over a long table, the first and last of its blocks among them: the values lie where slot // bs says."""
+    c = Cache(heads=1, d=64, bs=bs, lens=[70000], seed=bs)
+    per = c.tables.shape[1]
+    edge = np.arange(0, per, max(1, per // 300))
+    slots = np.unique(np.concatenate([edge * bs, edge * bs + bs - 1, c.rng.integers(0, per * bs, size=400)]))
+    n = len(slots)
+    k, v = c.normal(n, 1, 64), c.normal(n, 1, 64)
+    ws = _ws()
+    pic.pic_write_tokens(c.ctx, _i32(np.zeros(n)), k, v, _i32(np.zeros(n)), _i32(slots), c.d_tables, c.k[0], c.v[0], workspace=ws)
+    assert _status(c, ws) == 0
+    rows = torch.from_numpy(c.tables[0][slots // bs].astype(np.int64)).to(DEV), torch.from_numpy(slots % bs).to(DEV)
+    assert torch.equal(c.v[0][rows], v) and torch.equal(c.k[0][rows], k)
+    c.close()
+
+
 # ---------------------------------------------------------------- attention
 
 def _attend(c, hq, out_type, layer=0, weights=True, scale=None, q=None):
