@@ -33,8 +33,8 @@
 //
 // Measured (GB300, 32 query over 8 KV heads of 128 dims, blocks of 16): 64
 // requests of 16,384 slots, fp32 out, 622-640 us (6.7-6.9 TB/s of rows); 64 of
-// 1-8,192 with weights 232 us (without 197: 6.6 TB/s); one of 131,071 with
-// weights 107 us (without 91: 5.9 TB/s); one of 777 9.4 us.
+// 1-8,192 with weights 230 us (without 196: 6.6 TB/s); one of 131,071 with
+// weights 106 us (without 91: 5.9 TB/s); one of 777 8.5-9.5 us; 3,000 of 64 77 us.
 #include <cfloat>
 
 #include <cuda_bf16.h>
@@ -493,8 +493,8 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
 // The three barriers of a step come between these; two CTAs per SM cover each
 // other's.  Bound: the chain of a step's three parts and mma.sync's rate (400
 // products a step of 37 KB; 600 TFLOP/s measured for mma.sync alone).
-// Measured: 64 requests of 8,192 slots, 16 heads, 135-141 us (4.3-4.5 TB/s of
-// rows); 128 heads 950 us (150 TFLOP/s of useful products).
+// Measured: 64 requests of 8,192 slots, 16 heads, 132 us (4.6 TB/s of
+// rows); 128 heads 927 us (158 TFLOP/s of useful products).
 constexpr int kLatDims = 512, kLatRow = 576;
 constexpr int kLatRowBytes = kLatRow * 2, kLatChunks = kLatRowBytes / 16;
 constexpr int kLatHeads = 16;
