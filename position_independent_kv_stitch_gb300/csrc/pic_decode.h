@@ -140,7 +140,7 @@ struct EvictUnit {           // per (layer, request, weight head), in the worksp
   int32_t n_keep;            // kept tokens (0: nothing to move)
   int32_t first_moved;       // kept tokens before this rank stay where they are
 };
-constexpr int kEvictMoveThreads = 256;   // threads and
+constexpr int kEvictMoveThreads = 384;   // threads and
 constexpr int kEvictMoveCtas = 4;        // CTAs per SM of the move
 constexpr int kEvictCachedSlots = 46000; // weights the selection keeps in shared memory
 struct EvictParams {

@@ -34,10 +34,10 @@
 // tokens before the first evicted one are in place already.
 //
 // Measured on fresh weights (GB300): 32k -> 4k tokens in 16 layers of 8 heads, each
-// head its own set, keys turned, 129 us (selection 28; 559 MB, 4.3 TB/s); 12 of
-// 16 sequences cut to 2k in 8 layers, heads together, 257 us (1.61 GB, 6.3 TB/s);
-// MLA, 16k -> 8k, 3 sequences, 16 layers 205 us (910 MB, 4.4 TB/s); 2,064 -> 2,048
-// in one layer 11.5 us.
+// head its own set, keys turned, 126 us (selection 28; 559 MB, 4.4 TB/s); 12 of
+// 16 sequences cut to 2k in 8 layers, heads together, 241 us (1.61 GB, 6.7 TB/s);
+// MLA, 16k -> 8k, 3 sequences, 16 layers 197 us (910 MB, 4.6 TB/s); 2,064 -> 2,048
+// in one layer 11.7 us.
 #include "pic_decode.h"
 #include "pic_device.cuh"
 #include "pic_paged.cuh"
@@ -353,7 +353,11 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
 constexpr int kMoveThreads = kEvictMoveThreads;
 constexpr int kMoveCtas = kEvictMoveCtas;
 constexpr int kMoveBatch = 1;    // items per thread and tile
-constexpr int kMoveStages = 5;   // tiles in shared memory, most of them on their way
+constexpr int kMoveStages = 3;   // tiles in shared memory, most of them on their way
+// Threads x CTAs per SM x stages, on the three large cases below (us): 384 x 4 x 3
+// 126 / 241 / 197; 256 x 4 x 5 130 / 259 / 206, 256 x 5 x 4 130 / 243 / 204, 320 x 4 x 4
+// 126 / 249 / 197, 384 x 4 x 4 131 / 244 / 204, 512 x 3 x 3 148 / 242 / 241.  Three tiles of
+// 12 KB each of four CTAs cover the latency; the slices follow from the threads.
 constexpr int kMoveSmem = kMoveStages * kMoveBatch * kMoveThreads * (2 * 16 + 4);
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
