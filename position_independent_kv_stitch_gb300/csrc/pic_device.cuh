@@ -44,25 +44,24 @@ __device__ __forceinline__ uint32_t& word(uint4& v, int w) {
 }
 
 // Neox pair-vector: a holds x_a of frequencies f0..f0+7, b holds x_b of the same.
+__device__ __forceinline__ void rotate_neox_word(uint32_t& a, uint32_t& b, const float* c, const float* s) {
+  const float a0 = bf_lo(a), a1 = bf_hi(a), b0 = bf_lo(b), b1 = bf_hi(b);
+  a = bf_pack(a0 * c[0] - b0 * s[0], a1 * c[1] - b1 * s[1]);
+  b = bf_pack(a0 * s[0] + b0 * c[0], a1 * s[1] + b1 * c[1]);
+}
 __device__ __forceinline__ void rotate_neox(uint4& a, uint4& b, const float* c, const float* s) {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t aw = word(a, w), bw = word(b, w);
-    const float a0 = bf_lo(aw), a1 = bf_hi(aw), b0 = bf_lo(bw), b1 = bf_hi(bw);
-    const float c0 = c[2 * w], s0 = s[2 * w], c1 = c[2 * w + 1], s1 = s[2 * w + 1];
-    word(a, w) = bf_pack(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
-    word(b, w) = bf_pack(a0 * s0 + b0 * c0, a1 * s1 + b1 * c1);
-  }
+  for (int w = 0; w < 4; ++w) rotate_neox_word(word(a, w), word(b, w), c + 2 * w, s + 2 * w);
 }
 
 // Interleaved vector: word w holds the pair (x, y) of frequency f0 + w.
+__device__ __forceinline__ void rotate_interleaved_word(uint32_t& v, float c, float s) {
+  const float x = bf_lo(v), y = bf_hi(v);
+  v = bf_pack(x * c - y * s, x * s + y * c);
+}
 __device__ __forceinline__ void rotate_interleaved(uint4& v, const float* c, const float* s) {
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t vw = word(v, w);
-    const float x = bf_lo(vw), y = bf_hi(vw);
-    word(v, w) = bf_pack(x * c[w] - y * s[w], x * s[w] + y * c[w]);
-  }
+  for (int w = 0; w < 4; ++w) rotate_interleaved_word(word(v, w), c[w], s[w]);
 }
 
 // ------------------------------------------------ mbarriers and bulk copies

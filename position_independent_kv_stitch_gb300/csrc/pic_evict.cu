@@ -34,10 +34,10 @@
 // tokens before the first evicted one are in place already.
 //
 // Measured on fresh weights (GB300): 32k -> 4k tokens in 16 layers of 8 heads, each
-// head its own set, keys turned, 126 us (selection 28; 559 MB, 4.4 TB/s); 12 of
-// 16 sequences cut to 2k in 8 layers, heads together, 241 us (1.61 GB, 6.7 TB/s);
-// MLA, 16k -> 8k, 3 sequences, 16 layers 197 us (910 MB, 4.6 TB/s); 2,064 -> 2,048
-// in one layer 11.7 us.
+// head its own set, keys turned, 136 us (selection 28; 559 MB, 4.1 TB/s); 12 of
+// 16 sequences cut to 2k in 8 layers, heads together, 240 us (1.61 GB, 6.7 TB/s);
+// MLA, 16k -> 8k, 3 sequences, 16 layers 209 us (910 MB, 4.4 TB/s); 2,064 -> 2,048
+// in one layer 11.2 us.
 #include "pic_decode.h"
 #include "pic_device.cuh"
 #include "pic_paged.cuh"
@@ -354,7 +354,8 @@ constexpr int kMoveThreads = kEvictMoveThreads;
 constexpr int kMoveCtas = kEvictMoveCtas;
 constexpr int kMoveBatch = 1;    // items per thread and tile
 constexpr int kMoveStages = 3;   // tiles in shared memory, most of them on their way
-// Threads x CTAs per SM x stages, on the three large cases below (us): 384 x 4 x 3
+// Threads x CTAs per SM x stages, on the three large cases above (us; with the
+// hardware's sine and cosine, which are less exact than turn_cossin2's): 384 x 4 x 3
 // 126 / 241 / 197; 256 x 4 x 5 130 / 259 / 206, 256 x 5 x 4 130 / 243 / 204, 320 x 4 x 4
 // 126 / 249 / 197, 384 x 4 x 4 131 / 244 / 204, 512 x 3 x 3 148 / 242 / 241.  Three tiles of
 // 12 KB each of four CTAs cover the latency; the slices follow from the threads.
@@ -367,7 +368,7 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-template <int PAIRING>
+template <int PAIRING, bool TURN>
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __grid_constant__ EvictParams P) {
   constexpr bool NEOX = PAIRING == kNeox;
   // stream = ((layer, request), tensor, piece of the heads, slice of the piece)
@@ -395,7 +396,6 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __
   const int item = slice * P.slice_items + tid - my_row * P.slice_items;   // within the piece
   const int h = item / P.head_items, in_head = item - h * P.head_items;
   const bool rope = tensor == 0 && in_head < P.rope_items;
-  const bool turns = rope && P.renumber;
   const int run = tensor != 0 || rope ? P.rope_items : P.head_items - P.rope_items;   // items (GQA: the head's) between the two chunks
   const int off_a = h * P.head_bytes + (rope ? P.rope_off + in_head * 16 : (tensor == 0 ? in_head - P.rope_items : in_head) * 16);
   const int off_b = off_a + run * 16;
@@ -407,9 +407,11 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __
   // only orders the CTA's reads of a tile before its writes.
   extern __shared__ __align__(16) uint4 s_ring[];   // [stage][item][2][thread], then the slots [stage][item][thread]
   int* s_slot = reinterpret_cast<int*>(s_ring + kMoveStages * kMoveBatch * 2 * kMoveThreads);
-  __shared__ __align__(16) float2 s_freq[kMaxFreqs];
-  if (tid < kMaxFreqs) s_freq[tid] = P.freq.turns[tid];
-  __syncthreads();
+  __shared__ float4 s_freq[TURN ? kMaxFreqs / 2 : 1];
+  if (TURN) {
+    if (tid < kMaxFreqs) put_freq(s_freq, tid, P.freq.turns[tid]);
+    __syncthreads();
+  }
   auto place = [&](int stage, int i) { return stage * kMoveBatch + i; };
   auto load_slots = [&](int base, int (&slot)[kMoveBatch]) {
 #pragma unroll
@@ -483,22 +485,25 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __
         if (slot < 0) continue;
         const int j = base + i * per_pass + my_row;
         uint4 a = s_ring[place(stage, i) * 2 * kMoveThreads + tid], b = s_ring[(place(stage, i) * 2 + 1) * kMoveThreads + tid];
-        if (turns && slot != j) {
-          const float shift = static_cast<float>(j - slot);
-          float c[8], s[8];
-          // neox: frequencies 8 i ..; interleaved: 4 i .. of the first chunk, 4 (i + run) .. of the second
-          const int f0 = NEOX ? 8 * in_head : 4 * in_head, f1 = NEOX ? f0 + 4 : 4 * (in_head + run);
-#pragma unroll
-          for (int f = 0; f < 8; f += 2) {
-            const float4 w = *reinterpret_cast<const float4*>(s_freq + (f < 4 ? f0 + f : f1 + f - 4));
-            turn_cossin(shift, make_float2(w.x, w.y), c[f], s[f]);
-            turn_cossin(shift, make_float2(w.z, w.w), c[f + 1], s[f + 1]);
-          }
+        if (TURN && rope && slot != j) {
+          const float2 shift = make_float2(static_cast<float>(j - slot), static_cast<float>(j - slot));
+          // Pairs of frequencies.  All first and then the rotation for neox, word by
+          // word for interleaved: 136 us (evict_prompt) and 209 (evict_latent); the
+          // other way about 149 and 219.
           if (NEOX) {
+            float c[8], s[8];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) turn_cossin2(shift, s_freq[4 * in_head + f], c + 2 * f, s + 2 * f);
             rotate_neox(a, b, c, s);
-          } else {
-            rotate_interleaved(a, c, s);
-            rotate_interleaved(b, c + 4, s + 4);
+          } else {   // 2 i .. of the first chunk, 2 (i + run) .. of the second
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              float c[2], s[2];
+              turn_cossin2(shift, s_freq[2 * (in_head + (f < 2 ? 0 : run)) + (f & 1)], c, s);
+              uint4& v = f < 2 ? a : b;
+              rotate_interleaved_word(word(v, 2 * (f & 1)), c[0], s[0]);
+              rotate_interleaved_word(word(v, 2 * (f & 1) + 1), c[1], s[1]);
+            }
           }
         }
         uint8_t* p = row_at(to[x][i], j);
@@ -516,14 +521,15 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) k_evict_move(const __
 cudaError_t launch_evict(const EvictParams& p, int pairing, cudaStream_t s) {
   const int64_t lr = static_cast<int64_t>(p.layers) * p.n_req;
   const int smem = p.sel_cap * static_cast<int>(sizeof(float));
-  static std::atomic<uint32_t> select_done{0}, move_done[2] = {{0}, {0}};
+  static std::atomic<uint32_t> select_done{0}, move_done[3] = {{0}, {0}, {0}};
   cudaError_t e = allow_smem(k_evict_select, kEvictCachedSlots * static_cast<int>(sizeof(float)), select_done);
   if (e != cudaSuccess) return e;
   k_evict_select<<<static_cast<unsigned>(lr * p.weight_heads), kSelThreads, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto move = pairing == kNeox ? k_evict_move<kNeox> : k_evict_move<kInterleaved>;
-  e = allow_smem(move, kMoveSmem, move_done[pairing == kNeox ? 0 : 1]);
+  const int variant = p.renumber == 0 ? 0 : (pairing == kNeox ? 1 : 2);
+  auto move = variant == 0 ? k_evict_move<kNeox, false> : (variant == 1 ? k_evict_move<kNeox, true> : k_evict_move<kInterleaved, true>);
+  e = allow_smem(move, kMoveSmem, move_done[variant]);
   if (e != cudaSuccess) return e;
   move<<<static_cast<unsigned>(lr * p.tensors * p.pieces * p.slices), kMoveThreads, kMoveSmem, s>>>(p);
   return cudaGetLastError();

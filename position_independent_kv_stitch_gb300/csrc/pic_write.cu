@@ -14,7 +14,7 @@
 // their own.  Rows are asked for before anything they do not depend on, and
 // positions, slots and blocks are looked at after that.
 // Measured (GB300, 32 + 8 heads of 128 dims): 16,384 tokens of three axes 61.0 us,
-// 403 MB at 6.6 TB/s; 64 tokens 3.0 us; one token 2.8 us.  MLA, 16 query heads,
+// 403 MB at 6.6 TB/s; 64 tokens 2.9 us; one token 2.7 us.  MLA, 16 query heads,
 // 2,048 tokens: 16.0 us, 5.0 TB/s.
 #include "pic_decode.h"
 #include "pic_device.cuh"
@@ -34,7 +34,7 @@ constexpr int kLatentChunks = 512 * 2 / 16;   // 16-byte chunks of a latent (pic
 template <int PAIRING>
 __global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_constant__ WriteParams P) {
   constexpr bool NEOX = PAIRING == kNeox;
-  __shared__ __align__(16) float2 s_freq[kWriteWarps][kMaxFreqs];   // lanes read eight of their own
+  __shared__ float4 s_freq[kWriteWarps][kMaxFreqs / 2];   // lanes read eight of their own
   __shared__ __align__(8) uint8_t s_axis[kWriteWarps][kMaxFreqs];
   const int lane = threadIdx.x & 31;
   const int tasks = P.rot_parts + P.copy_parts;
@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_
         }
       };
       load(h_begin, a[0], b[0]);
-      float2* freq = s_freq[threadIdx.x >> 5];
+      float4* freq = s_freq[threadIdx.x >> 5];
       uint8_t* axis = s_axis[threadIdx.x >> 5];
       for (int i = lane; i < 8 * lph; i += 32) {
-        freq[i] = P.freq.turns[i];
+        put_freq(freq, i, P.freq.turns[i]);
         axis[i] = P.axis[i];
       }
       __syncwarp();
@@ -102,14 +102,15 @@ __global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_
       // interleaved turns the pairs of chunks 2j and 2j + 1
       float c[8], s[8];
       const uint2 axes = *reinterpret_cast<const uint2*>(axis + 8 * j);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      auto position = [&](int i) {
         const int x = ((i < 4 ? axes.x : axes.y) >> (8 * (i & 3))) & 255u;
         int p = pos[0];
 #pragma unroll
         for (int y = 1; y < PIC_MAX_AXES; ++y) p = x == y ? pos[y] : p;
-        turn_cossin(static_cast<float>(p), freq[8 * j + i], c[i], s[i]);
-      }
+        return static_cast<float>(p);   // exact for |p| < 2^24
+      };
+#pragma unroll
+      for (int i = 0; i < 4; ++i) turn_cossin2(make_float2(position(2 * i), position(2 * i + 1)), freq[4 * j + i], c + 2 * i, s + 2 * i);
       uint8_t* qd = P.q_out + tok * P.q_out_stride;
       uint8_t* kd = P.k_cache + row * row_bytes - static_cast<int64_t>(P.q_heads) * P.head_bytes;
       const int step = kRotBatch * hpi;

@@ -886,3 +886,52 @@ def test_evict_selection_borders(kind, n):
     got = c.w[0, torch.from_numpy(c.tables[0][np.arange(n // 3) // 16]).long().to(DEV), 0, torch.from_numpy(np.arange(n // 3) % 16).to(DEV)]
     np.testing.assert_array_equal(got.double().cpu().numpy(), by_slot[want])
     c.close()
+
+
+def _assert_small_angles(got, x, angle):
+    """got = x sin(angle), |angle| < pi / 4, an element that is small beside its partner x: its own half step of bf16, and 2^-20
+    for fp32 (the angle in turns, its sine and the product are each within a few 2^-24 of themselves), relative all of them."""
+    want = x * np.sin(angle)
+    err = np.abs(got - want) - (2.0 ** -8 + 2.0 ** -20) * np.abs(want)
+    assert err.max() <= 0, f"{(err > 0).sum()} of {err.size} off, worst by {(np.abs(got - want) / np.abs(want)).max():.2e} of the value"
+
+
+@pytest.mark.parametrize("pairing", ["neox", "interleaved"])
+@pytest.mark.parametrize("kind", ["gqa", "mla"])
+def test_small_angles_keep_their_relative_precision(kind, pairing):
+    """Pairs (x, 0) turned by small angles, in a write and in a renumbering eviction: the second element is right
+    to bf16's precision of itself, not of x."""
+    c = Cache(kind, heads=2, d=128, bs=16, lens=[40], room=16, pairing=pairing, seed=60)
+    n_rope, off = c.m.rope_dim, c.m.rope_offset
+    a, b = (off + np.asarray(i) for i in oracle.rope_pairs(n_rope, c.pairing))
+    theta, second = np.asarray(c.theta), torch.as_tensor(b, device=DEV)
+    pos = np.array([1, 2, 7, 40, 1000, -3])
+    n = len(pos)
+    q, k = c.normal(n, 4, c.d), c.normal(n, c.heads, c.d)
+    q[..., second], k[..., second] = 0.0, 0.0
+    v = c.normal(n, c.heads, c.d) if kind == "gqa" else None
+    slot = np.arange(40, 40 + n)
+    q_out, ws = torch.empty_like(q), _ws(1 << 16)
+    pic.pic_write_tokens(c.ctx, _i32(pos), k, v, _i32(np.zeros(n)), _i32(slot), c.d_tables, c.k[0], None if v is None else c.v[0],
+                         q=q, q_out=q_out, workspace=ws)
+    rows = np.stack([_f64(c.k[0])[c.tables[0][s // 16], s % 16] for s in slot])
+    angle = pos[:, None] * theta
+    near = np.broadcast_to((np.abs(angle) < math.pi / 4)[:, None], q.shape[:2] + angle.shape[1:])
+    assert near.mean() > 0.3
+    for got, x in ((_f64(q_out), _f64(q)), (rows, _f64(k))):
+        m = near[:, :x.shape[1]]
+        _assert_small_angles(got[..., b][m], x[..., a][m], np.broadcast_to(angle[:, None], m.shape)[m])
+    # an eviction that keeps the first and the last tokens turns the last by the budget less the length
+    c.k[..., second] = 0.0
+    before, budget = c.host()[0], 37
+    kept, new = torch.empty(1, 1, c.wh, budget, dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    pic.pic_evict_tokens(c.ctx, c.k, c.v, c.w, c.d_tables, c.d_lens, budget, kept, new, n_first=10, n_recent=budget - 10,
+                         renumber=True, workspace=ws)
+    assert _status(c, ws) == 0
+    after = c.host()[0]
+    m = np.abs(3 * theta) < math.pi / 4
+    for j in range(10, budget):
+        x = before[c.tables[0][(j + 3) // 16], (j + 3) % 16][:, a][:, m]
+        got = after[c.tables[0][j // 16], j % 16][:, b][:, m]
+        _assert_small_angles(got, x, np.broadcast_to(-3.0 * theta[m], x.shape))
+    c.close()
