@@ -702,7 +702,8 @@ size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t
  * Per layer, request and weight head the first n_first and last n_recent
  * tokens stay, and of those between the ones of largest weight, equal weights
  * to the lower slot (NaN counts below everything, -0 as 0).  The kept tokens
- * move, in order, to slots [0, budget) with their values and weights.
+ * move, in order, to slots [0, budget) with their values and weights, bit for
+ * bit.
  *   renumber  0: keys keep the positions they were rotated for (the caller goes
  *             on counting positions); 1: a key moving from slot s to slot j is
  *             turned by R(j - s), all axes alike (the sequence is again one of

@@ -13,7 +13,7 @@
 //
 // k_evict_select, one CTA per (layer, request, weight head).  The weights are
 // read once and kept in shared memory as sort keys (those past its size are read
-// again from L2); a NaN comes back from its key as the plain NaN, -0 as 0.
+// again from L2); only -0 and NaNs do not come back from their keys.
 // The weight of the last token that fits is found by radix selection over the
 // weights' bits, from the top: 11, 11 and 10 bits, counted in shared memory.
 // Every warp takes a contiguous run of slots; a sweep counts what surely stays in
@@ -59,10 +59,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   const uint32_t u = __float_as_uint(w + 0.0f);
   return (u & 0x80000000u) != 0 ? ~u : (u | 0x80000000u);
 }
-// The weight of a key (a NaN for any NaN, 0 for -0).
+// The weight of a key, for all but those of lossy().
 __device__ __forceinline__ float key_weight(uint32_t k) {
   return __uint_as_float(k == 0u ? 0x7fffffffu : ((k & 0x80000000u) != 0 ? k ^ 0x80000000u : ~k));
 }
+// Whether a weight cannot be had back from its key: -0, which counts as 0, and NaN.
+__device__ __forceinline__ bool lossy(float w) { return w != w || __float_as_uint(w) == 0x80000000u; }
 // Bits i of 4 with i < n.
 __device__ __forceinline__ uint32_t below(int n) { return 0xfu >> (4 - min(max(n, 0), 4)); }
 
@@ -159,12 +161,14 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   const bool vec = (bs & 3) == 0 && ((reinterpret_cast<uintptr_t>(P.weights) | static_cast<uintptr_t>(P.weights_ls)) & 15) == 0;
   auto count_top = [&](uint32_t key) { atomicAdd(&s_hist[key >> 21], 1); };
   auto is_cand = [&](int s) { return s >= lo && s < hi; };
+  bool lost = false;   // a weight that has to be moved from memory
   if (vec) {
 #pragma unroll 4
     for (int s = 4 * tid; s < cached; s += 4 * kSelThreads) {
       const float4 x = __ldcg(reinterpret_cast<const float4*>(at(s)));
       const uint4 k = make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
       *reinterpret_cast<uint4*>(s_key + s) = k;
+      lost |= lossy(x.x) || lossy(x.y) || lossy(x.z) || lossy(x.w);
       const uint32_t cand = below(hi - s) & ~below(lo - s);
       if (cand & 1u) count_top(k.x);
       if (cand & 2u) count_top(k.y);
@@ -174,14 +178,16 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   } else {
 #pragma unroll 4
     for (int s = tid; s < cached; s += kSelThreads) {
-      const uint32_t k = weight_key(__ldcg(at(s)));
+      const float w = __ldcg(at(s));
+      const uint32_t k = weight_key(w);
       s_key[s] = k;
+      lost |= lossy(w);
       if (is_cand(s)) count_top(k);
     }
   }
   for (int s = cached + tid; s < len; s += kSelThreads)
     if (is_cand(s)) count_top(weight_key(__ldcg(at(s))));
-  __syncthreads();
+  const bool from_keys = __syncthreads_or(lost) == 0;
 
   // The digit in which the count from the top reaches `left`, two digits a
   // thread; what is left within it.  The counts return to 0.
@@ -332,17 +338,17 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   __syncthreads();
   if (tid == 0) P.units[unit] = EvictUnit{P.budget, s_first_moved};
   // the weights move with their tokens (kept[] is this CTA's own, written above)
-  if (cached == len) {
+  if (cached == len && from_keys) {
     for (int j = s_first_moved + tid; j < P.budget; j += kSelThreads) *at(j) = key_weight(s_key[kept[j]]);
     return;
   }
-  // some are only in memory: in order, a tile's reads before its writes
+  // some are only in memory as they were: in order, a tile's reads before its writes
   for (int base = s_first_moved; base < P.budget; base += kSelThreads) {
     const int j = base + tid;
     float x = 0.0f;
     if (j < P.budget) {
       const int s = kept[j];
-      x = s < cached ? key_weight(s_key[s]) : __ldcg(at(s));
+      x = s < cached && from_keys ? key_weight(s_key[s]) : __ldcg(at(s));
     }
     // the barrier takes a value made of the loaded one: every load has arrived
     __syncthreads_or(__float_as_uint(x) == 0x7fc12345u);

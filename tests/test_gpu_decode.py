@@ -935,3 +935,33 @@ def test_small_angles_keep_their_relative_precision(kind, pairing):
         got = after[c.tables[0][j // 16], j % 16][:, b][:, m]
         _assert_small_angles(got, x, np.broadcast_to(-3.0 * theta[m], x.shape))
     c.close()
+
+
+@pytest.mark.parametrize("n,budget", [(700, 300), (4099, 1000), (60000, 30000)])
+@pytest.mark.parametrize("heads,bs", [(2, 16), (1, 7)])
+def test_evict_moves_weights_bit_for_bit(n, budget, heads, bs):
+    """Signed zeros and NaNs with payloads arrive as they were, in short sequences and in ones whose weights
+    shared memory does not hold; slots behind the budget keep theirs."""
+    c = Cache(heads=heads, d=64, bs=bs, lens=[n, 0, n // 2], seed=n + heads)
+    raw = c.w.view(torch.int32)
+    pick = torch.randint(0, 8, raw.shape, generator=c.g, device=DEV)
+    odd = torch.tensor([-2 ** 31, 0x7fc00001, 0x7f800123, -4194000, 0, 0x7fffffff], dtype=torch.int32, device=DEV)   # -0, NaNs, 0
+    c.w = torch.where(pick < 6, odd[pick.clamp(max=5)], raw).view(torch.float32)
+    before = c.w.clone()
+    kept, new = torch.empty(1, 3, heads, budget, dtype=torch.int32, device=DEV), torch.empty(3, dtype=torch.int32, device=DEV)
+    ws = _ws(pic.pic_evict_workspace_bytes(c.ctx, 1, 3, heads))
+    pic.pic_evict_tokens(c.ctx, c.k, c.v, c.w, c.d_tables, c.d_lens, budget, kept, new, n_first=2, n_recent=60, workspace=ws)
+    assert _status(c, ws) == 0
+    bits32 = lambda t: t.view(torch.int32).cpu().numpy()  # noqa: E731
+    want, old = bits32(before), bits32(before)
+    for r, length in enumerate(c.lens):
+        if length <= budget:
+            continue
+        page, row = c.tables[r].astype(np.int64)[np.arange(length) // bs], np.arange(length) % bs
+        for h in range(heads):
+            w = before[0, torch.from_numpy(page).to(DEV), h, torch.from_numpy(row).to(DEV)].double().cpu().numpy()
+            src = kept[0, r, h].cpu().numpy()
+            assert src.tolist() == oracle.kept_slots(w, length, budget, 2, 60)
+            want[0, page[:budget], h, row[:budget]] = old[0, page[src], h, row[src]]
+    np.testing.assert_array_equal(bits32(c.w), want)
+    c.close()
