@@ -602,7 +602,9 @@ pic_status pic_attend_decode(pic_ctx* ctx, const pic_plan* const* plans, int32_t
  * again after an error; pic_query_device_status reads it whenever the caller
  * wants to know, for instance once in many steps.  Calls whose work may run at
  * the same time need workspaces of their own.  Every buffer is memory of the
- * current device (PIC_ERR_UNSUPPORTED / PIC_ERR_INVALID_ARG otherwise).
+ * current device (PIC_ERR_UNSUPPORTED / PIC_ERR_INVALID_ARG otherwise).  A call
+ * of no tokens or no requests does nothing; the buffers that would hold
+ * nothing may then be NULL.
  */
 
 /*

@@ -181,15 +181,16 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache
     if (t->freq_axis[i] >= t->n_axes)
       return fail(ctx, PIC_ERR_INVALID_ARG, "freq_axis[%d] is %d, there are %d axes", i, t->freq_axis[i], t->n_axes);
   if (!d_ws || ws_bytes < PIC_STATUS_BYTES) return fail(ctx, PIC_ERR_CAPACITY, "workspace needs %d bytes", PIC_STATUS_BYTES);
+  if (t->n_tokens == 0) return set_error(ctx, PIC_OK, "");   // an empty batch has no buffers
   const bool with_q = t->num_q_heads > 0, with_k = t->k != nullptr;
   if (!with_q && !with_k) return fail(ctx, PIC_ERR_INVALID_ARG, "neither queries nor keys given");
-  if (t->n_tokens > 0 && (!t->d_pos || (with_q && (!t->q || !t->q_out))))
+  if (!t->d_pos || (with_q && (!t->q || !t->q_out)))
     return fail(ctx, PIC_ERR_INVALID_ARG, "null positions, queries or query output");
   if (with_k) {
     if (!mla != (t->v != nullptr)) return fail(ctx, PIC_ERR_INVALID_ARG, "GQA tokens have keys and values, MLA tokens keys only");
-    if (!k_cache || (!mla && !v_cache) || !d_tables || !t->d_req || !t->d_slot)
-      return fail(ctx, PIC_ERR_INVALID_ARG, "null cache, block table, request or slot list");
     if (n_tables < 0 || max_blocks < 0) return fail(ctx, PIC_ERR_INVALID_ARG, "bad block table shape");
+    if (!k_cache || (!mla && !v_cache) || (!d_tables && n_tables > 0 && max_blocks > 0) || !t->d_req || !t->d_slot)
+      return fail(ctx, PIC_ERR_INVALID_ARG, "null cache, block table, request or slot list");
     if (d_weights && !weight_heads_ok(c, weight_heads))
       return fail(ctx, PIC_ERR_INVALID_ARG, "weight_heads must be 1 or num_kv_heads");
   } else if (t->v) {
@@ -210,7 +211,6 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache
   if (!aligned(t->d_pos, 4) || !aligned(t->d_req, 4) || !aligned(t->d_slot, 4) || !aligned(d_tables, 4) ||
       !aligned(d_weights, 4) || !aligned(d_ws, kWsAlign))
     return fail(ctx, PIC_ERR_ALIGNMENT, "index arrays and weights must be 4-byte aligned, the workspace 256-byte");
-  if (t->n_tokens == 0) return set_error(ctx, PIC_OK, "");
   const Buffer bufs[] = {{"q", with_q ? t->q : nullptr}, {"q_out", with_q ? t->q_out : nullptr}, {"k", t->k}, {"v", t->v},
                          {"positions", t->d_pos}, {"requests", with_k ? t->d_req : nullptr},
                          {"slots", with_k ? t->d_slot : nullptr}, {"k_cache", with_k ? k_cache : nullptr},
@@ -293,7 +293,8 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
   if (d_weights && !weight_heads_ok(c, weight_heads))
     return fail(ctx, PIC_ERR_INVALID_ARG, "weight_heads must be 1 or num_kv_heads");
   if (mla) v_cache = nullptr;  // the latent serves as value
-  if (!q || !k_cache || (!mla && !v_cache) || !d_tables || !d_seq_lens || !out || !d_ws)
+  const bool some = n_req > 0;   // an empty batch has no buffers of its own, a table without columns no address
+  if (!k_cache || (!mla && !v_cache) || !d_ws || (some && (!q || (!d_tables && max_blocks > 0) || !d_seq_lens || !out)))
     return fail(ctx, PIC_ERR_INVALID_ARG, "null q, cache, block table, lengths, out or workspace");
   const int64_t q_bytes = static_cast<int64_t>(num_q_heads) * m.head_dim * 2;
   const int64_t row_bytes = static_cast<int64_t>(m.num_kv_heads) * m.head_dim * 2;
@@ -373,7 +374,9 @@ pic_status pic_evict_tokens(pic_ctx* ctx, int32_t num_layers, void* k_cache, voi
   if (!weight_heads_ok(c, weight_heads)) return fail(ctx, PIC_ERR_INVALID_ARG, "weight_heads must be 1 or num_kv_heads");
   if (budget < 1 || n_first < 0 || n_recent < 0 || static_cast<int64_t>(n_first) + n_recent > budget)
     return fail(ctx, PIC_ERR_INVALID_ARG, "need budget >= 1 and n_first + n_recent <= budget");
-  if (!k_cache || (!mla && !v_cache) || !d_weights || !d_tables || !d_seq_lens || !d_kept || !d_new_lens || !d_ws)
+  const bool some = n_req > 0;
+  if (!k_cache || (!mla && !v_cache) || !d_weights || !d_ws ||
+      (some && ((!d_tables && max_blocks > 0) || !d_seq_lens || !d_kept || !d_new_lens)))
     return fail(ctx, PIC_ERR_INVALID_ARG, "null cache, weights, block table, lengths, output or workspace");
   if (mla) v_cache = nullptr;  // a latent row is key and value
   const int64_t rows = static_cast<int64_t>(c.num_cache_blocks) * m.block_size;

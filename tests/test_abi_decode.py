@@ -192,3 +192,23 @@ def test_binding_wants_latent_outputs_whether_or_not_a_value_cache_is_given(mla)
             pic.pic_attend_paged(mla, q, 1.0, cache, v, i.view(2, 1), i, 16, torch.empty(2, 4, 576))
         with pytest.raises(ValueError, match="CUDA device"):
             pic.pic_attend_paged(mla, q, 1.0, cache, v, i.view(2, 1), i, 16, torch.empty(2, 4, 512))
+
+
+def test_empty_batches_need_no_buffers_of_their_own(gqa, mla):
+    """What an empty tensor gives as its address is null: no tokens and no requests are no error."""
+    none = dict(d_pos=None, q=None, q_out=None, k=None, v=None, d_req=None, d_slot=None)
+    for ctx in (gqa, mla):
+        for heads in (0, 4):
+            assert _write(ctx, mla=ctx is mla, n_tokens=0, num_q_heads=heads, **none) == 0
+    assert _write(gqa, n_tokens=0, n_tables=0, tables=None, **none) == 0
+    none = dict(n_req=0, q=None, lens=None, out=None, lse=None)
+    assert _attend(gqa, **none) == 0 and _attend(gqa, tables=None, **none) == 0
+    assert _attend(gqa, weights=P, heads=1, **none) == 0
+    assert _attend(mla, hq=16, q_stride=16 * 1152, v=None, **none) == 0
+    none = dict(n_req=0, lens=None, kept=None, new=None)
+    assert _evict(gqa, **none) == 0 and _evict(gqa, tables=None, **none) == 0
+    assert _evict(mla, heads=1, v=None, cls=64 * 16 * 1152, **none) == 0
+    # what has nothing to do with the batch is still looked at
+    assert _write(gqa, n_tokens=0, n_axes=0) == INVALID and _write(gqa, n_tokens=0, ws=None) == CAPACITY
+    assert _attend(gqa, n_req=0, hq=3) == INVALID and _attend(gqa, n_req=0, ws=None) == INVALID
+    assert _evict(gqa, n_req=0, budget=0) == INVALID and _evict(gqa, n_req=0, k=None) == INVALID

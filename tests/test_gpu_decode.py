@@ -965,3 +965,44 @@ def test_evict_moves_weights_bit_for_bit(n, budget, heads, bs):
             want[0, page[:budget], h, row[:budget]] = old[0, page[src], h, row[src]]
     np.testing.assert_array_equal(bits32(c.w), want)
     c.close()
+
+
+@pytest.mark.parametrize("kind", ["gqa", "mla"])
+def test_empty_batches(kind):
+    """No token and no request, as a serving loop without a live request calls: nothing happens."""
+    c = Cache(kind, heads=2, d=128, lens=[20], seed=70)
+    hq, dv, before = 4, c.d if kind == "gqa" else 512, (c.k.clone(), c.w.clone())
+    i0, q0 = torch.empty(0, dtype=torch.int32, device=DEV), c.normal(3, hq, c.d)[:0]
+    k0, v = c.normal(3, c.heads, c.d)[:0], None if c.v is None else c.v[0]
+    v0 = None if c.v is None else k0
+    ws = _ws(1 << 25)
+    for tables in (c.d_tables[:0], c.d_tables):
+        for q in (None, q0):
+            pic.pic_write_tokens(c.ctx, i0, k0, v0, i0, i0, tables, c.k[0], v, q=q, q_out=q, weights=c.w[0], workspace=ws)
+        pic.pic_write_tokens(c.ctx, i0.view(2, 0), None, None, None, None, None, None, None, q=q0, q_out=q0, workspace=ws,
+                             freq_axis=[0, 1] * (c.m.rope_dim // 4))
+        for w in (None, c.w[0]):
+            pic.pic_attend_paged(c.ctx, q0, 0.1, c.k[0], v, tables, i0, 20, torch.empty(0, hq, dv, device=DEV),
+                                 lse=torch.empty(0, hq, device=DEV), weights=w, workspace=ws)
+        pic.pic_evict_tokens(c.ctx, c.k, c.v, c.w, tables, i0, 7, torch.empty(1, 0, c.wh, 7, dtype=torch.int32, device=DEV), i0,
+                             n_first=1, n_recent=2, workspace=ws)
+    assert _status(c, ws) == 0 and torch.equal(c.k, before[0]) and torch.equal(c.w, before[1])
+    c.close()
+
+
+def test_requests_without_blocks():
+    """Tables of no blocks and sequences of no slots: outputs 0, nothing kept, keys without a place raise."""
+    c = Cache(heads=2, d=128, lens=[20], seed=71)
+    tables, lens = torch.empty(2, 0, dtype=torch.int32, device=DEV), _i32([0, 0])
+    q, ws = c.normal(2, 4, 128), _ws(1 << 25)
+    out, lse = torch.full((2, 4, 128), 7.0, device=DEV), torch.empty(2, 4, device=DEV)
+    before = c.k.clone()
+    pic.pic_attend_paged(c.ctx, q, 0.1, c.k[0], c.v[0], tables, lens, 0, out, lse=lse, weights=c.w[0], workspace=ws)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    kept, new = torch.empty(1, 2, 2, 3, dtype=torch.int32, device=DEV), torch.full((2,), 7, dtype=torch.int32, device=DEV)
+    pic.pic_evict_tokens(c.ctx, c.k, c.v, c.w, tables, lens, 3, kept, new, workspace=ws)
+    assert bool((kept == -1).all()) and new.tolist() == [0, 0] and _status(c, ws) == 0
+    pic.pic_write_tokens(c.ctx, lens, c.normal(2, 2, 128), c.normal(2, 2, 128), _i32([0, 1]), _i32([-1, 0]), tables, c.k[0], c.v[0],
+                         workspace=ws)
+    assert _status(c, ws) == pic.PIC_DEV_BAD_BLOCK and torch.equal(c.k, before)
+    c.close()
