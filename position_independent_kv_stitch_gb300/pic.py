@@ -160,7 +160,7 @@ _SIGNATURES = {
 }
 
 _lib = None
-_torch = _BF16 = _F32 = _I32 = None   # set by load()
+_torch = _BF16 = _F32 = _I32 = None   # set by the first decode-loop call
 # (cache blocks, (block size, KV heads, head dim), frequencies) of each live context, by handle
 _geometry = {}
 
@@ -171,7 +171,7 @@ def lib_path() -> str:
 
 def load(build_if_missing: bool = False):
     """Loads libpic.so (building it first only when asked); raises if absent."""
-    global _lib, _torch, _BF16, _F32, _I32
+    global _lib
     if _lib is not None:
         return _lib
     if build_if_missing and (not os.path.exists(_build.LIB_PATH) or _build.is_stale()):
@@ -184,8 +184,6 @@ def load(build_if_missing: bool = False):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    import torch
-    _torch, _BF16, _F32, _I32 = torch, torch.bfloat16, torch.float32, torch.int32
     _lib = lib
     return lib
 
@@ -681,6 +679,16 @@ def pic_attend_decode(ctx, plans, source, q, softmax_scale, k_pool, v_pool, k_ca
 # These calls are made once per layer and token, so the checks are lean: shapes
 # fetched once and compared whole, addresses passed as integers, no views.
 
+def _with_torch():
+    """The library, with torch and the types of the tensors at hand (the library's host calls run without torch)."""
+    global _torch, _BF16, _F32, _I32
+    lib = load()
+    import torch
+    _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+    _torch = torch
+    return lib
+
+
 def _launch(ctx, fn, device, stream, args):
     """fn(ctx, *args, stream) with `device` (an index) current.  The library
     itself refuses buffers of another device or of the host."""
@@ -771,7 +779,7 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
     [n_tokens][q_heads][head_dim], q_out may be q.  weights: float32
     [blocks][weight_heads][block_size], zeroed at the written slots.
     workspace: uint8, PIC_STATUS_BYTES, zeroed when made (its status is sticky)."""
-    lib = _lib or load()
+    lib = _lib if _torch is not None else _with_torch()
     shape = positions.shape
     axes, n = shape if len(shape) == 2 else (1, shape[0])
     if positions.dtype is not _I32 or not positions.is_contiguous():
@@ -835,7 +843,7 @@ def pic_attend_paged(ctx, q, softmax_scale, k_cache, v_cache, block_tables, seq_
     [blocks][weight_heads][block_size] or None, each slot's attention weight is
     added to it.  workspace: uint8, pic_attend_paged_workspace_bytes, its first
     PIC_STATUS_BYTES zeroed when made."""
-    lib = _lib or load()
+    lib = _lib if _torch is not None else _with_torch()
     shape = q.shape
     stride = _token_rows(q, "q", shape)
     n_req, hq, d = shape
@@ -870,7 +878,7 @@ def pic_evict_tokens(ctx, k_cache, v_cache, weights, block_tables, seq_lens, bud
     [layers][n_req][weight_heads][budget].  renumber: keys are re-rotated to
     their new slots.  workspace: uint8, pic_evict_workspace_bytes, its first
     PIC_STATUS_BYTES zeroed when made."""
-    lib = _lib or load()
+    lib = _lib if _torch is not None else _with_torch()
     n_req = seq_lens.numel()
     max_blocks = _table_shape(block_tables, n_req)[1]
     cache, _ = _check_caches(ctx, k_cache, v_cache, 5)

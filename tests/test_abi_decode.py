@@ -212,3 +212,26 @@ def test_empty_batches_need_no_buffers_of_their_own(gqa, mla):
     assert _write(gqa, n_tokens=0, n_axes=0) == INVALID and _write(gqa, n_tokens=0, ws=None) == CAPACITY
     assert _attend(gqa, n_req=0, hq=3) == INVALID and _attend(gqa, n_req=0, ws=None) == INVALID
     assert _evict(gqa, n_req=0, budget=0) == INVALID and _evict(gqa, n_req=0, k=None) == INVALID
+
+
+def test_host_calls_need_no_torch():
+    """Registry, plans and windows run where torch cannot be imported; only the calls that take tensors want it."""
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.modules["torch"] = None
+from position_independent_kv_stitch_gb300 import pic
+ctx = pic.pic_create(pic.PIC_KIND_GQA, 2, 2, 128, 128, 0, pic.PIC_PAIRING_NEOX_HALF, 16, 1e4, 64)
+chunk = pic.pic_register_chunk(ctx, b"a" * 32, 0, 40)[0]
+plan, table = pic.pic_build_block_table(ctx, [chunk], 8)
+assert len(table) == 8 and pic.pic_evict_workspace_bytes(ctx, 2, 3, 2) > 0
+pic.pic_free_request(ctx, plan)
+try:
+    pic.pic_write_tokens(ctx, None, None, None, None, None, None, None, None)
+except ImportError:
+    print("wants torch")
+pic.pic_destroy(ctx)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=pic._build.ROOT)
+    assert r.returncode == 0 and r.stdout.strip() == "wants torch", r.stderr
