@@ -10,6 +10,7 @@ immediately -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 from dataclasses import dataclass
@@ -812,7 +813,8 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
     if freq_axis is not None:
         if want is not None and len(freq_axis) != want[2]:
             raise ValueError(f"freq_axis holds an axis for each of the {want[2]} frequencies")
-        axis_bytes = bytes(freq_axis)
+        # (bytes() of an array would be its memory, whatever its type)
+        axis_bytes = bytes(freq_axis if type(freq_axis) in (list, tuple, bytes) else [operator.index(a) for a in freq_axis])
         if axis_bytes not in _axis_arrays:
             _axis_arrays[axis_bytes] = ctypes.create_string_buffer(axis_bytes, len(axis_bytes))
         freq_axis = ctypes.addressof(_axis_arrays[axis_bytes])

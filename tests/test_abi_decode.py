@@ -235,3 +235,35 @@ pic.pic_destroy(ctx)
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=pic._build.ROOT)
     assert r.returncode == 0 and r.stdout.strip() == "wants torch", r.stderr
+
+
+def _axes_passed(monkeypatch, ctx, freq_axis):
+    """The frequency axes that the library would be given."""
+    import torch
+    seen = []
+    monkeypatch.setattr(pic, "_launch", lambda ctx, fn, device, stream, args: seen.append(
+        ctypes.string_at(pic._NEW_TOKENS.unpack(args[0])[3], 64)))
+    q = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
+    pic.pic_write_tokens(ctx, torch.zeros(4, 2, dtype=torch.int32), None, None, None, None, None, None, None, q=q, q_out=q,
+                         freq_axis=freq_axis)
+    return list(seen[0])
+
+
+def test_frequency_axes_of_any_integers(gqa, monkeypatch):
+    """Lists, tuples, bytes, and arrays and tensors of any integer type name the same axes."""
+    import array
+
+    import numpy as np
+    import torch
+    axes = [f * 4 // 64 for f in range(64)]
+    for x in (axes, tuple(axes), bytes(axes), bytearray(axes), array.array("i", axes), torch.tensor(axes), torch.tensor(axes, dtype=torch.uint8),
+              *(np.array(axes, dtype=t) for t in (np.int64, np.int32, np.uint8, np.uint16)), np.array(axes * 2)[:64][::1]):
+        assert _axes_passed(monkeypatch, gqa, x) == axes, type(x)
+    for bad in (axes[:-1], axes + [0]):
+        with pytest.raises(ValueError, match="frequencies"):
+            _axes_passed(monkeypatch, gqa, bad)
+    for bad in ([-1] + axes[1:], [256] + axes[1:], np.array([-1] + axes[1:])):
+        with pytest.raises(ValueError):
+            _axes_passed(monkeypatch, gqa, bad)
+    with pytest.raises(TypeError):
+        _axes_passed(monkeypatch, gqa, np.array(axes, dtype=np.float32))
