@@ -92,7 +92,7 @@ class pic_new_tokens(ctypes.Structure):
 
 _NEW_TOKENS = struct.Struct("@iii4xPPPqPqPqPqPP")
 assert _NEW_TOKENS.size == ctypes.sizeof(pic_new_tokens)
-_axis_arrays = {}   # frequency axes in use, as C arrays
+_last_axes = (None, None)   # the frequency axes passed last, and as a C array (a model's calls all pass the same)
 
 _c_void_p = ctypes.c_void_p
 _i32, _i64, _u32, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
@@ -780,6 +780,7 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
     [n_tokens][q_heads][head_dim], q_out may be q.  weights: float32
     [blocks][weight_heads][block_size], zeroed at the written slots.
     workspace: uint8, PIC_STATUS_BYTES, zeroed when made (its status is sticky)."""
+    global _last_axes
     lib = _lib if _torch is not None else _with_torch()
     shape = positions.shape
     axes, n = shape if len(shape) == 2 else (1, shape[0])
@@ -815,9 +816,10 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
             raise ValueError(f"freq_axis holds an axis for each of the {want[2]} frequencies")
         # (bytes() of an array would be its memory, whatever its type)
         axis_bytes = bytes(freq_axis if type(freq_axis) in (list, tuple, bytes) else [operator.index(a) for a in freq_axis])
-        if axis_bytes not in _axis_arrays:
-            _axis_arrays[axis_bytes] = ctypes.create_string_buffer(axis_bytes, len(axis_bytes))
-        freq_axis = ctypes.addressof(_axis_arrays[axis_bytes])
+        axes_kept = _last_axes   # held here until the call has read it
+        if axes_kept[0] != axis_bytes:
+            axes_kept = _last_axes = (axis_bytes, ctypes.create_string_buffer(axis_bytes, len(axis_bytes)))
+        freq_axis = ctypes.addressof(axes_kept[1])
     # a pic_new_tokens, packed (filling in a ctypes structure takes longer than the call)
     t = _NEW_TOKENS.pack(
         n, q_heads, axes, freq_axis or 0, positions.data_ptr(),

@@ -267,3 +267,28 @@ def test_frequency_axes_of_any_integers(gqa, monkeypatch):
             _axes_passed(monkeypatch, gqa, bad)
     with pytest.raises(TypeError):
         _axes_passed(monkeypatch, gqa, np.array(axes, dtype=np.float32))
+
+
+def test_frequency_axes_are_not_kept(gqa, monkeypatch):
+    """However many different lists are passed, the binding holds no more than the last one."""
+    import gc
+    import weakref
+    made, array_of = [], ctypes.create_string_buffer
+
+    class Kept:   # a buffer whose end can be seen
+        def __init__(self, *a):
+            self.buffer = array_of(*a)
+
+    def buffer(*a):
+        k = Kept(*a)
+        made.append(weakref.ref(k))
+        return k
+
+    monkeypatch.setattr(ctypes, "create_string_buffer", buffer)
+    monkeypatch.setattr(ctypes, "addressof", lambda k, _f=ctypes.addressof: _f(k.buffer))
+    for i in range(20):
+        axes = [(f >> (i % 5)) % 4 for f in range(64)]
+        axes[i] = 3 - axes[i]
+        assert _axes_passed(monkeypatch, gqa, axes) == axes
+    gc.collect()
+    assert len(made) == 20 and sum(r() is not None for r in made) <= 1
