@@ -680,8 +680,9 @@ size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32
  * pic_attend_decode), v_t its latent; v_cache is ignored and may be NULL.
  *   q           bf16 [n_req][num_q_heads][head_dim], q_stride bytes between
  *               requests, rotated (pic_write_tokens' q_out).
- *   max_seq_len longest sequence (host bound, at most max_blocks * block_size);
- *               sizes the workspace when weights are kept.
+ *   max_seq_len longest sequence (host bound, at most max_blocks * block_size
+ *               and 2^31 - 8193); sizes the workspace when weights are kept:
+ *               4 bytes for every request, query head and slot up to it.
  *   out         [n_req][num_q_heads][head_dim] (MLA: the 512 latent dims) of
  *               out_type PIC_F32 or PIC_BF16.
  *   lse         float [n_req][num_q_heads] or NULL.

@@ -83,13 +83,12 @@ void fill_freq(const CtxView& c, FreqTable* t) { std::memcpy(t->turns, c.freq, c
 int32_t table_capacity(const CtxView& c, int32_t max_blocks) {
   if (c.num_cache_blocks == 0) return 0;
   const int64_t n = static_cast<int64_t>(max_blocks) * c.model->block_size;
-  return static_cast<int32_t>(std::min<int64_t>(n, std::numeric_limits<int32_t>::max() - 2 * kPagedTile));
+  return static_cast<int32_t>(std::min<int64_t>(n, kPagedMaxSlots));
 }
 
 // Rows of the cache: a sequence whose blocks are all its own is no longer.
 int32_t cache_rows(const CtxView& c) {
-  return static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(c.num_cache_blocks) * c.model->block_size,
-                                                std::numeric_limits<int32_t>::max() - 2 * kPagedTile));
+  return static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(c.num_cache_blocks) * c.model->block_size, kPagedMaxSlots));
 }
 
 bool weight_heads_ok(const CtxView& c, int32_t n) { return n == 1 || n == c.model->num_kv_heads; }

@@ -41,6 +41,11 @@ struct CtxView {
 };
 CtxView ctx_view(const pic_ctx* ctx);
 
+// Longest sequence.  Kernels count slots in 32 bits and look past the end of a
+// sequence before they compare: 111 slots in the attention over latent rows, a
+// sweep of 4 x 1,024 in the selection, five tiles of 384 in the move.
+constexpr int32_t kPagedMaxSlots = INT32_MAX - 8192;
+
 constexpr int kMaxFreqs = 128;  // rope_dim / 2 of the widest head
 
 // The paged cache as the kernels see it: one layer's tables and geometry.

@@ -292,3 +292,13 @@ def test_frequency_axes_are_not_kept(gqa, monkeypatch):
         assert _axes_passed(monkeypatch, gqa, axes) == axes
     gc.collect()
     assert len(made) == 20 and sum(r() is not None for r in made) <= 1
+
+
+def test_lengths_near_the_integer_limit_are_refused():
+    """A table that repeats its blocks may hold more slots than 31 bits count: what kernels add to a slot (steps
+    looked up ahead, whole steps behind the end) must not pass the limit."""
+    c = _ctx("mla", bs=256)
+    blocks, cap = 1 << 23, 2 ** 31 - 1 - 8192
+    for n, status in ((cap, CAPACITY), (cap + 1, RANGE), (2 ** 31 - 33, RANGE), (2 ** 31 - 1, RANGE)):
+        assert _attend(c, hq=16, q_stride=16 * 1152, v=None, max_blocks=blocks, max_len=n, ws_bytes=0) == status, n
+    pic.pic_destroy(c)
