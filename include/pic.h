@@ -662,7 +662,7 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* tokens, void* k_
                             const int32_t* d_block_tables, int32_t n_tables, int32_t max_blocks, float* d_weights,
                             int32_t weight_heads, void* d_workspace, size_t workspace_bytes, pic_stream_t stream);
 
-/* Workspace bytes of pic_attend_paged (for sequences up to max_seq_len). */
+/* Workspace bytes of pic_attend_paged (for sequences up to max_seq_len); 0 for sizes that it refuses. */
 size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32_t num_q_heads, int32_t max_seq_len,
                                         int32_t with_weights);
 
@@ -696,7 +696,7 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
                             int32_t max_seq_len, void* out, int32_t out_type, float* lse, float* d_weights,
                             int32_t weight_heads, void* d_workspace, size_t workspace_bytes, pic_stream_t stream);
 
-/* Workspace bytes of pic_evict_tokens. */
+/* Workspace bytes of pic_evict_tokens; 0 for sizes that it refuses. */
 size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t n_req, int32_t weight_heads);
 
 /*

@@ -120,6 +120,14 @@ PagedLayout paged_layout(const CtxView& c, int64_t n_req, int64_t q_heads, int64
 bool paged_heads_ok(const CtxView& c, int32_t num_q_heads) {
   return num_q_heads > 0 && num_q_heads % c.model->num_kv_heads == 0;
 }
+// What one call takes: sizes beyond it would overflow the kernels' counts (and a workspace's size).
+bool paged_size_ok(int64_t n_req, int64_t num_q_heads) {
+  return num_q_heads <= kPagedMaxHeads && n_req * num_q_heads <= std::numeric_limits<int32_t>::max() / 2;
+}
+bool evict_size_ok(const CtxView& c, int64_t num_layers, int64_t n_req) {
+  const int64_t row_items = static_cast<int64_t>(c.model->num_kv_heads) * c.model->head_dim * 2 / 32;
+  return num_layers <= c.model->num_layers && num_layers * n_req <= std::numeric_limits<int32_t>::max() / 2 / row_items;
+}
 
 // How finely the move slices the kept rows of each (layer, request, tensor,
 // and head where heads keep sets of their own): into as many slices of whole
@@ -272,7 +280,7 @@ size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32
                                         int32_t with_weights) {
   if (!ctx || n_req < 0 || max_seq_len < 0) return 0;
   const CtxView c = ctx_view(ctx);
-  if (!paged_heads_ok(c, num_q_heads)) return 0;
+  if (!paged_heads_ok(c, num_q_heads) || !paged_size_ok(n_req, num_q_heads) || max_seq_len > kPagedMaxSlots) return 0;
   return paged_layout(c, n_req, num_q_heads, max_seq_len, with_weights != 0).total;
 }
 
@@ -297,10 +305,8 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
     return fail(ctx, PIC_ERR_INVALID_ARG, "null q, cache, block table, lengths, out or workspace");
   const int64_t q_bytes = static_cast<int64_t>(num_q_heads) * m.head_dim * 2;
   const int64_t row_bytes = static_cast<int64_t>(m.num_kv_heads) * m.head_dim * 2;
-  if (row_bytes > std::numeric_limits<int32_t>::max() || num_q_heads > kPagedMaxHeads || q_bytes > std::numeric_limits<int32_t>::max())
-    return fail(ctx, PIC_ERR_RANGE, "too many heads");
-  if (static_cast<int64_t>(n_req) * num_q_heads > std::numeric_limits<int32_t>::max() / 2)
-    return fail(ctx, PIC_ERR_RANGE, "more than 2^30 query heads in all");
+  if (row_bytes > std::numeric_limits<int32_t>::max() || !paged_size_ok(n_req, num_q_heads))
+    return fail(ctx, PIC_ERR_RANGE, "more than %d query heads, or 2^30 in all", kPagedMaxHeads);
   if (n_req > 1 && q_stride < q_bytes) return fail(ctx, PIC_ERR_RANGE, "q_stride smaller than a request's heads");
   if (max_seq_len > table_capacity(c, max_blocks))
     return fail(ctx, PIC_ERR_RANGE, "max_seq_len %d exceeds the %d slots a block table holds", max_seq_len,
@@ -355,7 +361,9 @@ pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32
 }
 
 size_t pic_evict_workspace_bytes(const pic_ctx* ctx, int32_t num_layers, int32_t n_req, int32_t weight_heads) {
-  if (!ctx || num_layers <= 0 || n_req < 0 || !weight_heads_ok(ctx_view(ctx), weight_heads)) return 0;
+  if (!ctx || num_layers <= 0 || n_req < 0) return 0;
+  const CtxView c = ctx_view(ctx);
+  if (!weight_heads_ok(c, weight_heads) || !evict_size_ok(c, num_layers, n_req)) return 0;
   return evict_layout(num_layers, n_req, weight_heads).total;
 }
 
@@ -387,7 +395,7 @@ pic_status pic_evict_tokens(pic_ctx* ctx, int32_t num_layers, void* k_cache, voi
   if (!aligned(d_weights, 4) || (weights_ls & 3) || !aligned(d_tables, 4) || !aligned(d_seq_lens, 4) ||
       !aligned(d_kept, 4) || !aligned(d_new_lens, 4) || !aligned(d_ws, kWsAlign))
     return fail(ctx, PIC_ERR_ALIGNMENT, "weights, tables, lengths and lists must be 4-byte aligned, the workspace 256-byte");
-  if (static_cast<int64_t>(num_layers) * n_req * (row_bytes / 32) > std::numeric_limits<int32_t>::max() / 2)
+  if (!evict_size_ok(c, num_layers, n_req))
     return fail(ctx, PIC_ERR_RANGE, "layers x requests x row slices must stay below 2^30");
   const EvictLayout L = evict_layout(num_layers, n_req, weight_heads);
   if (ws_bytes < L.total) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, L.total);

@@ -302,3 +302,15 @@ def test_lengths_near_the_integer_limit_are_refused():
     for n, status in ((cap, CAPACITY), (cap + 1, RANGE), (2 ** 31 - 33, RANGE), (2 ** 31 - 1, RANGE)):
         assert _attend(c, hq=16, q_stride=16 * 1152, v=None, max_blocks=blocks, max_len=n, ws_bytes=0) == status, n
     pic.pic_destroy(c)
+
+def test_workspace_sizes_of_what_the_calls_refuse_are_zero(gqa, mla):
+    """No size wraps around: what is more than a call takes has no workspace."""
+    size = pic.load().pic_attend_paged_workspace_bytes
+    assert size(gqa, 1, 4096, 64, 1) > 0 and size(gqa, 1, 4098, 64, 1) == 0
+    longest = 2 ** 31 - 1 - 8192
+    assert size(gqa, 1 << 18, 4096, longest, 1) == 0 and size(gqa, 1, 4, longest + 1, 0) == 0
+    assert size(gqa, 2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 1, 1) == 0
+    assert size(mla, (1 << 18) - 1, 4096, longest, 1) > 2 ** 60
+    size = pic.load().pic_evict_workspace_bytes
+    assert size(gqa, 2, 1000, 2) > 0 and size(gqa, 3, 1000, 2) == 0
+    assert size(gqa, 2, 2 ** 31 - 1, 2) == 0
