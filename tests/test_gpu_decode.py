@@ -1006,3 +1006,105 @@ def test_requests_without_blocks():
                          workspace=ws)
     assert _status(c, ws) == pic.PIC_DEV_BAD_BLOCK and torch.equal(c.k, before)
     c.close()
+
+
+@pytest.mark.parametrize("kind,heads,hq,d,pairing,n_tok", [("gqa", 8, 32, 128, "neox", 5000), ("gqa", 4, 9, 256, "interleaved", 5001),
+                                                           ("gqa", 2, 61, 64, "neox", 4999), ("mla", 1, 64, 576, "interleaved", 2500)])
+def test_write_tokens_prompts(kind, heads, hq, d, pairing, n_tok):
+    """As many tokens as make a warp take all heads of its token, in several rounds of its two row buffers."""
+    c = Cache(kind, heads=heads, d=d, pairing=pairing, lens=[3, 40], room=-(-n_tok // 2) + 16, seed=hq)
+    _write(c, n_tok, 3, hq)
+    c.close()
+
+
+@pytest.mark.parametrize("kind", ["gqa", "mla"])
+@pytest.mark.parametrize("renumber", [False, True])
+def test_evict_layers_apart(kind, renumber):
+    """Caches and weights whose layers are slices of larger tensors: nothing between the layers is touched."""
+    c = Cache(kind, heads=2, d=64, layers=3, lens=[150, 61, 90], seed=80)
+    joint = c.normal(3, 2, *c.k.shape[1:])
+    weights = torch.rand((3, 5, *c.w.shape[1:]), generator=c.g, device=DEV)
+    joint[:, 0], weights[:, 2] = c.k, c.w
+    if kind == "gqa":
+        joint[:, 1] = c.v
+        c.v = joint[:, 1]
+    between = weights.clone(), joint[:, 1].clone()
+    c.k, c.w = joint[:, 0], weights[:, 2]
+    assert not c.k.is_contiguous() and not c.w.is_contiguous()
+    _evict(c, 60, 3, 20, renumber)
+    assert all(torch.equal(weights[:, i], between[0][:, i]) for i in (0, 1, 3, 4))
+    if kind == "mla":
+        assert torch.equal(joint[:, 1], between[1])
+    c.close()
+
+
+@pytest.mark.parametrize("out_type", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hq", [5, 16, 33])
+def test_attend_paged_mla_steps(hq, out_type):
+    """Lengths around one and two 16-slot tiles, which make up a 32-slot step, weights kept."""
+    c = Cache("mla", bs=16, lens=[15, 16, 17, 31, 32, 33, 47, 48, 49, 1, 63, 64, 65, 0, 80], seed=hq)
+    _attend(c, hq, out_type, scale=0.03)
+    c.close()
+
+
+def test_attend_paged_mla_ranges_of_several_steps():
+    """Hundreds of requests of one to seven tiles: ranges hold several requests and steps, and end within a step."""
+    lens = [int(x) for x in np.random.default_rng(9).integers(0, 112, size=240)] + [31, 32, 33, 47, 48, 49]
+    c = Cache("mla", bs=16, lens=lens, seed=81)
+    hq, n, scale = 20, len(lens), 0.03
+    q = c.normal(n, hq, 576) * 2
+    out, lse = torch.empty(n, hq, 512, device=DEV), torch.empty(n, hq, device=DEV)
+    ws, w = _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, n, hq, max(lens), True)), c.w[0].clone()
+    pic.pic_attend_paged(c.ctx, q, scale, c.k[0], None, c.d_tables, c.d_lens, max(lens), out, lse=lse, weights=w, workspace=ws)
+    assert _status(c, ws) == 0
+    _check_batch(c, q, c.k[0], c.k[0][..., :512], scale, out, lse, w)
+    c.close()
+
+
+def _check_batch(c, q, k, v, scale, out, lse, w):
+    """_check_attend's bounds for a batch at once, in 64 bits on the device (the largest score error serves all)."""
+    n, hq, T = len(c.lens), q.shape[1], max(c.lens)
+    pages, heads = c.d_tables.long(), k.shape[2]
+    rows = k[pages].flatten(1, 2).double()                                    # [request, slot, head, dim]
+    live = torch.arange(rows.shape[1], device=DEV)[None] < c.d_lens[:, None]
+    qg = q.double().reshape(n, heads, hq // heads, -1)
+    x = scale * torch.einsum("rhgd,rthd->rhgt", qg, rows)
+    s_err = scale * torch.einsum("rhgd,rthd->rhgt", qg.abs(), rows.abs()).max().item() * (q.shape[2] + 8) * 2.0 ** -23
+    del rows
+    x.masked_fill_(~live[:, None, None], -math.inf)
+    want_lse = torch.logsumexp(x, -1).reshape(n, hq)
+    p = torch.softmax(x, -1).nan_to_num(0.0)
+    vals = v[pages].flatten(1, 2).double() * live[..., None, None]
+    want = torch.einsum("rhgt,rthd->rhgd", p, vals).reshape(n, hq, -1)
+    size = torch.einsum("rhgt,rthd->rhgd", p, vals.abs()).reshape(n, hq, -1)
+    rel = 2 * s_err + 2.0 ** -20 + T * 2.0 ** -23
+    bf16 = out.dtype == torch.bfloat16
+    lim = (rel + (2.0 ** -16 if bf16 else 0)) * size + (2.0 ** -8 * want.abs() * (1 + rel) if bf16 else 0)
+    assert bool(((out.double() - want).abs() <= lim).all())
+    some = c.d_lens > 0
+    assert bool(((lse.double() - want_lse).abs() <= s_err + rel + 2.0 ** -22 * want_lse.abs())[some].all())
+    assert bool(torch.isneginf(lse[~some]).all())
+    if w is not None:
+        share = p.reshape(n, w.shape[1], -1, p.shape[-1]).sum(2)              # [request, weight head, slot]
+        share = share.reshape(n, w.shape[1], -1, c.bs).transpose(1, 2)        # [request, page, weight head, row]
+        at = c.w[0].double()
+        add = torch.zeros_like(at)
+        add[pages.flatten()] = share.flatten(0, 1)
+        assert bool(((w.double() - at - add).abs() <= rel * add + 2.0 ** -22 * torch.where(add > 0, at + add, 0)).all())
+
+
+@pytest.mark.parametrize("out_type", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heads,group,d,weights", [(2, 16, 128, True), (1, 9, 64, True), (1, 24, 128, True), (2, 12, 256, False),
+                                                   (1, 40, 256, True), (3, 17, 64, False)])
+def test_attend_paged_wide_groups_over_long_sequences(heads, group, d, weights, out_type):
+    """9 and more query heads per KV head over ranges of many tiles: the ring goes round, scores leave many times,
+    and requests end within a range."""
+    c = Cache(heads=heads, d=d, bs=16, lens=[9001, 40, 0, 20000, 333, 4097], seed=group, weight_heads=1 if group == 24 else heads)
+    n, hq, T, scale = len(c.lens), heads * group, max(c.lens), d ** -0.5
+    q = c.normal(n, hq, d) * 2
+    out, lse = torch.empty(n, hq, d, dtype=out_type, device=DEV), torch.empty(n, hq, device=DEV)
+    ws, w = _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, n, hq, T, weights)), c.w[0].clone() if weights else None
+    pic.pic_attend_paged(c.ctx, q, scale, c.k[0], c.v[0], c.d_tables, c.d_lens, T, out, lse=lse, weights=w, workspace=ws)
+    assert _status(c, ws) == 0
+    _check_batch(c, q, c.k[0], c.v[0], scale, out, lse, w)
+    c.close()
