@@ -675,7 +675,9 @@ size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32
  * A request with nothing to attend (length 0) gets out 0 and lse -inf.  A length below 0 or above
  * max_seq_len raises PIC_DEV_BAD_LENGTH and counts as 0; slots in a block outside
  * the cache raise PIC_DEV_BAD_BLOCK and are left out.  What the cache holds
- * behind a sequence's end does not matter.
+ * behind a sequence's end does not matter.  Within it values should be finite:
+ * p enters the value product in parts, so an infinite value makes its
+ * dimension NaN or infinite for the heads that read it (and no other).
  * MLA models: k_t is the whole row (q absorbed into the latent space, as for
  * pic_attend_decode), v_t its latent; v_cache is ignored and may be NULL.
  *   q           bf16 [n_req][num_q_heads][head_dim], q_stride bytes between

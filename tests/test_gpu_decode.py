@@ -1108,3 +1108,17 @@ def test_attend_paged_wide_groups_over_long_sequences(heads, group, d, weights, 
     assert _status(c, ws) == 0
     _check_batch(c, q, c.k[0], c.v[0], scale, out, lse, w)
     c.close()
+
+
+def test_attend_paged_infinite_values_stay_in_their_dimension():
+    """An infinite value leaves its dimension of the heads that read it without a number, and changes nothing else."""
+    c = Cache(heads=2, d=128, bs=16, lens=[100, 50], seed=82)
+    q = c.normal(2, 8, 128)
+    clean, lse = _attend(c, 8, torch.float32, weights=False, q=q)
+    c.v[0, int(c.tables[0][2]), 5, 1, 77] = float("inf")
+    out, got, ws = torch.empty_like(clean), torch.empty_like(lse), _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, 2, 8, 100))
+    pic.pic_attend_paged(c.ctx, q, 128 ** -0.5, c.k[0], c.v[0], c.d_tables, c.d_lens, 100, out, lse=got, workspace=ws)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0, 4:, 77] = True
+    assert not bool(torch.isfinite(out[hit]).any()) and torch.equal(out[~hit], clean[~hit]) and torch.equal(got, lse)
+    c.close()
