@@ -689,8 +689,8 @@ size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32
  *               out_type PIC_F32 or PIC_BF16.
  *   lse         float [n_req][num_q_heads] or NULL.
  *   d_weights   one layer of the weights, or NULL.
- * Requests may share blocks, but with d_weights a block may appear once in
- * all tables.  Results do not depend on timing: no atomics are summed.
+ * Requests may share blocks, but with d_weights a block in use may appear once
+ * in all tables.  Results do not depend on timing: no atomics are summed.
  */
 pic_status pic_attend_paged(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_req, int32_t num_q_heads,
                             float softmax_scale, const void* k_cache, const void* v_cache,

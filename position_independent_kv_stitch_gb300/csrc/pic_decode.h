@@ -100,10 +100,10 @@ cudaError_t launch_write(const WriteParams& p, int pairing, cudaStream_t s);
 constexpr int kPagedTile = 16;          // positions of one step of a warp
 constexpr int kPagedMaxSms = 256;       // SMs used (workspace sizing)
 // Up to here the joins walk the requests' lengths themselves, while they wait
-// for the records: 64 requests of 64 slots take 8.5 us (12.9 with weights),
-// against 9.6 (14.7) from what the attention kernel left.  256 of 64 slots take
-// 13.2 (21.7) by walking and 12.7 (18.3) from what was left, 1,024 of 128 slots
-// 45 (70) and 39 (57).
+// for the records: 64 requests of 64 slots take 8.7 us (11.4 with weights),
+// against 9.6 (12.4) from what the attention kernel left.  256 of 64 slots take
+// 13.0 (21.7) by walking and 12.7 (18.4) from what was left, 1,024 of 128 slots
+// with weights 66 and 54.
 constexpr int kPagedWalkRequests = 128;
 constexpr int kPagedMaxHeads = 4096;    // query heads
 

@@ -26,15 +26,16 @@
 // Products: S = Q K^T and O += P V on mma.sync m16n8k16 (bf16 in, fp32
 // accumulate).  A tile has one row per query head of a KV head, 1 to 16 of
 // them: tcgen05's 64 or 128 rows would be mostly padding, and the step waits for
-// memory.  K and V enter as stored; P is an fp32 value and is split into bf16
+// memory.  (32 to 128 heads over latent rows would fill such a tile; they too are
+// done here 16 at a time, see k_paged_latent.)  K and V enter as stored; P is an fp32 value and is split into bf16
 // hi + lo parts (a third part when the output is fp32), each a product of its
 // own, so P keeps 16 (24) significant bits.  With up to 8 query heads the hi and
 // lo parts share one product, in rows g and g + 8.
 //
 // Measured (GB300, 32 query over 8 KV heads of 128 dims, blocks of 16): 64
-// requests of 16,384 slots, fp32 out, 622-640 us (6.7-6.9 TB/s of rows); 64 of
-// 1-8,192 with weights 230 us (without 196: 6.6 TB/s); one of 131,071 with
-// weights 106 us (without 91: 5.9 TB/s); one of 777 8.5-9.5 us; 3,000 of 64 77 us.
+// requests of 16,384 slots, fp32 out, 622-643 us (6.7-6.9 TB/s of rows); 64 of
+// 1-8,192 with weights 229 us (without 196: 6.6 TB/s); one of 131,071 with
+// weights 106 us (without 91: 5.9 TB/s); one of 777 8.4-9.5 us; 3,000 of 64 77 us.
 #include <cfloat>
 
 #include <cuda_bf16.h>
@@ -54,8 +55,10 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 // Warps and ring depth: as many warps as the registers of the running values
 // allow, and the ring that then fits.  Measured (bf16 out, no weights, GB/s): 64
-// dims 12 x 4 5,490 (8 x 6 4,510, 16 x 2 5,570 but spilling), 128 dims 8 x 3
-// 6,780 (12 x 2 6,560, 6 x 4 6,570), 256 dims 4 x 3 5,100 (6 x 2 4,900).
+// dims 12 x 4 5,490 (8 x 6 4,510, 16 x 2 5,570 with spills), 128 dims 8 x 3
+// 6,780 (12 x 2 6,560, 6 x 4 6,570), 256 dims 4 x 3 5,100 (6 x 2 4,900).  At 256
+// dims all 255 registers are used and 24 to 180 bytes a thread spilled; with 16
+// query heads, whose running values are 256 registers' worth, that leaves 3,200 to 3,900.
 __host__ __device__ constexpr int paged_warps(int D) { return D <= 64 ? 12 : (D <= 128 ? 8 : 4); }
 __host__ __device__ constexpr int paged_stages(int D) { return D <= 64 ? 4 : 3; }
 __host__ __device__ constexpr int stage_bytes(int D) { return 2 * TT * D * 2; }
@@ -224,7 +227,8 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
   const int n_heads = min(16, P.group - g0);
   const int hq0 = hk * P.group + g0;
   const int g = lane >> 2, tq = lane & 3;
-  // the rows pass through L2 once; the scores, read again at the end, may stay
+  // the rows pass through L2 once (groups of more than 16 heads: once a pass, by
+  // warps side by side); the scores, read again at the end, may stay
   uint64_t stream_once;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream_once));
 
@@ -405,7 +409,8 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
         ldsm4_t(vb + v_row * D * 2 + (((j + (mi >> 1)) ^ (v_row & 7)) << 4), b);
         if (F32) {
           // the tensor cores round sums towards zero: over a long range that
-          // would show in fp32, so each tile's product is added here instead
+          // would show in fp32 (1e-5 of the result over 16,384 slots; bf16 rounds
+          // by 2e-3), so each tile's product is added here instead
           float y0[4] = {}, y1[4] = {};
 #pragma unroll
           for (int x = 0; x < NP; ++x) {
@@ -492,9 +497,12 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
 //   * warp w adds latent dims 64 w .. 64 w + 63 of every head.
 // The three barriers of a step come between these; two CTAs per SM cover each
 // other's.  Bound: the chain of a step's three parts and mma.sync's rate (400
-// products a step of 37 KB; 600 TFLOP/s measured for mma.sync alone).
+// products a step of 37 KB; 600 TFLOP/s measured for mma.sync alone).  104 bytes a
+// thread are spilled with fp32 output, 28 with bf16.
 // Measured: 64 requests of 8,192 slots, 16 heads, 132 us (4.6 TB/s of
-// rows); 128 heads 927 us (158 TFLOP/s of useful products).
+// rows; fp32 out 159); 128 heads 927 us (158 TFLOP/s of useful products, ten times the
+// time of the rows or the products alone: eight passes of 16 heads; products of
+// 64 or 128 heads on tcgen05, over tiles found from the lengths as here, are not built).
 constexpr int kLatDims = 512, kLatRow = 576;
 constexpr int kLatRowBytes = kLatRow * 2, kLatChunks = kLatRowBytes / 16;
 constexpr int kLatHeads = 16;
@@ -714,8 +722,6 @@ __global__ void __launch_bounds__(kLatThreads, kLatCtas) k_paged_latent(const __
 constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
 constexpr int kFinishWeightCtas = 2;   // per SM, of 3 that fit: the joins run beside them
-
-
 
 // The records of request r: the ranges that cross its n tiles (first: its
 // first tile in the list).
