@@ -27,8 +27,8 @@
 // accumulate).  A tile has one row per query head of a KV head, 1 to 16 of
 // them: tcgen05's 64 or 128 rows would be mostly padding, and the step waits for
 // memory.  (32 to 128 heads over latent rows would fill such a tile; they too are
-// done here 16 at a time, see k_paged_latent.)  K and V enter as stored; P is an fp32 value and is split into bf16
-// hi + lo parts (a third part when the output is fp32), each a product of its
+// done here 16 at a time, see k_paged_latent.)  K and V enter as stored; P is an
+// fp32 value and is split into bf16 hi + lo parts (a third part when the output is fp32), each a product of its
 // own, so P keeps 16 (24) significant bits.  With up to 8 query heads the hi and
 // lo parts share one product, in rows g and g + 8.
 //

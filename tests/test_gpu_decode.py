@@ -1122,3 +1122,86 @@ def test_attend_paged_infinite_values_stay_in_their_dimension():
     hit[0, 4:, 77] = True
     assert not bool(torch.isfinite(out[hit]).any()) and torch.equal(out[~hit], clean[~hit]) and torch.equal(got, lse)
     c.close()
+
+
+def test_attend_captured_many_requests_and_other_lengths():
+    """A graph of an attention over more requests than the joins walk, replayed for other lengths, none among them."""
+    n, longest = 300, 90
+    c = Cache(heads=2, d=64, bs=16, lens=[longest] * n, seed=90)
+    q = c.normal(n, 8, 64) * 2
+    out, lse = torch.empty(n, 8, 64, device=DEV), torch.empty(n, 8, device=DEV)
+    ws, w, lens = _ws(pic.pic_attend_paged_workspace_bytes(c.ctx, n, 8, longest, True)), c.w[0].clone(), c.d_lens.clone()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            pic.pic_attend_paged(c.ctx, q, 0.125, c.k[0], c.v[0], c.d_tables, lens, longest, out, lse=lse, weights=w, workspace=ws)
+    torch.cuda.synchronize()
+    rng = np.random.default_rng(1)
+    for new in (np.full(n, longest), rng.integers(0, longest + 1, n), np.zeros(n, int), np.arange(n) % 2, (np.arange(n) == 299) * 17):
+        c.lens, c.d_lens = [int(x) for x in new], _i32(new)
+        lens.copy_(c.d_lens)
+        w.copy_(c.w[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        if max(c.lens) == 0:
+            assert bool((out == 0).all()) and bool(torch.isneginf(lse).all()) and torch.equal(w, c.w[0])
+        else:
+            _check_batch(c, q, c.k[0], c.v[0], 0.125, out, lse, w)
+    assert _status(c, ws) == 0
+    c.close()
+
+
+@pytest.mark.parametrize("kind", ["gqa", "mla"])
+def test_two_loops_at_once(kind):
+    """Two streams write, attend and evict at the same time, each on caches and a workspace of its own: what they
+    leave is what each leaves alone, whichever way the stream is named."""
+    hq, budget = 8, 200
+
+    def prepare(c, stream, how):
+        g = torch.Generator(device=DEV).manual_seed(5)
+        n, dv = len(c.lens), 512 if kind == "mla" else c.d
+        lens, ws = c.d_lens.clone(), _ws(1 << 26)
+        out, kept = torch.empty(n, hq, dv, device=DEV), torch.empty(1, n, c.wh, budget, dtype=torch.int32, device=DEV)
+        rows = torch.randn((6, n, hq + 2 * c.heads, c.d), generator=g, device=DEV).to(torch.bfloat16)
+        q_out, req, v_cache = torch.empty(n, hq, c.d, dtype=torch.bfloat16, device=DEV), _i32(range(n)), None if c.v is None else c.v[0]
+        longest, slot = c.tables.shape[1] * c.bs, torch.empty_like(lens)
+        s = dict(stream=None if how == "current" else stream if how == "object" else stream.cuda_stream)
+
+        def step(x):
+            with torch.cuda.stream(stream):
+                slot.copy_(lens)
+                lens.add_(1)
+                v = x[:, hq + c.heads:] if kind == "gqa" else None
+                pic.pic_write_tokens(c.ctx, slot, x[:, hq:hq + c.heads], v, req, slot, c.d_tables, c.k[0], v_cache, q=x[:, :hq],
+                                     q_out=q_out, weights=c.w[0], workspace=ws, **s)
+                pic.pic_attend_paged(c.ctx, q_out, 0.05, c.k[0], v_cache, c.d_tables, lens, longest, out, weights=c.w[0],
+                                     workspace=ws, **s)
+                pic.pic_evict_tokens(c.ctx, c.k, c.v, c.w, c.d_tables, lens, budget, kept, lens, n_first=4, n_recent=20,
+                                     renumber=True, workspace=ws, **s)
+        return [lambda x=x: step(x) for x in rows], (out, kept, lens, c.k, c.v, c.w, ws)
+
+    def caches():
+        return [Cache(kind, heads=2, d=128, lens=[900, 300, 2000 + i, 190], room=16, seed=91 + i) for i in range(2)]
+
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    alone, together = caches(), caches()
+    want, got = [], []
+    for c, stream in zip(alone, streams):
+        steps, left = prepare(c, stream, "current")
+        torch.cuda.synchronize()
+        for step in steps:
+            step()
+        torch.cuda.synchronize()
+        want.append(left)
+    both = [prepare(c, stream, how) for c, stream, how in zip(together, streams, ("object", "handle"))]
+    got = [left for _, left in both]
+    torch.cuda.synchronize()
+    for one, other in zip(both[0][0], both[1][0]):
+        one()
+        other()
+    torch.cuda.synchronize()
+    for a, b, c in zip(want, got, together):
+        assert _status(c, b[-1]) == 0
+        assert all(x is None and y is None or torch.equal(x, y) for x, y in zip(a[:-1], b[:-1]))
+    for c in alone + together:
+        c.close()
