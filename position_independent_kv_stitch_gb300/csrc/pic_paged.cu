@@ -28,9 +28,9 @@
 // them: tcgen05's 64 or 128 rows would be mostly padding, and the step waits for
 // memory.  (32 to 128 heads over latent rows would fill such a tile; they too are
 // done here 16 at a time, see k_paged_latent.)  K and V enter as stored; P is an
-// fp32 value and is split into bf16 hi + lo parts (a third part when the output is fp32), each a product of its
-// own, so P keeps 16 (24) significant bits.  With up to 8 query heads the hi and
-// lo parts share one product, in rows g and g + 8.
+// fp32 value and is split into bf16 hi + lo parts (a third part when the output is
+// fp32), each a product of its own, so P keeps 16 (24) significant bits.  With up to
+// 8 query heads the hi and lo parts share one product, in rows g and g + 8.
 //
 // Measured (GB300, 32 query over 8 KV heads of 128 dims, blocks of 16): 64
 // requests of 16,384 slots, fp32 out, 622-643 us (6.7-6.9 TB/s of rows); 64 of
