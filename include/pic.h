@@ -101,9 +101,10 @@ enum { PIC_F32 = 0, PIC_BF16 = 1 };
 #define PIC_DEV_TIMEOUT 0x2u   /* a bounded wait inside a kernel gave up (never expected) */
 #define PIC_DEV_BAD_TOKEN 0x4u /* chunking: a token id outside [0, vocab); its Gear value taken as 0 */
 #define PIC_DEV_BAD_DOCS 0x8u  /* chunking: document offsets not non-decreasing within [0, n_tokens] */
-#define PIC_DEV_CAPACITY 0x10u /* chunking: more chunks than capacity; the rest were not written */
+#define PIC_DEV_CAPACITY 0x10u /* chunking: more chunks than capacity; the rest were not written
+                                  (token maps: too few free blocks, token rows or places for given-back blocks) */
 #define PIC_DEV_BAD_SPAN 0x20u /* fingerprints: a span outside [0, n_tokens] or with end < start */
-#define PIC_DEV_BAD_LENGTH 0x40u /* decode loop: a sequence length below 0 or beyond its limit */
+#define PIC_DEV_BAD_LENGTH 0x40u /* decode loop: a sequence length, slot, offset or count below 0 or beyond its limit */
 #define PIC_DEV_BAD_POS 0x80u  /* token writes: a position beyond +-PIC_MAX_ABS_DELTA */
 
 /*
@@ -662,6 +663,34 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* tokens, void* k_
                             const int32_t* d_block_tables, int32_t n_tables, int32_t max_blocks, float* d_weights,
                             int32_t weight_heads, void* d_workspace, size_t workspace_bytes, pic_stream_t stream);
 
+/*
+ * Norms of the heads of new tokens (pic_write_normed_tokens): a head x becomes
+ * x / sqrt(mean(x^2) + eps) * (offset + weight), element by element.
+ *   q_weight     [head_dim], for every query head; NULL: queries as they are.  MLA
+ *                models: NULL (queries are in the latent space).
+ *   k_weight     GQA: [head_dim], for every key head; MLA: [512], for the latent of a
+ *                row, whose rope key stays as it is.  NULL: keys as they are.
+ *   weight_type  PIC_F32 or PIC_BF16, both weights; 16-byte aligned.
+ *   eps          >= 0; offset: finite, 0 for weights that multiply as they are.
+ */
+typedef struct pic_head_norms {
+  const void* q_weight;
+  const void* k_weight;
+  int32_t weight_type;
+  float eps;
+  float offset;
+} pic_head_norms;
+
+/*
+ * pic_write_tokens with the heads normalised before they are turned, in the same
+ * pass: norm and rotation in fp32, one rounding to bf16.  Values are written as
+ * they are.  Everything else as pic_write_tokens.
+ */
+pic_status pic_write_normed_tokens(pic_ctx* ctx, const pic_new_tokens* tokens, const pic_head_norms* norms, void* k_cache,
+                                   void* v_cache, const int32_t* d_block_tables, int32_t n_tables, int32_t max_blocks,
+                                   float* d_weights, int32_t weight_heads, void* d_workspace, size_t workspace_bytes,
+                                   pic_stream_t stream);
+
 /* Workspace bytes of pic_attend_paged (for sequences up to max_seq_len); 0 for sizes that it refuses. */
 size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32_t num_q_heads, int32_t max_seq_len,
                                         int32_t with_weights);
@@ -730,6 +759,132 @@ pic_status pic_evict_tokens(pic_ctx* ctx, int32_t num_layers, void* k_cache, voi
                             const int32_t* d_seq_lens, int32_t budget, int32_t n_first, int32_t n_recent,
                             int32_t renumber, int32_t* d_kept, int32_t* d_new_lens, void* d_workspace,
                             size_t workspace_bytes, pic_stream_t stream);
+
+/* ------------------------------------------ a serving step's other calls */
+
+/*
+ * The calls around a decode loop's: which block and slot each new token gets,
+ * attention of any number of new tokens per request (prompts, recomputed chunk
+ * heads, decode tokens), and decode attention of requests that share a prefix.
+ * They keep the decode loop's conventions: device arrays, sticky status,
+ * nothing uploaded, allocated or waited for, captured at will, buffers of the
+ * current device, workspaces of their own for calls that may run at once.
+ */
+
+/*
+ * One step of a serving loop in blocks and slots.  Request r holds d_seq_lens[r]
+ * slots, ceil(length / block_size) blocks of its row of the tables, and changes by
+ * d_grow[r]:
+ *   below 0  its last slots go; blocks that hold none any more are put on the pile
+ *            of free blocks, in the order of requests and then of the table (whose
+ *            entries stay as they were);
+ *   above 0  it gets that many new tokens; the blocks it needs for them are taken
+ *            from the top of the pile, in the order of requests and then of the
+ *            table, after everything that was given back in this call.
+ * The pile is d_free_blocks[0 .. *d_n_free).  A request whose blocks are not
+ * there any more, or whose tokens do not all fit n_tokens, raises
+ * PIC_DEV_CAPACITY and is refused: no blocks, its length unchanged, its tokens
+ * slot -1 (pic_write_tokens and pic_attend_tokens take them as padding).  What it
+ * would have needed counts against the requests behind it, so that the outcome
+ * does not depend on anything but the order.  A request that needs no new block is not
+ * refused for want of one.  Blocks given back that would overflow the pile
+ * (tables that share blocks) raise PIC_DEV_CAPACITY and leave their request unchanged,
+ * and every shrinking request behind it.
+ * A length below 0 or beyond the table, before or after, raises
+ * PIC_DEV_BAD_LENGTH; the request is refused.  So does *d_n_free outside [0,
+ * num_cache_blocks], which counts as 0.  A block outside the cache is moved like any
+ * other and raises PIC_DEV_BAD_BLOCK.
+ *   n_req, max_blocks  rows and columns of d_block_tables.
+ *   d_block_tables     int32 [n_req][max_blocks], new blocks are filled in.
+ *   d_free_blocks      int32 [num_cache_blocks].
+ *   d_n_free           int32 [1]; d_new_n_free: after the call, may be d_n_free.
+ *   d_new_lens         int32 [n_req]: lengths after the call, may be d_seq_lens.
+ *   n_tokens           rows of the token lists, at least the tokens of all requests.
+ *   d_indptr           int32 [n_req + 1]: request r's tokens are rows [indptr[r],
+ *                      indptr[r + 1]) (refused ones too, as far as there are rows).
+ *   d_req, d_slot      int32 [n_tokens]: request and slot of each row; rows behind
+ *                      the last request's: 0 and -1.
+ *   d_shift, d_pos     d_pos (or NULL) int32 [n_tokens]: slot + d_shift[r] (int32
+ *                      [n_req], NULL: 0), the token's position where tokens before
+ *                      it have been evicted; 0 where the slot is -1.
+ * No input may be an output but for the two pairs named.
+ */
+typedef struct pic_token_map {
+  int32_t n_req;
+  int32_t max_blocks;
+  int32_t n_tokens;
+  const int32_t* d_seq_lens;
+  const int32_t* d_grow;
+  int32_t* d_block_tables;
+  int32_t* d_free_blocks;
+  const int32_t* d_n_free;
+  const int32_t* d_shift;
+  int32_t* d_new_lens;
+  int32_t* d_new_n_free;
+  int32_t* d_indptr;
+  int32_t* d_req;
+  int32_t* d_slot;
+  int32_t* d_pos;
+} pic_token_map;
+
+size_t pic_map_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_req);
+pic_status pic_map_tokens(pic_ctx* ctx, const pic_token_map* map, void* d_workspace, size_t workspace_bytes,
+                          pic_stream_t stream);
+
+/*
+ * New tokens attend to the paged cache of their requests (GQA models; one
+ * layer).  Row i of q, a token of request r where indptr[r] <= i < indptr[r + 1],
+ * with slot s = d_slot[i], sees the slots t <= s of its request that lie in the
+ * window, t > s - window, or among the first, t < n_first (window 0: all t <= s):
+ *   out_i = sum_t p_t v_t,  p = softmax over those of softmax_scale * q_i . k_t,
+ *   lse_i = log sum_t exp(softmax_scale * q_i . k_t).
+ * The tokens' own keys and values are in the cache before the call
+ * (pic_write_tokens).  A row with slot < 0 sees nothing: out 0, lse -inf.  Rows before
+ * indptr[0] or from indptr[n_req] on stay as they are.  Slots of a request may
+ * come in any order and more than once: the recompute list of a stitch
+ * (d_recompute_idx, d_recompute_indptr) is a d_slot and d_indptr.
+ * A slot that its table does not hold raises PIC_DEV_BAD_LENGTH and its row sees
+ * nothing; so do the offsets where they are not non-decreasing inside [0, n_tokens]
+ * (rows of such requests are then unspecified).  Slots in a block outside the cache raise
+ * PIC_DEV_BAD_BLOCK and are left out.  Blocks of slots that no token of the
+ * request can see, those before the window of its lowest slot but for the first n_first
+ * and those behind its highest, are not looked at (they may have been given back),
+ * and what the cache holds at such slots does not matter.  Between them values
+ * should be finite: an infinite one makes its dimension NaN or infinite for other
+ * rows of its request too.
+ *   q         bf16 [n_tokens][num_q_heads][head_dim], q_stride bytes between rows.
+ *   out       bf16 [n_tokens][num_q_heads][head_dim], dense; must not overlap q.
+ *   lse       float [n_tokens][num_q_heads] or NULL.
+ *   softmax_scale  finite.
+ * Results do not depend on timing.  PIC_ERR_UNSUPPORTED for MLA models.
+ */
+size_t pic_attend_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_tokens, int32_t n_req, int32_t num_q_heads);
+pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_tokens, int32_t num_q_heads,
+                             float softmax_scale, const void* k_cache, const void* v_cache, const int32_t* d_block_tables,
+                             int32_t n_req, int32_t max_blocks, const int32_t* d_indptr, const int32_t* d_slot,
+                             int32_t window, int32_t n_first, void* out, float* lse, void* d_workspace,
+                             size_t workspace_bytes, pic_stream_t stream);
+
+/*
+ * pic_attend_paged for requests that share their first *d_prefix_len slots: these
+ * are read through d_prefix_table, once for all requests, and the slots from
+ * there to d_seq_lens[r] through each request's own row of d_block_tables
+ * (whose entries for slots of the prefix are not looked at).  The prefix may
+ * end inside a block.  A request shorter than the prefix attends to its first
+ * d_seq_lens[r] slots; one of length 0 gets out 0 and lse -inf.
+ *   d_prefix_table  int32 [prefix_blocks].
+ *   d_prefix_len    int32 [1]; outside [0, prefix_blocks * block_size] it
+ *                   raises PIC_DEV_BAD_LENGTH and counts as 0.
+ *   out             bf16 [n_req][num_q_heads][head_dim], dense.
+ * Everything else as for pic_attend_paged (no weights, and values of the prefix
+ * should be finite for every request).  PIC_ERR_UNSUPPORTED for MLA models.
+ */
+size_t pic_attend_shared_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32_t num_q_heads);
+pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_req, int32_t num_q_heads,
+                             float softmax_scale, const void* k_cache, const void* v_cache, const int32_t* d_prefix_table,
+                             int32_t prefix_blocks, const int32_t* d_prefix_len, const int32_t* d_block_tables,
+                             int32_t max_blocks, const int32_t* d_seq_lens, int32_t max_seq_len, void* out, float* lse,
+                             void* d_workspace, size_t workspace_bytes, pic_stream_t stream);
 
 /* ------------------------------------------- content-defined chunking */
 

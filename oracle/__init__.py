@@ -114,3 +114,4 @@ from .pic_oracle import (  # noqa: F401
     attention_decode,
     sink_bias,
 )
+from . import serve_oracle as serve  # noqa: F401

@@ -1,129 +1,16 @@
 // Host entries of the decode-loop operators: pic_write_tokens,
-// pic_attend_paged and pic_evict_tokens (include/pic.h).  They check their
+// pic_write_normed_tokens, pic_attend_paged and pic_evict_tokens (include/pic.h).  They check their
 // arguments, fill the launch parameters and launch; they allocate nothing,
 // upload nothing and wait for nothing, so they can be captured into a graph.
-#include "pic_decode.h"
+#include "pic_entry.h"
 
-#include <algorithm>
-#include <cstdarg>
-#include <cstdio>
-#include <cstring>
-#include <limits>
+#include <cmath>
 
 namespace {
 
 using namespace pic;
+using namespace pic::entry;
 
-pic_status fail(pic_ctx* ctx, pic_status st, const char* fmt, ...) __attribute__((format(printf, 3, 4)));
-pic_status fail(pic_ctx* ctx, pic_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  return set_error(ctx, st, buf);
-}
-pic_status cuda_fail(pic_ctx* ctx, cudaError_t e, const char* what) {
-  return fail(ctx, PIC_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// The launching device, and that every buffer is memory of that device: these
-// operators stream with no regard to the host link, and a pageable host
-// pointer would fault.
-struct Buffer {
-  const char* name;
-  const void* ptr;
-};
-pic_status check_device(pic_ctx* ctx, const Buffer* bufs, int n, int* sm_count) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaGetDevice");
-  static std::atomic<int> sms_of[32];   // 0: not asked for yet
-  *sm_count = dev < 32 ? sms_of[dev].load(std::memory_order_relaxed) : 0;
-  if (*sm_count == 0) {
-    e = cudaDeviceGetAttribute(sm_count, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaDeviceGetAttribute");
-    if (dev < 32) sms_of[dev].store(*sm_count, std::memory_order_relaxed);
-  }
-  for (int i = 0; i < n; ++i) {
-    if (!bufs[i].ptr) continue;
-    cudaPointerAttributes a;
-    e = cudaPointerGetAttributes(&a, bufs[i].ptr);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return fail(ctx, PIC_ERR_INVALID_ARG, "%s is not memory the GPU can reach", bufs[i].name);
-    }
-    if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
-      return fail(ctx, PIC_ERR_UNSUPPORTED, "%s must be device memory", bufs[i].name);
-    if (a.type == cudaMemoryTypeDevice && a.device != dev)
-      return fail(ctx, PIC_ERR_INVALID_ARG, "%s is on device %d, the current device is %d", bufs[i].name, a.device, dev);
-  }
-  return PIC_OK;
-}
-
-PagedView paged_view(const CtxView& c, const int32_t* d_tables, int32_t n_tables, int32_t max_blocks) {
-  PagedView v{};
-  v.tables = d_tables;
-  v.n_tables = n_tables;
-  v.max_blocks = max_blocks;
-  v.num_cache_blocks = c.num_cache_blocks;
-  v.block_size = c.model->block_size;
-  int32_t log2 = 0;
-  while (int64_t{1} << log2 < v.block_size) ++log2;
-  v.block_shift = 31 + log2;
-  v.block_mul = static_cast<uint32_t>(((uint64_t{1} << v.block_shift) + v.block_size - 1) / v.block_size);
-  return v;
-}
-
-void fill_freq(const CtxView& c, FreqTable* t) { std::memcpy(t->turns, c.freq, c.model->rope_dim / 2 * sizeof(float2)); }
-
-// Longest sequence a block table can hold (none, where the cache has no block).
-int32_t table_capacity(const CtxView& c, int32_t max_blocks) {
-  if (c.num_cache_blocks == 0) return 0;
-  const int64_t n = static_cast<int64_t>(max_blocks) * c.model->block_size;
-  return static_cast<int32_t>(std::min<int64_t>(n, kPagedMaxSlots));
-}
-
-// Rows of the cache: a sequence whose blocks are all its own is no longer.
-int32_t cache_rows(const CtxView& c) {
-  return static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(c.num_cache_blocks) * c.model->block_size, kPagedMaxSlots));
-}
-
-bool weight_heads_ok(const CtxView& c, int32_t n) { return n == 1 || n == c.model->num_kv_heads; }
-
-struct PagedLayout {
-  size_t first, lse2, rec_ml, rec_acc, scores, total;
-  int64_t score_stride;
-};
-int32_t paged_passes(int32_t group) { return (group + 15) / 16; }
-// Width of an output row: the head's, or the latent's.
-int32_t paged_out_dim(const CtxView& c) { return c.model->kind == PIC_KIND_MLA ? c.model->rope_offset : c.model->head_dim; }
-int64_t paged_max_parts(int32_t v_heads, int head_dim) {
-  return std::max<int64_t>(1, static_cast<int64_t>(kPagedMaxSms) * paged_ranges_per_sm(head_dim) / v_heads);
-}
-PagedLayout paged_layout(const CtxView& c, int64_t n_req, int64_t q_heads, int64_t max_len, bool weights) {
-  const int d = paged_out_dim(c);
-  const int32_t group = static_cast<int32_t>(q_heads / c.model->num_kv_heads);
-  const int64_t recs = paged_max_parts(c.model->num_kv_heads * paged_passes(group), c.model->head_dim) + n_req;
-  PagedLayout L{};
-  L.score_stride = weights ? n_req * ((max_len + kPagedTile - 1) / kPagedTile) * kPagedTile : 0;
-  L.first = sizeof(WsHeader);
-  L.lse2 = align_up(L.first + (n_req + 1) * sizeof(int64_t), kWsAlign);
-  L.rec_ml = align_up(L.lse2 + (weights ? n_req * q_heads * sizeof(float) : 0), kWsAlign);
-  L.rec_acc = align_up(L.rec_ml + recs * q_heads * sizeof(float2), kWsAlign);
-  L.scores = align_up(L.rec_acc + recs * q_heads * d * sizeof(float), kWsAlign);
-  L.total = align_up(L.scores + static_cast<size_t>(q_heads) * L.score_stride * sizeof(float), kWsAlign);
-  return L;
-}
-bool paged_heads_ok(const CtxView& c, int32_t num_q_heads) {
-  return num_q_heads > 0 && num_q_heads % c.model->num_kv_heads == 0;
-}
-// What one call takes: sizes beyond it would overflow the kernels' counts (and a workspace's size).
-bool paged_size_ok(int64_t n_req, int64_t num_q_heads) {
-  return num_q_heads <= kPagedMaxHeads && n_req * num_q_heads <= std::numeric_limits<int32_t>::max() / 2;
-}
 bool evict_size_ok(const CtxView& c, int64_t num_layers, int64_t n_req) {
   const int64_t row_items = static_cast<int64_t>(c.model->num_kv_heads) * c.model->head_dim * 2 / 32;
   return num_layers <= c.model->num_layers && num_layers * n_req <= std::numeric_limits<int32_t>::max() / 2 / row_items;
@@ -169,13 +56,10 @@ EvictLayout evict_layout(int64_t layers, int64_t n_req, int64_t weight_heads) {
   return L;
 }
 
-}  // namespace
-
-extern "C" {
-
-pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache, void* v_cache,
-                            const int32_t* d_tables, int32_t n_tables, int32_t max_blocks, float* d_weights,
-                            int32_t weight_heads, void* d_ws, size_t ws_bytes, pic_stream_t stream) {
+// pic_write_tokens (norms null) and pic_write_normed_tokens
+pic_status write_tokens(pic_ctx* ctx, const pic_new_tokens* t, const pic_head_norms* norms, void* k_cache, void* v_cache,
+                        const int32_t* d_tables, int32_t n_tables, int32_t max_blocks, float* d_weights, int32_t weight_heads,
+                        void* d_ws, size_t ws_bytes, pic_stream_t stream) {
   if (!ctx || !t) return fail(ctx, PIC_ERR_INVALID_ARG, "null ctx or tokens");
   const CtxView c = ctx_view(ctx);
   const pic_model_desc& m = *c.model;
@@ -187,6 +71,15 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache
   for (int32_t i = 0; t->freq_axis && i < half; ++i)
     if (t->freq_axis[i] >= t->n_axes)
       return fail(ctx, PIC_ERR_INVALID_ARG, "freq_axis[%d] is %d, there are %d axes", i, t->freq_axis[i], t->n_axes);
+  if (norms) {
+    if (mla && norms->q_weight) return fail(ctx, PIC_ERR_INVALID_ARG, "queries in the latent space have no norm");
+    if (norms->weight_type != PIC_F32 && norms->weight_type != PIC_BF16)
+      return fail(ctx, PIC_ERR_INVALID_ARG, "unknown weight_type %d", norms->weight_type);
+    if (!(norms->eps >= 0.0f) || std::isinf(norms->eps) || !std::isfinite(norms->offset))
+      return fail(ctx, PIC_ERR_INVALID_ARG, "eps must be finite and not negative, offset finite");
+    if (!aligned(norms->q_weight, 16) || !aligned(norms->k_weight, 16))
+      return fail(ctx, PIC_ERR_ALIGNMENT, "norm weights must be 16-byte aligned");
+  }
   if (!d_ws || ws_bytes < PIC_STATUS_BYTES) return fail(ctx, PIC_ERR_CAPACITY, "workspace needs %d bytes", PIC_STATUS_BYTES);
   if (t->n_tokens == 0) return set_error(ctx, PIC_OK, "");   // an empty batch has no buffers
   const bool with_q = t->num_q_heads > 0, with_k = t->k != nullptr;
@@ -222,7 +115,9 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache
                          {"positions", t->d_pos}, {"requests", with_k ? t->d_req : nullptr},
                          {"slots", with_k ? t->d_slot : nullptr}, {"k_cache", with_k ? k_cache : nullptr},
                          {"v_cache", with_k && !mla ? v_cache : nullptr}, {"block tables", with_k ? d_tables : nullptr},
-                         {"weights", with_k ? d_weights : nullptr}, {"workspace", d_ws}};
+                         {"weights", with_k ? d_weights : nullptr}, {"workspace", d_ws},
+                         {"q norm", norms && with_q ? norms->q_weight : nullptr},
+                         {"k norm", norms && with_k ? norms->k_weight : nullptr}};
   int sms = 0;
   const pic_status st = check_device(ctx, bufs, sizeof(bufs) / sizeof(bufs[0]), &sms);
   if (st != PIC_OK) return st;
@@ -251,8 +146,16 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache
   const int lanes = half / 8;  // eight frequencies a lane: 4, 8 or 16
   p.lph_shift = lanes == 4 ? 2 : (lanes == 8 ? 3 : 4);
   const int latent_chunks = mla ? m.rope_offset * 2 / 16 : 0;
+  if (norms) {
+    p.q_norm = with_q ? static_cast<const uint8_t*>(norms->q_weight) : nullptr;
+    p.k_norm = with_k ? static_cast<const uint8_t*>(norms->k_weight) : nullptr;
+    p.norm_f32 = norms->weight_type == PIC_F32;
+    p.norm_eps = norms->eps;
+    p.norm_offset = norms->offset;
+    p.latent_norm = mla && p.k_norm != nullptr;
+  }
   p.q_copy_chunks = with_q && t->q != t->q_out ? latent_chunks : 0;
-  p.k_copy_chunks = with_k ? latent_chunks : 0;
+  p.k_copy_chunks = with_k && !p.latent_norm ? latent_chunks : 0;
   p.k_cache = static_cast<uint8_t*>(k_cache);
   p.v_cache = static_cast<uint8_t*>(v_cache);
   p.weights = with_k ? d_weights : nullptr;
@@ -269,11 +172,31 @@ pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache
   const int64_t chunks = static_cast<int64_t>(p.q_heads) * p.q_copy_chunks + p.k_copy_chunks +
                          (t->v ? row_bytes / 16 : 0);
   p.copy_parts = static_cast<int32_t>((chunks + 255) / 256);
-  if (static_cast<int64_t>(t->n_tokens) * (p.rot_parts + p.copy_parts) > std::numeric_limits<int32_t>::max())
+  if (static_cast<int64_t>(t->n_tokens) * (p.rot_parts + p.copy_parts + p.latent_norm) > std::numeric_limits<int32_t>::max())
     return fail(ctx, PIC_ERR_RANGE, "more than 2^31 warps of work: write fewer tokens at a time");
-  const cudaError_t e = launch_write(p, m.pairing, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = p.q_norm || p.k_norm ? launch_write_normed(p, m.pairing, cs) : launch_write(p, m.pairing, cs);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "token write launch");
   return set_error(ctx, PIC_OK, "");
+}
+
+}  // namespace
+
+extern "C" {
+
+pic_status pic_write_tokens(pic_ctx* ctx, const pic_new_tokens* t, void* k_cache, void* v_cache,
+                            const int32_t* d_tables, int32_t n_tables, int32_t max_blocks, float* d_weights,
+                            int32_t weight_heads, void* d_ws, size_t ws_bytes, pic_stream_t stream) {
+  return write_tokens(ctx, t, nullptr, k_cache, v_cache, d_tables, n_tables, max_blocks, d_weights, weight_heads, d_ws, ws_bytes,
+                      stream);
+}
+
+pic_status pic_write_normed_tokens(pic_ctx* ctx, const pic_new_tokens* t, const pic_head_norms* norms, void* k_cache, void* v_cache,
+                                   const int32_t* d_tables, int32_t n_tables, int32_t max_blocks, float* d_weights,
+                                   int32_t weight_heads, void* d_ws, size_t ws_bytes, pic_stream_t stream) {
+  if (!norms) return fail(ctx, PIC_ERR_INVALID_ARG, "null norms");
+  return write_tokens(ctx, t, norms, k_cache, v_cache, d_tables, n_tables, max_blocks, d_weights, weight_heads, d_ws, ws_bytes,
+                      stream);
 }
 
 size_t pic_attend_paged_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32_t num_q_heads, int32_t max_seq_len,

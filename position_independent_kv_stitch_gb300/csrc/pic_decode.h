@@ -92,9 +92,39 @@ struct WriteParams {
   uint8_t* v_cache;
   float* weights;            // [blocks][weight_heads][block_size] or null
   int32_t weight_heads;
+  // norms of the heads (launch_write_normed)
+  const uint8_t* q_norm;     // [dims] or null: q as it is
+  const uint8_t* k_norm;     // [dims] or null; MLA: of the latent
+  int32_t norm_f32;          // their type: fp32 or bf16
+  int32_t latent_norm;       // 1: a warp task per token of its own normalises the latent
+  float norm_eps, norm_offset;
   uint32_t* status;
 };
 cudaError_t launch_write(const WriteParams& p, int pairing, cudaStream_t s);
+cudaError_t launch_write_normed(const WriteParams& p, int pairing, cudaStream_t s);
+
+// ---- block tables and token lists
+struct MapParams {
+  int32_t* tables;           // [n_req][max_blocks]
+  int32_t n_req, max_blocks, block_size;
+  int32_t max_len;           // slots a table holds
+  int32_t num_blocks;        // of the cache, and places of the pile
+  const int32_t* lens;       // [n_req]
+  const int32_t* grow;       // [n_req]
+  int32_t* free_blocks;      // [num_blocks], the first *n_free of them free
+  const int32_t* n_free;
+  int32_t* new_lens;         // may be lens
+  int32_t* new_n_free;       // may be n_free
+  int32_t n_tokens;
+  int32_t* indptr;           // [n_req + 1]
+  int32_t* req;              // [n_tokens]
+  int32_t* slot;
+  int32_t* pos;              // or null
+  const int32_t* shift;      // [n_req] or null
+  uint32_t* ticket;          // CTAs that have read their inputs; left at 0
+  uint32_t* status;
+};
+cudaError_t launch_map(const MapParams& p, int sm_count, cudaStream_t s);
 
 // ---- paged attention
 constexpr int kPagedTile = 16;          // positions of one step of a warp
@@ -107,8 +137,25 @@ constexpr int kPagedMaxSms = 256;       // SMs used (workspace sizing)
 constexpr int kPagedWalkRequests = 128;
 constexpr int kPagedMaxHeads = 4096;    // query heads
 
+// What a query row attends to, where it is not simply a request's whole sequence
+// (pic_attend_tokens, pic_attend_shared; the kernels' ROWS variants).  The row's slots are
+// counted without the gap between those that it sees: the first `head` are slots
+// 0 .. head - 1, number v from there on is slot v + gap.
+struct RowsParams {
+  int32_t shared;            // 0: tokens of requests; 1: one token a request, the prefix shared
+  const int32_t* indptr;     // [n_req + 1] tokens: rows of each request
+  const int32_t* slot;       // [rows] tokens: slot of each
+  int32_t n_req;             // tokens: requests
+  int32_t capacity;          // slots a table holds
+  int32_t window, n_first;   // window 0: every slot before
+  const int32_t* prefix_table;   // shared: [prefix_blocks]
+  const int32_t* prefix_len;     // shared: [1]
+  int32_t prefix_blocks, max_prefix;
+};
+
 struct PagedParams {
   PagedView paged;
+  RowsParams rows;
   const uint8_t* q;
   int64_t q_stride;          // bytes between requests
   const int32_t* lens;       // [n_req]
@@ -139,6 +186,7 @@ struct PagedParams {
 };
 int paged_ranges_per_sm(int head_dim);  // ranges an SM works on at a time (head_dim 576: MLA rows)
 cudaError_t launch_paged(const PagedParams& p, int head_dim, int sm_count, cudaStream_t s);
+cudaError_t launch_paged_rows(const PagedParams& p, int head_dim, int sm_count, cudaStream_t s);   // bf16 out, no weights
 
 // ---- eviction
 struct EvictUnit {           // per (layer, request, weight head), in the workspace

@@ -44,7 +44,8 @@ struct WsHeader {
   uint32_t status;      // PIC_DEV_* bits raised by kernels
   uint32_t bad_req;     // a block-table row that held a bad entry (diagnostic)
   uint32_t bad_pos;     // the position it was asked for
-  uint32_t pad[61];
+  uint32_t ticket;      // CTAs of a launch that have read their inputs (pic_map_tokens; 0 between launches)
+  uint32_t pad[60];
 };
 static_assert(sizeof(WsHeader) == 256, "WsHeader layout");
 

@@ -116,6 +116,47 @@ __device__ __forceinline__ int legal_len(int len, int max_len, uint32_t* status,
   return 0;
 }
 
+// ROWS: what row r attends to (RowsParams).
+struct Span {
+  int len, head, gap;
+};
+// Request of row i of pic_attend_tokens, -1 for a row of none.
+__device__ __forceinline__ int request_of(const RowsParams& R, int i) {
+  if (i < __ldg(R.indptr) || i >= __ldg(R.indptr + R.n_req)) return -1;
+  int lo = 0, hi = R.n_req;   // indptr[lo] <= i < indptr[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(R.indptr + mid) <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+__device__ __forceinline__ int prefix_of(const PagedParams& P, bool raise) {
+  return legal_len(__ldg(P.rows.prefix_len), P.rows.max_prefix, P.status, raise);
+}
+__device__ __forceinline__ Span span_of(const PagedParams& P, int r, bool raise) {
+  const RowsParams& R = P.rows;
+  if (R.shared != 0) {
+    const int len = legal_len(__ldg(P.lens + r), P.max_len, P.status, raise);
+    return Span{len, min(prefix_of(P, raise), len), 0};
+  }
+  const int s = __ldg(R.slot + r);
+  if (s < 0 || r < __ldg(R.indptr) || r >= __ldg(R.indptr + R.n_req)) return Span{0, 0, 0};
+  if (s >= R.capacity) {
+    if (raise) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_BAD_LENGTH));
+    return Span{0, 0, 0};
+  }
+  const int lo = R.window > 0 ? max(0, s + 1 - R.window) : 0;   // window below 2^31 - 1
+  const int head = min(R.n_first, lo);
+  return Span{head + s + 1 - lo, head, lo - head};
+}
+// Length of row r as the tile list counts it.
+template <bool ROWS>
+__device__ __forceinline__ int row_len(const PagedParams& P, int r, bool raise) {
+  if constexpr (ROWS) return span_of(P, r, raise).len;
+  else return legal_len(__ldg(P.lens + r), P.max_len, P.status, raise);
+}
+
 // The tile list all kernels share: request r owns ceil(len / 16) tiles, in
 // order; range p of n holds tiles [T p / n, T (p + 1) / n).
 struct TileList {
@@ -123,15 +164,27 @@ struct TileList {
   int64_t parts;   // n: fewer than P.parts when there are few tiles
   __device__ int64_t begin(int64_t p) const { return total * p / parts; }
 };
+template <bool ROWS>
 __device__ __forceinline__ int tiles_of(const PagedParams& P, int r, bool raise) {
-  return (legal_len(__ldg(P.lens + r), P.max_len, P.status, raise) + TT - 1) / TT;
+  return (row_len<ROWS>(P, r, raise) + TT - 1) / TT;
 }
 __device__ __forceinline__ int64_t parts_of(const PagedParams& P, int64_t total) {   // at least a tile each
   return total < P.parts ? (total < 1 ? 1 : total) : P.parts;
 }
+template <bool ROWS>
 __device__ __forceinline__ TileList tile_list(const PagedParams& P, int lane, bool raise) {
   int64_t n = 0;
-  for (int r = lane; r < P.n_req; r += 32) n += tiles_of(P, r, raise);
+  for (int r = lane; r < P.n_req; r += 32) n += tiles_of<ROWS>(P, r, raise);
+  if constexpr (ROWS) {
+    if (raise && P.rows.shared == 0) {   // offsets that are not non-decreasing inside [0, rows]
+      bool bad = false;
+      for (int r = lane; r <= P.rows.n_req; r += 32) {
+        const int at = __ldg(P.rows.indptr + r), before = r > 0 ? __ldg(P.rows.indptr + r - 1) : 0;
+        bad |= at < before || at > P.n_req;
+      }
+      if (bad) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_BAD_LENGTH));
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
   TileList L;
@@ -141,11 +194,12 @@ __device__ __forceinline__ TileList tile_list(const PagedParams& P, int lane, bo
 }
 // The request that holds tile t of the list, and its first tile (warp-wide;
 // t below the total).
+template <bool ROWS>
 __device__ __forceinline__ void find_tile(const PagedParams& P, int64_t t, int lane, int& req, int64_t& first) {
   int64_t base = 0;
   for (int r0 = 0; r0 < P.n_req; r0 += 32) {
     const int r = r0 + lane;
-    int64_t n = r < P.n_req ? tiles_of(P, r, false) : 0;
+    int64_t n = r < P.n_req ? tiles_of<ROWS>(P, r, false) : 0;
     int64_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -165,18 +219,20 @@ __device__ __forceinline__ void find_tile(const PagedParams& P, int64_t t, int l
   first = base;
 }
 // First tile of request r (warp-wide).
+template <bool ROWS>
 __device__ __forceinline__ int64_t first_tile(const PagedParams& P, int r, int lane) {
   int64_t n = 0;
-  for (int i = lane; i < r; i += 32) n += tiles_of(P, i, false);
+  for (int i = lane; i < r; i += 32) n += tiles_of<ROWS>(P, i, false);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
   return n;
 }
 // Leaves the first tiles of the requests that begin in tiles [t, t_end) of the
 // list to the joins (warp-wide; t is in request r, whose first tile is `base`).
+template <bool ROWS>
 __device__ __forceinline__ void leave_first_tiles(const PagedParams& P, int64_t t, int64_t t_end, int r, int64_t base, int lane) {
   for (; r < P.n_req && base < t_end; r += 32) {
-    const int64_t n = r + lane < P.n_req ? tiles_of(P, r + lane, false) : 0;
+    const int64_t n = r + lane < P.n_req ? tiles_of<ROWS>(P, r + lane, false) : 0;
     int64_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -193,7 +249,25 @@ __device__ __forceinline__ void leave_first_tiles(const PagedParams& P, int64_t 
 struct Place {
   int req, tile, len;
   int64_t first;   // the request's first tile in the list
+  // ROWS: the gap in the row's slots, and its block table
+  int head, gap;
+  const int32_t* table;
 };
+// Fills in a place's request (req below n_req).
+template <bool ROWS>
+__device__ __forceinline__ void open_place(const PagedParams& P, Place& x) {
+  if constexpr (ROWS) {
+    const Span s = span_of(P, x.req, false);
+    x.len = s.len;
+    x.head = s.head;
+    x.gap = s.gap;
+    const int row = P.rows.shared != 0 || s.len == 0 ? x.req : request_of(P.rows, x.req);
+    x.table = P.paged.tables + static_cast<int64_t>(row) * P.paged.max_blocks;
+  } else {
+    x.len = row_len<false>(P, x.req, false);
+  }
+}
+template <bool ROWS>
 __device__ __forceinline__ void advance(const PagedParams& P, Place& x) {
   if (x.req >= P.n_req) return;   // past the list
   const int n = (x.len + TT - 1) / TT;
@@ -202,17 +276,18 @@ __device__ __forceinline__ void advance(const PagedParams& P, Place& x) {
   x.tile = 0;
   do {
     ++x.req;
-    x.len = x.req < P.n_req ? legal_len(__ldg(P.lens + x.req), P.max_len, P.status, false) : 0;
+    x.len = 0;
+    if (x.req < P.n_req) open_place<ROWS>(P, x);
   } while (x.len == 0 && x.req < P.n_req);
 }
 
 // WIDE: 9 to 16 query heads per warp, one per row of the products; else up to
 // 8, in rows 0-7 (rows 8-15 carry the lo parts of P).  F32: fp32 output.
-template <int D, bool WIDE, bool F32>
+template <int D, bool WIDE, bool F32, bool ROWS>
 __device__ __forceinline__ void attend_range(const PagedParams& P, const TileList& L, int64_t w, uint8_t* smem) {
   constexpr int KS = D / 16, NT = D / 8, CH = D / 8;  // k-steps, output n-tiles, 16-byte chunks of a row
   constexpr int NS = paged_stages(D);
-  constexpr int ROWS = 32 / CH > 0 ? 32 / CH : 1;     // rows one warp-wide copy covers
+  constexpr int COPY_ROWS = 32 / CH > 0 ? 32 / CH : 1;   // rows one warp-wide copy covers
   constexpr int COPIES = TT * CH / 32;                // warp-wide copies of a K (or V) tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + warp * NS * stage_bytes(D);
@@ -233,10 +308,11 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream_once));
 
   Place load;
-  find_tile(P, t_begin, lane, load.req, load.first);
-  if (P.first != nullptr && vh == 0) leave_first_tiles(P, t_begin, t_end, load.req, load.first, lane);
+  find_tile<ROWS>(P, t_begin, lane, load.req, load.first);
+  if (P.first != nullptr && vh == 0) leave_first_tiles<ROWS>(P, t_begin, t_end, load.req, load.first, lane);
   load.tile = static_cast<int>(t_begin - load.first);
-  load.len = load.req < P.n_req ? legal_len(__ldg(P.lens + load.req), P.max_len, P.status, false) : 0;
+  load.len = 0;
+  if (load.req < P.n_req) open_place<ROWS>(P, load);
   Place cur = load;
   int64_t t_load = t_begin;
 
@@ -244,6 +320,18 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
   auto row_of = [&](const Place& x) -> int {
     const int slot = x.tile * TT + (lane & (TT - 1));
     if (slot >= x.len) return -1;
+    if constexpr (ROWS) {
+      // (a slot that a row sees is below its table's capacity)
+      const bool head = slot < x.head;
+      const int at = head ? slot : slot + x.gap;
+      const int b = block_of(P.paged, at);
+      const int32_t block = __ldg((head && P.rows.shared != 0 ? P.rows.prefix_table : x.table) + b);
+      if (block < 0 || block >= P.paged.num_cache_blocks) {
+        if (lane < TT) raise_block(P.status, x.req, at);
+        return -1;
+      }
+      return static_cast<int>(static_cast<int64_t>(block) * P.paged.block_size + (at - b * P.paged.block_size));
+    }
     const int64_t row = paged_row(P.paged, x.req, slot);
     if (row < 0 && lane < TT) raise_block(P.status, x.req, slot);
     return static_cast<int>(row);   // below 2^31 (checked when the context was made)
@@ -252,7 +340,7 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
     const uint32_t k_dst = ring + stage * stage_bytes(D), v_dst = k_dst + TT * D * 2;
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
-      const int r = CH >= 32 ? i : i * ROWS + lane / CH, c = lane % CH;
+      const int r = CH >= 32 ? i : i * COPY_ROWS + lane / CH, c = lane % CH;
       const int src_row = __shfl_sync(kFull, row, r);
       const bool live = src_row >= 0;
       const int64_t off = static_cast<int64_t>(live ? src_row : 0) * P.row_bytes + hk * D * 2 + c * 16;
@@ -273,7 +361,7 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
       issue(i, next_row);
       ++t_load;
       if (t_load < t_end) {
-        advance(P, load);
+        advance<ROWS>(P, load);
         next_row = row_of(load);
       }
     }
@@ -305,7 +393,7 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
           issue(fs, next_row);
           ++t_load;
           if (t_load < t_end) {
-            advance(P, load);
+            advance<ROWS>(P, load);
             next_row = row_of(load);
           }
         }
@@ -464,23 +552,23 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
         }
         opened = false;
       }
-      if (t < t_end) advance(P, cur);
+      if (t < t_end) advance<ROWS>(P, cur);
     }
   }
   bulk_wait_all();
 }
 
-template <int D, bool WIDE, bool F32>
+template <int D, bool WIDE, bool F32, bool ROWS>
 __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const __grid_constant__ PagedParams P) {
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(128) uint8_t smem[];
-  const TileList L = tile_list(P, threadIdx.x & 31, blockIdx.x == 0 && threadIdx.x < 32);
+  const TileList L = tile_list<ROWS>(P, threadIdx.x & 31, blockIdx.x == 0 && threadIdx.x < 32);
   if (P.first != nullptr && blockIdx.x == 0 && threadIdx.x == 0) P.first[P.n_req] = L.total;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * paged_warps(D);
   // one range each; more only when there are more heads than warps
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * paged_warps(D) + (threadIdx.x >> 5);
        w < static_cast<int64_t>(P.parts) * P.v_heads; w += warps)
-    attend_range<D, WIDE, F32>(P, L, w, smem);
+    attend_range<D, WIDE, F32, ROWS>(P, L, w, smem);
 }
 
 // ---- MLA: latent rows
@@ -541,7 +629,7 @@ __global__ void __launch_bounds__(kLatThreads, kLatCtas) k_paged_latent(const __
   const uint32_t p_at = smem_u32(S.p[0][a_row]) + (lane >> 4) * 16;
   const uint32_t row_at = smem_u32(S.kv[0][my_row]) + (tid & 7) * 16;
   constexpr uint32_t kStage = kLatSlots * kLatRowPitch;
-  const TileList L = tile_list(P, lane, blockIdx.x == 0 && warp == 0);
+  const TileList L = tile_list<false>(P, lane, blockIdx.x == 0 && warp == 0);
   uint64_t policy;   // rows that no other CTA reads pass through L2 first-out
   if (P.passes == 1) asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   else asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
@@ -554,8 +642,8 @@ __global__ void __launch_bounds__(kLatThreads, kLatCtas) k_paged_latent(const __
     const int64_t t_end = L.begin(part + 1);
     int64_t t = L.begin(part), first;
     int r;
-    find_tile(P, t, lane, r, first);
-    if (P.first != nullptr && hq0 == 0 && warp == 0) leave_first_tiles(P, t, t_end, r, first, lane);
+    find_tile<false>(P, t, lane, r, first);
+    if (P.first != nullptr && hq0 == 0 && warp == 0) leave_first_tiles<false>(P, t, t_end, r, first, lane);
     // the range, request by request: slots [s0, s_end) of request r, in tiles up to slot s_pad
     for (; t < t_end; ++r) {
       const int len = legal_len(__ldg(P.lens + r), P.max_len, P.status, false);
@@ -743,11 +831,12 @@ __device__ __forceinline__ Records records_of(const TileList& L, int64_t first, 
 // Of few requests the lengths are walked again, before the wait; of many
 // (P.first set) the attention kernel has left what is needed in the workspace:
 // the total, and the first tile of each request that has any.
+template <bool ROWS>
 __device__ __forceinline__ Records join_records(const PagedParams& P, const TileList& walked, int r, int lane) {
-  const int n = tiles_of(P, r, false);
+  const int n = tiles_of<ROWS>(P, r, false);
   Records x;
   if (P.first == nullptr) {
-    x = records_of(walked, first_tile(P, r, lane), n, r);
+    x = records_of(walked, first_tile<ROWS>(P, r, lane), n, r);
     asm volatile("griddepcontrol.wait;" ::: "memory");
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -869,7 +958,7 @@ __device__ __forceinline__ WeightRun weight_run(const PagedParams& P, const Tile
   x.end = L.total * (part + 1) / all;
   x.r = 0;
   x.first = 0;
-  if (x.begin < x.end) find_tile(P, x.begin, lane, x.r, x.first);
+  if (x.begin < x.end) find_tile<false>(P, x.begin, lane, x.r, x.first);
   return x;
 }
 __device__ __forceinline__ void add_weights(const PagedParams& P, const WeightRun& run) {
@@ -973,7 +1062,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_paged_lse(const __grid_const
   const int64_t task = static_cast<int64_t>(blockIdx.x) * kFinishWarps + (threadIdx.x >> 5);
   const int r = static_cast<int>(task / P.q_heads), hq = static_cast<int>(task % P.q_heads);
   if (r >= P.n_req) return;
-  const Records x = join_records(P, P.first == nullptr ? tile_list(P, lane, false) : TileList{0, 1}, r, lane);
+  const Records x = join_records<false>(P, P.first == nullptr ? tile_list<false>(P, lane, false) : TileList{0, 1}, r, lane);
   float M, sum;
   join_stats(P, x, hq, lane, M, sum);
   if (lane == 0) P.lse2[task] = sum == 0.0f ? INFINITY : M + log2f(sum);   // nothing attended: every share 0
@@ -982,18 +1071,24 @@ __global__ void __launch_bounds__(kFinishThreads) k_paged_lse(const __grid_const
 // The first CTAs add the weights (the longer part); the others join the
 // records into the outputs: one CTA per (request, query head) while these are
 // few (few requests, each cut into many ranges), else one warp for each.
-template <int D>
+template <int D, bool ROWS>
 __global__ void __launch_bounds__(kFinishThreads, 3) k_paged_finish(const __grid_constant__ PagedParams P) {
   __shared__ float s_part[kFinishWarps * D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int block = static_cast<int>(blockIdx.x) - P.weight_ctas;
-  const TileList L = P.first == nullptr || block < 0 ? tile_list(P, lane, false) : TileList{0, 1};
+  const TileList L = P.first == nullptr || block < 0 ? tile_list<ROWS>(P, lane, false) : TileList{0, 1};
   if (block >= 0) {
     const bool all = P.join_wide != 0;
     const int64_t task = all ? block : static_cast<int64_t>(block) * kFinishWarps + warp;
     const int r = static_cast<int>(task / P.q_heads), hq = static_cast<int>(task % P.q_heads);
     if (r >= P.n_req) return;
-    const Records x = join_records(P, L, r, lane);
+    if constexpr (ROWS) {
+      if (P.rows.shared == 0 && request_of(P.rows, r) < 0) {   // a row of no request stays as it is
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+      }
+    }
+    const Records x = join_records<ROWS>(P, L, r, lane);
     if (all) join_output<D, true>(P, x, r, hq, s_part);
     else join_output<D, false>(P, x, r, hq, s_part);
     return;
@@ -1021,9 +1116,9 @@ cudaError_t launch_after(void (*kern)(PagedParams), unsigned grid, const PagedPa
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int D, bool WIDE, bool F32>
+template <int D, bool WIDE, bool F32, bool ROWS = false>
 cudaError_t launch_attend_d(const PagedParams& p, int grid, cudaStream_t s) {
-  auto kern = k_paged_attend<D, WIDE, F32>;
+  auto kern = k_paged_attend<D, WIDE, F32, ROWS>;
   constexpr int smem = paged_warps(D) * (paged_stages(D) * stage_bytes(D) + score_stage(D, WIDE) * static_cast<int>(sizeof(float)));
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<uint32_t> done{0};
@@ -1046,7 +1141,7 @@ cudaError_t launch_latent(const PagedParams& p, int sm_count, cudaStream_t s) {
 }
 
 // The kernels after the attention: D is the width of an output row.
-template <int D>
+template <int D, bool ROWS = false>
 cudaError_t launch_join(PagedParams p, int sm_count, cudaStream_t s) {
   const int64_t tasks = static_cast<int64_t>(p.n_req) * p.q_heads;
   p.join_wide = tasks <= 2 * sm_count;
@@ -1056,7 +1151,7 @@ cudaError_t launch_join(PagedParams p, int sm_count, cudaStream_t s) {
     const cudaError_t e = launch_after(k_paged_lse, static_cast<unsigned>((tasks + kFinishWarps - 1) / kFinishWarps), p, s);
     if (e != cudaSuccess) return e;
   }
-  return launch_after(k_paged_finish<D>, static_cast<unsigned>(p.weight_ctas + join_ctas), p, s);
+  return launch_after(k_paged_finish<D, ROWS>, static_cast<unsigned>(p.weight_ctas + join_ctas), p, s);
 }
 
 template <int D>
@@ -1066,6 +1161,12 @@ cudaError_t launch_d(const PagedParams& p, int sm_count, cudaStream_t s) {
   if (p.group > 8) e = p.out_bf16 ? launch_attend_d<D, true, false>(p, grid, s) : launch_attend_d<D, true, true>(p, grid, s);
   else e = p.out_bf16 ? launch_attend_d<D, false, false>(p, grid, s) : launch_attend_d<D, false, true>(p, grid, s);
   return e != cudaSuccess ? e : launch_join<D>(p, sm_count, s);
+}
+template <int D>
+cudaError_t launch_rows_d(const PagedParams& p, int sm_count, cudaStream_t s) {
+  const cudaError_t e = p.group > 8 ? launch_attend_d<D, true, false, true>(p, sm_count, s)
+                                    : launch_attend_d<D, false, false, true>(p, sm_count, s);
+  return e != cudaSuccess ? e : launch_join<D, true>(p, sm_count, s);
 }
 
 }  // namespace
@@ -1080,6 +1181,12 @@ cudaError_t launch_paged(const PagedParams& p, int head_dim, int sm_count, cudaS
   if (head_dim == 64) return launch_d<64>(p, sm_count, s);
   if (head_dim == 128) return launch_d<128>(p, sm_count, s);
   return launch_d<256>(p, sm_count, s);
+}
+
+cudaError_t launch_paged_rows(const PagedParams& p, int head_dim, int sm_count, cudaStream_t s) {
+  if (head_dim == 64) return launch_rows_d<64>(p, sm_count, s);
+  if (head_dim == 128) return launch_rows_d<128>(p, sm_count, s);
+  return launch_rows_d<256>(p, sm_count, s);
 }
 
 }  // namespace pic

@@ -1,0 +1,217 @@
+// Host entries of a serving step's operators: pic_map_tokens, pic_attend_tokens
+// and pic_attend_shared (include/pic.h).  Like the decode loop's they check their
+// arguments, fill the launch parameters and launch; they allocate nothing,
+// upload nothing and wait for nothing, so they can be captured into a graph.
+#include "pic_entry.h"
+
+#include <cmath>
+
+namespace {
+
+using namespace pic;
+using namespace pic::entry;
+
+// The parts of PagedParams that a call over rows takes from its arguments.
+PagedParams rows_params(const CtxView& c, const void* q, int64_t q_stride, int32_t n_rows, int32_t num_q_heads, float scale,
+                        const void* k_cache, const void* v_cache, void* out, float* lse, uint8_t* ws, int sms) {
+  const pic_model_desc& m = *c.model;
+  const PagedLayout L = paged_layout(c, n_rows, num_q_heads, 0, false);
+  PagedParams p{};
+  p.q = static_cast<const uint8_t*>(q);
+  p.q_stride = q_stride;
+  p.n_req = n_rows;
+  p.q_heads = num_q_heads;
+  p.kv_heads = m.num_kv_heads;
+  p.group = num_q_heads / m.num_kv_heads;
+  p.passes = paged_passes(p.group);
+  p.v_heads = p.kv_heads * p.passes;
+  const int used = std::min(sms, kPagedMaxSms);
+  p.parts = static_cast<int32_t>(std::max<int64_t>(1, static_cast<int64_t>(used) * paged_ranges_per_sm(m.head_dim) / p.v_heads));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.row_bytes = m.num_kv_heads * m.head_dim * 2;
+  p.first = n_rows > kPagedWalkRequests ? reinterpret_cast<int64_t*>(ws + L.first) : nullptr;
+  p.rec_acc = reinterpret_cast<float*>(ws + L.rec_acc);
+  p.rec_ml = reinterpret_cast<float2*>(ws + L.rec_ml);
+  p.out = out;
+  p.out_bf16 = 1;
+  p.lse = lse;
+  p.status = &reinterpret_cast<WsHeader*>(ws)->status;
+  return p;
+}
+
+// Arguments that both attentions share; PIC_OK to go on.
+pic_status check_rows(pic_ctx* ctx, const CtxView& c, const void* q, int64_t q_stride, int32_t n_rows, int32_t num_q_heads,
+                      float scale, const void* k_cache, const void* v_cache, const void* out, const float* lse, const void* ws) {
+  const pic_model_desc& m = *c.model;
+  if (m.kind != PIC_KIND_GQA)
+    return fail(ctx, PIC_ERR_UNSUPPORTED, "MLA models: attend with pic_attend_paged or pic_attend_decode");
+  if (!paged_heads_ok(c, num_q_heads))
+    return fail(ctx, PIC_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
+  if (!std::isfinite(scale)) return fail(ctx, PIC_ERR_INVALID_ARG, "softmax_scale must be finite");
+  if (!k_cache || !v_cache || !ws || (n_rows > 0 && (!q || !out)))
+    return fail(ctx, PIC_ERR_INVALID_ARG, "null q, cache, out or workspace");
+  const int64_t q_bytes = static_cast<int64_t>(num_q_heads) * m.head_dim * 2;
+  if (static_cast<int64_t>(m.num_kv_heads) * m.head_dim * 2 > std::numeric_limits<int32_t>::max() ||
+      !paged_size_ok(n_rows, num_q_heads))
+    return fail(ctx, PIC_ERR_RANGE, "more than %d query heads, or 2^30 in all", kPagedMaxHeads);
+  if (n_rows > 1 && q_stride < q_bytes) return fail(ctx, PIC_ERR_RANGE, "q_stride smaller than a token's heads");
+  if (!aligned(q, 16) || (q_stride & 15) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+    return fail(ctx, PIC_ERR_ALIGNMENT, "q, its stride, caches and out must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(ws, kWsAlign))
+    return fail(ctx, PIC_ERR_ALIGNMENT, "lse must be 4-byte aligned, the workspace 256-byte");
+  return PIC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pic_map_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_req) { return ctx && n_req >= 0 ? sizeof(WsHeader) : 0; }
+
+pic_status pic_map_tokens(pic_ctx* ctx, const pic_token_map* t, void* d_ws, size_t ws_bytes, pic_stream_t stream) {
+  if (!ctx || !t) return fail(ctx, PIC_ERR_INVALID_ARG, "null ctx or map");
+  const CtxView c = ctx_view(ctx);
+  if (t->n_req < 0 || t->max_blocks < 0 || t->n_tokens < 0) return fail(ctx, PIC_ERR_INVALID_ARG, "negative size");
+  const bool some = t->n_req > 0;
+  if (!t->d_n_free || !t->d_new_n_free || !t->d_indptr || (c.num_cache_blocks > 0 && !t->d_free_blocks) ||
+      (some && (!t->d_seq_lens || !t->d_grow || !t->d_new_lens || (!t->d_block_tables && t->max_blocks > 0))) ||
+      (t->n_tokens > 0 && (!t->d_req || !t->d_slot)))
+    return fail(ctx, PIC_ERR_INVALID_ARG, "null lengths, growth, block tables, free blocks, offsets or token lists");
+  if (!d_ws || ws_bytes < sizeof(WsHeader)) return fail(ctx, PIC_ERR_CAPACITY, "workspace needs %zu bytes", sizeof(WsHeader));
+  for (const void* x : {static_cast<const void*>(t->d_seq_lens), static_cast<const void*>(t->d_grow),
+                        static_cast<const void*>(t->d_block_tables), static_cast<const void*>(t->d_free_blocks),
+                        static_cast<const void*>(t->d_n_free), static_cast<const void*>(t->d_shift),
+                        static_cast<const void*>(t->d_new_lens), static_cast<const void*>(t->d_new_n_free),
+                        static_cast<const void*>(t->d_indptr), static_cast<const void*>(t->d_req),
+                        static_cast<const void*>(t->d_slot), static_cast<const void*>(t->d_pos)})
+    if (!aligned(x, 4)) return fail(ctx, PIC_ERR_ALIGNMENT, "lists must be 4-byte aligned");
+  if (!aligned(d_ws, kWsAlign)) return fail(ctx, PIC_ERR_ALIGNMENT, "the workspace must be 256-byte aligned");
+  const bool tokens = t->n_tokens > 0;
+  const Buffer bufs[] = {{"lengths", some ? t->d_seq_lens : nullptr}, {"growth", some ? t->d_grow : nullptr},
+                         {"block tables", some ? t->d_block_tables : nullptr}, {"free blocks", t->d_free_blocks},
+                         {"free count", t->d_n_free}, {"shifts", some ? t->d_shift : nullptr},
+                         {"new lengths", some ? t->d_new_lens : nullptr}, {"new free count", t->d_new_n_free},
+                         {"offsets", t->d_indptr}, {"requests", tokens ? t->d_req : nullptr},
+                         {"slots", tokens ? t->d_slot : nullptr}, {"positions", tokens ? t->d_pos : nullptr}, {"workspace", d_ws}};
+  int sms = 0;
+  const pic_status st = check_device(ctx, bufs, sizeof(bufs) / sizeof(bufs[0]), &sms);
+  if (st != PIC_OK) return st;
+  MapParams p{};
+  p.tables = t->d_block_tables;
+  p.n_req = t->n_req;
+  p.max_blocks = t->max_blocks;
+  p.block_size = c.model->block_size;
+  p.max_len = static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(t->max_blocks) * c.model->block_size, kPagedMaxSlots));
+  p.num_blocks = c.num_cache_blocks;
+  p.lens = t->d_seq_lens;
+  p.grow = t->d_grow;
+  p.free_blocks = t->d_free_blocks;
+  p.n_free = t->d_n_free;
+  p.new_lens = t->d_new_lens;
+  p.new_n_free = t->d_new_n_free;
+  p.n_tokens = t->n_tokens;
+  p.indptr = t->d_indptr;
+  p.req = t->d_req;
+  p.slot = t->d_slot;
+  p.pos = t->d_pos;
+  p.shift = t->d_shift;
+  WsHeader* h = static_cast<WsHeader*>(d_ws);
+  p.ticket = &h->ticket;
+  p.status = &h->status;
+  const cudaError_t e = launch_map(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "token map launch");
+  return set_error(ctx, PIC_OK, "");
+}
+
+size_t pic_attend_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_tokens, int32_t n_req, int32_t num_q_heads) {
+  if (!ctx || n_tokens < 0 || n_req < 0) return 0;
+  const CtxView c = ctx_view(ctx);
+  if (c.model->kind != PIC_KIND_GQA || !paged_heads_ok(c, num_q_heads) || !paged_size_ok(n_tokens, num_q_heads)) return 0;
+  return paged_layout(c, n_tokens, num_q_heads, 0, false).total;
+}
+
+pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_tokens, int32_t num_q_heads,
+                             float softmax_scale, const void* k_cache, const void* v_cache, const int32_t* d_tables, int32_t n_req,
+                             int32_t max_blocks, const int32_t* d_indptr, const int32_t* d_slot, int32_t window, int32_t n_first,
+                             void* out, float* lse, void* d_ws, size_t ws_bytes, pic_stream_t stream) {
+  if (!ctx) return fail(nullptr, PIC_ERR_INVALID_ARG, "null ctx");
+  const CtxView c = ctx_view(ctx);
+  if (n_tokens < 0 || n_req < 0 || max_blocks < 0) return fail(ctx, PIC_ERR_INVALID_ARG, "negative size");
+  if (window < 0 || n_first < 0) return fail(ctx, PIC_ERR_INVALID_ARG, "window and n_first must not be negative");
+  const pic_status ok = check_rows(ctx, c, q, q_stride, n_tokens, num_q_heads, softmax_scale, k_cache, v_cache, out, lse, d_ws);
+  if (ok != PIC_OK) return ok;
+  const bool some = n_tokens > 0 && n_req > 0;
+  if (some && (!d_indptr || !d_slot || (!d_tables && max_blocks > 0)))
+    return fail(ctx, PIC_ERR_INVALID_ARG, "null block table, offsets or slots");
+  if (!aligned(d_tables, 4) || !aligned(d_indptr, 4) || !aligned(d_slot, 4))
+    return fail(ctx, PIC_ERR_ALIGNMENT, "tables, offsets and slots must be 4-byte aligned");
+  const size_t need = paged_layout(c, n_tokens, num_q_heads, 0, false).total;
+  if (ws_bytes < need) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  if (!some) return set_error(ctx, PIC_OK, "");
+  const Buffer bufs[] = {{"q", q}, {"k_cache", k_cache}, {"v_cache", v_cache}, {"block tables", d_tables}, {"offsets", d_indptr},
+                         {"slots", d_slot}, {"out", out}, {"lse", lse}, {"workspace", d_ws}};
+  int sms = 0;
+  const pic_status st = check_device(ctx, bufs, sizeof(bufs) / sizeof(bufs[0]), &sms);
+  if (st != PIC_OK) return st;
+  PagedParams p = rows_params(c, q, q_stride, n_tokens, num_q_heads, softmax_scale, k_cache, v_cache, out, lse,
+                              static_cast<uint8_t*>(d_ws), sms);
+  p.paged = paged_view(c, d_tables, n_req, max_blocks);
+  p.rows.indptr = d_indptr;
+  p.rows.slot = d_slot;
+  p.rows.n_req = n_req;
+  p.rows.capacity = table_capacity(c, max_blocks);
+  p.rows.window = window;
+  p.rows.n_first = n_first;
+  const cudaError_t e = launch_paged_rows(p, c.model->head_dim, std::min(sms, kPagedMaxSms), reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "token attention launch");
+  return set_error(ctx, PIC_OK, "");
+}
+
+size_t pic_attend_shared_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32_t num_q_heads) {
+  return pic_attend_tokens_workspace_bytes(ctx, n_req, n_req, num_q_heads);
+}
+
+pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_req, int32_t num_q_heads, float softmax_scale,
+                             const void* k_cache, const void* v_cache, const int32_t* d_prefix_table, int32_t prefix_blocks,
+                             const int32_t* d_prefix_len, const int32_t* d_tables, int32_t max_blocks, const int32_t* d_seq_lens,
+                             int32_t max_seq_len, void* out, float* lse, void* d_ws, size_t ws_bytes, pic_stream_t stream) {
+  if (!ctx) return fail(nullptr, PIC_ERR_INVALID_ARG, "null ctx");
+  const CtxView c = ctx_view(ctx);
+  if (n_req < 0 || max_blocks < 0 || max_seq_len < 0 || prefix_blocks < 0) return fail(ctx, PIC_ERR_INVALID_ARG, "negative size");
+  const pic_status ok = check_rows(ctx, c, q, q_stride, n_req, num_q_heads, softmax_scale, k_cache, v_cache, out, lse, d_ws);
+  if (ok != PIC_OK) return ok;
+  const bool some = n_req > 0;
+  if (some && (!d_seq_lens || !d_prefix_len || (!d_tables && max_blocks > 0) || (!d_prefix_table && prefix_blocks > 0)))
+    return fail(ctx, PIC_ERR_INVALID_ARG, "null block table, prefix table or lengths");
+  if (max_seq_len > table_capacity(c, max_blocks))
+    return fail(ctx, PIC_ERR_RANGE, "max_seq_len %d exceeds the %d slots a block table holds", max_seq_len,
+                table_capacity(c, max_blocks));
+  if (!aligned(d_tables, 4) || !aligned(d_seq_lens, 4) || !aligned(d_prefix_table, 4) || !aligned(d_prefix_len, 4))
+    return fail(ctx, PIC_ERR_ALIGNMENT, "tables and lengths must be 4-byte aligned");
+  const size_t need = paged_layout(c, n_req, num_q_heads, 0, false).total;
+  if (ws_bytes < need) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  if (!some) return set_error(ctx, PIC_OK, "");
+  const Buffer bufs[] = {{"q", q}, {"k_cache", k_cache}, {"v_cache", v_cache}, {"prefix table", d_prefix_table},
+                         {"prefix length", d_prefix_len}, {"block tables", d_tables}, {"lengths", d_seq_lens}, {"out", out},
+                         {"lse", lse}, {"workspace", d_ws}};
+  int sms = 0;
+  const pic_status st = check_device(ctx, bufs, sizeof(bufs) / sizeof(bufs[0]), &sms);
+  if (st != PIC_OK) return st;
+  PagedParams p = rows_params(c, q, q_stride, n_req, num_q_heads, softmax_scale, k_cache, v_cache, out, lse,
+                              static_cast<uint8_t*>(d_ws), sms);
+  p.paged = paged_view(c, d_tables, n_req, max_blocks);
+  p.lens = d_seq_lens;
+  p.max_len = max_seq_len;
+  p.rows.shared = 1;
+  p.rows.prefix_table = d_prefix_table;
+  p.rows.prefix_len = d_prefix_len;
+  p.rows.prefix_blocks = prefix_blocks;
+  p.rows.max_prefix = table_capacity(c, prefix_blocks);
+  const cudaError_t e = launch_paged_rows(p, c.model->head_dim, std::min(sms, kPagedMaxSms), reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "shared-prefix attention launch");
+  return set_error(ctx, PIC_OK, "");
+}
+
+}  // extern "C"

@@ -13,6 +13,12 @@
 // head of the run and stay in registers.  Copies (values, latents) are warps of
 // their own.  Rows are asked for before anything they do not depend on, and
 // positions, slots and blocks are looked at after that.
+// With norms (pic_write_normed_tokens) a head x is first replaced by
+// x / sqrt(mean(x^2) + eps) * w.  The lanes that turn a head hold all of it, so the sum of
+// its squares is joined by 2 to 4 shuffles between its load and its rotation, all
+// in fp32, and a value is rounded once.  The weights lie in shared memory as fp32:
+// in registers they would be 32 more, for q and k.  The latent of an MLA row is
+// normalised by a warp of its own, two chunks a lane.
 // Measured (GB300, 32 + 8 heads of 128 dims): 16,384 tokens of three axes 61.0 us,
 // 403 MB at 6.6 TB/s; 64 tokens 2.9 us; one token 2.7 us.  MLA, 16 query heads,
 // 2,048 tokens: 16.0 us, 5.0 TB/s.
@@ -31,13 +37,43 @@ constexpr int kRotBatch = 2;    // heads in flight per lane
 constexpr int kCopyBatch = 8;   // 16-byte chunks in flight per lane
 constexpr int kLatentChunks = 512 * 2 / 16;   // 16-byte chunks of a latent (pic_create admits no other width)
 
-template <int PAIRING>
+constexpr int kNormDims = 256;   // of the widest head that is normalised whole
+
+// Eight weights of a norm, from element 8 i on, as they multiply.
+__device__ __forceinline__ void norm_weights(const WriteParams& P, const uint8_t* w, int i, float* out) {
+  if (P.norm_f32) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(w) + 2 * i), b = __ldg(reinterpret_cast<const float4*>(w) + 2 * i + 1);
+    out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w;
+    out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
+  } else {
+    uint4 a = __ldg(reinterpret_cast<const uint4*>(w) + i);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      out[2 * x] = bf_lo(word(a, x));
+      out[2 * x + 1] = bf_hi(word(a, x));
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 8; ++x) out[x] += P.norm_offset;
+}
+__device__ __forceinline__ float sum_squares(uint4 v) {
+  float s = 0.0f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const float2 y = bf_pair(word(v, x));
+    s = __fmaf_rn(y.x, y.x, __fmaf_rn(y.y, y.y, s));
+  }
+  return s;
+}
+
+template <int PAIRING, bool NORM>
 __global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_constant__ WriteParams P) {
   constexpr bool NEOX = PAIRING == kNeox;
   __shared__ float4 s_freq[kWriteWarps][kMaxFreqs / 2];   // lanes read eight of their own
   __shared__ __align__(8) uint8_t s_axis[kWriteWarps][kMaxFreqs];
   const int lane = threadIdx.x & 31;
-  const int tasks = P.rot_parts + P.copy_parts;
+  __shared__ __align__(16) float s_norm[NORM ? kWriteWarps : 1][NORM ? 2 : 1][NORM ? kNormDims : 4];   // weights of q and k
+  const int tasks = P.rot_parts + P.copy_parts + (NORM ? P.latent_norm : 0);
   const int64_t task = static_cast<int64_t>(blockIdx.x) * kWriteWarps + (threadIdx.x >> 5);
   const int row_bytes = P.kv_heads * P.head_bytes;
   const int tok = static_cast<int>(task / tasks), part = static_cast<int>(task - static_cast<int64_t>(tok) * tasks);
@@ -95,6 +131,15 @@ __global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_
         put_freq(freq, i, P.freq.turns[i]);
         axis[i] = P.axis[i];
       }
+      float(*norm)[NORM ? kNormDims : 4] = s_norm[NORM ? threadIdx.x >> 5 : 0];
+      if constexpr (NORM) {
+        // (MLA: heads as they are, its latent has a warp of its own)
+        for (int i = lane; i < 4 * lph && P.latent_norm == 0; i += 32) {
+          const int kind = i / (2 * lph), chunk = i - kind * 2 * lph;
+          const uint8_t* w = kind == 0 ? P.q_norm : P.k_norm;
+          if (w != nullptr) norm_weights(P, w, chunk, &norm[kind][8 * chunk]);
+        }
+      }
       __syncwarp();
       if (bad_position()) return;
       const int64_t row = find_row();
@@ -114,13 +159,45 @@ __global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_
       uint8_t* qd = P.q_out + tok * P.q_out_stride;
       uint8_t* kd = P.k_cache + row * row_bytes - static_cast<int64_t>(P.q_heads) * P.head_bytes;
       const int step = kRotBatch * hpi;
-      for (int h0 = h_begin; h0 < h_end; h0 += 2 * step) {
+      // (with norms all lanes leave the loop together: they meet in shuffles)
+      for (int h0 = h_begin; (NORM ? h0 - sub : h0) < h_end; h0 += 2 * step) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           load(h0 + (x + 1) * step, a[x ^ 1], b[x ^ 1]);
 #pragma unroll
           for (int u = 0; u < kRotBatch; ++u) {
             const int h = h0 + x * step + u * hpi;
+            if constexpr (NORM) {
+              // (every lane takes part in the shuffles; a head past the end is not stored)
+              const int kind = h < P.q_heads ? 0 : 1;
+              const bool normed = P.latent_norm == 0 && (kind == 0 ? P.q_norm : P.k_norm) != nullptr;
+              float sum = h < h_end ? sum_squares(a[x][u]) + sum_squares(b[x][u]) : 0.0f;
+              for (int o = 1; o < lph; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              if (h >= h_end || (h >= P.q_heads && row < 0)) continue;
+              if (normed) {
+                const float r = rsqrtf(sum / static_cast<float>(16 * lph) + P.norm_eps);
+                const float* wa = &norm[kind][8 * (NEOX ? j : 2 * j)];
+                const float* wb = &norm[kind][8 * (NEOX ? j + lph : 2 * j + 1)];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 ya = bf_pair(word(a[x][u], e)), yb = bf_pair(word(b[x][u], e));
+                  const float a0 = ya.x * r * wa[2 * e], a1 = ya.y * r * wa[2 * e + 1];
+                  const float b0 = yb.x * r * wb[2 * e], b1 = yb.y * r * wb[2 * e + 1];
+                  if (NEOX) {   // pairs (a, b) of frequencies 2 e and 2 e + 1
+                    const float c0 = c[2 * e], c1 = c[2 * e + 1], s0 = s[2 * e], s1 = s[2 * e + 1];
+                    word(a[x][u], e) = bf_pack(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
+                    word(b[x][u], e) = bf_pack(a0 * s0 + b0 * c0, a1 * s1 + b1 * c1);
+                  } else {      // pairs (a0, a1) of frequency e, (b0, b1) of 4 + e
+                    word(a[x][u], e) = bf_pack(a0 * c[e] - a1 * s[e], a0 * s[e] + a1 * c[e]);
+                    word(b[x][u], e) = bf_pack(b0 * c[4 + e] - b1 * s[4 + e], b0 * s[4 + e] + b1 * c[4 + e]);
+                  }
+                }
+                uint8_t* dst = (h < P.q_heads ? qd : kd) + static_cast<int64_t>(h) * P.head_bytes;
+                *reinterpret_cast<uint4*>(dst + off_a) = a[x][u];
+                *reinterpret_cast<uint4*>(dst + off_b) = b[x][u];
+                continue;
+              }
+            }
             if (h >= h_end || (h >= P.q_heads && row < 0)) continue;
             if (NEOX) {
               rotate_neox(a[x][u], b[x][u], c, s);
@@ -135,6 +212,38 @@ __global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_
         }
       }
       return;
+    }
+    auto clear_weights = [&](int64_t row) {
+      const int64_t block = row / P.paged.block_size, at = row % P.paged.block_size;
+      for (int h = lane; h < P.weight_heads; h += 32)
+        P.weights[(block * P.weight_heads + h) * P.paged.block_size + at] = 0.0f;
+    };
+    if constexpr (NORM) {
+      if (part == P.rot_parts + P.copy_parts) {   // the latent of the key row
+        const uint4* from = reinterpret_cast<const uint4*>(P.k + tok * P.k_stride);
+        uint4 v[2] = {from[lane], from[lane + 32]};
+        float w[2][8];
+        norm_weights(P, P.k_norm, lane, w[0]);
+        norm_weights(P, P.k_norm, lane + 32, w[1]);
+        float sum = sum_squares(v[0]) + sum_squares(v[1]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float r = rsqrtf(sum * (1.0f / (8 * kLatentChunks)) + P.norm_eps);
+        if (bad_position()) return;
+        const int64_t row = find_row();
+        if (row < 0) return;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = bf_pair(word(v[x], e));
+            word(v[x], e) = bf_pack(y.x * r * w[x][2 * e], y.y * r * w[x][2 * e + 1]);
+          }
+          reinterpret_cast<uint4*>(P.k_cache + row * row_bytes)[lane + 32 * x] = v[x];
+        }
+        if (P.weights != nullptr && P.copy_parts == 0) clear_weights(row);
+        return;
+      }
     }
     // copies: the query heads' latent chunks, then the key row's, then the value row
     const int nq = P.q_heads * P.q_copy_chunks, nk = P.k_copy_chunks;
@@ -163,22 +272,24 @@ __global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_
       else to = P.v_cache + row * row_bytes + (i - nq - nk) * 16;
       *reinterpret_cast<uint4*>(to) = x[u];
     }
-    if (P.weights != nullptr && row >= 0 && part == P.rot_parts) {
-      const int64_t block = row / P.paged.block_size, at = row % P.paged.block_size;
-      for (int h = lane; h < P.weight_heads; h += 32)
-        P.weights[(block * P.weight_heads + h) * P.paged.block_size + at] = 0.0f;
-    }
+    if (P.weights != nullptr && row >= 0 && part == P.rot_parts) clear_weights(row);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_write(const WriteParams& p, int pairing, cudaStream_t s) {
-  const int64_t warps = static_cast<int64_t>(p.n_tokens) * (p.rot_parts + p.copy_parts);
+namespace {
+template <bool NORM>
+cudaError_t launch(const WriteParams& p, int pairing, cudaStream_t s) {
+  const int64_t warps = static_cast<int64_t>(p.n_tokens) * (p.rot_parts + p.copy_parts + p.latent_norm);
   const unsigned grid = static_cast<unsigned>((warps + kWriteWarps - 1) / kWriteWarps);
-  if (pairing == kNeox) k_write_tokens<kNeox><<<grid, kWriteThreads, 0, s>>>(p);
-  else k_write_tokens<kInterleaved><<<grid, kWriteThreads, 0, s>>>(p);
+  if (pairing == kNeox) k_write_tokens<kNeox, NORM><<<grid, kWriteThreads, 0, s>>>(p);
+  else k_write_tokens<kInterleaved, NORM><<<grid, kWriteThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
+}  // namespace
+
+cudaError_t launch_write(const WriteParams& p, int pairing, cudaStream_t s) { return launch<false>(p, pairing, s); }
+cudaError_t launch_write_normed(const WriteParams& p, int pairing, cudaStream_t s) { return launch<true>(p, pairing, s); }
 
 }  // namespace pic

@@ -92,6 +92,24 @@ class pic_new_tokens(ctypes.Structure):
 
 _NEW_TOKENS = struct.Struct("@iii4xPPPqPqPqPqPP")
 assert _NEW_TOKENS.size == ctypes.sizeof(pic_new_tokens)
+class pic_head_norms(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_type", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
+
+
+class pic_token_map(ctypes.Structure):
+    _fields_ = [
+        ("n_req", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+        ("d_seq_lens", ctypes.c_void_p), ("d_grow", ctypes.c_void_p), ("d_block_tables", ctypes.c_void_p),
+        ("d_free_blocks", ctypes.c_void_p), ("d_n_free", ctypes.c_void_p), ("d_shift", ctypes.c_void_p),
+        ("d_new_lens", ctypes.c_void_p), ("d_new_n_free", ctypes.c_void_p), ("d_indptr", ctypes.c_void_p),
+        ("d_req", ctypes.c_void_p), ("d_slot", ctypes.c_void_p), ("d_pos", ctypes.c_void_p),
+    ]
+
+
+_HEAD_NORMS = struct.Struct("@PPiff4x")
+_TOKEN_MAP = struct.Struct("@iii4xPPPPPPPPPPPP")
+assert _HEAD_NORMS.size == ctypes.sizeof(pic_head_norms) and _TOKEN_MAP.size == ctypes.sizeof(pic_token_map)
 _last_axes = (None, None)   # the frequency axes passed last, and as a C array (a model's calls all pass the same)
 
 _c_void_p = ctypes.c_void_p
@@ -149,6 +167,18 @@ _SIGNATURES = {
     "pic_s1_windows": (ctypes.c_int, [_i64, _i64, _i32, _P(_i64), _P(_i64), _i64, _P(_i64)]),
     "pic_write_tokens": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i32,
                                         _c_void_p, _i32, _c_void_p, _sz, _c_void_p]),
+    "pic_write_normed_tokens": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i32,
+                                               _c_void_p, _i32, _c_void_p, _sz, _c_void_p]),
+    "pic_map_tokens_workspace_bytes": (_sz, [_c_void_p, _i32]),
+    "pic_map_tokens": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p]),
+    "pic_attend_tokens_workspace_bytes": (_sz, [_c_void_p, _i32, _i32, _i32]),
+    "pic_attend_tokens": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i32, _i32, ctypes.c_float, _c_void_p, _c_void_p, _c_void_p,
+                                         _i32, _i32, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _c_void_p, _c_void_p, _sz,
+                                         _c_void_p]),
+    "pic_attend_shared_workspace_bytes": (_sz, [_c_void_p, _i32, _i32]),
+    "pic_attend_shared": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i32, _i32, ctypes.c_float, _c_void_p, _c_void_p, _c_void_p,
+                                         _i32, _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p,
+                                         _sz, _c_void_p]),
     "pic_attend_paged_workspace_bytes": (_sz, [_c_void_p, _i32, _i32, _i32, _i32]),
     "pic_attend_paged": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i32, _i32, ctypes.c_float, _c_void_p, _c_void_p,
                                         _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _c_void_p, _i32,
@@ -780,6 +810,36 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
     [n_tokens][q_heads][head_dim], q_out may be q.  weights: float32
     [blocks][weight_heads][block_size], zeroed at the written slots.
     workspace: uint8, PIC_STATUS_BYTES, zeroed when made (its status is sticky)."""
+    _write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_cache, q, q_out, freq_axis, weights, workspace, stream,
+                  None)
+
+
+def pic_write_normed_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_cache, q_norm=None, k_norm=None,
+                            eps=1e-6, offset=0.0, q=None, q_out=None, freq_axis=None, weights=None, workspace=None, stream=None):
+    """pic_write_tokens with every head x normalised before it is turned:
+    x / sqrt(mean(x^2) + eps) * (offset + norm).  q_norm, k_norm: float32 or
+    bf16 [head_dim] (MLA: q_norm None, k_norm [512], of the latent), or None: heads
+    as they are."""
+    norms = [x for x in (q_norm, k_norm) if x is not None]
+    if _torch is None:
+        _with_torch()
+    for x in norms:
+        if x.dtype not in (_F32, _BF16) or x.dtype is not norms[0].dtype or x.dim() != 1 or not x.is_contiguous():
+            raise ValueError("q_norm and k_norm must be contiguous vectors, both float32 or both bf16")
+    want = _geometry.get(ctx.value)
+    if want is not None:
+        d = want[1][2]
+        if (q_norm is not None and q_norm.numel() != d) or \
+                (k_norm is not None and k_norm.numel() != (PIC_LATENT_DIM if d == _LATENT_ROW else d)):
+            raise ValueError("a norm has a weight for each dim of a head (MLA: of the latent)")
+    packed = _HEAD_NORMS.pack(0 if q_norm is None else q_norm.data_ptr(), 0 if k_norm is None else k_norm.data_ptr(),
+                              PIC_F32 if norms and norms[0].dtype is _F32 else PIC_BF16, eps, offset)
+    _write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_cache, q, q_out, freq_axis, weights, workspace, stream,
+                  packed)
+
+
+def _write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_cache, q, q_out, freq_axis, weights, workspace, stream,
+                  norms):
     global _last_axes
     lib = _lib if _torch is not None else _with_torch()
     shape = positions.shape
@@ -826,8 +886,9 @@ def pic_write_tokens(ctx, positions, k, v, req, slot, block_tables, k_cache, v_c
         0 if q is None else q.data_ptr(), q_stride, 0 if q is None else q_out.data_ptr(), out_stride,
         0 if k is None else k.data_ptr(), k_stride, 0 if v is None else v.data_ptr(), v_stride,
         0 if k is None else req.data_ptr(), 0 if k is None else slot.data_ptr())
-    _launch(ctx, lib.pic_write_tokens, positions.get_device(), stream,
-            (t, _addr(k_cache), _addr(v_cache), _addr(block_tables), n_tables, max_blocks, _addr(weights), heads,
+    fn, t = (lib.pic_write_tokens, (t,)) if norms is None else (lib.pic_write_normed_tokens, (t, norms))
+    _launch(ctx, fn, positions.get_device(), stream,
+            t + (_addr(k_cache), _addr(v_cache), _addr(block_tables), n_tables, max_blocks, _addr(weights), heads,
              _addr(workspace), _size(workspace)))
 
 
@@ -900,6 +961,110 @@ def pic_evict_tokens(ctx, k_cache, v_cache, weights, block_tables, seq_lens, bud
             (layers, k_cache.data_ptr(), _addr(v_cache), stride * 2, weights.data_ptr(), weights.stride()[0] * 4, heads,
              block_tables.data_ptr(), n_req, max_blocks, seq_lens.data_ptr(), budget, n_first, n_recent, 1 if renumber else 0,
              kept.data_ptr(), new_lens.data_ptr(), _addr(workspace), _size(workspace)))
+
+
+def pic_map_tokens_workspace_bytes(ctx, n_req: int) -> int:
+    return int(load().pic_map_tokens_workspace_bytes(ctx, int(n_req)))
+
+
+def pic_map_tokens(ctx, seq_lens, grow, block_tables, free_blocks, n_free, new_lens, new_n_free, indptr, req, slot, positions=None,
+                   shift=None, workspace=None, stream=None):
+    """Blocks and slots of one serving step, all CUDA int32.  seq_lens, grow [n_req]:
+    request r gets grow[r] new tokens (below 0: loses its last slots).
+    block_tables [n_req][max_blocks], new blocks filled in; free_blocks
+    [num_cache_blocks], of which the first n_free [1] are free, given-back blocks put on top.
+    Writes new_lens [n_req] (may be seq_lens), new_n_free [1] (may be n_free), indptr
+    [n_req + 1] (each request's rows of the token lists), req and slot [n_tokens]
+    (slot -1: padding, or a request that was refused) and positions [n_tokens] = slot +
+    shift[r] (shift [n_req] or None).  workspace: uint8,
+    pic_map_tokens_workspace_bytes, its first PIC_STATUS_BYTES zeroed when made."""
+    lib = _lib if _torch is not None else _with_torch()
+    n_req, n = seq_lens.numel(), slot.numel()
+    max_blocks = _table_shape(block_tables, n_req)[1]
+    _dense_int32(seq_lens, "seq_lens")
+    _dense_int32(slot, "slot")
+    for t, name, numel in ((grow, "grow", n_req), (new_lens, "new_lens", n_req), (n_free, "n_free", 1), (new_n_free, "new_n_free", 1),
+                           (indptr, "indptr", n_req + 1), (req, "req", n)):
+        _dense_int32(t, name, numel)
+    if positions is not None:
+        _dense_int32(positions, "positions", n)
+    if shift is not None:
+        _dense_int32(shift, "shift", n_req)
+    want = _geometry.get(ctx.value)
+    _dense_int32(free_blocks, "free_blocks", None if want is None else want[0])
+    t = _TOKEN_MAP.pack(n_req, max_blocks, n, seq_lens.data_ptr(), grow.data_ptr(), block_tables.data_ptr(), free_blocks.data_ptr(),
+                        n_free.data_ptr(), 0 if shift is None else shift.data_ptr(), new_lens.data_ptr(), new_n_free.data_ptr(),
+                        indptr.data_ptr(), req.data_ptr(), slot.data_ptr(), 0 if positions is None else positions.data_ptr())
+    _launch(ctx, lib.pic_map_tokens, indptr.get_device(), stream, (t, _addr(workspace), _size(workspace)))
+
+
+def _rows_out(q, out, lse, cache):
+    """Checks out and lse of an attention over rows q [rows][q_heads][head_dim]."""
+    rows, hq, d = q.shape
+    if d != cache[3] or out.dtype is not _BF16 or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape, heads of the cache's head_dim")
+    if lse is not None and (lse.dtype is not _F32 or lse.numel() != rows * hq or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [rows][q_heads]")
+
+
+def pic_attend_tokens_workspace_bytes(ctx, n_tokens: int, n_req: int, num_q_heads: int) -> int:
+    return int(load().pic_attend_tokens_workspace_bytes(ctx, int(n_tokens), int(n_req), int(num_q_heads)))
+
+
+def pic_attend_tokens(ctx, q, softmax_scale, k_cache, v_cache, block_tables, indptr, slot, out, window: int = 0, n_first: int = 0,
+                      lse=None, workspace=None, stream=None):
+    """New tokens attend to the slots before them (and their own) in their requests'
+    paged caches.  q: bf16 [n_tokens][q_heads][head_dim], any token stride; k_cache,
+    v_cache: one layer [blocks][block_size][kv_heads][head_dim]; block_tables: CUDA
+    int32 [n_req][max_blocks]; indptr: CUDA int32 [n_req + 1], request r's tokens are rows
+    [indptr[r], indptr[r + 1]); slot: CUDA int32 [n_tokens], below 0: padding.  window > 0:
+    of the slots before, the last `window` and the n_first first.  out: bf16 of q's
+    shape; lse: float32 [n_tokens][q_heads] or None.  workspace: uint8,
+    pic_attend_tokens_workspace_bytes, its first PIC_STATUS_BYTES zeroed when made."""
+    lib = _lib if _torch is not None else _with_torch()
+    shape = q.shape
+    stride = _token_rows(q, "q", shape)
+    n, hq, _ = shape
+    n_req = indptr.numel() - 1
+    if n_req < 0:
+        raise ValueError("indptr holds n_req + 1 offsets")
+    _dense_int32(indptr, "indptr")
+    _dense_int32(slot, "slot", n)
+    max_blocks = _table_shape(block_tables, n_req)[1]
+    cache, _ = _check_caches(ctx, k_cache, v_cache, 4)
+    _rows_out(q, out, lse, cache)
+    _launch(ctx, lib.pic_attend_tokens, q.get_device(), stream,
+            (q.data_ptr(), stride, n, hq, softmax_scale, k_cache.data_ptr(), _addr(v_cache), block_tables.data_ptr(), n_req,
+             max_blocks, indptr.data_ptr(), slot.data_ptr(), window, n_first, out.data_ptr(), _addr(lse), _addr(workspace),
+             _size(workspace)))
+
+
+def pic_attend_shared_workspace_bytes(ctx, n_req: int, num_q_heads: int) -> int:
+    return int(load().pic_attend_shared_workspace_bytes(ctx, int(n_req), int(num_q_heads)))
+
+
+def pic_attend_shared(ctx, q, softmax_scale, k_cache, v_cache, prefix_table, prefix_len, block_tables, seq_lens, max_seq_len: int,
+                      out, lse=None, workspace=None, stream=None):
+    """One new token per request over its cached sequence, whose first prefix_len
+    slots all requests share.  prefix_table: CUDA int32 [prefix_blocks], the blocks of those
+    slots; prefix_len: CUDA int32 [1]; the others as for pic_attend_paged, the rows of
+    block_tables holding the slots behind the prefix at their places.  out: bf16 of
+    q's shape.  workspace: uint8, pic_attend_shared_workspace_bytes, its first
+    PIC_STATUS_BYTES zeroed when made."""
+    lib = _lib if _torch is not None else _with_torch()
+    shape = q.shape
+    stride = _token_rows(q, "q", shape)
+    n_req, hq, _ = shape
+    _dense_int32(seq_lens, "seq_lens", n_req)
+    _dense_int32(prefix_table, "prefix_table")
+    _dense_int32(prefix_len, "prefix_len", 1)
+    max_blocks = _table_shape(block_tables, n_req)[1]
+    cache, _ = _check_caches(ctx, k_cache, v_cache, 4)
+    _rows_out(q, out, lse, cache)
+    _launch(ctx, lib.pic_attend_shared, q.get_device(), stream,
+            (q.data_ptr(), stride, n_req, hq, softmax_scale, k_cache.data_ptr(), _addr(v_cache), prefix_table.data_ptr(),
+             prefix_table.numel(), prefix_len.data_ptr(), block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(), max_seq_len,
+             out.data_ptr(), _addr(lse), _addr(workspace), _size(workspace)))
 
 
 def pic_debug_stall_next_launch(ctx, stall_tile: int, max_spins: int = 0):
