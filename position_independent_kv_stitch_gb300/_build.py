@@ -25,9 +25,9 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["pic_host.cpp", "pic_kernels.cu", "pic_kernels_tma.cu", "pic_attention.cu", "pic_attention_tc.cu",
            "pic_noalloc.cu", "pic_cdc.cu", "pic_stage.cu", "pic_decode.cpp", "pic_write.cu", "pic_paged.cu", "pic_evict.cu",
-           "pic_serve.cpp", "pic_map.cu"]
+           "pic_serve.cpp", "pic_map.cu", "pic_tile.cu"]
 HEADERS = [os.path.join(CSRC, "pic_internal.h"), os.path.join(CSRC, "pic_decode.h"), os.path.join(CSRC, "pic_entry.h"),
-           os.path.join(CSRC, "pic_device.cuh"), os.path.join(CSRC, "pic_paged.cuh"),
+           os.path.join(CSRC, "pic_device.cuh"), os.path.join(CSRC, "pic_paged.cuh"), os.path.join(CSRC, "pic_tc.cuh"),
            os.path.join(INCLUDE, "pic.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -142,7 +142,9 @@ constexpr int kPagedMaxHeads = 4096;    // query heads
 // counted without the gap between those that it sees: the first `head` are slots
 // 0 .. head - 1, number v from there on is slot v + gap.
 struct RowsParams {
-  int32_t shared;            // 0: tokens of requests; 1: one token a request, the prefix shared
+  int32_t shared;            // 0: tokens of requests; 1: one token a request, the prefix shared; 2: the same
+                             // without the prefix, whose part of each row is in the records `extra`
+  int32_t singles;           // tokens: 1 where requests of more than one token are another kernel's
   const int32_t* indptr;     // [n_req + 1] tokens: rows of each request
   const int32_t* slot;       // [rows] tokens: slot of each
   int32_t n_req;             // tokens: requests
@@ -151,6 +153,9 @@ struct RowsParams {
   const int32_t* prefix_table;   // shared: [prefix_blocks]
   const int32_t* prefix_len;     // shared: [1]
   int32_t prefix_blocks, max_prefix;
+  int32_t n_extra;           // records per row of the prefix's parts: [n_extra][n_req][q_heads]
+  const float* extra_acc;    // [..][D]; not written where the sum is 0
+  const float2* extra_ml;
 };
 
 struct PagedParams {
@@ -187,6 +192,45 @@ struct PagedParams {
 int paged_ranges_per_sm(int head_dim);  // ranges an SM works on at a time (head_dim 576: MLA rows)
 cudaError_t launch_paged(const PagedParams& p, int head_dim, int sm_count, cudaStream_t s);
 cudaError_t launch_paged_rows(const PagedParams& p, int head_dim, int sm_count, cudaStream_t s);   // bf16 out, no weights
+
+// ---- attention of tiles of query rows (pic_tile.cu)
+constexpr int kTileRows = 128;          // rows of a product: (token, query head of the KV head) pairs
+__host__ __device__ constexpr int tile_groups(int head_dim) { return head_dim <= 128 ? 2 : 1; }   // tiles of a CTA
+__host__ __device__ constexpr int tile_slots(int head_dim) { return head_dim <= 128 ? 128 : 64; } // slots of a step
+struct TileMaps {
+  CUtensorMap k, v;
+};
+struct TileParams {
+  PagedView paged;           // tokens: the requests' tables; prefix: its table, alone
+  const uint8_t* q;
+  int64_t q_stride;          // bytes between tokens
+  int32_t n_tokens;
+  int32_t q_heads, kv_heads, group;
+  // tokens: rows of requests
+  const int32_t* indptr;     // [n_req + 1]; null: one request of all tokens, the prefix's readers
+  const int32_t* slot;       // [n_tokens]
+  int32_t n_req;
+  int32_t capacity;          // slots a table holds
+  int32_t window, n_first;
+  // prefix: a token sees the first min(lens, prefix) slots
+  const int32_t* lens;       // [n_tokens]
+  const int32_t* prefix_len;
+  int32_t max_len;
+  int32_t least;             // tokens: requests of fewer tokens are another kernel's
+  float scale_log2;          // of |scale| (1 where it is 0)
+  int32_t sign;              // of scale: the queries enter as they are, negated, or as 0
+  int32_t blocks;            // row blocks launched per KV head, at least those there are
+  int32_t splits;            // parts of a row block's slots
+  int32_t box;               // slots of one copy
+  int32_t cache_rows;        // one past the last row of the cache
+  void* out;                 // splits == 1 of tokens: bf16 [n_tokens][q_heads][D]
+  float* lse;
+  float* rec_acc;            // else [splits][n_tokens][q_heads][D]
+  float2* rec_ml;            // and the running max (log2 units) and sum
+  uint32_t* status;
+};
+cudaError_t launch_tile(const TileParams& p, const TileMaps& maps, int head_dim, cudaStream_t s);
+cudaError_t launch_tile_join(const TileParams& p, int head_dim, cudaStream_t s);
 
 // ---- eviction
 struct EvictUnit {           // per (layer, request, weight head), in the workspace

@@ -968,28 +968,11 @@ struct AttnLayout {
   size_t freq_off, stages_off, tiles_off, toks_off, keys_off, records_off, total;
 };
 
-// cuTensorMapEncodeTiled, looked up once through the runtime (no link to the
-// driver library).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
-
 // A view of MLA rows as [layers][rows][576] bf16, read in boxes of box_rows
 // rows x 64 dims with 128-byte swizzle; rows past `rows` read as zeros.
 bool encode_mla_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t layers, int64_t layer_stride,
                      uint32_t box_rows) {
-  EncodeTiledFn enc = encode_tiled();
+  pic::EncodeTiledFn enc = pic::encode_tiled();
   if (!enc || !base || rows <= 0 || layers <= 0 || (layer_stride & 15) || rows > (int64_t{1} << 32)) return false;
   if (layers > 1 && layer_stride < rows * 1152) return false;
   const cuuint64_t dims[3] = {576, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(layers)};
@@ -2234,6 +2217,20 @@ pic_status pic_attend_decode(pic_ctx* ctx, const pic_plan* const* plans, int32_t
 namespace pic {
 
 pic_status set_error(pic_ctx* ctx, pic_status st, const char* msg) { return fail(ctx, st, "%s", msg); }
+
+// cuTensorMapEncodeTiled, looked up once through the runtime (no link to the
+// driver library).
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
 
 CtxView ctx_view(const pic_ctx* ctx) { return CtxView{&ctx->model, ctx->freq_turns.data(), ctx->num_cache_blocks}; }
 

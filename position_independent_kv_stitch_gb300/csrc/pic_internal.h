@@ -241,6 +241,11 @@ struct TcTileRec {
 };
 static_assert(sizeof(TcTileRec) == 176, "TcTileRec layout: 44 ints");
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();   // null where the driver has none
+
 struct TcMaps {
   CUtensorMap pool[4];
   CUtensorMap cache[4];

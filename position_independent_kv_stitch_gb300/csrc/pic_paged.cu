@@ -131,17 +131,23 @@ __device__ __forceinline__ int request_of(const RowsParams& R, int i) {
   }
   return lo;
 }
+// Whether row r of pic_attend_tokens is this kernel's.
+__device__ __forceinline__ bool owns_row(const RowsParams& R, int r) {
+  if (R.singles == 0) return r >= __ldg(R.indptr) && r < __ldg(R.indptr + R.n_req);
+  const int x = request_of(R, r);
+  return x >= 0 && __ldg(R.indptr + x + 1) - __ldg(R.indptr + x) == 1;
+}
 __device__ __forceinline__ int prefix_of(const PagedParams& P, bool raise) {
   return legal_len(__ldg(P.rows.prefix_len), P.rows.max_prefix, P.status, raise);
 }
 __device__ __forceinline__ Span span_of(const PagedParams& P, int r, bool raise) {
   const RowsParams& R = P.rows;
   if (R.shared != 0) {
-    const int len = legal_len(__ldg(P.lens + r), P.max_len, P.status, raise);
-    return Span{len, min(prefix_of(P, raise), len), 0};
+    const int len = legal_len(__ldg(P.lens + r), P.max_len, P.status, raise), head = min(prefix_of(P, raise), len);
+    return R.shared == 1 ? Span{len, head, 0} : Span{len - head, 0, head};
   }
   const int s = __ldg(R.slot + r);
-  if (s < 0 || r < __ldg(R.indptr) || r >= __ldg(R.indptr + R.n_req)) return Span{0, 0, 0};
+  if (s < 0 || !owns_row(R, r)) return Span{0, 0, 0};
   if (s >= R.capacity) {
     if (raise) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_BAD_LENGTH));
     return Span{0, 0, 0};
@@ -862,8 +868,15 @@ __device__ __forceinline__ float2 load_ml(const PagedParams& P, const Records& x
 }
 // Largest running maximum of a query head's records, and the sum of their
 // sums brought to it (warp-wide).
-__device__ __forceinline__ void join_stats(const PagedParams& P, const Records& x, int hq, int lane, float& M, float& sum) {
+__device__ __forceinline__ void join_stats(const PagedParams& P, const Records& x, int hq, int lane, float& M, float& sum,
+                                           const float2* extra = nullptr, int n_extra = 0, int64_t pitch = 0) {
   float m = -FLT_MAX, s = 0.0f;
+  for (int k = lane; k < n_extra; k += 32) {
+    const float2 ml = __ldcg(extra + k * pitch);
+    const float up = fmaxf(m, ml.x);
+    s = s * ex2(m - up) + ml.y * ex2(ml.x - up);
+    m = up;
+  }
   for (int k = lane; k < x.count; k += 32) {
     const float2 ml = load_ml(P, x, k, hq);
     const float up = fmaxf(m, ml.x);
@@ -906,14 +919,34 @@ __device__ __forceinline__ void store_out(const PagedParams& P, int64_t at, floa
 
 // out and lse of (request, query head) `task`, by one warp or (ALL) by all
 // warps of the CTA, which share the records.
-template <int D, bool ALL>
+template <int D, bool ALL, bool ROWS>
 __device__ __forceinline__ void join_output(const PagedParams& P, const Records& x, int r, int hq, float* part) {
   constexpr int V = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float M, sum, acc[V];
-  join_stats(P, x, hq, lane, M, sum);
-  join_values<D>(P, x, hq, lane, M, ALL ? warp : 0, ALL ? kFinishWarps : 1, acc);
   const int64_t task = static_cast<int64_t>(r) * P.q_heads + hq;
+  if constexpr (ROWS) {   // the prefix's parts first
+    const int64_t pitch = static_cast<int64_t>(P.n_req) * P.q_heads;
+    const float2* ml = P.rows.extra_ml + task;
+    join_stats(P, x, hq, lane, M, sum, ml, P.rows.n_extra, pitch);
+    join_values<D>(P, x, hq, lane, M, ALL ? warp : 0, ALL ? kFinishWarps : 1, acc);
+#pragma unroll 4
+    for (int k = ALL ? warp : 0; k < P.rows.n_extra; k += ALL ? kFinishWarps : 1) {
+      const float2 y = __ldcg(ml + k * pitch);
+      if (y.y == 0.0f) continue;   // nothing was written beside it
+      const float e = ex2(y.x - M);
+      const float* a = P.rows.extra_acc + (k * pitch + task) * D + lane * V;
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float2 z = __ldcg(reinterpret_cast<const float2*>(a + i));
+        acc[i] += e * z.x;
+        acc[i + 1] += e * z.y;
+      }
+    }
+  } else {
+    join_stats(P, x, hq, lane, M, sum);
+    join_values<D>(P, x, hq, lane, M, ALL ? warp : 0, ALL ? kFinishWarps : 1, acc);
+  }
   if (ALL) {
 #pragma unroll
     for (int i = 0; i < V; ++i) part[warp * D + lane * V + i] = acc[i];
@@ -1083,14 +1116,14 @@ __global__ void __launch_bounds__(kFinishThreads, 3) k_paged_finish(const __grid
     const int r = static_cast<int>(task / P.q_heads), hq = static_cast<int>(task % P.q_heads);
     if (r >= P.n_req) return;
     if constexpr (ROWS) {
-      if (P.rows.shared == 0 && request_of(P.rows, r) < 0) {   // a row of no request stays as it is
+      if (P.rows.shared == 0 && !owns_row(P.rows, r)) {   // a row of no request stays as it is
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
       }
     }
     const Records x = join_records<ROWS>(P, L, r, lane);
-    if (all) join_output<D, true>(P, x, r, hq, s_part);
-    else join_output<D, false>(P, x, r, hq, s_part);
+    if (all) join_output<D, true, ROWS>(P, x, r, hq, s_part);
+    else join_output<D, false, ROWS>(P, x, r, hq, s_part);
     return;
   }
   const int64_t warps = static_cast<int64_t>(P.weight_ctas) * kFinishWarps;

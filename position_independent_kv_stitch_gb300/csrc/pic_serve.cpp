@@ -41,6 +41,78 @@ PagedParams rows_params(const CtxView& c, const void* q, int64_t q_stride, int32
   return p;
 }
 
+// ---- tiles of rows (pic_tile.cu)
+
+// Row blocks per KV head, at most: of n_tokens tokens of n_req requests.
+int64_t tile_blocks(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
+  const int64_t rows = static_cast<int64_t>(kTileRows) * tile_groups(c.model->head_dim);
+  return n_tokens * (num_q_heads / c.model->num_kv_heads) / rows + std::min(n_req, n_tokens);
+}
+// Parts that a row block's slots are dealt to: as many as there are SMs for, and at
+// least four steps each.
+int32_t tile_splits(const CtxView& c, int64_t blocks, int sms, int64_t max_slots) {
+  const int64_t fit = sms / std::max<int64_t>(1, blocks * c.model->num_kv_heads);
+  const int64_t useful = max_slots / (4 * tile_slots(c.model->head_dim));
+  return static_cast<int32_t>(std::max<int64_t>(1, std::min(fit, useful)));
+}
+// Workspace of a call: the row-by-row kernels' part, then the records of split tiles.
+struct RowsLayout {
+  size_t acc, ml, total;
+};
+RowsLayout rows_layout(const CtxView& c, int64_t n_tokens, int64_t num_q_heads, int64_t splits) {
+  RowsLayout L{};
+  const int64_t n = splits * n_tokens * num_q_heads;
+  L.acc = paged_layout(c, n_tokens, num_q_heads, 0, false).total;
+  L.ml = align_up(L.acc + n * c.model->head_dim * sizeof(float), kWsAlign);
+  L.total = align_up(L.ml + n * sizeof(float2), kWsAlign);
+  return L;
+}
+// Parts at most, whatever the device and the slots (workspace sizing).
+int64_t most_splits(const CtxView& c, int64_t blocks) {
+  return tile_splits(c, blocks, kPagedMaxSms, std::numeric_limits<int64_t>::max());
+}
+
+// One cache tensor as the tiles read it: whole groups of 8 rows, planes of 64 dims
+// inside; or, where blocks are no multiple of 8, rows of one plane.  Rows past the end read as zeros.
+bool encode_cache(CUtensorMap* map, const void* base, const CtxView& c, int32_t box) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const pic_model_desc& m = *c.model;
+  const cuuint64_t rows = static_cast<cuuint64_t>(c.num_cache_blocks) * m.block_size, row = static_cast<cuuint64_t>(m.num_kv_heads) * m.head_dim * 2;
+  const cuuint64_t heads = m.num_kv_heads, d = m.head_dim;
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const auto run = [&](cuuint32_t rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* boxes) {
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, boxes, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (box >= 8) {
+    const cuuint64_t dims[5] = {64, 8, d / 64, rows / 8, heads}, strides[4] = {row, 128, 8 * row, d * 2};
+    const cuuint32_t boxes[5] = {64, 8, static_cast<cuuint32_t>(d / 64), static_cast<cuuint32_t>(box / 8), 1};
+    return run(5, dims, strides, boxes);
+  }
+  const cuuint64_t dims[3] = {d, heads, rows}, strides[2] = {d * 2, row};
+  const cuuint32_t boxes[3] = {64, 1, static_cast<cuuint32_t>(box)};
+  return run(3, dims, strides, boxes);
+}
+
+// The tiles' parameters that follow from a call's rows; false without a tensor map.
+bool tile_params(const CtxView& c, const PagedParams& p, float scale, TileParams* t, TileMaps* maps) {
+  const pic_model_desc& m = *c.model;
+  t->q = p.q;
+  t->q_stride = p.q_stride;
+  t->n_tokens = p.n_req;
+  t->q_heads = p.q_heads;
+  t->kv_heads = p.kv_heads;
+  t->group = p.group;
+  t->sign = scale > 0.0f ? 1 : (scale < 0.0f ? -1 : 0);
+  t->scale_log2 = t->sign == 0 ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
+  t->box = std::min(m.block_size & -m.block_size, tile_slots(m.head_dim));
+  t->cache_rows = c.num_cache_blocks * m.block_size;
+  t->status = p.status;
+  return encode_cache(&maps->k, p.k_cache, c, t->box) && encode_cache(&maps->v, p.v_cache, c, t->box);
+}
+
 // Arguments that both attentions share; PIC_OK to go on.
 pic_status check_rows(pic_ctx* ctx, const CtxView& c, const void* q, int64_t q_stride, int32_t n_rows, int32_t num_q_heads,
                       float scale, const void* k_cache, const void* v_cache, const void* out, const float* lse, const void* ws) {
@@ -62,6 +134,14 @@ pic_status check_rows(pic_ctx* ctx, const CtxView& c, const void* q, int64_t q_s
   if (!aligned(lse, 4) || !aligned(ws, kWsAlign))
     return fail(ctx, PIC_ERR_ALIGNMENT, "lse must be 4-byte aligned, the workspace 256-byte");
   return PIC_OK;
+}
+
+size_t tokens_bytes(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
+  const int64_t splits = n_tokens > n_req ? most_splits(c, tile_blocks(c, n_tokens, n_req, num_q_heads)) : 1;
+  return rows_layout(c, n_tokens, num_q_heads, splits > 1 ? splits : 0).total;
+}
+size_t shared_bytes(const CtxView& c, int64_t n_req, int32_t num_q_heads) {
+  return rows_layout(c, n_req, num_q_heads, most_splits(c, tile_blocks(c, n_req, 1, num_q_heads))).total;
 }
 
 }  // namespace
@@ -129,7 +209,7 @@ size_t pic_attend_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_tokens, i
   if (!ctx || n_tokens < 0 || n_req < 0) return 0;
   const CtxView c = ctx_view(ctx);
   if (c.model->kind != PIC_KIND_GQA || !paged_heads_ok(c, num_q_heads) || !paged_size_ok(n_tokens, num_q_heads)) return 0;
-  return paged_layout(c, n_tokens, num_q_heads, 0, false).total;
+  return tokens_bytes(c, n_tokens, n_req, num_q_heads);
 }
 
 pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_tokens, int32_t num_q_heads,
@@ -147,7 +227,7 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     return fail(ctx, PIC_ERR_INVALID_ARG, "null block table, offsets or slots");
   if (!aligned(d_tables, 4) || !aligned(d_indptr, 4) || !aligned(d_slot, 4))
     return fail(ctx, PIC_ERR_ALIGNMENT, "tables, offsets and slots must be 4-byte aligned");
-  const size_t need = paged_layout(c, n_tokens, num_q_heads, 0, false).total;
+  const size_t need = tokens_bytes(c, n_tokens, n_req, num_q_heads);
   if (ws_bytes < need) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   if (!some) return set_error(ctx, PIC_OK, "");
   const Buffer bufs[] = {{"q", q}, {"k_cache", k_cache}, {"v_cache", v_cache}, {"block tables", d_tables}, {"offsets", d_indptr},
@@ -164,13 +244,53 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
   p.rows.capacity = table_capacity(c, max_blocks);
   p.rows.window = window;
   p.rows.n_first = n_first;
-  const cudaError_t e = launch_paged_rows(p, c.model->head_dim, std::min(sms, kPagedMaxSms), reinterpret_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(ctx, e, "token attention launch");
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int used = std::min(sms, kPagedMaxSms);
+  // Requests of several tokens go in tiles of rows, single tokens row by row, each
+  // request by its own count, which is on the device: both kernels are
+  // launched and each leaves the other's alone.  One suffices where there are no more tokens than
+  // requests, or one request.
+  const bool tiles = n_tokens > n_req;
+  if (tiles) {
+    TileParams t{};
+    TileMaps maps;
+    if (!tile_params(c, p, softmax_scale, &t, &maps)) return fail(ctx, PIC_ERR_CUDA, "no tensor map of the cache");
+    t.paged = p.paged;
+    t.indptr = d_indptr;
+    t.slot = d_slot;
+    t.n_req = n_req;
+    t.capacity = p.rows.capacity;
+    t.window = window;
+    t.n_first = n_first;
+    t.least = n_req > 1 ? 2 : 1;
+    const int64_t blocks = tile_blocks(c, n_tokens, n_req, num_q_heads);
+    t.blocks = static_cast<int32_t>(blocks);
+    const int64_t slots = window > 0 ? std::min<int64_t>(t.capacity, static_cast<int64_t>(window) + n_first + n_tokens) : t.capacity;
+    t.splits = tile_splits(c, blocks, used, slots);
+    t.out = out;
+    t.lse = lse;
+    if (t.splits > 1) {
+      const RowsLayout L = rows_layout(c, n_tokens, num_q_heads, t.splits);
+      t.rec_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + L.acc);
+      t.rec_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + L.ml);
+    }
+    cudaError_t e = launch_tile(t, maps, c.model->head_dim, cs);
+    if (e == cudaSuccess && t.splits > 1) e = launch_tile_join(t, c.model->head_dim, cs);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "token attention launch");
+    p.rows.singles = 1;
+  }
+  if (!tiles || n_req > 1) {
+    const cudaError_t e = launch_paged_rows(p, c.model->head_dim, used, cs);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "token attention launch");
+  }
   return set_error(ctx, PIC_OK, "");
 }
 
 size_t pic_attend_shared_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32_t num_q_heads) {
-  return pic_attend_tokens_workspace_bytes(ctx, n_req, n_req, num_q_heads);
+  if (!ctx || n_req < 0) return 0;
+  const CtxView c = ctx_view(ctx);
+  if (c.model->kind != PIC_KIND_GQA || !paged_heads_ok(c, num_q_heads) || !paged_size_ok(n_req, num_q_heads)) return 0;
+  return shared_bytes(c, n_req, num_q_heads);
 }
 
 pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_req, int32_t num_q_heads, float softmax_scale,
@@ -190,7 +310,7 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
                 table_capacity(c, max_blocks));
   if (!aligned(d_tables, 4) || !aligned(d_seq_lens, 4) || !aligned(d_prefix_table, 4) || !aligned(d_prefix_len, 4))
     return fail(ctx, PIC_ERR_ALIGNMENT, "tables and lengths must be 4-byte aligned");
-  const size_t need = paged_layout(c, n_req, num_q_heads, 0, false).total;
+  const size_t need = shared_bytes(c, n_req, num_q_heads);
   if (ws_bytes < need) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   if (!some) return set_error(ctx, PIC_OK, "");
   const Buffer bufs[] = {{"q", q}, {"k_cache", k_cache}, {"v_cache", v_cache}, {"prefix table", d_prefix_table},
@@ -209,7 +329,34 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
   p.rows.prefix_len = d_prefix_len;
   p.rows.prefix_blocks = prefix_blocks;
   p.rows.max_prefix = table_capacity(c, prefix_blocks);
-  const cudaError_t e = launch_paged_rows(p, c.model->head_dim, std::min(sms, kPagedMaxSms), reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int used = std::min(sms, kPagedMaxSms);
+  cudaError_t e = cudaSuccess;
+  if (p.rows.max_prefix > 0) {
+    // the prefix in tiles of all requests' rows, whose records the join adds to those of the rest
+    TileParams t{};
+    TileMaps maps;
+    if (!tile_params(c, p, softmax_scale, &t, &maps)) return fail(ctx, PIC_ERR_CUDA, "no tensor map of the cache");
+    t.paged = paged_view(c, d_prefix_table, 1, prefix_blocks);
+    t.n_req = 1;
+    t.least = 1;
+    t.capacity = p.rows.max_prefix;
+    t.lens = d_seq_lens;
+    t.prefix_len = d_prefix_len;
+    t.max_len = max_seq_len;
+    const int64_t blocks = tile_blocks(c, n_req, 1, num_q_heads);
+    t.blocks = static_cast<int32_t>(blocks);
+    t.splits = tile_splits(c, blocks, used, t.capacity);
+    const RowsLayout L = rows_layout(c, n_req, num_q_heads, t.splits);
+    t.rec_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + L.acc);
+    t.rec_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + L.ml);
+    e = launch_tile(t, maps, c.model->head_dim, cs);
+    p.rows.shared = 2;
+    p.rows.n_extra = t.splits;
+    p.rows.extra_acc = t.rec_acc;
+    p.rows.extra_ml = t.rec_ml;
+  }
+  if (e == cudaSuccess) e = launch_paged_rows(p, c.model->head_dim, used, cs);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "shared-prefix attention launch");
   return set_error(ctx, PIC_OK, "");
 }

@@ -1,0 +1,709 @@
+// Attention of many query rows over the paged cache on the fifth-generation
+// tensor cores (tcgen05 with TMEM accumulators, TMA tensor copies), sm_103a:
+// prompts, chunked prompts, the tokens recomputed after a stitch, and all
+// requests' queries over the prefix they share.
+//
+//   s_it = scale * q_i . k_t where row i sees slot t (else -inf),
+//   out_i = sum_t p_it v_t,  p_i = softmax(s_i),  lse_i = log sum_t exp(s_it).
+//
+// Rows are (token, query head) pairs of one request and KV head, in the order of
+// tokens; a CTA takes 256 of them (two tiles of 128; 128 rows where heads have 256 dims) and
+// walks the slots that some of them see, 128 (64) at a time: the first n_first slots, then
+// from the lowest window's start to the highest slot.  One pass, with a running maximum and
+// sum.  Where there are too few row blocks for the SMs, a block's slots are
+// dealt to several CTAs, which leave records (O, max, sum) that a later kernel joins.
+//
+// Warps by role, per step of K and V tiles in a shared ring:
+//   * three producer warps look up the blocks of the step's slots and
+//     copy them with TMA, a whole block of all dims at a time: the cache is mapped as
+//     [head][8-row group][64-dim plane][8 rows][64 dims], so that a copy lands as rows of 128
+//     swizzled bytes in groups of 8, whichever blocks follow each other.  (A block size that is
+//     no multiple of 8 goes by 4, 2 or 1 rows and one plane at a time.)
+//   * one warp issues the products: S = Q K^T, M = 128 rows, N = slots, and
+//     O += P V with P read from TMEM and V as an MN-major operand;
+//   * four warps per tile, a thread per row: read S from TMEM, mask, raise the
+//     maximum when a score passes it by more than 2^8 (O and the sum are then rescaled, which
+//     after the first steps hardly happens), write P = exp2(s - m) as bf16 over S.
+// Two tiles take turns: while one is in its softmax, the tensor cores work on the other's.
+// (256 dims: O alone takes half of TMEM, so one tile, with the next step's S made ahead.)
+//
+// P is rounded to bf16 (2^-8 of each weight, where the output's own rounding is 2^-8 of
+// their sum), unnormalised: between 2^-8 and 2^8 at the maximum.  Sums, maxima and O
+// are fp32.  Masked scores are replaced, so what K holds there does not matter; V's
+// rows that no row of the CTA sees are zeroed in shared memory before the product.
+// Every wait is bounded: one that runs out raises PIC_DEV_TIMEOUT, tells the other
+// roles to stop, and the CTA frees its TMEM before it leaves.
+#include <cfloat>
+
+#include <cuda_bf16.h>
+
+#include "pic_decode.h"
+#include "pic_device.cuh"
+#include "pic_paged.cuh"
+#include "pic_tc.cuh"
+
+namespace pic {
+namespace {
+
+using namespace dev;
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLazy = 8.0f;   // log2 units a maximum may be passed by before O is rescaled
+constexpr int kProducers = 3;   // with them a CTA has 12 warps, three per scheduler: 168 registers a thread
+constexpr int kMetas = 8;       // steps whose bad slots are kept: more than the ring holds
+constexpr uint32_t kTmemCols = 512, kOCol = 256;
+
+template <int D>
+struct Cfg {
+  static constexpr int NQ = tile_groups(D);            // tiles of rows
+  static constexpr int BN = tile_slots(D);             // slots of a step
+  static constexpr int PL = D / 64;                    // 64-dim planes
+  static constexpr int kStage = BN * D * 2;            // K or V of a step
+  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kQTile = kTileRows * D * 2;
+  static constexpr int kSoftmaxWarps = 4 * NQ;
+  static constexpr int kMmaWarp = kSoftmaxWarps;
+  static constexpr int kProducer0 = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kProducers);
+  // shared memory, from a 1024-byte aligned base
+  static constexpr int kRing = NQ * kQTile;
+  static constexpr int kMeta = kRing + kStages * kStage;        // uint32 [kMetas][4]
+  static constexpr int kBars = kMeta + kMetas * 16;
+  // full[kStages] empty[kStages] meta[kMetas] s_full[2] p_full[2] o_full[2] pv_done done
+  static constexpr int kNumBars = 2 * kStages + kMetas + 8;
+  static constexpr int kMisc = kBars + kNumBars * 8;            // TMEM slot, abort flag, int [2][warps]
+  static constexpr int kTotal = kMisc + 16 + 2 * 4 * (kThreads / 32);
+  static constexpr int kAlloc = kTotal + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
+  static_assert(NQ * D + kOCol <= kTmemCols && 2 * BN <= static_cast<int>(kOCol), "TMEM columns");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// a box of 8-row groups of all planes, and one of rows of one plane
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int group, int head, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(head), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// the low n bits of a word (n anything)
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? kFull : (1u << n) - 1u); }
+
+// The rows of a CTA.
+struct Work {
+  int table;      // row of the block tables
+  int token0;     // first token of its request
+  int n_rows;     // rows of its request (one KV head)
+  int row0;       // first of the CTA's
+};
+// What a step covers, and what the rows of the CTA see.
+struct Slots {
+  int lo, hi;          // slots lo .. hi of some window (hi < lo: nothing is seen)
+  int n_first;         // slots below are seen by every row behind them
+  int s_min;           // lowest slot of a row (of those that see any)
+  int window;
+  int steps_a;         // steps over the first slots, when they are apart from the rest
+  int base;            // first slot of the steps after those
+  int steps;
+  __device__ __forceinline__ int first_slot(int j, int bn) const { return j < steps_a ? j * bn : base + (j - steps_a) * bn; }
+  __device__ __forceinline__ bool some(int a, int b) const {   // whether any of slots [a, b) is seen by a row
+    return a <= hi && (b > lo || a < n_first);
+  }
+  __device__ __forceinline__ bool seen(int t) const { return t <= hi && (t >= lo || t < n_first); }
+  __device__ __forceinline__ bool all_seen(int a, int b) const {   // whether some row sees each of [a, b)
+    return b - 1 <= hi && (a >= lo || b <= n_first || n_first >= lo);
+  }
+};
+
+// Finds row block `index` of one KV head, the last of the last request first (the
+// longest of a prompt, so that the short ones fill the gaps at the end); warp-wide.
+template <int RC>
+__device__ __forceinline__ bool find_rows(const TileParams& P, int64_t index, int lane, Work& w) {
+  if (P.indptr == nullptr) {
+    const int n = P.n_tokens * P.group, blocks = (n + RC - 1) / RC;
+    if (index >= blocks) return false;
+    w = Work{0, 0, n, static_cast<int>(blocks - 1 - index) * RC};
+    return true;
+  }
+  int64_t base = 0;
+  for (int i0 = 0; i0 < P.n_req; i0 += 32) {
+    const int r = P.n_req - 1 - (i0 + lane);
+    int begin = 0, rows = 0;
+    if (r >= 0) {
+      begin = min(max(__ldg(P.indptr + r), 0), P.n_tokens);
+      const int count = min(max(__ldg(P.indptr + r + 1), begin), P.n_tokens) - begin;
+      rows = count >= P.least ? count * P.group : 0;
+    }
+    const int blocks = (rows + RC - 1) / RC;
+    int64_t incl = blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const unsigned hit = __ballot_sync(kFull, base + incl > index);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      const int k = static_cast<int>(index - base - __shfl_sync(kFull, incl - blocks, src));
+      w.table = P.n_req - 1 - (i0 + src);
+      w.token0 = __shfl_sync(kFull, begin, src);
+      w.n_rows = __shfl_sync(kFull, rows, src);
+      w.row0 = (__shfl_sync(kFull, blocks, src) - 1 - k) * RC;
+      return true;
+    }
+    base += __shfl_sync(kFull, incl, 31);
+  }
+  return false;
+}
+
+// Slot of a token's row, -1: it sees nothing.
+__device__ __forceinline__ int row_slot(const TileParams& P, int token, bool raise) {
+  if (P.indptr == nullptr) {
+    int len = __ldg(P.lens + token), prefix = __ldg(P.prefix_len);
+    // (lengths and prefix are raised by the kernel that reads the requests' own slots)
+    if (len < 0 || len > P.max_len) len = 0;
+    if (prefix < 0 || prefix > P.capacity) prefix = 0;
+    return min(len, prefix) - 1;
+  }
+  const int s = __ldg(P.slot + token);
+  if (s >= P.capacity) {
+    if (raise) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_BAD_LENGTH));
+    return -1;
+  }
+  return s < 0 ? -1 : s;
+}
+
+template <int D, bool WIDE_BOX>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __grid_constant__ TileParams P,
+                                                                     const __grid_constant__ TileMaps maps) {
+  using C = Cfg<D>;
+  constexpr int NQ = C::NQ, BN = C::BN, PL = C::PL, RC = NQ * kTileRows;
+  constexpr uint32_t kIdS = idesc(128, BN, 0), kIdPV = idesc(128, D, 0, 1);
+  asm volatile("griddepcontrol.launch_dependents;");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base_u32 = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
+  uint64_t* full = bars;                        // a stage's rows landed
+  uint64_t* empty = full + C::kStages;          // the products that read it finished
+  uint64_t* meta_full = empty + C::kStages;     // a step's live slots are written
+  uint64_t* s_full = meta_full + kMetas;        // S is made (by buffer, as below)
+  uint64_t* p_full = s_full + 2;                // P is written
+  uint64_t* o_full = p_full + 2;                // a tile's O is complete
+  uint64_t* pv_done = o_full + 2;               // (256 dims) a step's value product finished
+  uint64_t* done = pv_done + 1;
+  uint32_t* meta = reinterpret_cast<uint32_t*>(smem + C::kMeta);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
+  int* s_range = reinterpret_cast<int*>(smem + C::kMisc + 16);   // [2][warps]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = static_cast<int>(blockIdx.x % P.splits);
+  const int64_t unit = blockIdx.x / P.splits;
+  const int hk = static_cast<int>(unit % P.kv_heads);
+  if (P.indptr != nullptr && blockIdx.x == 0 && warp == 0) {   // offsets that are not non-decreasing inside [0, n_tokens]
+    bool bad = false;
+    for (int r = lane; r <= P.n_req; r += 32) {
+      const int at = __ldg(P.indptr + r), before = r > 0 ? __ldg(P.indptr + r - 1) : 0;
+      bad |= at < before || at > P.n_tokens;
+    }
+    if (bad) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_BAD_LENGTH));
+  }
+  Work w{};
+  if (!find_rows<RC>(P, unit / P.kv_heads, lane, w)) return;   // the same in every warp
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], kProducers);   // each warp announces its own copies
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kMetas; ++i) mbar_init(&meta_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(pv_done, 1);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // this thread's row (softmax warps)
+  const int my_row = w.row0 + tid;
+  const bool has_row = warp < C::kSoftmaxWarps && my_row < w.n_rows;
+  const int my_token = w.token0 + (has_row ? my_row / P.group : 0);
+  const int my_head = hk * P.group + (has_row ? my_row % P.group : 0);
+  const int my_slot = has_row ? row_slot(P, my_token, hk == 0 && split == 0) : -1;
+  const int my_lo = P.window > 0 ? max(0, my_slot + 1 - P.window) : 0;   // its window's first
+  {
+    const int lo = __reduce_min_sync(kFull, my_slot >= 0 ? my_slot : INT32_MAX), hi = __reduce_max_sync(kFull, my_slot);
+    if (lane == 0) {
+      s_range[warp] = lo;
+      s_range[C::kThreads / 32 + warp] = hi;
+    }
+  }
+  // queries, as rows of 128 swizzled bytes, one 64-dim plane after the other
+  const uint32_t keep = P.sign == 0 ? 0u : kFull, flip = P.sign < 0 ? 0x80008000u : 0u;
+  for (int i = tid; i < RC * (D / 8); i += C::kThreads) {
+    const int row = i / (D / 8), c = i % (D / 8), at = w.row0 + row;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (at < w.n_rows) {
+      const int token = w.token0 + at / P.group, head = hk * P.group + at % P.group;
+      x = __ldg(reinterpret_cast<const uint4*>(P.q + token * P.q_stride + static_cast<int64_t>(head) * D * 2) + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) word(x, e) = (word(x, e) & keep) ^ flip;
+    }
+    const int r = row & 127;
+    *reinterpret_cast<uint4*>(smem + (row >> 7) * C::kQTile + (c >> 3) * (kTileRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+
+  Slots S;
+  {
+    int lo = INT32_MAX, hi = -1;
+#pragma unroll
+    for (int i = 0; i < C::kSoftmaxWarps; ++i) {
+      lo = min(lo, s_range[i]);
+      hi = max(hi, s_range[C::kThreads / 32 + i]);
+    }
+    S.s_min = lo;
+    S.hi = hi;
+    S.window = P.window;
+    S.lo = P.window > 0 && hi >= 0 ? max(0, lo + 1 - P.window) : 0;
+    S.n_first = min(P.n_first, S.lo);
+    // the first slots apart from the window, where steps over them end before it
+    const int steps_a = (S.n_first + BN - 1) / BN;
+    const bool apart = S.n_first > 0 && static_cast<int64_t>(steps_a) * BN < S.lo / P.box * P.box;
+    S.steps_a = apart ? steps_a : 0;
+    S.base = apart || S.n_first == 0 ? S.lo / P.box * P.box : 0;
+    S.steps = hi < 0 ? 0 : S.steps_a + (hi - S.base) / BN + 1;
+  }
+  // this CTA's part of the steps
+  const int j_begin = static_cast<int>(static_cast<int64_t>(S.steps) * split / P.splits);
+  const int n = static_cast<int>(static_cast<int64_t>(S.steps) * (split + 1) / P.splits) - j_begin;
+  const int tiles = NQ == 2 && w.row0 + kTileRows >= w.n_rows ? 1 : NQ;   // tiles with rows
+  auto fail = [&]() {
+    atomicOr(P.status, kDevTimeout);
+    *abort_flag = 1;
+  };
+
+  if (warp >= C::kProducer0 && n > 0) {
+    // -------------------------------------------------------------- producers
+    const int prod = warp - C::kProducer0;
+    const int32_t* table = P.paged.tables + static_cast<int64_t>(w.table) * P.paged.max_blocks;
+    const int boxes = BN / P.box;
+    const int copies = WIDE_BOX ? boxes : boxes * PL;   // of K, and of V; copy c is warp c % 3's
+    const uint32_t bytes = P.box * (WIDE_BOX ? D : 64) * 2;
+    const uint32_t my_bytes = ((copies + kProducers - 1 - prod) / kProducers) * bytes;
+    // cache row of a slot, cache_rows: nothing is read (nobody sees it, or its block is bad)
+    auto row_at = [&](int slot, int first, int last) -> int {
+      if (!S.some(first, last)) return P.cache_rows;
+      const int b = block_of(P.paged, slot);
+      const int32_t block = __ldg(table + b);
+      if (block < 0 || block >= P.paged.num_cache_blocks) return P.cache_rows;
+      return block * P.paged.block_size + (slot - b * P.paged.block_size);
+    };
+    bool ok = true;
+    int issued = 0;
+    for (int i = 0; i < n; ++i) {
+      const int t0 = S.first_slot(j_begin + i, BN);
+      // the row of this lane's first copy, before its stage is waited for
+      const int c0 = kProducers * lane + prod;
+      auto copy_row = [&](int c) {
+        const int t = t0 + (WIDE_BOX ? c : c / PL) * P.box;
+        return row_at(t, t, t + P.box);
+      };
+      const int row0 = c0 < copies ? copy_row(c0) : 0;
+      if (prod == 0) {
+        // which of the step's slots have a block
+#pragma unroll
+        for (int x = 0; x < BN / 32; ++x) {
+          const int t = t0 + 32 * x + lane;
+          const bool live = S.seen(t) && row_at(t, t, t + 1) != P.cache_rows;
+          if (S.seen(t) && !live) raise_block(P.status, w.table, t);
+          const unsigned word = __ballot_sync(kFull, live || !S.seen(t));
+          if (lane == 0) meta[(i % kMetas) * 4 + x] = word;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&meta_full[i % kMetas]);
+      }
+      for (int x = 0; x < 2 && ok; ++x) {   // K, then V
+        const int fill = 2 * i + x, st = fill % C::kStages;
+        if (fill >= C::kStages) ok = wait_or_abort(&empty[st], (fill / C::kStages - 1) & 1, abort_flag, kMaxSpins);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], my_bytes);
+        __syncwarp();
+        const CUtensorMap* map = x == 0 ? &maps.k : &maps.v;
+        const uint32_t dst = base_u32 + C::kRing + st * C::kStage;
+        for (int c = c0; c < copies; c += 32 * kProducers) {
+          const int row = c == c0 ? row0 : copy_row(c);
+          if constexpr (WIDE_BOX) {
+            tma_load_5d(dst + c * bytes, map, row >> 3, hk, &full[st]);
+          } else {
+            const int box = c / PL, plane = c - box * PL, at = box * P.box;
+            tma_load_3d(dst + (at >> 3) * (PL * 1024) + plane * 1024 + (at & 7) * 128, map, 64 * plane, hk, row, &full[st]);
+          }
+        }
+        issued = fill + 1;
+      }
+      if (!ok) {
+        if (lane == 0) fail();
+        break;
+      }
+    }
+    if (!ok && lane == 0) {
+      // wait (bounded) for the copies in flight
+      for (int fill = max(0, issued - C::kStages); fill < issued; ++fill)
+        mbar_wait_bounded(&full[fill % C::kStages], (fill / C::kStages) & 1, 1024);
+    }
+  } else if (warp == C::kMmaWarp && n > 0) {
+    // --------------------------------------------------------------- products
+    const uint64_t dq = sdesc(base_u32, 16, 1024);
+    bool ok = true;
+    auto ready = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(kFull, ok && wait_or_abort(bar, parity, abort_flag, kMaxSpins));
+      return ok;
+    };
+    auto score = [&](int q, int buf, int i) {   // S = Q K^T of step i
+      const int fill = 2 * i;
+      const uint64_t dk = sdesc(base_u32 + C::kRing + (fill % C::kStages) * C::kStage, 16, PL * 1024);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        tc_mma_elect(tmem + buf * BN, dq + ((q * C::kQTile + (ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) >> 4),
+                     dk + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), kIdS, ks > 0);
+      tc_commit_elect(&s_full[buf]);
+    };
+    auto value = [&](int q, int buf, int i) {   // O += P V of step i
+      const int fill = 2 * i + 1;
+      const uint64_t dv = sdesc(base_u32 + C::kRing + (fill % C::kStages) * C::kStage, 1024, PL * 1024);
+#pragma unroll
+      for (int ks = 0; ks < BN / 16; ++ks)
+        tc_mma_tmem_a_elect(tmem + kOCol + q * D, tmem + buf * BN + 8 * ks, dv + ((ks * 2 * PL * 1024) >> 4), kIdPV, i > 0 || ks > 0);
+    };
+    auto wait_k = [&](int i) { return ready(&full[(2 * i) % C::kStages], ((2 * i) / C::kStages) & 1); };
+    // V of step i has landed, and its rows that no row of the CTA sees are zeros
+    auto wait_v = [&](int i) {
+      const int fill = 2 * i + 1;
+      if (!ready(&full[fill % C::kStages], (fill / C::kStages) & 1)) return false;
+      const int t0 = S.first_slot(j_begin + i, BN);
+      if (!S.all_seen(t0, t0 + BN)) {
+        uint8_t* v = smem + C::kRing + (fill % C::kStages) * C::kStage;
+        for (int x = lane; x < BN * PL * 8; x += 32) {
+          const int row = x / (PL * 8), part = x % (PL * 8);
+          if (!S.seen(t0 + row))
+            *reinterpret_cast<uint4*>(v + (row >> 3) * (PL * 1024) + (part >> 3) * 1024 + (row & 7) * 128 + (part & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      return true;
+    };
+    auto release = [&](int fill) { tc_commit_elect(&empty[fill % C::kStages]); };
+    if (wait_k(0)) {
+      tc_fence_after();
+      for (int q = 0; q < tiles; ++q) score(q, q, 0);
+      release(0);
+      for (int i = 0; i < n && ok; ++i) {
+        if (NQ == 2) {
+          for (int q = 0; q < tiles; ++q) {
+            if (!ready(&p_full[q], i & 1)) break;
+            if (q == 0 && !wait_v(i)) break;
+            tc_fence_after();
+            value(q, q, i);
+            if (i == n - 1) tc_commit_elect(&o_full[q]);
+            if (q == tiles - 1) release(2 * i + 1);
+            if (i + 1 < n) {
+              if (q == 0 && !wait_k(i + 1)) break;
+              score(q, q, i + 1);
+              if (q == tiles - 1) release(2 * i + 2);
+            }
+          }
+        } else {
+          if (i + 1 < n) {
+            if (!wait_k(i + 1)) break;
+            tc_fence_after();
+            score(0, (i + 1) & 1, i + 1);
+            release(2 * i + 2);
+          }
+          if (!ready(&p_full[i & 1], (i >> 1) & 1) || !wait_v(i)) break;
+          tc_fence_after();
+          value(0, i & 1, i);
+          release(2 * i + 1);
+          tc_commit_elect(pv_done);
+          if (i == n - 1) tc_commit_elect(&o_full[0]);
+        }
+      }
+    }
+    if (!ok && lane == 0) fail();
+    tc_commit_elect(done);
+    mbar_wait_bounded(done, 0);
+  } else if (warp < C::kSoftmaxWarps && warp < 4 * tiles) {
+    // ---------------------------------------------------------------- softmax
+    const int q = warp >> 2;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t o_at = tl + kOCol + q * D;
+    const float scale = P.scale_log2;
+    float m_run = -FLT_MAX, l_run = 0.0f;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int buf = NQ == 2 ? q : i & 1;
+      const uint32_t parity = (NQ == 2 ? i : i >> 1) & 1;
+      ok = __all_sync(kFull, wait_or_abort(&meta_full[i % kMetas], (i / kMetas) & 1, abort_flag, kMaxSpins) &&
+                                 wait_or_abort(&s_full[buf], parity, abort_flag, kMaxSpins));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t s_at = tl + buf * BN;
+      float s[BN];
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) tmem_ld32(s_at + c, s + c);
+      tmem_wait_ld();
+      const int t0 = S.first_slot(j_begin + i, BN);
+      uint32_t live[BN / 32];
+      bool whole = t0 + BN - 1 <= S.s_min && (S.window == 0 || t0 > S.hi - S.window || t0 + BN <= P.n_first);
+#pragma unroll
+      for (int x = 0; x < BN / 32; ++x) {
+        live[x] = meta[(i % kMetas) * 4 + x];
+        whole &= live[x] == kFull;
+      }
+      if (!whole) {
+        // slots t <= my_slot that are in the window or among the first
+#pragma unroll
+        for (int x = 0; x < BN / 32; ++x) {
+          const int t = t0 + 32 * x;
+          const uint32_t mask = live[x] & low_bits(my_slot + 1 - t) & (~low_bits(my_lo - t) | low_bits(P.n_first - t));
+#pragma unroll
+          for (int y = 0; y < 32; ++y) s[32 * x + y] = (mask >> y) & 1u ? s[32 * x + y] : -INFINITY;
+        }
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int x = 4; x < BN; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+      if (i == 0) {
+        m_run = fmaxf(top, -FLT_MAX);
+      } else if (__any_sync(kFull, top > m_run + kLazy)) {
+        const float m_new = top > m_run + kLazy ? top : m_run;
+        const float alpha = ex2(m_run - m_new);
+        m_run = m_new;
+        l_run *= alpha;
+        if (NQ == 1) {
+          ok = __all_sync(kFull, wait_or_abort(pv_done, (i - 1) & 1, abort_flag, kMaxSpins));
+          if (!ok) break;
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          tmem_ld16(o_at + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[x] *= alpha;
+          tmem_st16(o_at + c, o);
+        }
+      }
+      const float2 sc = make_float2(scale, scale), neg = make_float2(-m_run, -m_run);
+      float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          float2 y = __ffma2_rn(make_float2(s[c + 2 * x], s[c + 2 * x + 1]), sc, neg);
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          sum = __fadd2_rn(sum, y);
+          p[x] = bf_pack(y.x, y.y);
+        }
+        tmem_st16u(s_at + c / 2, p);
+      }
+      l_run += sum.x + sum.y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[buf]);
+    }
+    if (!ok && lane == 0) fail();
+    // ---- the output, or this part's record
+    const bool direct = P.rec_acc == nullptr;
+    if (my_slot < 0) l_run = 0.0f;   // a row that sees nothing
+    if (n > 0 && ok) {
+      ok = __all_sync(kFull, wait_or_abort(&o_full[q], 0, abort_flag, kMaxSpins));
+      if (!ok && lane == 0) fail();
+      tc_fence_after();
+    }
+    const int64_t at = static_cast<int64_t>(my_token) * P.q_heads + my_head;
+    if (ok) {
+      const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (n > 0) {
+          tmem_ld32(o_at + c, o);
+          tmem_wait_ld();
+        }
+        if (has_row && direct) {
+          uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.out) + at * D + c);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (l_run != 0.0f) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) word(y, e) = bf_pack(o[8 * x + 2 * e] * inv, o[8 * x + 2 * e + 1] * inv);
+            }
+            to[x] = y;
+          }
+        } else if (has_row && l_run != 0.0f) {
+          float4* to = reinterpret_cast<float4*>(P.rec_acc + (static_cast<int64_t>(split) * P.n_tokens * P.q_heads + at) * D + c);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) to[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        }
+        __syncwarp();
+      }
+      if (has_row) {
+        if (!direct) P.rec_ml[static_cast<int64_t>(split) * P.n_tokens * P.q_heads + at] = make_float2(l_run == 0.0f ? -FLT_MAX : m_run, l_run);
+        else if (P.lse != nullptr) P.lse[at] = l_run == 0.0f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// One warp per (token, query head): joins the parts of a row's slots.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_tile_join(const __grid_constant__ TileParams P) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int64_t rows = static_cast<int64_t>(P.n_tokens) * P.q_heads;
+  if (task < rows) {
+    // rows of the requests that the tiles took
+    const int token = static_cast<int>(task / P.q_heads);
+    bool mine = token >= __ldg(P.indptr) && token < __ldg(P.indptr + P.n_req);
+    if (mine) {
+      int lo = 0, hi = P.n_req;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(P.indptr + mid) <= token) lo = mid;
+        else hi = mid;
+      }
+      mine = __ldg(P.indptr + lo + 1) - __ldg(P.indptr + lo) >= P.least;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (mine) {
+      float m = -FLT_MAX, sum = 0.0f, acc[V];
+      for (int k = lane; k < P.splits; k += 32) m = fmaxf(m, __ldcg(P.rec_ml + k * rows + task).x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[x] = 0.0f;
+#pragma unroll 4
+      for (int k = 0; k < P.splits; ++k) {
+        const float2 ml = __ldcg(P.rec_ml + k * rows + task);
+        if (ml.y == 0.0f) continue;   // nothing was written beside it
+        const float e = ex2(ml.x - m);
+        sum += ml.y * e;
+        const float* a = P.rec_acc + (k * rows + task) * D + lane * V;
+#pragma unroll
+        for (int x = 0; x < V; x += 2) {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(a + x));
+          acc[x] += e * y.x;
+          acc[x + 1] += e * y.y;
+        }
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(P.out) + task * D + lane * V);
+#pragma unroll
+      for (int x = 0; x < V; x += 2) to[x / 2] = bf_pack(acc[x] * inv, acc[x + 1] * inv);
+      if (P.lse != nullptr && lane == 0) P.lse[task] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+    }
+  }
+}
+
+template <int D, bool WIDE_BOX>
+cudaError_t launch_box(const TileParams& p, const TileMaps& maps, cudaStream_t s) {
+  auto kern = k_attend_tile<D, WIDE_BOX>;
+  static std::atomic<uint32_t> done{0};
+  const cudaError_t e = allow_smem(kern, Cfg<D>::kAlloc, done);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.blocks) * p.kv_heads * p.splits);
+  kern<<<grid, Cfg<D>::kThreads, Cfg<D>::kAlloc, s>>>(p, maps);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_d(const TileParams& p, const TileMaps& maps, cudaStream_t s) {
+  return p.box >= 8 ? launch_box<D, true>(p, maps, s) : launch_box<D, false>(p, maps, s);
+}
+template <int D>
+cudaError_t launch_join_d(const TileParams& p, cudaStream_t s) {
+  const int64_t warps = static_cast<int64_t>(p.n_tokens) * p.q_heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_tile_join<D>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_tile(const TileParams& p, const TileMaps& maps, int head_dim, cudaStream_t s) {
+  if (head_dim == 64) return launch_d<64>(p, maps, s);
+  if (head_dim == 128) return launch_d<128>(p, maps, s);
+  return launch_d<256>(p, maps, s);
+}
+cudaError_t launch_tile_join(const TileParams& p, int head_dim, cudaStream_t s) {
+  if (head_dim == 64) return launch_join_d<64>(p, s);
+  if (head_dim == 128) return launch_join_d<128>(p, s);
+  return launch_join_d<256>(p, s);
+}
+
+}  // namespace pic
