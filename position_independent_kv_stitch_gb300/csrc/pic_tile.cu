@@ -8,20 +8,20 @@
 //
 // Rows are (token, query head) pairs of one request and KV head, in the order of
 // tokens; a CTA takes 256 of them (two tiles of 128; 128 rows where heads have 256 dims) and
-// walks the slots that some of them see, 128 (64) at a time: the first n_first slots, then
-// from the lowest window's start to the highest slot.  One pass, with a running maximum and
+// walks the slots that some of them see, 128 (64) at a time: from the lowest window's
+// start to the highest slot, then the first n_first.  One pass, with a running maximum and
 // sum.  Where there are too few row blocks for the SMs, a block's slots are
 // dealt to several CTAs, which leave records (O, max, sum) that a later kernel joins.
 //
 // Warps by role, per step of K and V tiles in a shared ring:
-//   * three producer warps look up the blocks of the step's slots and
+//   * two producer warps look up the blocks of the step's slots and
 //     copy them with TMA, a whole block of all dims at a time: the cache is mapped as
 //     [head][8-row group][64-dim plane][8 rows][64 dims], so that a copy lands as rows of 128
 //     swizzled bytes in groups of 8, whichever blocks follow each other.  (A block size that is
 //     no multiple of 8 goes by 4, 2 or 1 rows and one plane at a time.)
-//   * one warp issues the products: S = Q K^T, M = 128 rows, N = slots, and
+//   * a warp per tile issues its products: S = Q K^T, M = 128 rows, N = slots, and
 //     O += P V with P read from TMEM and V as an MN-major operand;
-//   * four warps per tile, a thread per row: read S from TMEM, mask, raise the
+//   * eight warps per tile, two threads per row: read S from TMEM, mask, raise the
 //     maximum when a score passes it by more than 2^8 (O and the sum are then rescaled, which
 //     after the first steps hardly happens), write P = exp2(s - m) as bf16 over S.
 // Two tiles take turns: while one is in its softmax, the tensor cores work on the other's.
@@ -50,7 +50,7 @@ using namespace dev;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLazy = 8.0f;   // log2 units a maximum may be passed by before O is rescaled
-constexpr int kProducers = 3;   // with them a CTA has 12 warps, three per scheduler: 168 registers a thread
+constexpr int kProducers = 2;
 constexpr int kMetas = 8;       // steps whose bad slots are kept: more than the ring holds
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 
@@ -62,17 +62,23 @@ struct Cfg {
   static constexpr int kStage = BN * D * 2;            // K or V of a step
   static constexpr int kStages = D == 64 ? 8 : 5;
   static constexpr int kQTile = kTileRows * D * 2;
-  static constexpr int kSoftmaxWarps = 4 * NQ;
-  static constexpr int kMmaWarp = kSoftmaxWarps;
-  static constexpr int kProducer0 = kMmaWarp + 1;
-  static constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kProducers);
+  // Warps 0 and 1 issue the products, one for each tile: a wait, even for what has happened, and an
+  // issue each take their time, and one warp could not keep the tensor cores busy (382 us
+  // for a prompt of 8,192 tokens in a window of 4,096).  As the oldest of their schedulers they are not kept
+  // waiting by the softmax warps' arithmetic either (398 as the youngest).
+  static constexpr int kProducer0 = 2;
+  static constexpr int kSoftmax0 = kProducer0 + kProducers;   // a multiple of 4: warp w reads TMEM lanes 32 (w % 4) ..
+  static constexpr int kSoftmaxWarps = 8 * NQ;
+  static constexpr int kThreads = 32 * (kSoftmax0 + kSoftmaxWarps);   // 640 (384): 96 (168) registers a thread
+  static_assert(kSoftmax0 % 4 == 0, "TMEM lane quadrants");
   // shared memory, from a 1024-byte aligned base
   static constexpr int kRing = NQ * kQTile;
   static constexpr int kMeta = kRing + kStages * kStage;        // uint32 [kMetas][4]
   static constexpr int kBars = kMeta + kMetas * 16;
-  // full[kStages] empty[kStages] meta[kMetas] s_full[2] p_full[2] o_full[2] pv_done done
-  static constexpr int kNumBars = 2 * kStages + kMetas + 8;
-  static constexpr int kMisc = kBars + kNumBars * 8;            // TMEM slot, abort flag, int [2][warps]
+  // full[kStages] empty[kStages] meta[kMetas] s_full[2] p_full[2] o_full[2] pv_done done[2] q_full[2] turn[2]
+  static constexpr int kNumBars = 2 * kStages + kMetas + 13;
+  static constexpr int kTop = kBars + kNumBars * 8;             // float [rows]: a row's maximum, between its two threads
+  static constexpr int kMisc = kTop + 4 * NQ * kTileRows;       // TMEM slot, abort flag, int [2][warps]
   static constexpr int kTotal = kMisc + 16 + 2 * 4 * (kThreads / 32);
   static constexpr int kAlloc = kTotal + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory");
@@ -82,6 +88,11 @@ struct Cfg {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -113,6 +124,21 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+// Joins the two warps that share rows, at named barrier `id`: whether any thread's flag is set.
+__device__ __forceinline__ bool pair_any(uint32_t id, bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(flag ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 // the low n bits of a word (n anything)
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? kFull : (1u << n) - 1u); }
 
@@ -129,10 +155,11 @@ struct Slots {
   int n_first;         // slots below are seen by every row behind them
   int s_min;           // lowest slot of a row (of those that see any)
   int window;
-  int steps_a;         // steps over the first slots, when they are apart from the rest
-  int base;            // first slot of the steps after those
-  int steps;
-  __device__ __forceinline__ int first_slot(int j, int bn) const { return j < steps_a ? j * bn : base + (j - steps_a) * bn; }
+  // steps over the window, and after them over the first slots where those are apart
+  // (the few scores of the first would be a poor first maximum)
+  int base;            // first slot of the window's steps
+  int steps_w, steps;
+  __device__ __forceinline__ int first_slot(int j, int bn) const { return j < steps_w ? base + j * bn : (j - steps_w) * bn; }
   __device__ __forceinline__ bool some(int a, int b) const {   // whether any of slots [a, b) is seen by a row
     return a <= hi && (b > lo || a < n_first);
   }
@@ -218,16 +245,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
   uint64_t* p_full = s_full + 2;                // P is written
   uint64_t* o_full = p_full + 2;                // a tile's O is complete
   uint64_t* pv_done = o_full + 2;               // (256 dims) a step's value product finished
-  uint64_t* done = pv_done + 1;
+  uint64_t* done = pv_done + 1;                 // an issuer's products all finished
+  uint64_t* q_full = done + 2;                  // a tile's queries are in place
+  uint64_t* turn = q_full + 2;                    // a tile's products of a step may be issued
   uint32_t* meta = reinterpret_cast<uint32_t*>(smem + C::kMeta);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
   int* s_range = reinterpret_cast<int*>(smem + C::kMisc + 16);   // [2][warps]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = static_cast<int>(blockIdx.x % P.splits);
-  const int64_t unit = blockIdx.x / P.splits;
-  const int hk = static_cast<int>(unit % P.kv_heads);
+  const uint32_t unit = blockIdx.x / static_cast<uint32_t>(P.splits);
+  const int split = static_cast<int>(blockIdx.x - unit * P.splits);
+  const int hk = static_cast<int>(unit % static_cast<uint32_t>(P.kv_heads));
   if (P.indptr != nullptr && blockIdx.x == 0 && warp == 0) {   // offsets that are not non-decreasing inside [0, n_tokens]
     bool bad = false;
     for (int r = lane; r <= P.n_req; r += 32) {
@@ -237,32 +266,41 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
     if (bad) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_BAD_LENGTH));
   }
   Work w{};
-  if (!find_rows<RC>(P, unit / P.kv_heads, lane, w)) return;   // the same in every warp
+  if (!find_rows<RC>(P, unit / static_cast<uint32_t>(P.kv_heads), lane, w)) return;   // the same in every warp
+
+  const int tiles = NQ == 2 && w.row0 + kTileRows >= w.n_rows ? 1 : NQ;   // tiles with rows
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], kProducers);   // each warp announces its own copies
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], tiles);           // each tile's products have read it
     }
     for (int i = 0; i < kMetas; ++i) mbar_init(&meta_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(pv_done, 1);
-    mbar_init(done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&done[i], 1);
+      mbar_init(&q_full[i], 8);
+      mbar_init(&turn[i], 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == C::kMmaWarp) {
+  if (tid < 2)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tid == 0 ? &maps.k : &maps.v)) : "memory");
+  if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   // this thread's row (softmax warps)
-  const int my_row = w.row0 + tid;
-  const bool has_row = warp < C::kSoftmaxWarps && my_row < w.n_rows;
+  const int my_tile = (warp - C::kSoftmax0) >> 3, my_half = ((warp - C::kSoftmax0) >> 2) & 1;
+  const int my_row = w.row0 + my_tile * kTileRows + 32 * (warp & 3) + lane;
+  const bool has_row = warp >= C::kSoftmax0 && my_row < w.n_rows;
   const int my_token = w.token0 + (has_row ? my_row / P.group : 0);
   const int my_head = hk * P.group + (has_row ? my_row % P.group : 0);
   const int my_slot = has_row ? row_slot(P, my_token, hk == 0 && split == 0) : -1;
@@ -274,21 +312,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
       s_range[C::kThreads / 32 + warp] = hi;
     }
   }
-  // queries, as rows of 128 swizzled bytes, one 64-dim plane after the other
-  const uint32_t keep = P.sign == 0 ? 0u : kFull, flip = P.sign < 0 ? 0x80008000u : 0u;
-  for (int i = tid; i < RC * (D / 8); i += C::kThreads) {
-    const int row = i / (D / 8), c = i % (D / 8), at = w.row0 + row;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (at < w.n_rows) {
-      const int token = w.token0 + at / P.group, head = hk * P.group + at % P.group;
-      x = __ldg(reinterpret_cast<const uint4*>(P.q + token * P.q_stride + static_cast<int64_t>(head) * D * 2) + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) word(x, e) = (word(x, e) & keep) ^ flip;
-    }
-    const int r = row & 127;
-    *reinterpret_cast<uint4*>(smem + (row >> 7) * C::kQTile + (c >> 3) * (kTileRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -298,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
   {
     int lo = INT32_MAX, hi = -1;
 #pragma unroll
-    for (int i = 0; i < C::kSoftmaxWarps; ++i) {
+    for (int i = C::kSoftmax0; i < C::kThreads / 32; ++i) {
       lo = min(lo, s_range[i]);
       hi = max(hi, s_range[C::kThreads / 32 + i]);
     }
@@ -309,60 +332,51 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
     S.n_first = min(P.n_first, S.lo);
     // the first slots apart from the window, where steps over them end before it
     const int steps_a = (S.n_first + BN - 1) / BN;
-    const bool apart = S.n_first > 0 && static_cast<int64_t>(steps_a) * BN < S.lo / P.box * P.box;
-    S.steps_a = apart ? steps_a : 0;
-    S.base = apart || S.n_first == 0 ? S.lo / P.box * P.box : 0;
-    S.steps = hi < 0 ? 0 : S.steps_a + (hi - S.base) / BN + 1;
+    const int lo_box = S.lo & -P.box;   // boxes are powers of two
+    const bool apart = S.n_first > 0 && static_cast<int64_t>(steps_a) * BN < lo_box;
+    S.base = apart || S.n_first == 0 ? lo_box : 0;
+    S.steps_w = hi < 0 ? 0 : (hi - S.base) / BN + 1;
+    S.steps = S.steps_w + (apart ? steps_a : 0);
   }
   // this CTA's part of the steps
-  const int j_begin = static_cast<int>(static_cast<int64_t>(S.steps) * split / P.splits);
-  const int n = static_cast<int>(static_cast<int64_t>(S.steps) * (split + 1) / P.splits) - j_begin;
-  const int tiles = NQ == 2 && w.row0 + kTileRows >= w.n_rows ? 1 : NQ;   // tiles with rows
+  int j_begin = 0, n = S.steps;
+  if (P.splits > 1) {
+    const int each = S.steps / P.splits, rest = S.steps - each * P.splits;
+    j_begin = each * split + min(split, rest);
+    n = each + (split < rest ? 1 : 0);
+  }
   auto fail = [&]() {
     atomicOr(P.status, kDevTimeout);
     *abort_flag = 1;
   };
 
-  if (warp >= C::kProducer0 && n > 0) {
+  if (warp >= C::kProducer0 && warp < C::kSoftmax0 && n > 0) {
     // -------------------------------------------------------------- producers
     const int prod = warp - C::kProducer0;
     const int32_t* table = P.paged.tables + static_cast<int64_t>(w.table) * P.paged.max_blocks;
     const int boxes = BN / P.box;
-    const int copies = WIDE_BOX ? boxes : boxes * PL;   // of K, and of V; copy c is warp c % 3's
+    const int copies = WIDE_BOX ? boxes : boxes * PL;   // of K, and of V, dealt to the warps
     const uint32_t bytes = P.box * (WIDE_BOX ? D : 64) * 2;
     const uint32_t my_bytes = ((copies + kProducers - 1 - prod) / kProducers) * bytes;
-    // cache row of a slot, cache_rows: nothing is read (nobody sees it, or its block is bad)
-    auto row_at = [&](int slot, int first, int last) -> int {
-      if (!S.some(first, last)) return P.cache_rows;
-      const int b = block_of(P.paged, slot);
-      const int32_t block = __ldg(table + b);
+    // Block of a slot whose box (slots [first, last)) some row sees, else -1; looked at only when its copy is
+    // issued, as a warp stops where it touches a load that has not arrived.
+    auto block_at = [&](int slot, int first, int last) { return S.some(first, last) ? __ldg(table + block_of(P.paged, slot)) : -1; };
+    // cache row of a slot in that block, cache_rows: nothing is read (nobody sees it, or its block is bad)
+    auto row_in = [&](int32_t block, int slot) -> int {
       if (block < 0 || block >= P.paged.num_cache_blocks) return P.cache_rows;
-      return block * P.paged.block_size + (slot - b * P.paged.block_size);
+      return block * P.paged.block_size + (slot - block_of(P.paged, slot) * P.paged.block_size);
+    };
+    const int c0 = kProducers * lane + prod;   // this lane's first copy
+    auto copy_slot = [&](int i, int c) { return S.first_slot(j_begin + i, BN) + (WIDE_BOX ? c : c / PL) * P.box; };
+    auto copy_block = [&](int i, int c) {
+      const int t = copy_slot(i, c);
+      return block_at(t, t, t + P.box);
     };
     bool ok = true;
     int issued = 0;
+    int32_t next = c0 < copies ? copy_block(0, c0) : -1;
     for (int i = 0; i < n; ++i) {
-      const int t0 = S.first_slot(j_begin + i, BN);
-      // the row of this lane's first copy, before its stage is waited for
-      const int c0 = kProducers * lane + prod;
-      auto copy_row = [&](int c) {
-        const int t = t0 + (WIDE_BOX ? c : c / PL) * P.box;
-        return row_at(t, t, t + P.box);
-      };
-      const int row0 = c0 < copies ? copy_row(c0) : 0;
-      if (prod == 0) {
-        // which of the step's slots have a block
-#pragma unroll
-        for (int x = 0; x < BN / 32; ++x) {
-          const int t = t0 + 32 * x + lane;
-          const bool live = S.seen(t) && row_at(t, t, t + 1) != P.cache_rows;
-          if (S.seen(t) && !live) raise_block(P.status, w.table, t);
-          const unsigned word = __ballot_sync(kFull, live || !S.seen(t));
-          if (lane == 0) meta[(i % kMetas) * 4 + x] = word;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&meta_full[i % kMetas]);
-      }
+      const int32_t block0 = next;
       for (int x = 0; x < 2 && ok; ++x) {   // K, then V
         const int fill = 2 * i + x, st = fill % C::kStages;
         if (fill >= C::kStages) ok = wait_or_abort(&empty[st], (fill / C::kStages - 1) & 1, abort_flag, kMaxSpins);
@@ -373,7 +387,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
         const CUtensorMap* map = x == 0 ? &maps.k : &maps.v;
         const uint32_t dst = base_u32 + C::kRing + st * C::kStage;
         for (int c = c0; c < copies; c += 32 * kProducers) {
-          const int row = c == c0 ? row0 : copy_row(c);
+          const int row = row_in(c == c0 ? block0 : copy_block(i, c), copy_slot(i, c));
           if constexpr (WIDE_BOX) {
             tma_load_5d(dst + c * bytes, map, row >> 3, hk, &full[st]);
           } else {
@@ -387,44 +401,83 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
         if (lane == 0) fail();
         break;
       }
+      if (i + 1 < n && c0 < copies) next = copy_block(i + 1, c0);
+      if (prod == 0) {
+        // which of the step's slots have a block
+        int32_t block[BN / 32];
+#pragma unroll
+        for (int x = 0; x < BN / 32; ++x) {
+          const int t = S.first_slot(j_begin + i, BN) + 32 * x + lane;
+          block[x] = S.seen(t) ? __ldg(table + block_of(P.paged, t)) : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < BN / 32; ++x) {
+          const int t = S.first_slot(j_begin + i, BN) + 32 * x + lane;
+          const bool bad = S.seen(t) && (block[x] < 0 || block[x] >= P.paged.num_cache_blocks);
+          if (bad) raise_block(P.status, w.table, t);
+          const unsigned live = ~__ballot_sync(kFull, bad);
+          if (lane == 0) meta[(i % kMetas) * 4 + x] = live;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&meta_full[i % kMetas]);
+      }
     }
     if (!ok && lane == 0) {
       // wait (bounded) for the copies in flight
       for (int fill = max(0, issued - C::kStages); fill < issued; ++fill)
         mbar_wait_bounded(&full[fill % C::kStages], (fill / C::kStages) & 1, 1024);
     }
-  } else if (warp == C::kMmaWarp && n > 0) {
+  } else if (warp < tiles && n > 0) {
     // --------------------------------------------------------------- products
-    const uint64_t dq = sdesc(base_u32, 16, 1024);
+    const int q = warp;
+    // Descriptors are stepped in their low words (addresses in 16 bytes, which stay below
+    // 2^14): the high words are constants.
+    const auto desc = [](uint32_t lo, uint64_t like) {
+      uint64_t d;
+      asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(static_cast<uint32_t>(like >> 32)));
+      return d;
+    };
+    constexpr uint32_t kStep = C::kStage >> 4;
+    const uint64_t dq = sdesc(base_u32, 16, 1024), dk = sdesc(base_u32 + C::kRing, 16, PL * 1024),
+                   dv = sdesc(base_u32 + C::kRing, 1024, PL * 1024);
     bool ok = true;
     auto ready = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(kFull, ok && wait_or_abort(bar, parity, abort_flag, kMaxSpins));
+      ok = __all_sync(kFull, wait_or_abort(bar, parity, abort_flag, kMaxSpins));
       return ok;
     };
-    auto score = [&](int q, int buf, int i) {   // S = Q K^T of step i
-      const int fill = 2 * i;
-      const uint64_t dk = sdesc(base_u32 + C::kRing + (fill % C::kStages) * C::kStage, 16, PL * 1024);
+    // a place in the ring
+    struct Ring {
+      uint32_t stage, parity;
+      __device__ __forceinline__ void next() {   // two fills on: K to K, V to V
+        stage += 2;
+        if (stage >= C::kStages) {
+          stage -= C::kStages;
+          parity ^= 1;
+        }
+      }
+    };
+    auto score = [&](int buf, uint32_t stage) {   // S = Q K^T
+      const uint32_t a = static_cast<uint32_t>(dq) + q * (C::kQTile >> 4), b = static_cast<uint32_t>(dk) + stage * kStep;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
-        tc_mma_elect(tmem + buf * BN, dq + ((q * C::kQTile + (ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) >> 4),
-                     dk + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), kIdS, ks > 0);
+        tc_mma_elect(tmem + buf * BN, desc(a + (((ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) >> 4), dq),
+                     desc(b + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), dk), kIdS, ks > 0);
       tc_commit_elect(&s_full[buf]);
     };
-    auto value = [&](int q, int buf, int i) {   // O += P V of step i
-      const int fill = 2 * i + 1;
-      const uint64_t dv = sdesc(base_u32 + C::kRing + (fill % C::kStages) * C::kStage, 1024, PL * 1024);
+    auto value = [&](int buf, uint32_t stage, bool first) {   // O += P V
+      const uint32_t b = static_cast<uint32_t>(dv) + stage * kStep;
 #pragma unroll
       for (int ks = 0; ks < BN / 16; ++ks)
-        tc_mma_tmem_a_elect(tmem + kOCol + q * D, tmem + buf * BN + 8 * ks, dv + ((ks * 2 * PL * 1024) >> 4), kIdPV, i > 0 || ks > 0);
+        tc_mma_tmem_a_elect(tmem + kOCol + q * D, tmem + buf * BN + 8 * ks, desc(b + ((ks * 2 * PL * 1024) >> 4), dv), kIdPV,
+                            !first || ks > 0);
     };
-    auto wait_k = [&](int i) { return ready(&full[(2 * i) % C::kStages], ((2 * i) / C::kStages) & 1); };
-    // V of step i has landed, and its rows that no row of the CTA sees are zeros
-    auto wait_v = [&](int i) {
-      const int fill = 2 * i + 1;
-      if (!ready(&full[fill % C::kStages], (fill / C::kStages) & 1)) return false;
+    // V of step i has landed, and its rows that no row of the CTA sees are zeros (both tiles'
+    // warps write the same)
+    auto wait_v = [&](int i, const Ring& r) {
+      if (!ready(&full[r.stage], r.parity)) return false;
       const int t0 = S.first_slot(j_begin + i, BN);
       if (!S.all_seen(t0, t0 + BN)) {
-        uint8_t* v = smem + C::kRing + (fill % C::kStages) * C::kStage;
+        uint8_t* v = smem + C::kRing + r.stage * C::kStage;
         for (int x = lane; x < BN * PL * 8; x += 32) {
           const int row = x / (PL * 8), part = x % (PL * 8);
           if (!S.seen(t0 + row))
@@ -436,168 +489,249 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
       }
       return true;
     };
-    auto release = [&](int fill) { tc_commit_elect(&empty[fill % C::kStages]); };
-    if (wait_k(0)) {
+    Ring rk{0, 0}, rv{1, 0};   // of K of the step whose scores come next, of V of the current step
+    if (ready(&q_full[q], 0) && ready(&full[0], 0)) {
       tc_fence_after();
-      for (int q = 0; q < tiles; ++q) score(q, q, 0);
-      release(0);
-      for (int i = 0; i < n && ok; ++i) {
-        if (NQ == 2) {
-          for (int q = 0; q < tiles; ++q) {
-            if (!ready(&p_full[q], i & 1)) break;
-            if (q == 0 && !wait_v(i)) break;
-            tc_fence_after();
-            value(q, q, i);
-            if (i == n - 1) tc_commit_elect(&o_full[q]);
-            if (q == tiles - 1) release(2 * i + 1);
-            if (i + 1 < n) {
-              if (q == 0 && !wait_k(i + 1)) break;
-              score(q, q, i + 1);
-              if (q == tiles - 1) release(2 * i + 2);
-            }
-          }
-        } else {
-          if (i + 1 < n) {
-            if (!wait_k(i + 1)) break;
-            tc_fence_after();
-            score(0, (i + 1) & 1, i + 1);
-            release(2 * i + 2);
-          }
-          if (!ready(&p_full[i & 1], (i >> 1) & 1) || !wait_v(i)) break;
+      score(NQ == 2 ? q : 0, 0);
+      tc_commit_elect(&empty[0]);
+      rk.next();
+      for (int i = 0; i < n; ++i) {
+        const bool more = i + 1 < n;
+        const int buf = NQ == 2 ? q : i & 1;
+        const uint32_t parity = (NQ == 2 ? i : i >> 1) & 1;
+        // (what has landed long ago is looked at before what is waited for)
+        if (!wait_v(i, rv) || (more && !ready(&full[rk.stage], rk.parity))) break;
+        if (NQ == 1 && more) {
           tc_fence_after();
-          value(0, i & 1, i);
-          release(2 * i + 1);
-          tc_commit_elect(pv_done);
-          if (i == n - 1) tc_commit_elect(&o_full[0]);
+          score((i + 1) & 1, rk.stage);
+          tc_commit_elect(&empty[rk.stage]);
         }
+        if (!ready(&p_full[buf], parity)) break;
+        // The tiles take turns, so that one's products run during the other's softmax (each going its own
+        // way, both were soon in step, and both units idle half of the time: 394 us).
+        if (tiles == 2 && (q == 1 || i > 0) && !ready(&turn[q], (q == 1 ? i : i - 1) & 1)) break;
+        tc_fence_after();
+        value(buf, rv.stage, i == 0);
+        if (NQ == 2 && more) score(buf, rk.stage);
+        if (tiles == 2 && lane == 0) mbar_arrive(&turn[q ^ 1]);
+        if (NQ == 2 && more) tc_commit_elect(&empty[rk.stage]);
+        tc_commit_elect(&empty[rv.stage]);
+        if (NQ == 1) tc_commit_elect(pv_done);
+        if (!more) tc_commit_elect(&o_full[q]);
+        rk.next();
+        rv.next();
       }
     }
     if (!ok && lane == 0) fail();
-    tc_commit_elect(done);
-    mbar_wait_bounded(done, 0);
-  } else if (warp < C::kSoftmaxWarps && warp < 4 * tiles) {
+    tc_commit_elect(&done[q]);
+    mbar_wait_bounded(&done[q], 0);
+  } else if (warp >= C::kSoftmax0 && my_tile < tiles) {
     // ---------------------------------------------------------------- softmax
-    const int q = warp >> 2;
+    const int q = my_tile;
+    const int64_t at = has_row ? static_cast<int64_t>(my_token) * P.q_heads + my_head : -1;   // row of the outputs
+    // The queries of the warp's rows, as rows of 128 swizzled bytes, one 64-dim plane after the other.  Lanes
+    // share rows here and where results leave (a row a lane is 32 lines an instruction: it
+    // took 6,000 cycles).
+    if (n > 0) {
+      constexpr int CH = D / 8, RW = 32 / CH > 0 ? 32 / CH : 1;   // chunks of a row, rows of an instruction
+      const int64_t mine = has_row ? my_token * P.q_stride + static_cast<int64_t>(my_head) * D * 2 : -1;
+      const int c = lane % CH, sub = CH < 32 ? lane / CH : 0;
+      const uint32_t to = base_u32 + q * C::kQTile + (c >> 3) * (kTileRows * 128);
+#pragma unroll 8
+      for (int r0 = 16 * my_half; r0 < 16 * my_half + 16; r0 += RW) {
+        const int64_t from = __shfl_sync(kFull, mine, r0 + sub);
+        const int r = 32 * (warp & 3) + r0 + sub;
+        cp_async16_zfill(to + r * 128 + (((c & 7) ^ (r & 7)) << 4), P.q + (from >= 0 ? from : 0) + c * 16, from >= 0);
+      }
+      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+      if (P.sign <= 0) {   // queries of a negative scale enter negated, of scale 0 as zeros
+        for (int r0 = 16 * my_half; r0 < 16 * my_half + 16; r0 += RW) {
+          const int r = 32 * (warp & 3) + r0 + sub;
+          uint4* x = reinterpret_cast<uint4*>(smem + q * C::kQTile + (c >> 3) * (kTileRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+          uint4 v = *x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) word(v, e) = P.sign < 0 ? word(v, e) ^ 0x80008000u : 0u;
+          *x = v;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[q]);
+    }
+    // Two threads share a row, with half of a step's slots each.  They hold the row's maximum alike, and meet once a
+    // step to learn whether either must raise it.
+    constexpr int HN = BN / 2, HW = HN / 32;
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const uint32_t o_at = tl + kOCol + q * D;
+    const uint32_t pair = 1 + 4 * q + (warp & 3);   // named barrier of the two warps
+    float* s_top = reinterpret_cast<float*>(smem + C::kTop) + q * kTileRows + 32 * (warp & 3) + lane;
     const float scale = P.scale_log2;
     float m_run = -FLT_MAX, l_run = 0.0f;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const int buf = NQ == 2 ? q : i & 1;
       const uint32_t parity = (NQ == 2 ? i : i >> 1) & 1;
-      ok = __all_sync(kFull, wait_or_abort(&meta_full[i % kMetas], (i / kMetas) & 1, abort_flag, kMaxSpins) &&
-                                 wait_or_abort(&s_full[buf], parity, abort_flag, kMaxSpins));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t s_at = tl + buf * BN;
-      float s[BN];
-#pragma unroll
-      for (int c = 0; c < BN; c += 32) tmem_ld32(s_at + c, s + c);
-      tmem_wait_ld();
+      ok = __all_sync(kFull, wait_or_abort(&meta_full[i % kMetas], (i / kMetas) & 1, abort_flag, kMaxSpins));
+      // what this row sees of the step, before its scores are there
       const int t0 = S.first_slot(j_begin + i, BN);
-      uint32_t live[BN / 32];
+      uint32_t mask[HW];
       bool whole = t0 + BN - 1 <= S.s_min && (S.window == 0 || t0 > S.hi - S.window || t0 + BN <= P.n_first);
 #pragma unroll
-      for (int x = 0; x < BN / 32; ++x) {
-        live[x] = meta[(i % kMetas) * 4 + x];
-        whole &= live[x] == kFull;
+      for (int x = 0; x < HW; ++x) {
+        mask[x] = meta[(i % kMetas) * 4 + my_half * HW + x];
+        whole &= mask[x] == kFull;
       }
       if (!whole) {
         // slots t <= my_slot that are in the window or among the first
 #pragma unroll
-        for (int x = 0; x < BN / 32; ++x) {
-          const int t = t0 + 32 * x;
-          const uint32_t mask = live[x] & low_bits(my_slot + 1 - t) & (~low_bits(my_lo - t) | low_bits(P.n_first - t));
-#pragma unroll
-          for (int y = 0; y < 32; ++y) s[32 * x + y] = (mask >> y) & 1u ? s[32 * x + y] : -INFINITY;
+        for (int x = 0; x < HW; ++x) {
+          const int t = t0 + 32 * (my_half * HW + x);
+          mask[x] &= low_bits(my_slot + 1 - t) & (~low_bits(my_lo - t) | low_bits(P.n_first - t));
         }
+      }
+      ok = ok && __all_sync(kFull, wait_or_abort(&s_full[buf], parity, abort_flag, kMaxSpins));
+      // (a wait that ran out in one warp of a pair ends both: they meet below)
+      tc_fence_after();
+      const uint32_t s_at = tl + buf * BN + my_half * HN;
+      float s[HN];
+#pragma unroll
+      for (int c = 0; c < HN; c += 32) tmem_ld32(s_at + c, s + c);
+      tmem_wait_ld();
+      if (!__all_sync(kFull, whole)) {
+#pragma unroll
+        for (int x = 0; x < HN; ++x) s[x] = (mask[x / 32] >> (x & 31)) & 1u ? s[x] : -INFINITY;
       }
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int x = 4; x < BN; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-      if (i == 0) {
-        m_run = fmaxf(top, -FLT_MAX);
-      } else if (__any_sync(kFull, top > m_run + kLazy)) {
-        const float m_new = top > m_run + kLazy ? top : m_run;
+      for (int x = 4; x < HN - 4; x += 8) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[x + 2 * y], s[x + 2 * y + 1]);
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[HN - 4 + y]);
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+      if (pair_any(pair, !ok || i == 0 || top > m_run + kLazy)) {
+        // the second half's maximum goes to the first, which decides
+        if (my_half == 1) *s_top = ok ? top : INFINITY;
+        pair_any(pair, false);
+        if (my_half == 0) {
+          const float both = fmaxf(top, *s_top);
+          *s_top = i == 0 ? fmaxf(both, -FLT_MAX) : (both > m_run + kLazy ? both : m_run);
+        }
+        if (pair_any(pair, !ok)) {
+          ok = false;
+          break;
+        }
+        const float m_new = *s_top;
         const float alpha = ex2(m_run - m_new);
         m_run = m_new;
         l_run *= alpha;
-        if (NQ == 1) {
-          ok = __all_sync(kFull, wait_or_abort(pv_done, (i - 1) & 1, abort_flag, kMaxSpins));
-          if (!ok) break;
-          tc_fence_after();
-        }
+        if (i > 0) {
+          if (NQ == 1) {
+            ok = __all_sync(kFull, wait_or_abort(pv_done, (i - 1) & 1, abort_flag, kMaxSpins));
+            tc_fence_after();
+          }
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tmem_ld16(o_at + c, o);
-          tmem_wait_ld();
+          for (int c = my_half * (D / 2); c < (my_half + 1) * (D / 2); c += 16) {
+            float o[16];
+            tmem_ld16(o_at + c, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[x] *= alpha;
-          tmem_st16(o_at + c, o);
+            for (int x = 0; x < 16; ++x) o[x] *= alpha;
+            tmem_st16(o_at + c, o);
+          }
         }
       }
       const float2 sc = make_float2(scale, scale), neg = make_float2(-m_run, -m_run);
-      float2 sum = make_float2(0.0f, 0.0f);
+      float2 sum[2] = {};
 #pragma unroll
-      for (int c = 0; c < BN; c += 32) {
+      for (int c = 0; c < HN; c += 32) {
         uint32_t p[16];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          float2 y = __ffma2_rn(make_float2(s[c + 2 * x], s[c + 2 * x + 1]), sc, neg);
+        for (int e = 0; e < 16; ++e) {
+          float2 y = __ffma2_rn(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), sc, neg);
           y.x = ex2(y.x);
           y.y = ex2(y.y);
-          sum = __fadd2_rn(sum, y);
-          p[x] = bf_pack(y.x, y.y);
+          sum[e & 1] = __fadd2_rn(sum[e & 1], y);
+          p[e] = bf_pack(y.x, y.y);
         }
-        tmem_st16u(s_at + c / 2, p);
+        // (over scores that both threads of the row have read)
+        tmem_st16u(tl + buf * BN + (my_half * HN + c) / 2, p);
       }
-      l_run += sum.x + sum.y;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[buf]);
+      l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (!ok) break;
     }
     if (!ok && lane == 0) fail();
     // ---- the output, or this part's record
     const bool direct = P.rec_acc == nullptr;
-    if (my_slot < 0) l_run = 0.0f;   // a row that sees nothing
     if (n > 0 && ok) {
       ok = __all_sync(kFull, wait_or_abort(&o_full[q], 0, abort_flag, kMaxSpins));
       if (!ok && lane == 0) fail();
       tc_fence_after();
     }
-    const int64_t at = static_cast<int64_t>(my_token) * P.q_heads + my_head;
+    // 4 KB of the queries' memory for each warp (64 dims: each pair), of which every product has been made
+    uint8_t* stage = smem + q * C::kQTile + (D == 64 ? (warp & 3) * 4096 : ((warp & 3) * 2 + my_half) * 4096);
+    ok = !pair_any(pair, !ok);
+    {
+      // the row's sum: both halves'
+      float* x = reinterpret_cast<float*>(smem + q * C::kQTile + (warp & 3) * (D == 64 ? 4096 : 8192));
+      x[32 * my_half + lane] = l_run;
+      pair_any(pair, false);
+      l_run = x[lane] + x[32 + lane];
+      if (my_slot < 0) l_run = 0.0f;   // a row that sees nothing
+      pair_any(pair, false);
+    }
     if (ok) {
+      // 128 bytes of each of the warp's rows at a time
       const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+      uint8_t* out = direct ? static_cast<uint8_t*>(P.out)
+                            : reinterpret_cast<uint8_t*>(P.rec_acc + static_cast<int64_t>(split) * P.n_tokens * P.q_heads * D);
+      const int64_t pitch = D * (direct ? 2 : 4);
+      const int64_t mine = direct || l_run != 0.0f ? at : -1;   // nothing is kept beside a sum of 0
+      const int width = direct ? 64 : 32, halves = D == 64 ? 1 : 2;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = my_half < halves ? my_half * width : D; c < D; c += halves * width) {
         float o[32];
-        if (n > 0) {
-          tmem_ld32(o_at + c, o);
-          tmem_wait_ld();
-        }
-        if (has_row && direct) {
-          uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.out) + at * D + c);
+#pragma unroll 1
+        for (int h = 0; h < (direct ? 2 : 1); ++h) {
+          if (n > 0) {
+            tmem_ld32(o_at + c + 32 * h, o);
+            tmem_wait_ld();
+          }
+          if (l_run == 0.0f) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (l_run != 0.0f) {
+            for (int x = 0; x < 32; ++x) o[x] = 0.0f;
+          }
+          if (direct) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint4 y;
 #pragma unroll
               for (int e = 0; e < 4; ++e) word(y, e) = bf_pack(o[8 * x + 2 * e] * inv, o[8 * x + 2 * e + 1] * inv);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * h + x) ^ (lane & 7)) << 4)) = y;
             }
-            to[x] = y;
-          }
-        } else if (has_row && l_run != 0.0f) {
-          float4* to = reinterpret_cast<float4*>(P.rec_acc + (static_cast<int64_t>(split) * P.n_tokens * P.q_heads + at) * D + c);
+          } else {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) to[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<float4*>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) =
+                  make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + (lane >> 3);
+          const int64_t row = __shfl_sync(kFull, mine, r);
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (row >= 0) *reinterpret_cast<uint4*>(out + row * pitch + c * (direct ? 2 : 4) + (lane & 7) * 16) = y;
         }
         __syncwarp();
       }
-      if (has_row) {
+      if (has_row && my_half == 0) {
         if (!direct) P.rec_ml[static_cast<int64_t>(split) * P.n_tokens * P.q_heads + at] = make_float2(l_run == 0.0f ? -FLT_MAX : m_run, l_run);
         else if (P.lse != nullptr) P.lse[at] = l_run == 0.0f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
       }
@@ -606,7 +740,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
 
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kMmaWarp) {
+  if (warp == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
