@@ -144,10 +144,13 @@ constexpr int kPagedMaxHeads = 4096;    // query heads
 struct RowsParams {
   int32_t shared;            // 0: tokens of requests; 1: one token a request, the prefix shared; 2: the same
                              // without the prefix, whose part of each row is in the records `extra`
-  int32_t singles;           // tokens: 1 where requests of more than one token are another kernel's
+  int32_t singles;           // tokens: 1 where requests of more than one token are another kernel's; row r of
+                             // the list is then request r's token, else token r
+  int32_t n_tokens;          // tokens: rows of q and the outputs
   const int32_t* indptr;     // [n_req + 1] tokens: rows of each request
   const int32_t* slot;       // [rows] tokens: slot of each
   int32_t n_req;             // tokens: requests
+  int32_t after_tiles;       // 1: launched while the tiles that the join also reads may still run
   int32_t capacity;          // slots a table holds
   int32_t window, n_first;   // window 0: every slot before
   const int32_t* prefix_table;   // shared: [prefix_blocks]

@@ -131,11 +131,14 @@ __device__ __forceinline__ int request_of(const RowsParams& R, int i) {
   }
   return lo;
 }
-// Whether row r of pic_attend_tokens is this kernel's.
-__device__ __forceinline__ bool owns_row(const RowsParams& R, int r) {
-  if (R.singles == 0) return r >= __ldg(R.indptr) && r < __ldg(R.indptr + R.n_req);
-  const int x = request_of(R, r);
-  return x >= 0 && __ldg(R.indptr + x + 1) - __ldg(R.indptr + x) == 1;
+// Token of row r of the list; -1: none (pic_attend_tokens: a row of no request, or of one whose tokens are
+// another kernel's).
+__device__ __forceinline__ int token_of(const PagedParams& P, int r) {
+  const RowsParams& R = P.rows;
+  if (R.shared != 0) return r;
+  if (R.singles == 0) return r >= __ldg(R.indptr) && r < __ldg(R.indptr + R.n_req) ? r : -1;
+  const int i = __ldg(R.indptr + r);
+  return __ldg(R.indptr + r + 1) - i == 1 && i >= 0 && i < R.n_tokens ? i : -1;
 }
 __device__ __forceinline__ int prefix_of(const PagedParams& P, bool raise) {
   return legal_len(__ldg(P.rows.prefix_len), P.rows.max_prefix, P.status, raise);
@@ -146,8 +149,9 @@ __device__ __forceinline__ Span span_of(const PagedParams& P, int r, bool raise)
     const int len = legal_len(__ldg(P.lens + r), P.max_len, P.status, raise), head = min(prefix_of(P, raise), len);
     return R.shared == 1 ? Span{len, head, 0} : Span{len - head, 0, head};
   }
-  const int s = __ldg(R.slot + r);
-  if (s < 0 || !owns_row(R, r)) return Span{0, 0, 0};
+  const int i = token_of(P, r);
+  const int s = i >= 0 ? __ldg(R.slot + i) : -1;
+  if (s < 0) return Span{0, 0, 0};
   if (s >= R.capacity) {
     if (raise) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_BAD_LENGTH));
     return Span{0, 0, 0};
@@ -186,7 +190,7 @@ __device__ __forceinline__ TileList tile_list(const PagedParams& P, int lane, bo
       bool bad = false;
       for (int r = lane; r <= P.rows.n_req; r += 32) {
         const int at = __ldg(P.rows.indptr + r), before = r > 0 ? __ldg(P.rows.indptr + r - 1) : 0;
-        bad |= at < before || at > P.n_req;
+        bad |= at < before || at > P.rows.n_tokens;
       }
       if (bad) atomicOr(P.status, static_cast<uint32_t>(PIC_DEV_BAD_LENGTH));
     }
@@ -256,7 +260,7 @@ struct Place {
   int req, tile, len;
   int64_t first;   // the request's first tile in the list
   // ROWS: the gap in the row's slots, and its block table
-  int head, gap;
+  int head, gap, token;
   const int32_t* table;
 };
 // Fills in a place's request (req below n_req).
@@ -267,7 +271,8 @@ __device__ __forceinline__ void open_place(const PagedParams& P, Place& x) {
     x.len = s.len;
     x.head = s.head;
     x.gap = s.gap;
-    const int row = P.rows.shared != 0 || s.len == 0 ? x.req : request_of(P.rows, x.req);
+    x.token = s.len == 0 ? 0 : token_of(P, x.req);
+    const int row = P.rows.shared != 0 || P.rows.singles != 0 || s.len == 0 ? x.req : request_of(P.rows, x.req);
     x.table = P.paged.tables + static_cast<int64_t>(row) * P.paged.max_blocks;
   } else {
     x.len = row_len<false>(P, x.req, false);
@@ -411,7 +416,7 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
         l_run[0] = l_run[1] = 0.0f;
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-        const uint8_t* qp = P.q + cur.req * P.q_stride + static_cast<int64_t>(hq0) * D * 2;
+        const uint8_t* qp = P.q + (ROWS ? cur.token : cur.req) * P.q_stride + static_cast<int64_t>(hq0) * D * 2;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
 #pragma unroll
@@ -575,6 +580,10 @@ __global__ void __launch_bounds__(32 * paged_warps(D), 1) k_paged_attend(const _
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * paged_warps(D) + (threadIdx.x >> 5);
        w < static_cast<int64_t>(P.parts) * P.v_heads; w += warps)
     attend_range<D, WIDE, F32, ROWS>(P, L, w, smem);
+  // Launched while the tiles may still run, of which nothing is read here; the join behind this grid reads their
+  // records too, so this grid does not end before them.
+  if constexpr (ROWS)
+    if (P.rows.after_tiles != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- MLA: latent rows
@@ -924,23 +933,31 @@ __device__ __forceinline__ void join_output(const PagedParams& P, const Records&
   constexpr int V = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float M, sum, acc[V];
-  const int64_t task = static_cast<int64_t>(r) * P.q_heads + hq;
+  const int64_t task = static_cast<int64_t>(ROWS ? token_of(P, r) : r) * P.q_heads + hq;
   if constexpr (ROWS) {   // the prefix's parts first
     const int64_t pitch = static_cast<int64_t>(P.n_req) * P.q_heads;
     const float2* ml = P.rows.extra_ml + task;
     join_stats(P, x, hq, lane, M, sum, ml, P.rows.n_extra, pitch);
     join_values<D>(P, x, hq, lane, M, ALL ? warp : 0, ALL ? kFinishWarps : 1, acc);
+    for (int k0 = 0; k0 < P.rows.n_extra; k0 += 32) {
+      // lane k: the factor of part k (0: nothing was written beside its sum)
+      float mine = 0.0f;
+      if (k0 + lane < P.rows.n_extra) {
+        const float2 y = __ldcg(ml + (k0 + lane) * pitch);
+        mine = y.y == 0.0f ? 0.0f : ex2(y.x - M);
+      }
+      const int n = min(32, P.rows.n_extra - k0);
 #pragma unroll 4
-    for (int k = ALL ? warp : 0; k < P.rows.n_extra; k += ALL ? kFinishWarps : 1) {
-      const float2 y = __ldcg(ml + k * pitch);
-      if (y.y == 0.0f) continue;   // nothing was written beside it
-      const float e = ex2(y.x - M);
-      const float* a = P.rows.extra_acc + (k * pitch + task) * D + lane * V;
+      for (int k = ALL ? warp : 0; k < n; k += ALL ? kFinishWarps : 1) {
+        const float e = __shfl_sync(kFull, mine, k);
+        if (e == 0.0f) continue;
+        const float* a = P.rows.extra_acc + ((k0 + k) * pitch + task) * D + lane * V;
 #pragma unroll
-      for (int i = 0; i < V; i += 2) {
-        const float2 z = __ldcg(reinterpret_cast<const float2*>(a + i));
-        acc[i] += e * z.x;
-        acc[i + 1] += e * z.y;
+        for (int i = 0; i < V; i += 2) {
+          const float2 z = __ldcg(reinterpret_cast<const float2*>(a + i));
+          acc[i] += e * z.x;
+          acc[i + 1] += e * z.y;
+        }
       }
     }
   } else {
@@ -1116,7 +1133,7 @@ __global__ void __launch_bounds__(kFinishThreads, 3) k_paged_finish(const __grid
     const int r = static_cast<int>(task / P.q_heads), hq = static_cast<int>(task % P.q_heads);
     if (r >= P.n_req) return;
     if constexpr (ROWS) {
-      if (P.rows.shared == 0 && !owns_row(P.rows, r)) {   // a row of no request stays as it is
+      if (token_of(P, r) < 0) {   // a row of no request stays as it is
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
       }
@@ -1157,6 +1174,19 @@ cudaError_t launch_attend_d(const PagedParams& p, int grid, cudaStream_t s) {
   static std::atomic<uint32_t> done{0};
   const cudaError_t e = allow_smem(kern, smem, done);
   if (e != cudaSuccess) return e;
+  if (ROWS && p.rows.after_tiles != 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(32 * paged_warps(D));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+  }
   kern<<<grid, 32 * paged_warps(D), smem, s>>>(p);
   return cudaGetLastError();
 }

@@ -43,17 +43,22 @@ PagedParams rows_params(const CtxView& c, const void* q, int64_t q_stride, int32
 
 // ---- tiles of rows (pic_tile.cu)
 
+// Bytes of a shared prefix, counted for every request, up to which it is read row by row: 8 requests over
+// 1,000 slots 13 us (tiles 22), over 2,000 (63 MB) 17 (19), over 4,000 (125 MB) 23 (18).
+constexpr int64_t kSharedPrefixReads = int64_t{64} << 20;
+
 // Row blocks per KV head, at most: of n_tokens tokens of n_req requests.
 int64_t tile_blocks(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
   const int64_t rows = static_cast<int64_t>(kTileRows) * tile_groups(c.model->head_dim);
   return n_tokens * (num_q_heads / c.model->num_kv_heads) / rows + std::min(n_req, n_tokens);
 }
-// Parts that a row block's slots are dealt to: as many as there are SMs for, and at
-// least four steps each.
+// Parts that a row block's slots are dealt to.  As many as there are SMs for, of at least
+// four steps each; and, as blocks differ in length, parts enough for two rounds of the SMs
+// where a part keeps 16 steps (recomputed heads of 4 sequences of 16k: 244 us whole, 176 in two parts).
 int32_t tile_splits(const CtxView& c, int64_t blocks, int sms, int64_t max_slots) {
-  const int64_t fit = sms / std::max<int64_t>(1, blocks * c.model->num_kv_heads);
-  const int64_t useful = max_slots / (4 * tile_slots(c.model->head_dim));
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min(fit, useful)));
+  const int64_t ctas = std::max<int64_t>(1, blocks * c.model->num_kv_heads), step = tile_slots(c.model->head_dim);
+  const int64_t fill = std::min(sms / ctas, max_slots / (4 * step)), even = std::min((2 * sms - 1) / ctas + 1, max_slots / (16 * step));
+  return static_cast<int32_t>(std::max<int64_t>(1, std::max(fill, ctas < 2 * sms ? even : 0)));
 }
 // Workspace of a call: the row-by-row kernels' part, then the records of split tiles.
 struct RowsLayout {
@@ -241,6 +246,7 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
   p.rows.indptr = d_indptr;
   p.rows.slot = d_slot;
   p.rows.n_req = n_req;
+  p.rows.n_tokens = n_tokens;
   p.rows.capacity = table_capacity(c, max_blocks);
   p.rows.window = window;
   p.rows.n_first = n_first;
@@ -275,11 +281,16 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
       t.rec_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + L.ml);
     }
     cudaError_t e = launch_tile(t, maps, c.model->head_dim, cs);
+    if (e == cudaSuccess && n_req > 1) {
+      p.rows.singles = 1;
+      p.rows.after_tiles = 1;
+      p.n_req = n_req;   // the list is of requests (fewer than the tokens that the workspace is laid out for)
+      p.first = n_req > kPagedWalkRequests ? p.first : nullptr;
+      e = launch_paged_rows(p, c.model->head_dim, used, cs);
+    }
     if (e == cudaSuccess && t.splits > 1) e = launch_tile_join(t, c.model->head_dim, cs);
     if (e != cudaSuccess) return cuda_fail(ctx, e, "token attention launch");
-    p.rows.singles = 1;
-  }
-  if (!tiles || n_req > 1) {
+  } else {
     const cudaError_t e = launch_paged_rows(p, c.model->head_dim, used, cs);
     if (e != cudaSuccess) return cuda_fail(ctx, e, "token attention launch");
   }
@@ -332,7 +343,9 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const int used = std::min(sms, kPagedMaxSms);
   cudaError_t e = cudaSuccess;
-  if (p.rows.max_prefix > 0) {
+  // A short prefix is read row by row like the rest: a launch less, and its repeated reads come from L2.
+  const int64_t prefix_reads = static_cast<int64_t>(n_req) * p.rows.max_prefix * p.row_bytes * 2;
+  if (prefix_reads > kSharedPrefixReads) {
     // the prefix in tiles of all requests' rows, whose records the join adds to those of the rest
     TileParams t{};
     TileMaps maps;
@@ -352,6 +365,7 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     t.rec_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + L.ml);
     e = launch_tile(t, maps, c.model->head_dim, cs);
     p.rows.shared = 2;
+    p.rows.after_tiles = 1;
     p.rows.n_extra = t.splits;
     p.rows.extra_acc = t.rec_acc;
     p.rows.extra_ml = t.rec_ml;

@@ -51,7 +51,6 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLazy = 8.0f;   // log2 units a maximum may be passed by before O is rescaled
 constexpr int kProducers = 2;
-constexpr int kMetas = 8;       // steps whose bad slots are kept: more than the ring holds
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 
 template <int D>
@@ -73,10 +72,9 @@ struct Cfg {
   static_assert(kSoftmax0 % 4 == 0, "TMEM lane quadrants");
   // shared memory, from a 1024-byte aligned base
   static constexpr int kRing = NQ * kQTile;
-  static constexpr int kMeta = kRing + kStages * kStage;        // uint32 [kMetas][4]
-  static constexpr int kBars = kMeta + kMetas * 16;
-  // full[kStages] empty[kStages] meta[kMetas] s_full[2] p_full[2] o_full[2] pv_done done[2] q_full[2] turn[2]
-  static constexpr int kNumBars = 2 * kStages + kMetas + 13;
+  static constexpr int kBars = kRing + kStages * kStage;
+  // full[kStages] empty[kStages] s_full[2] p_full[2] o_full[2] pv_done done[2] q_full[2] turn[2]
+  static constexpr int kNumBars = 2 * kStages + 13;
   static constexpr int kTop = kBars + kNumBars * 8;             // float [rows]: a row's maximum, between its two threads
   static constexpr int kMisc = kTop + 4 * NQ * kTileRows;       // TMEM slot, abort flag, int [2][warps]
   static constexpr int kTotal = kMisc + 16 + 2 * 4 * (kThreads / 32);
@@ -94,6 +92,34 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
+}
+// Two fp32 operations at once.  (Written out: through the header's float2 functions a step's
+// exponentials took 646 cycles a warp where these take 431.)
+__device__ __forceinline__ uint64_t pair64(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t r) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// (x, y) as a bf16 pair, x in the low half
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -128,6 +154,18 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
+// Joins the softmax warps (PER threads a tile), at named barrier 15: whether any thread's flag is set.
+template <int PER>
+__device__ __forceinline__ bool softmax_any(int tiles, bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, 15, %1, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(PER * tiles), "r"(flag ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 // Joins the two warps that share rows, at named barrier `id`: whether any thread's flag is set.
 __device__ __forceinline__ bool pair_any(uint32_t id, bool flag) {
   uint32_t r;
@@ -153,12 +191,12 @@ struct Work {
 struct Slots {
   int lo, hi;          // slots lo .. hi of some window (hi < lo: nothing is seen)
   int n_first;         // slots below are seen by every row behind them
-  int s_min;           // lowest slot of a row (of those that see any)
-  int window;
   // steps over the window, and after them over the first slots where those are apart
   // (the few scores of the first would be a poor first maximum)
   int base;            // first slot of the window's steps
   int steps_w, steps;
+  int whole_lo, whole_hi;   // a step that begins between these is seen whole by every row
+  __device__ __forceinline__ int next_slot(int t, int j, int bn) const { return j == steps_w ? 0 : t + bn; }
   __device__ __forceinline__ int first_slot(int j, int bn) const { return j < steps_w ? base + j * bn : (j - steps_w) * bn; }
   __device__ __forceinline__ bool some(int a, int b) const {   // whether any of slots [a, b) is seen by a row
     return a <= hi && (b > lo || a < n_first);
@@ -240,15 +278,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBars);
   uint64_t* full = bars;                        // a stage's rows landed
   uint64_t* empty = full + C::kStages;          // the products that read it finished
-  uint64_t* meta_full = empty + C::kStages;     // a step's live slots are written
-  uint64_t* s_full = meta_full + kMetas;        // S is made (by buffer, as below)
+  uint64_t* s_full = empty + C::kStages;        // S is made (by buffer, as below)
   uint64_t* p_full = s_full + 2;                // P is written
   uint64_t* o_full = p_full + 2;                // a tile's O is complete
   uint64_t* pv_done = o_full + 2;               // (256 dims) a step's value product finished
   uint64_t* done = pv_done + 1;                 // an issuer's products all finished
   uint64_t* q_full = done + 2;                  // a tile's queries are in place
   uint64_t* turn = q_full + 2;                    // a tile's products of a step may be issued
-  uint32_t* meta = reinterpret_cast<uint32_t*>(smem + C::kMeta);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
   int* s_range = reinterpret_cast<int*>(smem + C::kMisc + 16);   // [2][warps]
@@ -275,7 +311,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
       mbar_init(&full[i], kProducers);   // each warp announces its own copies
       mbar_init(&empty[i], tiles);           // each tile's products have read it
     }
-    for (int i = 0; i < kMetas; ++i) mbar_init(&meta_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 8);
@@ -325,9 +360,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
       lo = min(lo, s_range[i]);
       hi = max(hi, s_range[C::kThreads / 32 + i]);
     }
-    S.s_min = lo;
     S.hi = hi;
-    S.window = P.window;
     S.lo = P.window > 0 && hi >= 0 ? max(0, lo + 1 - P.window) : 0;
     S.n_first = min(P.n_first, S.lo);
     // the first slots apart from the window, where steps over them end before it
@@ -337,6 +370,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
     S.base = apart || S.n_first == 0 ? lo_box : 0;
     S.steps_w = hi < 0 ? 0 : (hi - S.base) / BN + 1;
     S.steps = S.steps_w + (apart ? steps_a : 0);
+    S.whole_lo = P.window > 0 ? max(0, hi + 1 - P.window) : 0;
+    S.whole_hi = lo == INT32_MAX ? -1 : lo + 1 - BN;
   }
   // this CTA's part of the steps
   int j_begin = 0, n = S.steps;
@@ -373,13 +408,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
       return block_at(t, t, t + P.box);
     };
     bool ok = true;
-    int issued = 0;
+    int issued = 0, st = 0;
+    uint32_t round = 0;   // parity of the ring's round
     int32_t next = c0 < copies ? copy_block(0, c0) : -1;
     for (int i = 0; i < n; ++i) {
       const int32_t block0 = next;
-      for (int x = 0; x < 2 && ok; ++x) {   // K, then V
-        const int fill = 2 * i + x, st = fill % C::kStages;
-        if (fill >= C::kStages) ok = wait_or_abort(&empty[st], (fill / C::kStages - 1) & 1, abort_flag, kMaxSpins);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {   // K, then V
+        const int fill = 2 * i + x;
+        if (fill >= C::kStages) ok = wait_or_abort(&empty[st], round ^ 1, abort_flag, kMaxSpins);
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], my_bytes);
@@ -396,31 +433,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
           }
         }
         issued = fill + 1;
+        if (++st == C::kStages) {
+          st = 0;
+          round ^= 1;
+        }
       }
       if (!ok) {
         if (lane == 0) fail();
         break;
       }
       if (i + 1 < n && c0 < copies) next = copy_block(i + 1, c0);
-      if (prod == 0) {
-        // which of the step's slots have a block
-        int32_t block[BN / 32];
-#pragma unroll
-        for (int x = 0; x < BN / 32; ++x) {
-          const int t = S.first_slot(j_begin + i, BN) + 32 * x + lane;
-          block[x] = S.seen(t) ? __ldg(table + block_of(P.paged, t)) : 0;
-        }
-#pragma unroll
-        for (int x = 0; x < BN / 32; ++x) {
-          const int t = S.first_slot(j_begin + i, BN) + 32 * x + lane;
-          const bool bad = S.seen(t) && (block[x] < 0 || block[x] >= P.paged.num_cache_blocks);
-          if (bad) raise_block(P.status, w.table, t);
-          const unsigned live = ~__ballot_sync(kFull, bad);
-          if (lane == 0) meta[(i % kMetas) * 4 + x] = live;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&meta_full[i % kMetas]);
-      }
     }
     if (!ok && lane == 0) {
       // wait (bounded) for the copies in flight
@@ -473,9 +495,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
     };
     // V of step i has landed, and its rows that no row of the CTA sees are zeros (both tiles'
     // warps write the same)
-    auto wait_v = [&](int i, const Ring& r) {
+    auto wait_v = [&](int t0, const Ring& r) {
       if (!ready(&full[r.stage], r.parity)) return false;
-      const int t0 = S.first_slot(j_begin + i, BN);
       if (!S.all_seen(t0, t0 + BN)) {
         uint8_t* v = smem + C::kRing + r.stage * C::kStage;
         for (int x = lane; x < BN * PL * 8; x += 32) {
@@ -489,6 +510,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
       }
       return true;
     };
+    int t0 = S.first_slot(j_begin, BN);
     Ring rk{0, 0}, rv{1, 0};   // of K of the step whose scores come next, of V of the current step
     if (ready(&q_full[q], 0) && ready(&full[0], 0)) {
       tc_fence_after();
@@ -500,16 +522,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
         const int buf = NQ == 2 ? q : i & 1;
         const uint32_t parity = (NQ == 2 ? i : i >> 1) & 1;
         // (what has landed long ago is looked at before what is waited for)
-        if (!wait_v(i, rv) || (more && !ready(&full[rk.stage], rk.parity))) break;
+        if (!wait_v(t0, rv) || (more && !ready(&full[rk.stage], rk.parity))) break;
         if (NQ == 1 && more) {
           tc_fence_after();
           score((i + 1) & 1, rk.stage);
           tc_commit_elect(&empty[rk.stage]);
         }
-        if (!ready(&p_full[buf], parity)) break;
         // The tiles take turns, so that one's products run during the other's softmax (each going its own
         // way, both were soon in step, and both units idle half of the time: 394 us).
         if (tiles == 2 && (q == 1 || i > 0) && !ready(&turn[q], (q == 1 ? i : i - 1) & 1)) break;
+        if (!ready(&p_full[buf], parity)) break;
         tc_fence_after();
         value(buf, rv.stage, i == 0);
         if (NQ == 2 && more) score(buf, rk.stage);
@@ -520,6 +542,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
         if (!more) tc_commit_elect(&o_full[q]);
         rk.next();
         rv.next();
+        t0 = S.next_slot(t0, j_begin + i + 1, BN);
       }
     }
     if (!ok && lane == 0) fail();
@@ -566,30 +589,52 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
     const uint32_t pair = 1 + 4 * q + (warp & 3);   // named barrier of the two warps
     float* s_top = reinterpret_cast<float*>(smem + C::kTop) + q * kTileRows + 32 * (warp & 3) + lane;
     const float scale = P.scale_log2;
+    // Blocks outside the cache among those that some row sees: looked for once, all softmax warps together,
+    // so that steps need not ask (where there are any, each step does).
+    const int32_t* table = P.paged.tables + static_cast<int64_t>(w.table) * P.paged.max_blocks;
+    bool bad = false;
+    {
+      const int bs = P.paged.block_size, x0 = (warp - C::kSoftmax0) * 32 + lane, stride = 256 * tiles;
+      for (int part = 0; part < 2; ++part) {
+        // the CTA's steps over the window, then those over the first slots
+        const int ja = part == 0 ? j_begin : max(j_begin, S.steps_w), jb = part == 0 ? min(j_begin + n, S.steps_w) : j_begin + n;
+        if (ja >= jb) continue;
+        const int t = S.first_slot(ja, BN);
+        const int end = part == 0 ? min(S.hi + 1, t + (jb - ja) * BN) : min(S.n_first, t + (jb - ja) * BN);
+        const int b0 = block_of(P.paged, t), b1 = end > t ? block_of(P.paged, end - 1) : b0 - 1;
+        for (int b = b0 + x0; b <= b1; b += stride) {
+          if (!S.some(b * bs, b * bs + bs)) continue;
+          const int32_t block = __ldg(table + b);
+          if (block < 0 || block >= P.paged.num_cache_blocks) {
+            raise_block(P.status, w.table, b * bs);
+            bad = true;
+          }
+        }
+      }
+      bad = softmax_any<32 * 8>(tiles, bad);
+    }
     float m_run = -FLT_MAX, l_run = 0.0f;
     bool ok = true;
+    int t0 = S.first_slot(j_begin, BN);
     for (int i = 0; i < n; ++i) {
       const int buf = NQ == 2 ? q : i & 1;
       const uint32_t parity = (NQ == 2 ? i : i >> 1) & 1;
-      ok = __all_sync(kFull, wait_or_abort(&meta_full[i % kMetas], (i / kMetas) & 1, abort_flag, kMaxSpins));
       // what this row sees of the step, before its scores are there
-      const int t0 = S.first_slot(j_begin + i, BN);
+      const bool masked = bad || t0 < S.whole_lo || t0 > S.whole_hi;
       uint32_t mask[HW];
-      bool whole = t0 + BN - 1 <= S.s_min && (S.window == 0 || t0 > S.hi - S.window || t0 + BN <= P.n_first);
-#pragma unroll
-      for (int x = 0; x < HW; ++x) {
-        mask[x] = meta[(i % kMetas) * 4 + my_half * HW + x];
-        whole &= mask[x] == kFull;
-      }
-      if (!whole) {
-        // slots t <= my_slot that are in the window or among the first
+      if (masked) {
+        // slots t <= my_slot that are in the window or among the first, in blocks of the cache
 #pragma unroll
         for (int x = 0; x < HW; ++x) {
           const int t = t0 + 32 * (my_half * HW + x);
-          mask[x] &= low_bits(my_slot + 1 - t) & (~low_bits(my_lo - t) | low_bits(P.n_first - t));
+          mask[x] = low_bits(my_slot + 1 - t) & (~low_bits(my_lo - t) | low_bits(P.n_first - t));
+          if (bad) {
+            const int32_t block = S.seen(t + lane) ? __ldg(table + block_of(P.paged, t + lane)) : 0;
+            mask[x] &= __ballot_sync(kFull, block >= 0 && block < P.paged.num_cache_blocks);
+          }
         }
       }
-      ok = ok && __all_sync(kFull, wait_or_abort(&s_full[buf], parity, abort_flag, kMaxSpins));
+      ok = __all_sync(kFull, wait_or_abort(&s_full[buf], parity, abort_flag, kMaxSpins));
       // (a wait that ran out in one warp of a pair ends both: they meet below)
       tc_fence_after();
       const uint32_t s_at = tl + buf * BN + my_half * HN;
@@ -597,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
 #pragma unroll
       for (int c = 0; c < HN; c += 32) tmem_ld32(s_at + c, s + c);
       tmem_wait_ld();
-      if (!__all_sync(kFull, whole)) {
+      if (masked) {
 #pragma unroll
         for (int x = 0; x < HN; ++x) s[x] = (mask[x / 32] >> (x & 31)) & 1u ? s[x] : -INFINITY;
       }
@@ -642,28 +687,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
           }
         }
       }
-      const float2 sc = make_float2(scale, scale), neg = make_float2(-m_run, -m_run);
-      float2 sum[2] = {};
+      const uint64_t sc = pair64(scale, scale), neg = pair64(-m_run, -m_run);
+      uint64_t part[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < HN; c += 32) {
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float2 y = __ffma2_rn(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), sc, neg);
+          float2 y = unpair(fma2(pair64(s[c + 2 * e], s[c + 2 * e + 1]), sc, neg));
           y.x = ex2(y.x);
           y.y = ex2(y.y);
-          sum[e & 1] = __fadd2_rn(sum[e & 1], y);
-          p[e] = bf_pack(y.x, y.y);
+          part[e & 1] = add2(part[e & 1], pair64(y.x, y.y));
+          p[e] = pack2(y.x, y.y);
         }
         // (over scores that both threads of the row have read)
         tmem_st16u(tl + buf * BN + (my_half * HN + c) / 2, p);
       }
+      const float2 sum = unpair(add2(part[0], part[1]));
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[buf]);
-      l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      l_run += sum.x + sum.y;
       if (!ok) break;
+      t0 = S.next_slot(t0, j_begin + i + 1, BN);
     }
     if (!ok && lane == 0) fail();
     // ---- the output, or this part's record
