@@ -33,7 +33,8 @@ using namespace dev;
 
 constexpr int kWriteThreads = 128;
 constexpr int kWriteWarps = kWriteThreads / 32;
-constexpr int kRotBatch = 2;    // heads in flight per lane
+// heads in flight per lane (with norms one, at two more CTAs per SM: 86 us for 16,384 tokens against 90)
+__host__ __device__ constexpr int rot_batch(bool norm) { return norm ? 1 : 2; }
 constexpr int kCopyBatch = 8;   // 16-byte chunks in flight per lane
 constexpr int kLatentChunks = 512 * 2 / 16;   // 16-byte chunks of a latent (pic_create admits no other width)
 
@@ -67,7 +68,7 @@ __device__ __forceinline__ float sum_squares(uint4 v) {
 }
 
 template <int PAIRING, bool NORM>
-__global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_constant__ WriteParams P) {
+__global__ void __launch_bounds__(kWriteThreads, NORM ? 8 : 6) k_write_tokens(const __grid_constant__ WriteParams P) {
   constexpr bool NEOX = PAIRING == kNeox;
   __shared__ float4 s_freq[kWriteWarps][kMaxFreqs / 2];   // lanes read eight of their own
   __shared__ __align__(8) uint8_t s_axis[kWriteWarps][kMaxFreqs];
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(kWriteThreads, 6) k_write_tokens(const __grid_
       const int h_end = min(P.q_heads + P.kv_heads, (part + 1) * P.rot_iters * hpi);
       const uint8_t* qs = P.q + tok * P.q_stride;
       const uint8_t* ks = P.k + tok * P.k_stride - static_cast<int64_t>(P.q_heads) * P.head_bytes;
+      constexpr int kRotBatch = rot_batch(NORM);
       uint4 a[2][kRotBatch], b[2][kRotBatch];
       auto load = [&](int h0, uint4 (&xa)[kRotBatch], uint4 (&xb)[kRotBatch]) {
 #pragma unroll
