@@ -947,14 +947,13 @@ __device__ __forceinline__ void join_output(const PagedParams& P, const Records&
         mine = y.y == 0.0f ? 0.0f : ex2(y.x - M);
       }
       const int n = min(32, P.rows.n_extra - k0);
-#pragma unroll 4
+#pragma unroll (V > 4 ? 4 : 8)
       for (int k = ALL ? warp : 0; k < n; k += ALL ? kFinishWarps : 1) {
         const float e = __shfl_sync(kFull, mine, k);
-        if (e == 0.0f) continue;
         const float* a = P.rows.extra_acc + ((k0 + k) * pitch + task) * D + lane * V;
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
-          const float2 z = __ldcg(reinterpret_cast<const float2*>(a + i));
+          const float2 z = e != 0.0f ? __ldcg(reinterpret_cast<const float2*>(a + i)) : make_float2(0.0f, 0.0f);
           acc[i] += e * z.x;
           acc[i + 1] += e * z.y;
         }

@@ -339,6 +339,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
   const int my_token = w.token0 + (has_row ? my_row / P.group : 0);
   const int my_head = hk * P.group + (has_row ? my_row % P.group : 0);
   const int my_slot = has_row ? row_slot(P, my_token, hk == 0 && split == 0) : -1;
+  if (warp >= C::kSoftmax0 && my_tile < tiles) {
+    // The queries of the warp's rows (16 of a quadrant's 32 each), as rows of 128 swizzled bytes, one 64-dim
+    // plane after the other; asked for once the slots are known, which the first copies of K wait for.  Lanes share rows here and where results leave (a row a
+    // lane is 32 lines an instruction: it took 6,000 cycles).
+    constexpr int CH = D / 8, RW = 32 / CH;   // chunks of a row, rows of an instruction
+    const int64_t mine = has_row ? my_token * P.q_stride + static_cast<int64_t>(my_head) * D * 2 : -1;
+    const int c = lane % CH, sub = lane / CH;
+    const uint32_t to = base_u32 + my_tile * C::kQTile + (c >> 3) * (kTileRows * 128);
+#pragma unroll 8
+    for (int r0 = 16 * my_half; r0 < 16 * my_half + 16; r0 += RW) {
+      const int64_t from = __shfl_sync(kFull, mine, r0 + sub);
+      const int r = 32 * (warp & 3) + r0 + sub;
+      cp_async16_zfill(to + r * 128 + (((c & 7) ^ (r & 7)) << 4), P.q + (from >= 0 ? from : 0) + c * 16, from >= 0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   const int my_lo = P.window > 0 ? max(0, my_slot + 1 - P.window) : 0;   // its window's first
   {
     const int lo = __reduce_min_sync(kFull, my_slot >= 0 ? my_slot : INT32_MAX), hi = __reduce_max_sync(kFull, my_slot);
@@ -551,30 +567,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
   } else if (warp >= C::kSoftmax0 && my_tile < tiles) {
     // ---------------------------------------------------------------- softmax
     const int q = my_tile;
-    const int64_t at = has_row ? static_cast<int64_t>(my_token) * P.q_heads + my_head : -1;   // row of the outputs
-    // The queries of the warp's rows, as rows of 128 swizzled bytes, one 64-dim plane after the other.  Lanes
-    // share rows here and where results leave (a row a lane is 32 lines an instruction: it
-    // took 6,000 cycles).
+    const int at = has_row ? my_token * P.q_heads + my_head : -1;   // row of the outputs, below 2^30
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (n > 0) {
-      constexpr int CH = D / 8, RW = 32 / CH > 0 ? 32 / CH : 1;   // chunks of a row, rows of an instruction
-      const int64_t mine = has_row ? my_token * P.q_stride + static_cast<int64_t>(my_head) * D * 2 : -1;
-      const int c = lane % CH, sub = CH < 32 ? lane / CH : 0;
-      const uint32_t to = base_u32 + q * C::kQTile + (c >> 3) * (kTileRows * 128);
-#pragma unroll 8
-      for (int r0 = 16 * my_half; r0 < 16 * my_half + 16; r0 += RW) {
-        const int64_t from = __shfl_sync(kFull, mine, r0 + sub);
-        const int r = 32 * (warp & 3) + r0 + sub;
-        cp_async16_zfill(to + r * 128 + (((c & 7) ^ (r & 7)) << 4), P.q + (from >= 0 ? from : 0) + c * 16, from >= 0);
-      }
-      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
       if (P.sign <= 0) {   // queries of a negative scale enter negated, of scale 0 as zeros
-        for (int r0 = 16 * my_half; r0 < 16 * my_half + 16; r0 += RW) {
-          const int r = 32 * (warp & 3) + r0 + sub;
-          uint4* x = reinterpret_cast<uint4*>(smem + q * C::kQTile + (c >> 3) * (kTileRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-          uint4 v = *x;
+        __syncwarp();
+        for (int r0 = 16 * my_half; r0 < 16 * my_half + 16; ++r0) {
+          const int r = 32 * (warp & 3) + r0;
+          for (int c = lane; c < D / 8; c += 32) {
+            uint4* x = reinterpret_cast<uint4*>(smem + q * C::kQTile + (c >> 3) * (kTileRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            uint4 v = *x;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) word(v, e) = P.sign < 0 ? word(v, e) ^ 0x80008000u : 0u;
-          *x = v;
+            for (int e = 0; e < 4; ++e) word(v, e) = P.sign < 0 ? word(v, e) ^ 0x80008000u : 0u;
+            *x = v;
+          }
         }
       }
       fence_proxy_async_smem();
@@ -634,8 +640,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
           }
         }
       }
-      ok = __all_sync(kFull, wait_or_abort(&s_full[buf], parity, abort_flag, kMaxSpins));
-      // (a wait that ran out in one warp of a pair ends both: they meet below)
+      ok = __all_sync(kFull, ok && wait_or_abort(&s_full[buf], parity, abort_flag, kMaxSpins));
+      // (a wait that ran out in one warp of a pair ends both, where they meet)
       tc_fence_after();
       const uint32_t s_at = tl + buf * BN + my_half * HN;
       float s[HN];
@@ -709,7 +715,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[buf]);
       l_run += sum.x + sum.y;
-      if (!ok) break;
       t0 = S.next_slot(t0, j_begin + i + 1, BN);
     }
     if (!ok && lane == 0) fail();
@@ -738,45 +743,54 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
       uint8_t* out = direct ? static_cast<uint8_t*>(P.out)
                             : reinterpret_cast<uint8_t*>(P.rec_acc + static_cast<int64_t>(split) * P.n_tokens * P.q_heads * D);
       const int64_t pitch = D * (direct ? 2 : 4);
-      const int64_t mine = direct || l_run != 0.0f ? at : -1;   // nothing is kept beside a sum of 0
+      const int mine = direct || l_run != 0.0f ? at : -1;   // nothing is kept beside a sum of 0
       const int width = direct ? 64 : 32, halves = D == 64 ? 1 : 2;
-#pragma unroll 1
-      for (int c = my_half < halves ? my_half * width : D; c < D; c += halves * width) {
-        float o[32];
-#pragma unroll 1
-        for (int h = 0; h < (direct ? 2 : 1); ++h) {
-          if (n > 0) {
-            tmem_ld32(o_at + c + 32 * h, o);
-            tmem_wait_ld();
-          }
-          if (l_run == 0.0f) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = 0.0f;
-          }
-          if (direct) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint4 y;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) word(y, e) = bf_pack(o[8 * x + 2 * e] * inv, o[8 * x + 2 * e + 1] * inv);
-              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * h + x) ^ (lane & 7)) << 4)) = y;
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              *reinterpret_cast<float4*>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) =
-                  make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-          }
-        }
+      const auto send = [&](int c) {
         __syncwarp();
+        uint4 y[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int r = 4 * k + (lane >> 3);
-          const int64_t row = __shfl_sync(kFull, mine, r);
-          const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-          if (row >= 0) *reinterpret_cast<uint4*>(out + row * pitch + c * (direct ? 2 : 4) + (lane & 7) * 16) = y;
+          y[k] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = __shfl_sync(kFull, mine, 4 * k + (lane >> 3));
+          if (row >= 0) *reinterpret_cast<uint4*>(out + row * pitch + c * (direct ? 2 : 4) + (lane & 7) * 16) = y[k];
         }
         __syncwarp();
+      };
+#pragma unroll 1
+      for (int c = my_half < halves ? my_half * width : D; c < D; c += halves * width) {
+        float o[32];
+        if (direct) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (n > 0) {
+              tmem_ld32(o_at + c + 32 * h, o);
+              tmem_wait_ld();
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint4 y = make_uint4(0, 0, 0, 0);
+              if (l_run != 0.0f) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) word(y, e) = pack2(o[8 * x + 2 * e] * inv, o[8 * x + 2 * e + 1] * inv);
+              }
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * h + x) ^ (lane & 7)) << 4)) = y;
+            }
+          }
+        } else {
+          if (n > 0) {
+            tmem_ld32(o_at + c, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<float4*>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) =
+                make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        }
+        send(c);
       }
       if (has_row && my_half == 0) {
         if (!direct) P.rec_ml[static_cast<int64_t>(split) * P.n_tokens * P.q_heads + at] = make_float2(l_run == 0.0f ? -FLT_MAX : m_run, l_run);
