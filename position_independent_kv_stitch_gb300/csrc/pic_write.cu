@@ -16,12 +16,14 @@
 // With norms (pic_write_normed_tokens) a head x is first replaced by
 // x / sqrt(mean(x^2) + eps) * w.  The lanes that turn a head hold all of it, so the sum of
 // its squares is joined by 2 to 4 shuffles between its load and its rotation, all
-// in fp32, and a value is rounded once.  The weights lie in shared memory as fp32:
-// in registers they would be 32 more, for q and k.  The latent of an MLA row is
-// normalised by a warp of its own, two chunks a lane.
+// in fp32, and a value is rounded once.  The weights lie in shared memory as fp32, in the
+// order in which lanes read them: in registers they would be 32 more, for q and k.  The
+// latent of an MLA row is normalised by a warp of its own, two chunks a lane.
 // Measured (GB300, 32 + 8 heads of 128 dims): 16,384 tokens of three axes 61.0 us,
 // 403 MB at 6.6 TB/s; 64 tokens 2.9 us; one token 2.7 us.  MLA, 16 query heads,
-// 2,048 tokens: 16.0 us, 5.0 TB/s.
+// 2,048 tokens: 16.0 us, 5.0 TB/s.  With norms: 16,384 tokens of one axis 78 us (5.2 TB/s),
+// where shuffles, weights and the products with them keep the loads apart; one token 4.9 us;
+// MLA, 2,048 tokens: 16.7 us.
 #include "pic_decode.h"
 #include "pic_device.cuh"
 #include "pic_paged.cuh"
@@ -33,12 +35,10 @@ using namespace dev;
 
 constexpr int kWriteThreads = 128;
 constexpr int kWriteWarps = kWriteThreads / 32;
-// heads in flight per lane (with norms one, at two more CTAs per SM: 86 us for 16,384 tokens against 90)
+// heads in flight per lane; with norms one and the next, at two more CTAs per SM (16,384 tokens: 78 us, six CTAs 82)
 __host__ __device__ constexpr int rot_batch(bool norm) { return norm ? 1 : 2; }
 constexpr int kCopyBatch = 8;   // 16-byte chunks in flight per lane
 constexpr int kLatentChunks = 512 * 2 / 16;   // 16-byte chunks of a latent (pic_create admits no other width)
-
-constexpr int kNormDims = 256;   // of the widest head that is normalised whole
 
 // Eight weights of a norm, from element 8 i on, as they multiply.
 __device__ __forceinline__ void norm_weights(const WriteParams& P, const uint8_t* w, int i, float* out) {
@@ -57,14 +57,42 @@ __device__ __forceinline__ void norm_weights(const WriteParams& P, const uint8_t
 #pragma unroll
   for (int x = 0; x < 8; ++x) out[x] += P.norm_offset;
 }
-__device__ __forceinline__ float sum_squares(uint4 v) {
-  float s = 0.0f;
+// Packed fp32 arithmetic, written out.
+__device__ __forceinline__ uint64_t pair64(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+// a pair of fp32 values as bf16
+__device__ __forceinline__ uint32_t pack64(uint64_t v) {
+  const float2 f = unpair(v);
+  return bf_pack(f.x, f.y);
+}
+__device__ __forceinline__ float sum_squares(uint4 v, uint4 w) {
+  uint64_t s = 0, t = 0;
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
-    const float2 y = bf_pair(word(v, x));
-    s = __fmaf_rn(y.x, y.x, __fmaf_rn(y.y, y.y, s));
+    const uint64_t y = pair64(bf_lo(word(v, x)), bf_hi(word(v, x))), z = pair64(bf_lo(word(w, x)), bf_hi(word(w, x)));
+    s = fma2(y, y, s);
+    t = fma2(z, z, t);
   }
-  return s;
+  const float2 a = unpair(s), b = unpair(t);
+  return (a.x + a.y) + (b.x + b.y);
 }
 
 template <int PAIRING, bool NORM>
@@ -73,7 +101,8 @@ __global__ void __launch_bounds__(kWriteThreads, NORM ? 8 : 6) k_write_tokens(co
   __shared__ float4 s_freq[kWriteWarps][kMaxFreqs / 2];   // lanes read eight of their own
   __shared__ __align__(8) uint8_t s_axis[kWriteWarps][kMaxFreqs];
   const int lane = threadIdx.x & 31;
-  __shared__ __align__(16) float s_norm[NORM ? kWriteWarps : 1][NORM ? 2 : 1][NORM ? kNormDims : 4];   // weights of q and k
+  // weights of q and k as lanes read them: parts 0, 1 the first chunk of a lane, 2, 3 the second (16 lanes at most)
+  __shared__ float4 s_norm[NORM ? kWriteWarps : 1][NORM ? 2 : 1][4][NORM ? 16 : 1];
   const int tasks = P.rot_parts + P.copy_parts + (NORM ? P.latent_norm : 0);
   const int64_t task = static_cast<int64_t>(blockIdx.x) * kWriteWarps + (threadIdx.x >> 5);
   const int row_bytes = P.kv_heads * P.head_bytes;
@@ -133,13 +162,17 @@ __global__ void __launch_bounds__(kWriteThreads, NORM ? 8 : 6) k_write_tokens(co
         put_freq(freq, i, P.freq.turns[i]);
         axis[i] = P.axis[i];
       }
-      float(*norm)[NORM ? kNormDims : 4] = s_norm[NORM ? threadIdx.x >> 5 : 0];
+      float4(*norm)[4][NORM ? 16 : 1] = s_norm[NORM ? threadIdx.x >> 5 : 0];
       if constexpr (NORM) {
         // (MLA: heads as they are, its latent has a warp of its own)
-        for (int i = lane; i < 4 * lph && P.latent_norm == 0; i += 32) {
+        for (int i = lane; i < 4 * lph; i += 32) {
           const int kind = i / (2 * lph), chunk = i - kind * 2 * lph;
-          const uint8_t* w = kind == 0 ? P.q_norm : P.k_norm;
-          if (w != nullptr) norm_weights(P, w, chunk, &norm[kind][8 * chunk]);
+          const uint8_t* w = P.latent_norm != 0 ? nullptr : (kind == 0 ? P.q_norm : P.k_norm);
+          float x[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+          if (w != nullptr) norm_weights(P, w, chunk, x);
+          const int at = NEOX ? chunk & (lph - 1) : chunk >> 1, part = NEOX ? 2 * (chunk >> P.lph_shift) : 2 * (chunk & 1);
+          norm[kind][part][at] = make_float4(x[0], x[1], x[2], x[3]);
+          norm[kind][part + 1][at] = make_float4(x[4], x[5], x[6], x[7]);
         }
       }
       __syncwarp();
@@ -160,46 +193,56 @@ __global__ void __launch_bounds__(kWriteThreads, NORM ? 8 : 6) k_write_tokens(co
       for (int i = 0; i < 4; ++i) turn_cossin2(make_float2(position(2 * i), position(2 * i + 1)), freq[4 * j + i], c + 2 * i, s + 2 * i);
       uint8_t* qd = P.q_out + tok * P.q_out_stride;
       uint8_t* kd = P.k_cache + row * row_bytes - static_cast<int64_t>(P.q_heads) * P.head_bytes;
+      if constexpr (NORM) {
+        // one head at a time, the next one on its way; two elements at a time; heads that have no norm as with weights
+        // and factor 1 (one path: the second was in the way of the first's instructions)
+        const float inv_dims = 1.0f / (16 * lph);
+        // (all lanes leave the loop together: they meet in shuffles)
+#pragma unroll 1
+        for (int h = h_begin; h - sub < h_end; h += hpi) {
+          load(h + hpi, a[1], b[1]);
+          const int kind = h < P.q_heads ? 0 : 1;
+          float sum = h < h_end ? sum_squares(a[0][0], b[0][0]) : 0.0f;
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1)
+            if (o < lph) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (h < h_end && (kind == 0 || row >= 0)) {
+            const bool normed = P.latent_norm == 0 && (kind == 0 ? P.q_norm : P.k_norm) != nullptr;
+            const float r = normed ? rsqrtf(sum * inv_dims + P.norm_eps) : 1.0f;
+            const uint64_t rr = pair64(r, r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 fa = norm[kind][e >> 1][j], fb = norm[kind][2 + (e >> 1)][j];
+              const uint32_t va = word(a[0][0], e), vb = word(b[0][0], e);
+              const uint64_t xa = mul2(mul2(pair64(bf_lo(va), bf_hi(va)), rr), (e & 1) ? pair64(fa.z, fa.w) : pair64(fa.x, fa.y));
+              const uint64_t xb = mul2(mul2(pair64(bf_lo(vb), bf_hi(vb)), rr), (e & 1) ? pair64(fb.z, fb.w) : pair64(fb.x, fb.y));
+              if (NEOX) {   // pairs (a, b) of frequencies 2 e and 2 e + 1
+                const uint64_t cc = pair64(c[2 * e], c[2 * e + 1]), ss = pair64(s[2 * e], s[2 * e + 1]);
+                word(a[0][0], e) = pack64(fma2(xa, cc, mul2(xb, ss ^ 0x8000000080000000ull)));
+                word(b[0][0], e) = pack64(fma2(xa, ss, mul2(xb, cc)));
+              } else {      // pairs within a word: of frequency e, and 4 + e
+                const float2 ya = unpair(xa), yb = unpair(xb);
+                word(a[0][0], e) = bf_pack(ya.x * c[e] - ya.y * s[e], ya.x * s[e] + ya.y * c[e]);
+                word(b[0][0], e) = bf_pack(yb.x * c[4 + e] - yb.y * s[4 + e], yb.x * s[4 + e] + yb.y * c[4 + e]);
+              }
+            }
+            uint8_t* dst = (kind == 0 ? qd : kd) + static_cast<int64_t>(h) * P.head_bytes;
+            *reinterpret_cast<uint4*>(dst + off_a) = a[0][0];
+            *reinterpret_cast<uint4*>(dst + off_b) = b[0][0];
+          }
+          a[0][0] = a[1][0];
+          b[0][0] = b[1][0];
+        }
+        return;
+      }
       const int step = kRotBatch * hpi;
-      // (with norms all lanes leave the loop together: they meet in shuffles)
-      for (int h0 = h_begin; (NORM ? h0 - sub : h0) < h_end; h0 += 2 * step) {
+      for (int h0 = h_begin; h0 < h_end; h0 += 2 * step) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           load(h0 + (x + 1) * step, a[x ^ 1], b[x ^ 1]);
 #pragma unroll
           for (int u = 0; u < kRotBatch; ++u) {
             const int h = h0 + x * step + u * hpi;
-            if constexpr (NORM) {
-              // (every lane takes part in the shuffles; a head past the end is not stored)
-              const int kind = h < P.q_heads ? 0 : 1;
-              const bool normed = P.latent_norm == 0 && (kind == 0 ? P.q_norm : P.k_norm) != nullptr;
-              float sum = h < h_end ? sum_squares(a[x][u]) + sum_squares(b[x][u]) : 0.0f;
-              for (int o = 1; o < lph; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-              if (h >= h_end || (h >= P.q_heads && row < 0)) continue;
-              if (normed) {
-                const float r = rsqrtf(sum / static_cast<float>(16 * lph) + P.norm_eps);
-                const float* wa = &norm[kind][8 * (NEOX ? j : 2 * j)];
-                const float* wb = &norm[kind][8 * (NEOX ? j + lph : 2 * j + 1)];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float2 ya = bf_pair(word(a[x][u], e)), yb = bf_pair(word(b[x][u], e));
-                  const float a0 = ya.x * r * wa[2 * e], a1 = ya.y * r * wa[2 * e + 1];
-                  const float b0 = yb.x * r * wb[2 * e], b1 = yb.y * r * wb[2 * e + 1];
-                  if (NEOX) {   // pairs (a, b) of frequencies 2 e and 2 e + 1
-                    const float c0 = c[2 * e], c1 = c[2 * e + 1], s0 = s[2 * e], s1 = s[2 * e + 1];
-                    word(a[x][u], e) = bf_pack(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
-                    word(b[x][u], e) = bf_pack(a0 * s0 + b0 * c0, a1 * s1 + b1 * c1);
-                  } else {      // pairs (a0, a1) of frequency e, (b0, b1) of 4 + e
-                    word(a[x][u], e) = bf_pack(a0 * c[e] - a1 * s[e], a0 * s[e] + a1 * c[e]);
-                    word(b[x][u], e) = bf_pack(b0 * c[4 + e] - b1 * s[4 + e], b0 * s[4 + e] + b1 * c[4 + e]);
-                  }
-                }
-                uint8_t* dst = (h < P.q_heads ? qd : kd) + static_cast<int64_t>(h) * P.head_bytes;
-                *reinterpret_cast<uint4*>(dst + off_a) = a[x][u];
-                *reinterpret_cast<uint4*>(dst + off_b) = b[x][u];
-                continue;
-              }
-            }
             if (h >= h_end || (h >= P.q_heads && row < 0)) continue;
             if (NEOX) {
               rotate_neox(a[x][u], b[x][u], c, s);
@@ -227,7 +270,7 @@ __global__ void __launch_bounds__(kWriteThreads, NORM ? 8 : 6) k_write_tokens(co
         float w[2][8];
         norm_weights(P, P.k_norm, lane, w[0]);
         norm_weights(P, P.k_norm, lane + 32, w[1]);
-        float sum = sum_squares(v[0]) + sum_squares(v[1]);
+        float sum = sum_squares(v[0], v[1]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float r = rsqrtf(sum * (1.0f / (8 * kLatentChunks)) + P.norm_eps);
