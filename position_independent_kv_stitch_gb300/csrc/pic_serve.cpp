@@ -257,7 +257,7 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
   // request by its own count, which is on the device: both kernels are
   // launched and each leaves the other's alone.  One suffices where there are no more tokens than
   // requests, or one request.
-  const bool tiles = n_tokens > n_req;
+  const bool tiles = n_tokens > n_req && c.num_cache_blocks > 0;   // (of a cache without blocks there is no tensor map)
   if (tiles) {
     TileParams t{};
     TileMaps maps;

@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __gri
         const int end = part == 0 ? min(S.hi + 1, t + (jb - ja) * BN) : min(S.n_first, t + (jb - ja) * BN);
         const int b0 = block_of(P.paged, t), b1 = end > t ? block_of(P.paged, end - 1) : b0 - 1;
         for (int b = b0 + x0; b <= b1; b += stride) {
-          if (!S.some(b * bs, b * bs + bs)) continue;
+          if (!S.some(b * bs, b * bs + min(bs, S.hi + 1 - b * bs))) continue;   // (b * bs <= hi: no overflow)
           const int32_t block = __ldg(table + b);
           if (block < 0 || block >= P.paged.num_cache_blocks) {
             raise_block(P.status, w.table, b * bs);

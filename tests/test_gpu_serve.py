@@ -402,6 +402,23 @@ def test_attend_tokens_bad_offsets(indptr, n):
     c.close()
 
 
+@pytest.mark.parametrize("tokens", [1, 9])
+def test_attention_over_a_cache_without_blocks(tokens):
+    """No slot exists: every row but padding raises and sees nothing; an empty prefix and empty requests are fine."""
+    ctx = pic.pic_create(pic.PIC_KIND_GQA, 1, 2, 64, 64, 0, pic.PIC_PAIRING_NEOX_HALF, 16, 1e4, 0)
+    cache, q = torch.zeros(1, 16, 2, 64, dtype=torch.bfloat16, device=DEV), torch.ones(tokens, 4, 64, dtype=torch.bfloat16, device=DEV)
+    tables, out = _i32(np.zeros((1, 3))), torch.full_like(q, 7.0)
+    ws = _ws(max(pic.pic_attend_tokens_workspace_bytes(ctx, tokens, 1, 4), pic.pic_attend_shared_workspace_bytes(ctx, 1, 4)))
+    pic.pic_attend_tokens(ctx, q, 0.1, cache, cache, tables, _i32([0, tokens]), _i32(np.arange(tokens) - 1), out, workspace=ws)
+    want = 0 if tokens == 1 else pic.PIC_DEV_BAD_LENGTH
+    assert pic.pic_query_device_status(ctx, ws, raise_on_device_error=False) == want and bool((out == 0).all())
+    ws.zero_()
+    out.fill_(7.0)
+    pic.pic_attend_shared(ctx, q[:1], 0.1, cache, cache, tables[0], _i32([0]), tables, _i32([0]), 0, out[:1], workspace=ws)
+    assert pic.pic_query_device_status(ctx, ws) == 0 and bool((out[:1] == 0).all())
+    pic.pic_destroy(ctx)
+
+
 def test_attend_tokens_forms():
     """Query rows apart, a negative and a zero scale, another layer, no lse, dense caches of many layers."""
     c = Cache(heads=2, layers=3, lens=[200, 33], seed=4)
@@ -417,6 +434,44 @@ def test_attend_tokens_forms():
                           workspace=ws)
     assert torch.equal(out, again)
     c.close()
+
+
+def test_offsets_beyond_32_bits():
+    """Layers of 6.6 GB, blocks at both ends; query rows 5 MB apart; maps, writes and both attentions."""
+    nb, bs, heads, d, hq = 201_000, 16, 8, 128, 16
+    ctx = pic.pic_create(pic.PIC_KIND_GQA, 1, heads, d, d, 0, pic.PIC_PAIRING_NEOX_HALF, bs, 5e5, nb)
+    k_cache, v_cache = (torch.zeros(nb, bs, heads, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    g = torch.Generator(device=DEV).manual_seed(3)
+    free = np.arange(nb)
+    free[-20:] = [200_999, 0, 131_072, 131_071, 65_536, 200_998, 1, 196_608, 2, 131_073] + list(range(200_900, 200_910))
+    tables, lens, n_free = _i32(np.full((2, 10), -1)), _i32([0, 0]), _i32([nb])
+    n, pitch = 150, 5 * (1 << 20) // 256
+    indptr, req, slot, pos = _i32([0] * 3), _i32([0] * n), _i32([0] * n), _i32([0] * n)
+    ws = _ws(max(pic.pic_attend_tokens_workspace_bytes(ctx, n, 2, hq), pic.pic_attend_shared_workspace_bytes(ctx, 2, hq)))
+    pic.pic_map_tokens(ctx, lens, _i32([100, 50]), tables, _i32(free), n_free, lens, n_free, indptr, req, slot, positions=pos, workspace=ws)
+    host = tables.cpu().numpy()
+    assert host[0, :7].tolist() == free[-1:-8:-1].tolist()
+    wide = torch.zeros(n, pitch, d, dtype=torch.bfloat16, device=DEV)
+    wide[:, :hq + 2 * heads] = torch.randn((n, hq + 2 * heads, d), generator=g, device=DEV).to(torch.bfloat16)
+    q, k, v = wide[:, :hq], wide[:, hq:hq + heads], wide[:, hq + heads:hq + 2 * heads]
+    w = torch.ones(d, device=DEV)
+    pic.pic_write_normed_tokens(ctx, pos, k, v, req, slot, tables, k_cache, v_cache, q_norm=w, k_norm=w, q=q, q_out=q, workspace=ws)
+    out, lse = torch.empty(n, hq, d, dtype=torch.bfloat16, device=DEV), torch.empty(n, hq, device=DEV)
+    pic.pic_attend_tokens(ctx, q, d ** -0.5, k_cache, v_cache, tables, indptr, slot, out, lse=lse, workspace=ws)
+    for r, (a, b) in enumerate(((0, 100), (100, 150))):
+        assert torch.equal(v_cache[tables[r].long()[torch.arange(b - a, device=DEV) // bs], torch.arange(b - a, device=DEV) % bs], v[a:b])
+        rows = [_wide_rows(x, host[r], np.arange(b - a), bs) for x in (k_cache, v_cache)]
+        seen = torch.tril(torch.ones(b - a, b - a, dtype=torch.bool, device=DEV))
+        _assert_rows(q[a:b], *rows, seen, d ** -0.5, out[a:b], lse[a:b], r)
+    dec, dec_lse = torch.empty(2, hq, d, dtype=torch.bfloat16, device=DEV), torch.empty(2, hq, device=DEV)
+    pic.pic_attend_shared(ctx, q[:2], d ** -0.5, k_cache, v_cache, tables[0, :4], _i32([60]), tables, _i32([100, 60]), 160, dec, lse=dec_lse,
+                          workspace=ws)
+    rows = [_wide_rows(x, host[0], np.arange(100), bs) for x in (k_cache, v_cache)]
+    for r, m in enumerate((100, 60)):
+        _assert_rows(q[r:r + 1], *(x[:, :m] for x in rows), torch.ones(1, m, dtype=torch.bool, device=DEV), d ** -0.5, dec[r:r + 1],
+                     dec_lse[r:r + 1], r)
+    assert pic.pic_query_device_status(ctx, ws) == 0
+    pic.pic_destroy(ctx)
 
 
 def test_attend_tokens_extreme_scores():
