@@ -794,7 +794,7 @@ pic_status pic_evict_tokens(pic_ctx* ctx, int32_t num_layers, void* k_cache, voi
  * PIC_DEV_BAD_LENGTH; the request is refused.  So does *d_n_free outside [0,
  * num_cache_blocks], which counts as 0.  A block outside the cache is moved like any
  * other and raises PIC_DEV_BAD_BLOCK.
- *   n_req, max_blocks  rows and columns of d_block_tables.
+ *   n_req, max_blocks  rows (2^30 at most) and columns of d_block_tables.
  *   d_block_tables     int32 [n_req][max_blocks], new blocks are filled in.
  *   d_free_blocks      int32 [num_cache_blocks].
  *   d_n_free           int32 [1]; d_new_n_free: after the call, may be d_n_free.
@@ -856,7 +856,7 @@ pic_status pic_map_tokens(pic_ctx* ctx, const pic_token_map* map, void* d_worksp
  *   out       bf16 [n_tokens][num_q_heads][head_dim], dense; must not overlap q.
  *   lse       float [n_tokens][num_q_heads] or NULL.
  *   softmax_scale  finite.
- * Results do not depend on timing.  PIC_ERR_UNSUPPORTED for MLA models.
+ * Results do not depend on timing.  At most 2^30 requests.  PIC_ERR_UNSUPPORTED for MLA models.
  */
 size_t pic_attend_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_tokens, int32_t n_req, int32_t num_q_heads);
 pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_tokens, int32_t num_q_heads,

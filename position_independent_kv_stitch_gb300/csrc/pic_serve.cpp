@@ -41,6 +41,9 @@ PagedParams rows_params(const CtxView& c, const void* q, int64_t q_stride, int32
   return p;
 }
 
+// Requests of a call, at most: the kernels count to one past them, some in steps of 1,024, in 32 bits.
+constexpr int32_t kMaxRequests = 1 << 30;
+
 // ---- tiles of rows (pic_tile.cu)
 
 // Bytes of a shared prefix, counted for every request, up to which it is read row by row: 8 requests over
@@ -154,12 +157,15 @@ size_t shared_bytes(const CtxView& c, int64_t n_req, int32_t num_q_heads) {
 
 extern "C" {
 
-size_t pic_map_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_req) { return ctx && n_req >= 0 ? sizeof(WsHeader) : 0; }
+size_t pic_map_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_req) {
+  return ctx && n_req >= 0 && n_req <= kMaxRequests ? sizeof(WsHeader) : 0;
+}
 
 pic_status pic_map_tokens(pic_ctx* ctx, const pic_token_map* t, void* d_ws, size_t ws_bytes, pic_stream_t stream) {
   if (!ctx || !t) return fail(ctx, PIC_ERR_INVALID_ARG, "null ctx or map");
   const CtxView c = ctx_view(ctx);
   if (t->n_req < 0 || t->max_blocks < 0 || t->n_tokens < 0) return fail(ctx, PIC_ERR_INVALID_ARG, "negative size");
+  if (t->n_req > kMaxRequests) return fail(ctx, PIC_ERR_RANGE, "more than 2^30 requests");
   const bool some = t->n_req > 0;
   if (!t->d_n_free || !t->d_new_n_free || !t->d_indptr || (c.num_cache_blocks > 0 && !t->d_free_blocks) ||
       (some && (!t->d_seq_lens || !t->d_grow || !t->d_new_lens || (!t->d_block_tables && t->max_blocks > 0))) ||
@@ -212,7 +218,7 @@ pic_status pic_map_tokens(pic_ctx* ctx, const pic_token_map* t, void* d_ws, size
 }
 
 size_t pic_attend_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_tokens, int32_t n_req, int32_t num_q_heads) {
-  if (!ctx || n_tokens < 0 || n_req < 0) return 0;
+  if (!ctx || n_tokens < 0 || n_req < 0 || n_req > kMaxRequests) return 0;
   const CtxView c = ctx_view(ctx);
   if (c.model->kind != PIC_KIND_GQA || !paged_heads_ok(c, num_q_heads) || !paged_size_ok(n_tokens, num_q_heads)) return 0;
   return tokens_bytes(c, n_tokens, n_req, num_q_heads);
@@ -226,6 +232,7 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
   const CtxView c = ctx_view(ctx);
   if (n_tokens < 0 || n_req < 0 || max_blocks < 0) return fail(ctx, PIC_ERR_INVALID_ARG, "negative size");
   if (window < 0 || n_first < 0) return fail(ctx, PIC_ERR_INVALID_ARG, "window and n_first must not be negative");
+  if (n_req > kMaxRequests) return fail(ctx, PIC_ERR_RANGE, "more than 2^30 requests");
   const pic_status ok = check_rows(ctx, c, q, q_stride, n_tokens, num_q_heads, softmax_scale, k_cache, v_cache, out, lse, d_ws);
   if (ok != PIC_OK) return ok;
   const bool some = n_tokens > 0 && n_req > 0;
@@ -345,7 +352,7 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
   const int used = std::min(sms, kPagedMaxSms);
   cudaError_t e = cudaSuccess;
   // A short prefix is read row by row like the rest: a launch less, and its repeated reads come from L2.
-  const int64_t prefix_reads = static_cast<int64_t>(n_req) * p.rows.max_prefix * p.row_bytes * 2;
+  const double prefix_reads = 2.0 * n_req * p.rows.max_prefix * p.row_bytes;   // (may pass 64 bits)
   if (prefix_reads > kSharedPrefixReads) {
     // the prefix in tiles of all requests' rows, whose records the join adds to those of the rest
     TileParams t{};

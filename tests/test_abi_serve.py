@@ -154,3 +154,13 @@ def test_attention_of_nothing_and_of_latent_rows(gqa, mla):
         assert pic.pic_attend_tokens_workspace_bytes(gqa, n, 2, hq) == 0
     assert pic.pic_attend_tokens_workspace_bytes(gqa, 4, -1, 4) == 0
     assert 256 < pic.pic_attend_tokens_workspace_bytes(gqa, 4, 2, 4) < 1 << 30
+
+
+def test_more_requests_than_the_kernels_count(gqa):
+    most = 1 << 30
+    assert _map(gqa, n_req=most + 1) == RANGE and _attend(gqa, n_req=most + 1) == RANGE
+    assert _map(gqa, n_req=2 ** 31 - 1) == RANGE and _attend(gqa, n_req=2 ** 31 - 1) == RANGE
+    assert pic.pic_map_tokens_workspace_bytes(gqa, most + 1) == 0
+    assert pic.pic_attend_tokens_workspace_bytes(gqa, 4, most + 1, 4) == 0
+    assert pic.pic_map_tokens_workspace_bytes(gqa, most) == pic.PIC_STATUS_BYTES
+    assert pic.pic_attend_tokens_workspace_bytes(gqa, 4, most, 4) > 256
