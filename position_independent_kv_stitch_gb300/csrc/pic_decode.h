@@ -198,7 +198,7 @@ cudaError_t launch_paged_rows(const PagedParams& p, int head_dim, int sm_count, 
 
 // ---- attention of tiles of query rows (pic_tile.cu)
 constexpr int kTileRows = 128;          // rows of a product: (token, query head of the KV head) pairs
-__host__ __device__ constexpr int tile_groups(int head_dim) { return head_dim <= 128 ? 2 : 1; }   // tiles of a CTA
+__host__ __device__ constexpr int most_tiles(int head_dim) { return head_dim <= 128 ? 2 : 1; }    // tiles of a CTA
 __host__ __device__ constexpr int tile_slots(int head_dim) { return head_dim <= 128 ? 128 : 64; } // slots of a step
 struct TileMaps {
   CUtensorMap k, v;
@@ -222,6 +222,7 @@ struct TileParams {
   int32_t least;             // tokens: requests of fewer tokens are another kernel's
   float scale_log2;          // of |scale| (1 where it is 0)
   int32_t sign;              // of scale: the queries enter as they are, negated, or as 0
+  int32_t tiles;             // of a row block
   int32_t blocks;            // row blocks launched per KV head, at least those there are
   int32_t splits;            // parts of a row block's slots
   int32_t box;               // slots of one copy

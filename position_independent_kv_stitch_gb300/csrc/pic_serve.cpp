@@ -50,19 +50,67 @@ constexpr int32_t kMaxRequests = 1 << 30;
 // 1,000 slots 13 us (tiles 22), over 2,000 (63 MB) 17 (19), over 4,000 (125 MB) 23 (18).
 constexpr int64_t kSharedPrefixReads = int64_t{64} << 20;
 
-// Row blocks per KV head, at most: of n_tokens tokens of n_req requests (each may leave a block half filled).
-int64_t tile_blocks(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
-  const int64_t block = static_cast<int64_t>(kTileRows) * tile_groups(c.model->head_dim);
+// Row blocks of `tiles` tiles per KV head, at most: of n_tokens tokens of n_req requests (each may leave one half filled).
+int64_t tile_blocks(const CtxView& c, int32_t tiles, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
+  const int64_t block = static_cast<int64_t>(kTileRows) * tiles;
   const int64_t rows = n_tokens * (num_q_heads / c.model->num_kv_heads);
   return n_req <= 1 ? (rows + block - 1) / block : rows / block + std::min(n_req, n_tokens);
 }
-// Parts that a row block's slots are dealt to.  As many as there are SMs for, of at least
-// four steps each; and, as blocks differ in length, parts enough for two rounds of the SMs
+// Parts that a row block's slots are dealt to, at most: enough for two rounds of the SMs.
+int64_t most_splits(const CtxView& c, int64_t blocks, int sms) {
+  const int64_t ctas = std::max<int64_t>(1, blocks * c.model->num_kv_heads);
+  return ctas < 2 * sms ? (2 * sms - 1) / ctas + 1 : 1;
+}
+// Parts where several requests' blocks differ in length: as many as there are SMs for, of at least
+// four steps each; and parts enough for two rounds of the SMs
 // where a part keeps 16 steps (recomputed heads of 4 sequences of 16k: 244 us whole, 176 in two parts).
 int32_t tile_splits(const CtxView& c, int64_t blocks, int sms, int64_t max_slots) {
   const int64_t ctas = std::max<int64_t>(1, blocks * c.model->num_kv_heads), step = tile_slots(c.model->head_dim);
-  const int64_t fill = std::min(sms / ctas, max_slots / (4 * step)), even = std::min((2 * sms - 1) / ctas + 1, max_slots / (16 * step));
+  const int64_t fill = std::min(sms / ctas, max_slots / (4 * step)), even = std::min(most_splits(c, blocks, sms), max_slots / (16 * step));
   return static_cast<int32_t>(std::max<int64_t>(1, std::max(fill, ctas < 2 * sms ? even : 0)));
+}
+// Tiles of a row block, and its parts.  Two tiles keep the tensor cores busy, as one's products run during the other's
+// softmax: a step takes them 1.43 us, one tile 0.9.  But one tile starts and ends sooner, and twice as many
+// blocks are there for the SMs before slots have to be split and joined.  So both forms' time is
+// estimated, for blocks of equal length, as
+//   rounds of the SMs x (start and end + steps of a part) + half a part for the last round + the join,
+//   a launch and its records written and read,
+// and the smaller taken.  Measured (8 KV heads of 128 dims, 4 query heads each; two tiles, one): a prompt of 128 tokens 10.0,
+// 7.9 us, of 512 14.5, 10.7, of 4,096 104, 130; 16 tokens behind 16k slots 27.4, 21.8; 608 behind 4k 60, 33;
+// 128 behind 16k 38, 49; 64 requests over a prefix of 8k 38.6, 35.5, of 32k 90, 104.  Parts by the same estimate:
+// 400 tokens behind 64k 368 us in 6, 297 in 5 (the sixth began a third round of the SMs).
+// Of several requests only the whole is known here: one tile must be the better for all rows in one request, and
+// every request's blocks must fit the SMs at once (256 requests may as well be 255 of one token and a prompt).
+struct TileShape {
+  int32_t tiles, splits;
+  double us;
+};
+TileShape tile_shape_of(const CtxView& c, int32_t tiles, int64_t n_tokens, int32_t num_q_heads, int sms, int64_t max_slots) {
+  const double start = tiles == 2 ? 6.5 : 5.0, step_us = tiles == 2 ? 1.43 : 0.9;
+  const double record_us = 8.0 * static_cast<double>(n_tokens) * num_q_heads * c.model->head_dim / 8e6;   // of one part
+  const int64_t step = tile_slots(c.model->head_dim), steps = std::max<int64_t>(1, (max_slots + step - 1) / step);
+  const int64_t blocks = tile_blocks(c, tiles, n_tokens, 1, num_q_heads);
+  const int64_t ctas = std::max<int64_t>(1, blocks * c.model->num_kv_heads);
+  const int64_t most = std::max<int64_t>(1, std::min(most_splits(c, blocks, sms), steps / 4));
+  TileShape best{tiles, 1, 0.0};
+  for (int64_t s = 1; s <= most; ++s) {
+    const int64_t rounds = (ctas * s + sms - 1) / sms;
+    const double part = static_cast<double>((steps + s - 1) / s) * step_us;
+    const double us = static_cast<double>(rounds) * (start + part) + 0.5 * part + (s > 1 ? 4.0 + record_us * static_cast<double>(s) : 0.0);
+    if (s == 1 || us < best.us) best = {tiles, static_cast<int32_t>(s), us};
+  }
+  return best;
+}
+TileShape tile_shape(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads, int sms, int64_t max_slots) {
+  TileShape best = tile_shape_of(c, 1, n_tokens, num_q_heads, sms, max_slots);
+  // (rows of one tile: the same blocks)
+  if (most_tiles(c.model->head_dim) == 2 && n_tokens * (num_q_heads / c.model->num_kv_heads) > kTileRows) {
+    const TileShape two = tile_shape_of(c, 2, n_tokens, num_q_heads, sms, max_slots);
+    const bool at_once = n_req <= 1 || tile_blocks(c, 1, n_tokens, n_req, num_q_heads) * c.model->num_kv_heads <= sms;
+    if (two.us <= best.us || !at_once) best = two;
+  }
+  if (n_req > 1) best.splits = tile_splits(c, tile_blocks(c, best.tiles, n_tokens, n_req, num_q_heads), sms, max_slots);
+  return best;
 }
 // Workspace of a call: the row-by-row kernels' part, then the records of split tiles.
 struct RowsLayout {
@@ -76,9 +124,9 @@ RowsLayout rows_layout(const CtxView& c, int64_t n_tokens, int64_t num_q_heads, 
   L.total = align_up(L.ml + n * sizeof(float2), kWsAlign);
   return L;
 }
-// Parts at most, whatever the device and the slots (workspace sizing).
-int64_t most_splits(const CtxView& c, int64_t blocks) {
-  return tile_splits(c, blocks, kPagedMaxSms, std::numeric_limits<int64_t>::max());
+// Parts at most, whatever the device and the slots (workspace sizing): larger blocks are fewer, in more parts.
+int64_t any_splits(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
+  return most_splits(c, tile_blocks(c, most_tiles(c.model->head_dim), n_tokens, n_req, num_q_heads), kPagedMaxSms);
 }
 
 // One cache tensor as the tiles read it: whole groups of 8 rows, planes of 64 dims
@@ -146,11 +194,11 @@ pic_status check_rows(pic_ctx* ctx, const CtxView& c, const void* q, int64_t q_s
 }
 
 size_t tokens_bytes(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
-  const int64_t splits = n_tokens > n_req ? most_splits(c, tile_blocks(c, n_tokens, n_req, num_q_heads)) : 1;
+  const int64_t splits = n_tokens > n_req ? any_splits(c, n_tokens, n_req, num_q_heads) : 1;
   return rows_layout(c, n_tokens, num_q_heads, splits > 1 ? splits : 0).total;
 }
 size_t shared_bytes(const CtxView& c, int64_t n_req, int32_t num_q_heads) {
-  return rows_layout(c, n_req, num_q_heads, most_splits(c, tile_blocks(c, n_req, 1, num_q_heads))).total;
+  return rows_layout(c, n_req, num_q_heads, any_splits(c, n_req, 1, num_q_heads)).total;
 }
 
 }  // namespace
@@ -277,10 +325,11 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     t.window = window;
     t.n_first = n_first;
     t.least = n_req > 1 ? 2 : 1;
-    const int64_t blocks = tile_blocks(c, n_tokens, n_req, num_q_heads);
-    t.blocks = static_cast<int32_t>(blocks);
     const int64_t slots = window > 0 ? std::min<int64_t>(t.capacity, static_cast<int64_t>(window) + n_first + n_tokens) : t.capacity;
-    t.splits = tile_splits(c, blocks, used, slots);
+    const TileShape shape = tile_shape(c, n_tokens, n_req, num_q_heads, used, slots);
+    t.tiles = shape.tiles;
+    t.splits = shape.splits;
+    t.blocks = static_cast<int32_t>(tile_blocks(c, t.tiles, n_tokens, n_req, num_q_heads));
     t.out = out;
     t.lse = lse;
     if (t.splits > 1) {
@@ -365,11 +414,12 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     t.lens = d_seq_lens;
     t.prefix_len = d_prefix_len;
     t.max_len = max_seq_len;
-    const int64_t blocks = tile_blocks(c, n_req, 1, num_q_heads);
-    t.blocks = static_cast<int32_t>(blocks);
     // an eighth of the SMs is left to the slots behind the prefix, whose kernel starts beside the tiles (64
     // requests over 32k slots in 16 parts, 128 CTAs, 91 us; in 19 parts, on every SM, 104)
-    t.splits = tile_splits(c, blocks, used - used / 8, t.capacity);
+    const TileShape shape = tile_shape(c, n_req, 1, num_q_heads, used - used / 8, t.capacity);
+    t.tiles = shape.tiles;
+    t.splits = shape.splits;
+    t.blocks = static_cast<int32_t>(tile_blocks(c, t.tiles, n_req, 1, num_q_heads));
     const RowsLayout L = rows_layout(c, n_req, num_q_heads, t.splits);
     t.rec_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + L.acc);
     t.rec_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + L.ml);

@@ -7,8 +7,8 @@
 //   out_i = sum_t p_it v_t,  p_i = softmax(s_i),  lse_i = log sum_t exp(s_it).
 //
 // Rows are (token, query head) pairs of one request and KV head, in the order of
-// tokens; a CTA takes 256 of them (two tiles of 128; 128 rows where heads have 256 dims) and
-// walks the slots that some of them see, 128 (64) at a time: from the lowest window's
+// tokens; a CTA takes 256 of them (two tiles of 128) or 128 (one: heads of 256 dims, and
+// calls of few rows, see tile_shape_of in pic_serve.cpp) and walks the slots that some of them see, 128 (64) at a time: from the lowest window's
 // start to the highest slot, then the first n_first.  One pass, with a running maximum and
 // sum.  Where there are too few row blocks for the SMs, a block's slots are
 // dealt to several CTAs, which leave records (O, max, sum) that a later kernel joins.
@@ -25,7 +25,7 @@
 //     maximum when a score passes it by more than 2^8 (O and the sum are then rescaled, which
 //     after the first steps hardly happens), write P = exp2(s - m) as bf16 over S.
 // Two tiles take turns: while one is in its softmax, the tensor cores work on the other's.
-// (256 dims: O alone takes half of TMEM, so one tile, with the next step's S made ahead.)
+// (One tile: the next step's S is made ahead.  At 256 dims O alone takes half of TMEM.)
 //
 // P is rounded to bf16 (2^-8 of each weight, where the output's own rounding is 2^-8 of
 // their sum), unnormalised: between 2^-8 and 2^8 at the maximum.  Sums, maxima and O
@@ -34,7 +34,7 @@
 //
 // Bound by the chain of a step (products, scores read, maximum, exponentials, P seen by the
 // issuing warp), about 2,900 cycles for both tiles where the products alone are 2,060, and by 6 us in which a CTA
-// starts and ends.  256 rows, since two tiles are what registers, TMEM and shared memory hold and one would leave the
+// starts and ends (one tile 5).  256 rows, since two tiles are what registers, TMEM and shared memory hold and one would leave the
 // tensor cores idle during its softmax; steps of 128 slots, since S of both tiles and O fill TMEM.
 // Measured (GB300, 32 query over 8 KV heads of 128 dims, blocks of 16): a prompt of 8,192
 // tokens in a window of 4,096, 291 us (1.42 PFLOP/s of visible pairs); of 4,096, all visible, 103 (1.33); heads of 64 dims
@@ -61,13 +61,13 @@ constexpr float kLazy = 8.0f;   // log2 units a maximum may be passed by before 
 constexpr int kProducers = 2;
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 
-template <int D>
+template <int D, int TILES>
 struct Cfg {
-  static constexpr int NQ = tile_groups(D);            // tiles of rows
+  static constexpr int NQ = TILES;                     // tiles of rows
   static constexpr int BN = tile_slots(D);             // slots of a step
   static constexpr int PL = D / 64;                    // 64-dim planes
   static constexpr int kStage = BN * D * 2;            // K or V of a step
-  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kStages = D == 64 ? 8 : (D == 128 && NQ == 1 ? 6 : 5);
   static constexpr int kQTile = kTileRows * D * 2;
   // Warps 0 and 1 issue the products, one for each tile: a wait, even for what has happened, and an
   // issue each take their time, and one warp could not keep the tensor cores busy (382 us
@@ -273,10 +273,10 @@ __device__ __forceinline__ int row_slot(const TileParams& P, int token, bool rai
   return s < 0 ? -1 : s;
 }
 
-template <int D, bool WIDE_BOX>
-__global__ void __launch_bounds__(Cfg<D>::kThreads, 1) k_attend_tile(const __grid_constant__ TileParams P,
+template <int D, int TILES, bool WIDE_BOX>
+__global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, 1) k_attend_tile(const __grid_constant__ TileParams P,
                                                                      const __grid_constant__ TileMaps maps) {
-  using C = Cfg<D>;
+  using C = Cfg<D, TILES>;
   constexpr int NQ = C::NQ, BN = C::BN, PL = C::PL, RC = NQ * kTileRows;
   constexpr uint32_t kIdS = idesc(128, BN, 0), kIdPV = idesc(128, D, 0, 1);
   asm volatile("griddepcontrol.launch_dependents;");
@@ -866,19 +866,19 @@ __global__ void __launch_bounds__(kJoinThreads) k_tile_join(const __grid_constan
   }
 }
 
-template <int D, bool WIDE_BOX>
+template <int D, int TILES, bool WIDE_BOX>
 cudaError_t launch_box(const TileParams& p, const TileMaps& maps, cudaStream_t s) {
-  auto kern = k_attend_tile<D, WIDE_BOX>;
+  auto kern = k_attend_tile<D, TILES, WIDE_BOX>;
   static std::atomic<uint32_t> done{0};
-  const cudaError_t e = allow_smem(kern, Cfg<D>::kAlloc, done);
+  const cudaError_t e = allow_smem(kern, Cfg<D, TILES>::kAlloc, done);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.blocks) * p.kv_heads * p.splits);
-  kern<<<grid, Cfg<D>::kThreads, Cfg<D>::kAlloc, s>>>(p, maps);
+  kern<<<grid, Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kAlloc, s>>>(p, maps);
   return cudaGetLastError();
 }
-template <int D>
+template <int D, int TILES>
 cudaError_t launch_d(const TileParams& p, const TileMaps& maps, cudaStream_t s) {
-  return p.box >= 8 ? launch_box<D, true>(p, maps, s) : launch_box<D, false>(p, maps, s);
+  return p.box >= 8 ? launch_box<D, TILES, true>(p, maps, s) : launch_box<D, TILES, false>(p, maps, s);
 }
 template <int D>
 cudaError_t launch_join_d(const TileParams& p, cudaStream_t s) {
@@ -898,9 +898,9 @@ cudaError_t launch_join_d(const TileParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tile(const TileParams& p, const TileMaps& maps, int head_dim, cudaStream_t s) {
-  if (head_dim == 64) return launch_d<64>(p, maps, s);
-  if (head_dim == 128) return launch_d<128>(p, maps, s);
-  return launch_d<256>(p, maps, s);
+  if (head_dim == 64) return p.tiles == 2 ? launch_d<64, 2>(p, maps, s) : launch_d<64, 1>(p, maps, s);
+  if (head_dim == 128) return p.tiles == 2 ? launch_d<128, 2>(p, maps, s) : launch_d<128, 1>(p, maps, s);
+  return launch_d<256, 1>(p, maps, s);
 }
 cudaError_t launch_tile_join(const TileParams& p, int head_dim, cudaStream_t s) {
   if (head_dim == 64) return launch_join_d<64>(p, s);

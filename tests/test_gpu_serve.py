@@ -324,6 +324,67 @@ def test_attend_tokens_long(d, group):
     c.close()
 
 
+@pytest.mark.parametrize("heads,hq,d,bs", [(8, 16, 128, 16), (8, 32, 64, 16), (19, 19, 128, 1), (10, 30, 64, 4), (8, 8, 128, 128), (8, 24, 64, 5)])
+@pytest.mark.parametrize("window,n_first", [(0, 0), (70, 4), (333, 200)])
+def test_attend_tokens_in_two_tiles(heads, hq, d, bs, window, n_first):
+    """More requests' rows than SMs, of which some fill a tile, two, more, or a part of one."""
+    rng = np.random.default_rng(hq)
+    counts = [1, 7, 64, 128, 200, 0, 300] + rng.integers(2, 150, size=14).tolist()
+    lens = [n + int(x) for n, x in zip(counts, rng.integers(0, 300, size=len(counts)))]
+    c = Cache(heads=heads, d=d, bs=bs, lens=lens, seed=hq)
+    _attend(c, [list(range(n - k, n)) for n, k in zip(lens, counts)], hq, window, n_first, pad=2)
+    c.close()
+
+
+@pytest.mark.parametrize("window,n_first", [(0, 0), (40, 3)])
+def test_attend_tokens_in_two_tiles_ignores_what_no_token_sees(window, n_first):
+    """As below with more rows: junk where nobody sees, blocks given back there, and a bad block in one request."""
+    lens = [150 + 11 * r for r in range(24)]
+    c = Cache(heads=8, bs=16, lens=lens, room=40, seed=6)
+    q = c.normal(24 * 50, 16, 128)
+    slots = [list(range(n - 50, n)) for n in lens]
+    clean, clean_lse, _ = _attend(c, slots, 16, window, n_first, q=q, check=range(0, 24, 5))
+    for r, n in enumerate(lens):
+        seen = np.zeros(c.tables.shape[1] * 16, bool)
+        seen[max(0, n - 49 - window) if window else 0:n] = True
+        seen[:n_first] = True
+        for s in np.nonzero(~seen)[0]:
+            c.k[0, int(c.tables[r][s // 16]), s % 16] = float("nan") if s % 2 else float("inf")
+            c.v[0, int(c.tables[r][s // 16]), s % 16] = float("inf") if s % 3 else float("nan")
+        for b in range(c.tables.shape[1]):
+            if not seen[b * 16:(b + 1) * 16].any():
+                c.d_tables[r, b] = -1 if b % 2 else 2 ** 31 - 1
+    out, lse, _ = _attend(c, slots, 16, window, n_first, q=q, check=())
+    assert torch.equal(out, clean) and torch.equal(lse, clean_lse)
+    bad = (lens[3] - 20) // 16   # seen by the last tokens of request 3
+    c.d_tables[3, bad] = c.nb
+    out, lse, _ = _attend(c, slots, 16, window, n_first, q=q, status=pic.PIC_DEV_BAD_BLOCK, check=())
+    a = slice(150, 200)
+    others = torch.ones(len(out), dtype=torch.bool, device=DEV)
+    others[a] = False
+    assert torch.equal(out[others], clean[others]) and torch.equal(lse[others], clean_lse[others])
+    keep = np.array([s for s in range(lens[3]) if s // 16 != bad and (window == 0 or s >= lens[3] - 49 - window or s < n_first)])
+    seen = torch.from_numpy(np.stack([serve.sees(s, keep, window, n_first) for s in slots[3]])).to(DEV)
+    _assert_rows(q[a], *(_wide_rows(x[0], c.tables[3], keep, 16) for x in (c.k, c.v)), seen, 128 ** -0.5, out[a], lse[a], "bad block")
+    c.close()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens,context", [(31, 3000), (33, 3000), (128, 16384), (400, 4500), (512, 512), (608, 4600)])
+def test_attend_tokens_of_one_request(d, tokens, context):
+    """Row blocks of one tile and of two, whole and in parts."""
+    c = Cache(heads=8, d=d, lens=[context], seed=tokens)
+    q = c.normal(tokens, 32, d)
+    out, lse, _ = _attend(c, [list(range(context - tokens, context))], 32, q=q, check=())
+    k, v = (_wide_rows(x[0], c.tables[0], np.arange(context), c.bs) for x in (c.k, c.v))
+    for a in range(0, tokens, 32):
+        rows = slice(a, min(tokens, a + 32))
+        at = torch.arange(context - tokens + a, context - tokens + rows.stop, device=DEV)
+        seen = torch.arange(context, device=DEV)[None] <= at[:, None]
+        _assert_rows(q[rows], k, v, seen, d ** -0.5, out[rows], lse[rows], a)
+    c.close()
+
+
 def test_attend_tokens_many_requests():
     """Hundreds of requests of a few tokens, empty ones among them."""
     rng = np.random.default_rng(3)
@@ -547,6 +608,14 @@ def test_attend_shared_batches(n_req):
 def test_attend_shared_long_prefix():
     c = Shared(30011, [3, 900, None, 17], heads=2, seed=2)
     _shared(c, 8)
+    _shared(c, 32)
+    c.close()
+
+
+@pytest.mark.parametrize("d,n_req,prefix", [(128, 5, 33000), (128, 36, 33000), (64, 36, 40003), (128, 64, 8200), (64, 70, 9001)])
+def test_attend_shared_tile_forms(d, n_req, prefix):
+    """Prefixes in row blocks of one tile and of two."""
+    c = Shared(prefix, [3 * r % 50 for r in range(n_req)], heads=8, d=d, seed=n_req)
     _shared(c, 32)
     c.close()
 
