@@ -852,6 +852,10 @@ pic_status pic_map_tokens(pic_ctx* ctx, const pic_token_map* map, void* d_worksp
  * and what the cache holds at such slots does not matter.  Between them values
  * should be finite: an infinite one makes its dimension NaN or infinite for other
  * rows of its request too.
+ * A token that is its request's only one in the call has its p enter the value product with 16
+ * bits, as in pic_attend_paged.  The p of tokens that come several to a request are
+ * rounded to bf16 for it (2^-8 of each, relative; sums and lse take them unrounded), unless the
+ * call has no more tokens than requests.
  *   q         bf16 [n_tokens][num_q_heads][head_dim], q_stride bytes between rows.
  *   out       bf16 [n_tokens][num_q_heads][head_dim], dense; must not overlap q.
  *   lse       float [n_tokens][num_q_heads] or NULL.
@@ -876,8 +880,9 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
  *   d_prefix_len    int32 [1]; outside [0, prefix_blocks * block_size] it
  *                   raises PIC_DEV_BAD_LENGTH and counts as 0.
  *   out             bf16 [n_req][num_q_heads][head_dim], dense.
- * Everything else as for pic_attend_paged (no weights, and values of the prefix
- * should be finite for every request).  PIC_ERR_UNSUPPORTED for MLA models.
+ * Everything else as for pic_attend_paged, the precision of p too (no weights, and
+ * values of the prefix should be finite for every request).  PIC_ERR_UNSUPPORTED
+ * for MLA models.
  */
 size_t pic_attend_shared_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int32_t num_q_heads);
 pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_req, int32_t num_q_heads,

@@ -79,6 +79,8 @@ int32_t tile_splits(const CtxView& c, int64_t blocks, int sms, int64_t max_slots
 // 7.9 us, of 512 14.5, 10.7, of 4,096 104, 130; 16 tokens behind 16k slots 27.4, 21.8; 608 behind 4k 60, 33;
 // 128 behind 16k 38, 49; 64 requests over a prefix of 8k 38.6, 35.5, of 32k 90, 104.  Parts by the same estimate:
 // 400 tokens behind 64k 368 us in 6, 297 in 5 (the sixth began a third round of the SMs).
+// (Over a shared prefix, whose weights have two parts, a step takes 1.7 and 1.05 us, in about the same proportion: of nine
+// such calls the estimate chose the form and parts that were the fastest, or within 6 % of them.)
 // Of several requests only the whole is known here: one tile must be the better for all rows in one request, and
 // every request's blocks must fit the SMs at once (256 requests may as well be 255 of one token and a prompt).
 struct TileShape {
@@ -415,7 +417,8 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     t.prefix_len = d_prefix_len;
     t.max_len = max_seq_len;
     // an eighth of the SMs is left to the slots behind the prefix, whose kernel starts beside the tiles (64
-    // requests over 32k slots in 16 parts, 128 CTAs, 91 us; in 19 parts, on every SM, 104)
+    // requests over 32k slots and 1,000 of their own in 14 or 16 parts, 128 CTAs, 94-95 us; in 19 parts, on every SM, 95;
+    // in 22, a second round, 113)
     const TileShape shape = tile_shape(c, n_req, 1, num_q_heads, used - used / 8, t.capacity);
     t.tiles = shape.tiles;
     t.splits = shape.splits;

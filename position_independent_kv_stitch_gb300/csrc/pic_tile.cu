@@ -23,13 +23,20 @@
 //     O += P V with P read from TMEM and V as an MN-major operand;
 //   * eight warps per tile, two threads per row: read S from TMEM, mask, raise the
 //     maximum when a score passes it by more than 2^8 (O and the sum are then rescaled, which
-//     after the first steps hardly happens), write P = exp2(s - m) as bf16 over S.
+//     after the first steps hardly happens), write P = exp2(s - m) as bf16 over S, in one part
+//     or in two.
 // Two tiles take turns: while one is in its softmax, the tensor cores work on the other's.
 // (One tile: the next step's S is made ahead.  At 256 dims O alone takes half of TMEM.)
 //
 // P is rounded to bf16 (2^-8 of each weight, where the output's own rounding is 2^-8 of
-// their sum), unnormalised: between 2^-8 and 2^8 at the maximum.  Sums, maxima and O
-// are fp32.  Masked scores are replaced, so what K holds there does not matter; V's
+// their sum), unnormalised: between 2^-8 and 2^8 at the maximum.  So it is for the tokens of
+// requests.  Over a shared prefix (PARTS = 2) P keeps 16 bits, as in the row-by-row kernel that
+// attends to the rest of the same rows: what the rounding leaves, a second bf16 part, fills the other half of S's
+// columns and is multiplied with the same rows of V, half as many products again.  Measured: a
+// prefix of 32k slots beside 1-2,048 of their own for 64 requests 93 us a call with one part, 98 with
+// two, 256 requests over 2,003 slots 125 and 128; but prompts, which the products bound, 307
+// with one, 405 with two (errors against 64 bits 2.2e-3 and 1.6e-3, the latter the output's own
+// rounding), so tokens have one.  Sums, maxima and O are fp32.  Masked scores are replaced, so what K holds there does not matter; V's
 // rows that no row of the CTA sees are zeroed in shared memory before the product.
 //
 // Bound by the chain of a step (products, scores read, maximum, exponentials, P seen by the
@@ -273,7 +280,7 @@ __device__ __forceinline__ int row_slot(const TileParams& P, int token, bool rai
   return s < 0 ? -1 : s;
 }
 
-template <int D, int TILES, bool WIDE_BOX>
+template <int D, int TILES, bool WIDE_BOX, int PARTS>
 __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, 1) k_attend_tile(const __grid_constant__ TileParams P,
                                                                      const __grid_constant__ TileMaps maps) {
   using C = Cfg<D, TILES>;
@@ -508,12 +515,14 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, 1) k_attend_tile(cons
                      desc(b + (((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), dk), kIdS, ks > 0);
       tc_commit_elect(&s_full[buf]);
     };
-    auto value = [&](int buf, uint32_t stage, bool first) {   // O += P V
+    auto value = [&](int buf, uint32_t stage, bool first) {   // O += P V (both parts of P over the same rows of V)
       const uint32_t b = static_cast<uint32_t>(dv) + stage * kStep;
 #pragma unroll
-      for (int ks = 0; ks < BN / 16; ++ks)
-        tc_mma_tmem_a_elect(tmem + kOCol + q * D, tmem + buf * BN + 8 * ks, desc(b + ((ks * 2 * PL * 1024) >> 4), dv), kIdPV,
-                            !first || ks > 0);
+      for (int ks = 0; ks < BN / 16; ++ks) {
+        const uint64_t v = desc(b + ((ks * 2 * PL * 1024) >> 4), dv);
+        tc_mma_tmem_a_elect(tmem + kOCol + q * D, tmem + buf * BN + 8 * ks, v, kIdPV, !first || ks > 0);
+        if constexpr (PARTS == 2) tc_mma_tmem_a_elect(tmem + kOCol + q * D, tmem + buf * BN + BN / 2 + 8 * ks, v, kIdPV, true);
+      }
     };
     // V of step i has landed, and its rows that no row of the CTA sees are zeros (both tiles'
     // warps write the same)
@@ -704,7 +713,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, 1) k_attend_tile(cons
       uint64_t part[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < HN; c += 32) {
-        uint32_t p[16];
+        uint32_t p[16], rest[PARTS == 2 ? 16 : 1];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float2 y = unpair(fma2(pair64(s[c + 2 * e], s[c + 2 * e + 1]), sc, neg));
@@ -712,9 +721,11 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, 1) k_attend_tile(cons
           y.y = ex2(y.y);
           part[e & 1] = add2(part[e & 1], pair64(y.x, y.y));
           p[e] = pack2(y.x, y.y);
+          if constexpr (PARTS == 2) rest[e] = pack2(y.x - bf_lo(p[e]), y.y - bf_hi(p[e]));   // (exact differences)
         }
         // (over scores that both threads of the row have read)
         tmem_st16u(tl + buf * BN + (my_half * HN + c) / 2, p);
+        if constexpr (PARTS == 2) tmem_st16u(tl + buf * BN + BN / 2 + (my_half * HN + c) / 2, rest);
       }
       const float2 sum = unpair(add2(part[0], part[1]));
       tmem_wait_st();
@@ -866,9 +877,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_tile_join(const __grid_constan
   }
 }
 
-template <int D, int TILES, bool WIDE_BOX>
+template <int D, int TILES, bool WIDE_BOX, int PARTS>
 cudaError_t launch_box(const TileParams& p, const TileMaps& maps, cudaStream_t s) {
-  auto kern = k_attend_tile<D, TILES, WIDE_BOX>;
+  auto kern = k_attend_tile<D, TILES, WIDE_BOX, PARTS>;
   static std::atomic<uint32_t> done{0};
   const cudaError_t e = allow_smem(kern, Cfg<D, TILES>::kAlloc, done);
   if (e != cudaSuccess) return e;
@@ -876,9 +887,13 @@ cudaError_t launch_box(const TileParams& p, const TileMaps& maps, cudaStream_t s
   kern<<<grid, Cfg<D, TILES>::kThreads, Cfg<D, TILES>::kAlloc, s>>>(p, maps);
   return cudaGetLastError();
 }
+template <int D, int TILES, bool WIDE_BOX>
+cudaError_t launch_parts(const TileParams& p, const TileMaps& maps, cudaStream_t s) {
+  return p.indptr == nullptr ? launch_box<D, TILES, WIDE_BOX, 2>(p, maps, s) : launch_box<D, TILES, WIDE_BOX, 1>(p, maps, s);
+}
 template <int D, int TILES>
 cudaError_t launch_d(const TileParams& p, const TileMaps& maps, cudaStream_t s) {
-  return p.box >= 8 ? launch_box<D, TILES, true>(p, maps, s) : launch_box<D, TILES, false>(p, maps, s);
+  return p.box >= 8 ? launch_parts<D, TILES, true>(p, maps, s) : launch_parts<D, TILES, false>(p, maps, s);
 }
 template <int D>
 cudaError_t launch_join_d(const TileParams& p, cudaStream_t s) {
