@@ -11,11 +11,12 @@ namespace {
 using namespace pic;
 using namespace pic::entry;
 
-// The parts of PagedParams that a call over rows takes from its arguments.
-PagedParams rows_params(const CtxView& c, const void* q, int64_t q_stride, int32_t n_rows, int32_t num_q_heads, float scale,
-                        const void* k_cache, const void* v_cache, void* out, float* lse, uint8_t* ws, int sms) {
+// The parts of PagedParams that a call over rows takes from its arguments; n_list: the rows that the workspace
+// is laid out for.
+PagedParams rows_params(const CtxView& c, const void* q, int64_t q_stride, int32_t n_rows, int64_t n_list, int32_t num_q_heads,
+                        float scale, const void* k_cache, const void* v_cache, void* out, float* lse, uint8_t* ws, int sms) {
   const pic_model_desc& m = *c.model;
-  const PagedLayout L = paged_layout(c, n_rows, num_q_heads, 0, false);
+  const PagedLayout L = paged_layout(c, n_list, num_q_heads, 0, false);
   PagedParams p{};
   p.q = static_cast<const uint8_t*>(q);
   p.q_stride = q_stride;
@@ -114,14 +115,19 @@ TileShape tile_shape(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t 
   if (n_req > 1) best.splits = tile_splits(c, tile_blocks(c, best.tiles, n_tokens, n_req, num_q_heads), sms, max_slots);
   return best;
 }
-// Workspace of a call: the row-by-row kernels' part, then the records of split tiles.
+// Rows of the row-by-row kernels' list in pic_attend_tokens: beside tiles they take the requests, of which those of
+// one token are theirs; else the tokens, which are no more than the requests where the cache has blocks.
+int64_t listed_rows(const CtxView& c, int64_t n_tokens, int64_t n_req) {
+  return c.num_cache_blocks > 0 ? std::min(n_tokens, n_req) : n_tokens;
+}
+// Workspace of a call: the row-by-row kernels' part (n_list rows), then the records of split tiles.
 struct RowsLayout {
   size_t acc, ml, total;
 };
-RowsLayout rows_layout(const CtxView& c, int64_t n_tokens, int64_t num_q_heads, int64_t splits) {
+RowsLayout rows_layout(const CtxView& c, int64_t n_list, int64_t n_tokens, int64_t num_q_heads, int64_t splits) {
   RowsLayout L{};
   const int64_t n = splits * n_tokens * num_q_heads;
-  L.acc = paged_layout(c, n_tokens, num_q_heads, 0, false).total;
+  L.acc = paged_layout(c, n_list, num_q_heads, 0, false).total;
   L.ml = align_up(L.acc + n * c.model->head_dim * sizeof(float), kWsAlign);
   L.total = align_up(L.ml + n * sizeof(float2), kWsAlign);
   return L;
@@ -197,10 +203,10 @@ pic_status check_rows(pic_ctx* ctx, const CtxView& c, const void* q, int64_t q_s
 
 size_t tokens_bytes(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
   const int64_t splits = n_tokens > n_req ? any_splits(c, n_tokens, n_req, num_q_heads) : 1;
-  return rows_layout(c, n_tokens, num_q_heads, splits > 1 ? splits : 0).total;
+  return rows_layout(c, listed_rows(c, n_tokens, n_req), n_tokens, num_q_heads, splits > 1 ? splits : 0).total;
 }
 size_t shared_bytes(const CtxView& c, int64_t n_req, int32_t num_q_heads) {
-  return rows_layout(c, n_req, num_q_heads, any_splits(c, n_req, 1, num_q_heads)).total;
+  return rows_layout(c, n_req, n_req, num_q_heads, any_splits(c, n_req, 1, num_q_heads)).total;
 }
 
 }  // namespace
@@ -298,7 +304,8 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
   int sms = 0;
   const pic_status st = check_device(ctx, bufs, sizeof(bufs) / sizeof(bufs[0]), &sms);
   if (st != PIC_OK) return st;
-  PagedParams p = rows_params(c, q, q_stride, n_tokens, num_q_heads, softmax_scale, k_cache, v_cache, out, lse,
+  const int64_t n_list = listed_rows(c, n_tokens, n_req);
+  PagedParams p = rows_params(c, q, q_stride, n_tokens, n_list, num_q_heads, softmax_scale, k_cache, v_cache, out, lse,
                               static_cast<uint8_t*>(d_ws), sms);
   p.paged = paged_view(c, d_tables, n_req, max_blocks);
   p.rows.indptr = d_indptr;
@@ -335,7 +342,7 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     t.out = out;
     t.lse = lse;
     if (t.splits > 1) {
-      const RowsLayout L = rows_layout(c, n_tokens, num_q_heads, t.splits);
+      const RowsLayout L = rows_layout(c, n_list, n_tokens, num_q_heads, t.splits);
       t.rec_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + L.acc);
       t.rec_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + L.ml);
     }
@@ -343,7 +350,7 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     if (e == cudaSuccess && n_req > 1) {
       p.rows.singles = 1;
       p.rows.after_tiles = 1;
-      p.n_req = n_req;   // the list is of requests (fewer than the tokens that the workspace is laid out for)
+      p.n_req = n_req;   // the list is of requests
       p.first = n_req > kPagedWalkRequests ? p.first : nullptr;
       e = launch_paged_rows(p, c.model->head_dim, used, cs);
     }
@@ -389,7 +396,7 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
   int sms = 0;
   const pic_status st = check_device(ctx, bufs, sizeof(bufs) / sizeof(bufs[0]), &sms);
   if (st != PIC_OK) return st;
-  PagedParams p = rows_params(c, q, q_stride, n_req, num_q_heads, softmax_scale, k_cache, v_cache, out, lse,
+  PagedParams p = rows_params(c, q, q_stride, n_req, n_req, num_q_heads, softmax_scale, k_cache, v_cache, out, lse,
                               static_cast<uint8_t*>(d_ws), sms);
   p.paged = paged_view(c, d_tables, n_req, max_blocks);
   p.lens = d_seq_lens;
@@ -423,7 +430,7 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     t.tiles = shape.tiles;
     t.splits = shape.splits;
     t.blocks = static_cast<int32_t>(tile_blocks(c, t.tiles, n_req, 1, num_q_heads));
-    const RowsLayout L = rows_layout(c, n_req, num_q_heads, t.splits);
+    const RowsLayout L = rows_layout(c, n_req, n_req, num_q_heads, t.splits);
     t.rec_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + L.acc);
     t.rec_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + L.ml);
     e = launch_tile(t, maps, c.model->head_dim, cs);
