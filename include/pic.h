@@ -769,6 +769,8 @@ pic_status pic_evict_tokens(pic_ctx* ctx, int32_t num_layers, void* k_cache, voi
  * They keep the decode loop's conventions: device arrays, sticky status,
  * nothing uploaded, allocated or waited for, captured at will, buffers of the
  * current device, workspaces of their own for calls that may run at once.
+ * The workspace sizes do not fall where tokens, requests or query heads are
+ * added: a workspace for a loop's largest call serves the smaller ones too.
  */
 
 /*

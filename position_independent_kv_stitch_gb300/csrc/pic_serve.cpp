@@ -120,21 +120,38 @@ TileShape tile_shape(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t 
 int64_t listed_rows(const CtxView& c, int64_t n_tokens, int64_t n_req) {
   return c.num_cache_blocks > 0 ? std::min(n_tokens, n_req) : n_tokens;
 }
-// Workspace of a call: the row-by-row kernels' part (n_list rows), then the records of split tiles.
+// Records that a call's tiles leave, at most, whatever the device, the slots and the number of requests.  With rows R of
+// a KV head in row blocks of B, thus b = ceil(R / B) of them or more, a row is in at most (2 SMs - 1) / (b KV heads) + 1
+// parts, and R / b <= min(R, B):
+//   records <= (2 SMs - 1) min(R, B) + R KV heads,
+// the second term of pic_attend_shared, where one part leaves records too; the tokens' are only split where
+// b KV heads < 2 SMs, so R KV heads <= (2 SMs - 1) B.  As parts fall where blocks are added the records
+// themselves go up and down with the rows; this bound never falls, so that a workspace serves smaller calls too.
+int64_t tile_records(const CtxView& c, int64_t n_tokens, int32_t num_q_heads, bool shared) {
+  const int64_t kv = c.model->num_kv_heads, rows = n_tokens * (num_q_heads / kv);
+  const int64_t block = static_cast<int64_t>(kTileRows) * most_tiles(c.model->head_dim), parts = 2 * kPagedMaxSms - 1;
+  return parts * std::min(rows, block) + (shared ? rows * kv : std::min(rows * kv, parts * block));
+}
+// Workspace of a call: the row-by-row kernels' part (n_list rows), then the tiles' records.
 struct RowsLayout {
   size_t acc, ml, total;
 };
-RowsLayout rows_layout(const CtxView& c, int64_t n_list, int64_t n_tokens, int64_t num_q_heads, int64_t splits) {
+RowsLayout rows_layout(const CtxView& c, int64_t n_list, int64_t num_q_heads, int64_t records) {
+  const int64_t kv = c.model->num_kv_heads;
   RowsLayout L{};
-  const int64_t n = splits * n_tokens * num_q_heads;
   L.acc = paged_layout(c, n_list, num_q_heads, 0, false).total;
-  L.ml = align_up(L.acc + n * c.model->head_dim * sizeof(float), kWsAlign);
-  L.total = align_up(L.ml + n * sizeof(float2), kWsAlign);
+  // (a pass more over the query heads halves their ranges: fewer heads may take more)
+  for (int64_t p = 1; p < paged_passes(static_cast<int32_t>(num_q_heads / kv)); ++p)
+    L.acc = std::max(L.acc, paged_layout(c, n_list, 16 * p * kv, 0, false).total);
+  L.ml = align_up(L.acc + records * c.model->head_dim * sizeof(float), kWsAlign);
+  L.total = align_up(L.ml + records * sizeof(float2), kWsAlign);
   return L;
 }
-// Parts at most, whatever the device and the slots (workspace sizing): larger blocks are fewer, in more parts.
-int64_t any_splits(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
-  return most_splits(c, tile_blocks(c, most_tiles(c.model->head_dim), n_tokens, n_req, num_q_heads), kPagedMaxSms);
+RowsLayout tokens_layout(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
+  return rows_layout(c, listed_rows(c, n_tokens, n_req), num_q_heads, n_tokens > 1 ? tile_records(c, n_tokens, num_q_heads, false) : 0);
+}
+RowsLayout shared_layout(const CtxView& c, int64_t n_req, int32_t num_q_heads) {
+  return rows_layout(c, n_req, num_q_heads, tile_records(c, n_req, num_q_heads, true));
 }
 
 // One cache tensor as the tiles read it: whole groups of 8 rows, planes of 64 dims
@@ -199,14 +216,6 @@ pic_status check_rows(pic_ctx* ctx, const CtxView& c, const void* q, int64_t q_s
   if (!aligned(lse, 4) || !aligned(ws, kWsAlign))
     return fail(ctx, PIC_ERR_ALIGNMENT, "lse must be 4-byte aligned, the workspace 256-byte");
   return PIC_OK;
-}
-
-size_t tokens_bytes(const CtxView& c, int64_t n_tokens, int64_t n_req, int32_t num_q_heads) {
-  const int64_t splits = n_tokens > n_req ? any_splits(c, n_tokens, n_req, num_q_heads) : 1;
-  return rows_layout(c, listed_rows(c, n_tokens, n_req), n_tokens, num_q_heads, splits > 1 ? splits : 0).total;
-}
-size_t shared_bytes(const CtxView& c, int64_t n_req, int32_t num_q_heads) {
-  return rows_layout(c, n_req, n_req, num_q_heads, any_splits(c, n_req, 1, num_q_heads)).total;
 }
 
 }  // namespace
@@ -277,7 +286,7 @@ size_t pic_attend_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_tokens, i
   if (!ctx || n_tokens < 0 || n_req < 0 || n_req > kMaxRequests) return 0;
   const CtxView c = ctx_view(ctx);
   if (c.model->kind != PIC_KIND_GQA || !paged_heads_ok(c, num_q_heads) || !paged_size_ok(n_tokens, num_q_heads)) return 0;
-  return tokens_bytes(c, n_tokens, n_req, num_q_heads);
+  return tokens_layout(c, n_tokens, n_req, num_q_heads).total;
 }
 
 pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_tokens, int32_t num_q_heads,
@@ -296,8 +305,8 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     return fail(ctx, PIC_ERR_INVALID_ARG, "null block table, offsets or slots");
   if (!aligned(d_tables, 4) || !aligned(d_indptr, 4) || !aligned(d_slot, 4))
     return fail(ctx, PIC_ERR_ALIGNMENT, "tables, offsets and slots must be 4-byte aligned");
-  const size_t need = tokens_bytes(c, n_tokens, n_req, num_q_heads);
-  if (ws_bytes < need) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  const RowsLayout L = tokens_layout(c, n_tokens, n_req, num_q_heads);
+  if (ws_bytes < L.total) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, L.total);
   if (!some) return set_error(ctx, PIC_OK, "");
   const Buffer bufs[] = {{"q", q}, {"k_cache", k_cache}, {"v_cache", v_cache}, {"block tables", d_tables}, {"offsets", d_indptr},
                          {"slots", d_slot}, {"out", out}, {"lse", lse}, {"workspace", d_ws}};
@@ -342,7 +351,6 @@ pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     t.out = out;
     t.lse = lse;
     if (t.splits > 1) {
-      const RowsLayout L = rows_layout(c, n_list, n_tokens, num_q_heads, t.splits);
       t.rec_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + L.acc);
       t.rec_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + L.ml);
     }
@@ -367,7 +375,7 @@ size_t pic_attend_shared_workspace_bytes(const pic_ctx* ctx, int32_t n_req, int3
   if (!ctx || n_req < 0) return 0;
   const CtxView c = ctx_view(ctx);
   if (c.model->kind != PIC_KIND_GQA || !paged_heads_ok(c, num_q_heads) || !paged_size_ok(n_req, num_q_heads)) return 0;
-  return shared_bytes(c, n_req, num_q_heads);
+  return shared_layout(c, n_req, num_q_heads).total;
 }
 
 pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_req, int32_t num_q_heads, float softmax_scale,
@@ -387,8 +395,8 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
                 table_capacity(c, max_blocks));
   if (!aligned(d_tables, 4) || !aligned(d_seq_lens, 4) || !aligned(d_prefix_table, 4) || !aligned(d_prefix_len, 4))
     return fail(ctx, PIC_ERR_ALIGNMENT, "tables and lengths must be 4-byte aligned");
-  const size_t need = shared_bytes(c, n_req, num_q_heads);
-  if (ws_bytes < need) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  const RowsLayout L = shared_layout(c, n_req, num_q_heads);
+  if (ws_bytes < L.total) return fail(ctx, PIC_ERR_CAPACITY, "workspace has %zu bytes, needs %zu", ws_bytes, L.total);
   if (!some) return set_error(ctx, PIC_OK, "");
   const Buffer bufs[] = {{"q", q}, {"k_cache", k_cache}, {"v_cache", v_cache}, {"prefix table", d_prefix_table},
                          {"prefix length", d_prefix_len}, {"block tables", d_tables}, {"lengths", d_seq_lens}, {"out", out},
@@ -430,7 +438,6 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     t.tiles = shape.tiles;
     t.splits = shape.splits;
     t.blocks = static_cast<int32_t>(tile_blocks(c, t.tiles, n_req, 1, num_q_heads));
-    const RowsLayout L = rows_layout(c, n_req, n_req, num_q_heads, t.splits);
     t.rec_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + L.acc);
     t.rec_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(d_ws) + L.ml);
     e = launch_tile(t, maps, c.model->head_dim, cs);

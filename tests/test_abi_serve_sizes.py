@@ -31,6 +31,32 @@ def test_prompts_do_not_take_a_record_per_token(heads, hq, d, n_req):
     pic.pic_destroy(c)
 
 
+@pytest.mark.parametrize("heads,d", [(8, 128), (1, 64), (2, 256), (3, 128), (19, 64)])
+@pytest.mark.parametrize("blocks", [1000, 0])
+def test_a_workspace_serves_smaller_calls(heads, d, blocks):
+    """Sizes never fall with more tokens, requests or query heads."""
+    c = _ctx(heads, d, blocks)
+    counts = list(range(1, 20)) + [31, 32, 33, 63, 64, 65, 127, 128, 129, 130, 200, 255, 256, 257, 511, 512, 513, 1000, 4095, 4096, 4097, 70000]
+    groups = [1, 2, 3, 4, 7, 8, 15, 16, 17, 32, 33, 48, 49, 64, 200]
+    size = pic.pic_attend_tokens_workspace_bytes
+    for group in groups:
+        for n in counts:
+            by_requests = [size(c, n, r, heads * group) for r in counts]
+            assert by_requests == sorted(by_requests), (group, n)
+        for r in counts:
+            by_tokens = [size(c, n, r, heads * group) for n in counts]
+            assert by_tokens == sorted(by_tokens), (group, r)
+        shared = [pic.pic_attend_shared_workspace_bytes(c, r, heads * group) for r in counts]
+        assert shared == sorted(shared), group
+    for n in counts:
+        for r in (1, 64, 256, 4096):
+            by_heads = [size(c, n, r, heads * group) for group in groups]
+            assert by_heads == sorted(by_heads), (n, r)
+        by_heads = [pic.pic_attend_shared_workspace_bytes(c, n, heads * group) for group in groups]
+        assert by_heads == sorted(by_heads), n
+    pic.pic_destroy(c)
+
+
 def test_of_a_cache_without_blocks_every_token_has_a_record():
     c = _ctx(2, 64, blocks=0)
     assert pic.pic_attend_tokens_workspace_bytes(c, 5000, 1, 4) >= 5000 * 4 * 64 * 4
