@@ -1926,11 +1926,11 @@ pic_status pic_query_device_status(pic_ctx* ctx, const void* d_ws, pic_stream_t 
   if (status_out) *status_out = h.status;
   if (h.status != 0)
     return fail(ctx, PIC_ERR_DEVICE_CHECK,
-                "kernel reported device status 0x%x (bit 0x1: block-table entry outside the cache, table row %u, "
-                "position %u; bit 0x2: a bounded wait gave up; 0x4: token id outside the Gear table; "
+                "kernel reported device status 0x%x (bit 0x1: block-table entry outside the cache, table row %d (-1: the "
+                "shared prefix's), position %u; bit 0x2: a bounded wait gave up; 0x4: token id outside the Gear table; "
                 "0x8: bad document offsets; 0x10: more chunks than capacity; 0x20: bad span; 0x40: sequence length outside "
                 "its table; 0x80: position beyond 2^24 - 1)",
-                h.status, h.bad_req, h.bad_pos);
+                h.status, static_cast<int32_t>(h.bad_req), h.bad_pos);
   return ok(ctx);
 }
 

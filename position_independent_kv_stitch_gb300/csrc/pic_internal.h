@@ -42,7 +42,7 @@ __host__ __device__ inline int32_t run_kind(const RunDesc& r) { return r.ntok_ki
 // Workspace layout: [header 256 B][freq table][indptr][runs], each 256-B aligned.
 struct WsHeader {
   uint32_t status;      // PIC_DEV_* bits raised by kernels
-  uint32_t bad_req;     // a block-table row that held a bad entry (diagnostic)
+  uint32_t bad_req;     // a block-table row that held a bad entry, -1: a shared prefix's table (diagnostic)
   uint32_t bad_pos;     // the position it was asked for
   uint32_t ticket;      // CTAs of a launch that have read their inputs (pic_map_tokens; 0 between launches)
   uint32_t pad[60];

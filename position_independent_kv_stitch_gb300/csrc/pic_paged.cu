@@ -340,7 +340,9 @@ __device__ __forceinline__ void attend_range(const PagedParams& P, const TileLis
       const int b = block_of(P.paged, at);
       const int32_t block = __ldg((head && P.rows.shared != 0 ? P.rows.prefix_table : x.table) + b);
       if (block < 0 || block >= P.paged.num_cache_blocks) {
-        if (lane < TT) raise_block(P.status, x.req, at);
+        // (the row from its address: one more number kept for every place would be in the way)
+        if (lane < TT)
+          raise_block(P.status, head && P.rows.shared != 0 ? kPrefixTable : static_cast<int>((x.table - P.paged.tables) / P.paged.max_blocks), at);
         return -1;
       }
       return static_cast<int>(static_cast<int64_t>(block) * P.paged.block_size + (at - b * P.paged.block_size));

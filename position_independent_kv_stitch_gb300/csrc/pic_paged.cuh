@@ -67,7 +67,9 @@ __device__ __forceinline__ void turn_cossin2(float2 pos, float4 freq, float* c, 
   s[1] = __uint_as_float(__float_as_uint(sn.y) ^ odd_y);
 }
 
-// The status word and, beside it, where the last bad block was met (WsHeader).
+// The status word and, beside it, where the last bad block was met (WsHeader): a row of the block tables, or
+// kPrefixTable for a shared prefix's own table.
+constexpr int kPrefixTable = -1;
 __device__ __forceinline__ void raise_block(uint32_t* status, int req, int slot) {
   atomicOr(status, static_cast<uint32_t>(PIC_DEV_BAD_BLOCK));
   status[1] = static_cast<uint32_t>(req);

@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(Cfg<D, TILES>::kThreads, 1) k_attend_tile(cons
           if (!S.some(b * bs, b * bs + min(bs, S.hi + 1 - b * bs))) continue;   // (b * bs <= hi: no overflow)
           const int32_t block = __ldg(table + b);
           if (block < 0 || block >= P.paged.num_cache_blocks) {
-            raise_block(P.status, w.table, b * bs);
+            raise_block(P.status, P.indptr == nullptr ? kPrefixTable : w.table, b * bs);
             bad = true;
           }
         }
