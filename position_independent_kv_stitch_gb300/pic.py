@@ -998,6 +998,12 @@ def pic_map_tokens(ctx, seq_lens, grow, block_tables, free_blocks, n_free, new_l
     _launch(ctx, lib.pic_map_tokens, indptr.get_device(), stream, (t, _addr(workspace), _size(workspace)))
 
 
+def _in_int32(n, name):
+    # (of a longer number a 32-bit argument would take the low bits)
+    if not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"{name} {n} does not fit 32 bits")
+
+
 def _rows_out(q, out, lse, cache):
     """Checks out and lse of an attention over rows q [rows][q_heads][head_dim]."""
     rows, hq, d = q.shape
@@ -1028,6 +1034,8 @@ def pic_attend_tokens(ctx, q, softmax_scale, k_cache, v_cache, block_tables, ind
     n_req = indptr.numel() - 1
     if n_req < 0:
         raise ValueError("indptr holds n_req + 1 offsets")
+    _in_int32(window, "window")
+    _in_int32(n_first, "n_first")
     _dense_int32(indptr, "indptr")
     _dense_int32(slot, "slot", n)
     max_blocks = _table_shape(block_tables, n_req)[1]
@@ -1055,6 +1063,7 @@ def pic_attend_shared(ctx, q, softmax_scale, k_cache, v_cache, prefix_table, pre
     shape = q.shape
     stride = _token_rows(q, "q", shape)
     n_req, hq, _ = shape
+    _in_int32(max_seq_len, "max_seq_len")
     _dense_int32(seq_lens, "seq_lens", n_req)
     _dense_int32(prefix_table, "prefix_table")
     _dense_int32(prefix_len, "prefix_len", 1)
