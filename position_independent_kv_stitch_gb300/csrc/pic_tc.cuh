@@ -102,26 +102,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// The same in a plain loop that looks every few dozen cycles (try_wait puts the thread to
-// sleep, and waking it took 650 cycles where a step has 2,000): for waits that last about as
-// long as a step.  Bounded at about a quarter of a second.
-__device__ __forceinline__ bool poll_or_abort(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
-  const uint32_t at = smem_u32(bar);
-  for (uint32_t i = 0; i < (1u << 24); ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (ok != 0) return true;
-    if ((i & 63) == 63 && *abort_flag) return false;
-  }
-  return false;
-}
-
 // bounded wait that also gives up once another role has aborted
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const volatile int* abort_flag,
                                               uint32_t spins) {
