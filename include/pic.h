@@ -863,6 +863,10 @@ pic_status pic_map_tokens(pic_ctx* ctx, const pic_token_map* map, void* d_worksp
  *   lse       float [n_tokens][num_q_heads] or NULL.
  *   softmax_scale  finite.
  * Results do not depend on timing.  At most 2^30 requests.  PIC_ERR_UNSUPPORTED for MLA models.
+ * What a call costs follows from its sizes too.  One of no more tokens than requests reads
+ * the cache anew for every token (it is meant for single tokens), so a chunk wants fewer rows of requests than tokens.
+ * In a call with single tokens of many requests, a chunk's slots are not shared out over the SMs as they
+ * are in a call of its own: a few tokens at the end of a long sequence are then better called apart.
  */
 size_t pic_attend_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_tokens, int32_t n_req, int32_t num_q_heads);
 pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_tokens, int32_t num_q_heads,

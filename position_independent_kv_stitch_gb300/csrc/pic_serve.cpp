@@ -64,7 +64,9 @@ int64_t most_splits(const CtxView& c, int64_t blocks, int sms) {
 }
 // Parts where several requests' blocks differ in length: as many as there are SMs for, of at least
 // four steps each; and parts enough for two rounds of the SMs
-// where a part keeps 16 steps (recomputed heads of 4 sequences of 16k: 244 us whole, 176 in two parts).
+// where a part keeps 16 steps (recomputed heads of 4 sequences of 16k, 136 CTAs: 167 us in the three parts that it gives,
+// 189 whole, 197 in two, 181 in four).  Requests of one token count as a row block here, though the tiles take none of
+// them: a chunk beside many is not split.
 int32_t tile_splits(const CtxView& c, int64_t blocks, int sms, int64_t max_slots) {
   const int64_t ctas = std::max<int64_t>(1, blocks * c.model->num_kv_heads), step = tile_slots(c.model->head_dim);
   const int64_t fill = std::min(sms / ctas, max_slots / (4 * step)), even = std::min(most_splits(c, blocks, sms), max_slots / (16 * step));
@@ -432,8 +434,8 @@ pic_status pic_attend_shared(pic_ctx* ctx, const void* q, int64_t q_stride, int3
     t.prefix_len = d_prefix_len;
     t.max_len = max_seq_len;
     // an eighth of the SMs is left to the slots behind the prefix, whose kernel starts beside the tiles (64
-    // requests over 32k slots and 1,000 of their own in 14 or 16 parts, 128 CTAs, 94-95 us; in 19 parts, on every SM, 95;
-    // in 22, a second round, 113)
+    // requests over 32k slots and 1-2,048 of their own: 12 parts 101 us, 14 96, 16 (128 CTAs) 94, 18 95, 19 (every SM)
+    // 106)
     const TileShape shape = tile_shape(c, n_req, 1, num_q_heads, used - used / 8, t.capacity);
     t.tiles = shape.tiles;
     t.splits = shape.splits;
