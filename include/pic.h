@@ -854,19 +854,20 @@ pic_status pic_map_tokens(pic_ctx* ctx, const pic_token_map* map, void* d_worksp
  * and what the cache holds at such slots does not matter.  Between them values
  * should be finite: an infinite one makes its dimension NaN or infinite for other
  * rows of its request too.
- * A token that is its request's only one in the call has its p enter the value product with 16
- * bits, as in pic_attend_paged.  The p of tokens that come several to a request are
- * rounded to bf16 for it (2^-8 of each, relative; sums and lse take them unrounded), unless the
- * call has no more tokens than requests.
+ * In a call of no more tokens than requests, and beside other requests for a token that is
+ * its request's only one, p enters the value product with 16 bits, as in
+ * pic_attend_paged.  Other tokens have theirs rounded to bf16 for it (2^-8 of each,
+ * relative; sums and lse take them unrounded).
  *   q         bf16 [n_tokens][num_q_heads][head_dim], q_stride bytes between rows.
  *   out       bf16 [n_tokens][num_q_heads][head_dim], dense; must not overlap q.
  *   lse       float [n_tokens][num_q_heads] or NULL.
  *   softmax_scale  finite.
  * Results do not depend on timing.  At most 2^30 requests.  PIC_ERR_UNSUPPORTED for MLA models.
- * What a call costs follows from its sizes too.  One of no more tokens than requests reads
- * the cache anew for every token (it is meant for single tokens), so a chunk wants fewer rows of requests than tokens.
- * In a call with single tokens of many requests, a chunk's slots are not shared out over the SMs as they
- * are in a call of its own: a few tokens at the end of a long sequence are then better called apart.
+ * What a call costs follows from its sizes too.  One of no more tokens than requests
+ * reads the cache anew for every token (it is meant for single tokens), so a chunk wants
+ * fewer requests than tokens.  Beside single tokens of many requests a chunk's
+ * slots are not shared out over the SMs as they are in a call of its own: a few tokens at
+ * the end of a long sequence are then better called apart.
  */
 size_t pic_attend_tokens_workspace_bytes(const pic_ctx* ctx, int32_t n_tokens, int32_t n_req, int32_t num_q_heads);
 pic_status pic_attend_tokens(pic_ctx* ctx, const void* q, int64_t q_stride, int32_t n_tokens, int32_t num_q_heads,

@@ -31,12 +31,13 @@
 // P is rounded to bf16 (2^-8 of each weight, where the output's own rounding is 2^-8 of
 // their sum), unnormalised: between 2^-8 and 2^8 at the maximum.  So it is for the tokens of
 // requests.  Over a shared prefix (PARTS = 2) P keeps 16 bits, as in the row-by-row kernel that
-// attends to the rest of the same rows: what the rounding leaves, a second bf16 part, fills the other half of S's
-// columns and is multiplied with the same rows of V, half as many products again.  Measured: a
-// prefix of 32k slots beside 1-2,048 of their own for 64 requests 93 us a call with one part, 98 with
-// two, 256 requests over 2,003 slots 125 and 128; but prompts, which the products bound, 307
-// with one, 405 with two (errors against 64 bits 2.2e-3 and 1.6e-3, the latter the output's own
-// rounding), so tokens have one.  Sums, maxima and O are fp32.  Masked scores are replaced, so what K holds there does not matter; V's
+// attends to the rest of the same rows: what the rounding leaves, a second bf16 part, fills the
+// other half of S's columns and is multiplied with the same rows of V, half as many products
+// again.  Measured: a prefix of 32k slots beside 1-2,048 of their own for 64 requests 93 us a
+// call with one part, 98 with two, 256 requests over 2,003 slots 125 and 128; but a prompt of 8,192
+// tokens in a window of 4,096, which the products bound, 307 with one, 405 with two (errors against 64
+// bits 2.2e-3 and 1.6e-3, the latter the output's own rounding), so tokens have one.
+// Sums, maxima and O are fp32.  Masked scores are replaced, so what K holds there does not matter; V's
 // rows that no row of the CTA sees are zeroed in shared memory before the product.
 //
 // Bound by the chain of a step (products, scores read, maximum, exponentials, P seen by the
